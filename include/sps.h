@@ -357,6 +357,96 @@ sps_status sps_cosine_chunk_half(const sps_queries *q, const sps_items *items, i
                                  uint16_t *out, int64_t ld_out, double *row_sums, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Rows of scores: selection                                           */
+/* ------------------------------------------------------------------ */
+
+/* Element types of a view of scores. */
+enum { SPS_F32 = 0, SPS_F16 = 1, SPS_BF16 = 2 };
+
+/* Rows of scores, or a chunk of their columns: element (r, j) is at
+ * data[r * ld + j] and is the score of row r and column col_begin + j of the
+ * whole (for chunk c of a prepared corpus, col_begin = c * chunk_size).
+ * data: DEVICE, aligned to its element only; ld >= n_cols, so a view may be a
+ * part of a wider matrix. Rows, col_begin and col_begin + n_cols are below
+ * 2^31 - 1. */
+typedef struct {
+  const void *data;
+  int32_t dtype; /* SPS_F32, SPS_F16 (what sps_cosine_chunk_half writes) or SPS_BF16 */
+  int64_t n_rows;
+  int64_t n_cols;
+  int64_t ld;
+  int64_t col_begin;
+} sps_scores;
+
+/* Selection of the best scores, the step after the full matrix (§2.3: the
+ * pages keep every score; what a user then answers with are the best). The
+ * key of score x in row r is fl32(offset[r] + x); a key that is NaN or -inf
+ * is no candidate (a struck-out item is a score of -inf), every other one is,
+ * the type's lowest value and +inf included. Candidates are ordered by key,
+ * larger first, equal keys (both zeros are equal) by the lower row of their
+ * group, then by the lower column. Results are exact and bitwise
+ * reproducible, and do not depend on how the columns are cut into chunks. */
+
+/* Bytes of the workspace of sps_select_chunk (0 for many rows). Pure host. */
+sps_status sps_select_workspace_size(int64_t n_rows, int64_t n_cols, int32_t k, size_t *bytes);
+
+/* Join a chunk of columns to the running best k of every row (asynchronous).
+ * top_scores, top_cols: DEVICE float[n_rows * k], int32[n_rows * k]: row r's
+ * best so far, best first; places that no candidate fills hold -inf and -1.
+ * With first != 0 they need not be initialised, otherwise they are those of
+ * earlier calls with the same k and offsets over other columns (chunks in any
+ * order; a column offered twice takes two places). offsets (nullable): DEVICE
+ * float[n_rows]. k: 1..256. workspace: DEVICE, 16-byte aligned, used until the
+ * call's stream work is done (NULL where the sizing call says 0). Errors:
+ * SPS_ERR_INVALID_ARGUMENT, SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW. */
+sps_status sps_select_chunk(const sps_scores *scores, const float *offsets, int32_t k,
+                            int32_t first, float *top_scores, int32_t *top_cols, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Bytes of the workspace of sps_beam_select. Pure host. */
+sps_status sps_beam_workspace_size(int64_t n_rows, int64_t n_cols, int32_t k, size_t *bytes);
+
+/* One step of a beam search (asynchronous): rows [g * beams, (g + 1) * beams)
+ * are the beams of group g, and the best k of (beam, column) of each group are
+ * kept by the key fl32(beam_scores[row] + score). A beam whose score is -inf
+ * takes no part. Outputs, DEVICE, [n_rows / beams][k], best first: the keys,
+ * the parent's row (in 0..n_rows-1) and the column; places that no candidate
+ * fills hold -inf, -1 and -1. beam_scores: DEVICE float[n_rows] (nullable: 0).
+ * k: 1..256, and may differ from beams. n_rows is a multiple of beams.
+ * workspace: as for sps_select_chunk. */
+sps_status sps_beam_select(const sps_scores *scores, const float *beam_scores, int32_t beams,
+                           int32_t k, float *out_scores, int32_t *out_parents, int32_t *out_cols,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* The last part of a beam step whose columns came in chunks (asynchronous):
+ * top_scores and top_cols are the n_rows lists of k_in that sps_select_chunk
+ * kept with the beams' scores as its offsets; outputs as sps_beam_select's,
+ * and equal to them where k_in >= k. */
+sps_status sps_beam_join(const float *top_scores, const int32_t *top_cols, int64_t n_rows,
+                         int32_t k_in, int32_t beams, int32_t k, float *out_scores,
+                         int32_t *out_parents, int32_t *out_cols, void *stream);
+
+/* A state that every beam carries: n_rows rows of row_bytes bytes each,
+ * src_stride bytes apart, and room for n_out rows dst_stride bytes apart. */
+typedef struct {
+  const void *src;
+  void *dst;
+  int64_t row_bytes;
+  int64_t src_stride;
+  int64_t dst_stride;
+} sps_state;
+
+/* States follow their parents (asynchronous): row j of every dst becomes row
+ * parents[j] of its src, for j < n_out; zeros where parents[j] is outside
+ * [0, n_rows) (a place of sps_beam_select that stayed empty). One parent may
+ * have many rows. parents: DEVICE int32[n_out]; states: a HOST array, read
+ * before the call returns. Bytes between rows are not touched. Errors:
+ * SPS_ERR_INVALID_ARGUMENT (NULL, a stride below row_bytes, a dst that
+ * overlaps a src), SPS_ERR_OVERFLOW. */
+sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const int32_t *parents,
+                              int64_t n_out, int64_t n_rows, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Block-Sparse CSR codec                                              */
 /* ------------------------------------------------------------------ */
 

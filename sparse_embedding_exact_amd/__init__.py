@@ -20,6 +20,7 @@ Typical use::
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -63,6 +64,16 @@ class _SliceView(ctypes.Structure):
                 ("item_inv_norm", ctypes.c_void_p)]
 
 
+class _Scores(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("n_rows", ctypes.c_int64),
+                ("n_cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("col_begin", ctypes.c_int64)]
+
+
+class _State(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
+                ("src_stride", ctypes.c_int64), ("dst_stride", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -94,6 +105,12 @@ SIGNATURES = {
     "sps_items_half_workspace_size": (_I32, [_P, ctypes.POINTER(_SZ)]),
     "sps_items_enable_half": (_I32, [_P, _P, _SZ, _P]),
     "sps_cosine_chunk_half": (_I32, [_P, _P, _I32, _P, _I64, _P, _P]),
+    "sps_select_workspace_size": (_I32, [_I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "sps_select_chunk": (_I32, [ctypes.POINTER(_Scores), _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
+    "sps_beam_workspace_size": (_I32, [_I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "sps_beam_select": (_I32, [ctypes.POINTER(_Scores), _P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "sps_beam_join": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "sps_reorder_states": (_I32, [ctypes.POINTER(_State), _I32, _P, _I64, _I64, _P]),
     "sps_row_inv_norms": (_I32, [ctypes.POINTER(_Csr), _P, _P]),
     "sps_bsc_offsets_bytes": (_I32, [_I64, ctypes.POINTER(_SZ)]),
     "sps_bsc_encode_sizes": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P, ctypes.POINTER(_I64)]),
@@ -538,6 +555,210 @@ def cosine_stream_host(q: Queries, items: Items, chunk_begin: int, chunk_end: in
                                        host_out.data_ptr(), ld_host, b0.data_ptr(),
                                        b1.data_ptr(), ld_dev, rs, int(s.cuda_stream),
                                        int(cs.cuda_stream)))
+
+
+# ---------------------------------------------------------------------------
+# rows of scores: selection
+
+_SCORE_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _here(*tensors) -> None:
+    """Device tensors of the current device: a launch goes to that device's streams."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None:
+            assert t.is_cuda and t.get_device() == cur, \
+                "tensors must be on the current device (torch.cuda.set_device)"
+
+
+def _view(x: torch.Tensor, col_begin: int = 0) -> _Scores:
+    """A 2-d tensor of scores (rows contiguous, any row stride) as a view of columns
+    [col_begin, col_begin + x.shape[1])."""
+    assert x.dim() == 2 and x.dtype in _SCORE_TYPES, \
+        "scores must be (rows, columns) of float32, float16 or bfloat16"
+    n, m = x.shape
+    assert x.stride(1) == 1 or m <= 1, "rows must be contiguous"
+    ld = x.stride(0) if n > 1 else m
+    return _Scores(x.data_ptr() if n and m else None, _SCORE_TYPES[x.dtype], n, m, ld, col_begin)
+
+
+def _rows_f32(t, n: int, what: str):
+    """The address of a contiguous float32 vector of n values, None for None."""
+    if t is None:
+        return None
+    assert t.dtype == torch.float32 and t.is_contiguous() and t.numel() == n, \
+        "%s must be %d contiguous float32 values" % (what, n)
+    return t.data_ptr()
+
+
+def _on(stream):
+    """Allocations inside belong to `stream` (the current one for None)."""
+    return torch.cuda.stream(stream) if stream is not None else _NO_STREAM
+
+
+class _NoStream:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *a):
+        pass
+
+
+_NO_STREAM = _NoStream()
+
+
+@functools.lru_cache(maxsize=256)
+def _sized(name: str, *args) -> int:
+    n = _SZ()
+    _check(getattr(_lib, name)(*args, ctypes.byref(n)))
+    return n.value
+
+
+@dataclass
+class TopRows:
+    """The best k of every row, best first: scores float32 (n_rows, k) and columns int32
+    (n_rows, k); -inf and -1 where a row has fewer candidates."""
+    scores: torch.Tensor
+    cols: torch.Tensor
+
+    @property
+    def k(self) -> int:
+        return int(self.scores.shape[1])
+
+
+@dataclass
+class BeamStep:
+    """The best k of each group of beams, best first: scores float32, the parents' rows
+    int32 and the columns int32, each (groups, k); -inf, -1 and -1 in places that no
+    candidate fills."""
+    scores: torch.Tensor
+    parents: torch.Tensor
+    cols: torch.Tensor
+
+
+def top_rows(n_rows: int, k: int, device="cuda") -> TopRows:
+    """Room for the best k of n_rows rows (filled by select_chunk with first=True)."""
+    return TopRows(torch.empty(n_rows, k, dtype=torch.float32, device=device),
+                   torch.empty(n_rows, k, dtype=torch.int32, device=device))
+
+
+def select_chunk(scores: torch.Tensor, top: TopRows, col_begin: int = 0,
+                 offsets: torch.Tensor | None = None, first: bool = False, stream=None) -> None:
+    """Join a chunk of columns (scores[:, j] being column col_begin + j) to the running
+    best k of every row, by fl32(offsets[row] + score), ties to the lower column. NaN and
+    -inf are no candidates. first=True starts the lists; chunks may come in any order."""
+    load_library()
+    _here(scores, top.scores, top.cols, offsets)
+    v = _view(scores, col_begin)
+    n, k = v.n_rows, top.scores.shape[1]
+    assert top.scores.shape == (n, k) and top.cols.shape == (n, k)
+    assert top.scores.dtype == torch.float32 and top.cols.dtype == torch.int32
+    assert top.scores.is_contiguous() and top.cols.is_contiguous()
+    nb = _sized("sps_select_workspace_size", n, v.n_cols, k)
+    with _on(stream):
+        ws = torch.empty(nb, dtype=torch.uint8, device=scores.device) if nb else None
+        _check(_lib.sps_select_chunk(ctypes.byref(v), _rows_f32(offsets, n, "offsets"), k,
+                                     int(first), top.scores.data_ptr(), top.cols.data_ptr(),
+                                     ws.data_ptr() if nb else None, nb, _stream_ptr(stream)))
+
+
+def _beam_step(groups: int, k: int, device) -> BeamStep:
+    i = torch.empty(2, groups, k, dtype=torch.int32, device=device)
+    return BeamStep(torch.empty(groups, k, dtype=torch.float32, device=device), i[0], i[1])
+
+
+def beam_select(scores: torch.Tensor, beam_scores: torch.Tensor | None, beams: int,
+                k: int | None = None, col_begin: int = 0, stream=None) -> BeamStep:
+    """One step of a beam search over whole rows: of each group of `beams` consecutive rows,
+    the best k (default: beams) of (beam, column) by fl32(beam_scores[row] + score), ties to
+    the lower row, then the lower column. A beam whose score is -inf takes no part."""
+    load_library()
+    _here(scores, beam_scores)
+    v = _view(scores, col_begin)
+    k = beams if k is None else k
+    assert beams >= 1 and v.n_rows % beams == 0, "rows must be groups of %d beams" % beams
+    bs = _rows_f32(beam_scores, v.n_rows, "beam_scores")
+    nb = _sized("sps_beam_workspace_size", v.n_rows, v.n_cols, k)
+    with _on(stream):
+        out = _beam_step(v.n_rows // beams, k, scores.device)
+        ws = torch.empty(nb, dtype=torch.uint8, device=scores.device)
+        _check(_lib.sps_beam_select(ctypes.byref(v), bs, beams, k, out.scores.data_ptr(),
+                                    out.parents.data_ptr(), out.cols.data_ptr(), ws.data_ptr(), nb,
+                                    _stream_ptr(stream)))
+    return out
+
+
+def beam_join(top: TopRows, beams: int, k: int | None = None, stream=None) -> BeamStep:
+    """beam_select's step from the running lists that select_chunk kept over chunks of
+    columns with the beams' scores as its offsets (equal to it where top.k >= k)."""
+    load_library()
+    _here(top.scores, top.cols)
+    n, k_in = top.scores.shape
+    assert top.cols.shape == (n, k_in)
+    assert top.scores.dtype == torch.float32 and top.cols.dtype == torch.int32
+    assert top.scores.is_contiguous() and top.cols.is_contiguous()
+    assert beams >= 1 and n % beams == 0, "rows must be groups of %d beams" % beams
+    k = beams if k is None else k
+    with _on(stream):
+        out = _beam_step(n // beams, k, top.scores.device)
+        _check(_lib.sps_beam_join(top.scores.data_ptr(), top.cols.data_ptr(), n, k_in, beams, k,
+                                  out.scores.data_ptr(), out.parents.data_ptr(),
+                                  out.cols.data_ptr(), _stream_ptr(stream)))
+    return out
+
+
+def reorder_states(states, parents: torch.Tensor, outs=None, stream=None) -> list:
+    """States follow their parents: out[j] = state[parents[j]] for every tensor of `states`
+    (first dimension the beams' rows, each row contiguous, any types), zeros where parents[j]
+    is no row. parents: int32, any shape (BeamStep.parents). Returns the outs (allocated if
+    not given; they may not overlap any state)."""
+    load_library()
+    states = list(states)
+    _here(parents, *states)
+    assert parents.dtype == torch.int32 and parents.is_contiguous()
+    n = parents.numel()
+    rows = states[0].shape[0] if states else 0
+    with _on(stream):
+        if outs is None:
+            outs = [torch.empty((n,) + tuple(t.shape[1:]), dtype=t.dtype, device=t.device)
+                    for t in states]
+        else:
+            outs = list(outs)
+            _here(*outs)
+        assert len(outs) == len(states)
+        arr = (_State * max(len(states), 1))()
+        for i, (t, o) in enumerate(zip(states, outs)):
+            assert t.dim() >= 1 and t.shape[0] == rows, "states must have the same rows"
+            assert o.dtype == t.dtype and o.shape[0] == n and o.shape[1:] == t.shape[1:]
+            size = t.element_size()
+            width = size
+            for d in t.shape[1:]:
+                width *= d
+            for x in (t, o):  # a row is one run of bytes
+                assert x.is_contiguous() or x[:1].is_contiguous(), "rows must be contiguous"
+            arr[i] = _State(t.data_ptr(), o.data_ptr(), width,
+                            t.stride(0) * size if rows > 1 else width,
+                            o.stride(0) * size if n > 1 else width)
+        _check(_lib.sps_reorder_states(arr, len(states), parents.data_ptr(), n, rows,
+                                       _stream_ptr(stream)))
+    return outs
+
+
+def bulk_select(queries: CSR, items: CSR, k: int, chunk_size: int = 8192) -> TopRows:
+    """The best k items of every query, of all of them (exact): every chunk scored and
+    joined to the running lists. The score matrix is never kept; bulk_similarity's loop."""
+    it = prepare(items, chunk_size)
+    q = prepare_queries(queries, it)
+    dev = queries.indptr.device
+    top = top_rows(queries.n_rows, k, dev)
+    buf = torch.empty(queries.n_rows, min(chunk_size, it.n_items), dtype=torch.float32, device=dev)
+    if it.num_chunks == 0:
+        select_chunk(buf, top, 0, first=True)
+    for c in range(it.num_chunks):
+        cosine_chunk(q, it, c, buf)
+        select_chunk(buf[:, :it.chunk_len(c)], top, c * chunk_size, first=c == 0)
+    return top
 
 
 def row_inv_norms(m: CSR, stream=None) -> torch.Tensor:

@@ -224,6 +224,14 @@ struct sps_queries {
   double *rs_part;
 };
 
+int32_t sps::set_error(int32_t status, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return status;
+}
+
 namespace {
 // halves per 16-row group of a query batch's heavy-dim tiles: one tile per
 // block the items' slab holds

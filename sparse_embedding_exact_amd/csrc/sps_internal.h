@@ -8,6 +8,10 @@
 
 namespace sps {
 
+// Stores the calling thread's error message (sps_last_error_message) and
+// returns `status`, for the C entry points outside sps_api.hip.
+int32_t set_error(int32_t status, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+
 // flags block (device, 16 int32): [0] structural fault bits (1 indptr,
 // 4 index range), [1] other fault bits (2 order/duplicate, 8 non-finite),
 // [2..3] uint64 min key (row << 3 | reason code) of the first faulty row.

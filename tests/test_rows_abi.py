@@ -1,0 +1,114 @@
+"""The refusals of the entry points on rows of scores, without a GPU: every
+call here returns its documented status before any device work."""
+import ctypes
+
+import pytest
+
+import sparse_embedding_exact_amd as sps
+
+INV, WS, OVF = -1, -4, -6
+P = 0x10000  # stands for a device address: never read
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return sps.load_library()
+
+
+def view(data=P, dtype=0, rows=8, cols=100, ld=100, begin=0):
+    return ctypes.byref(sps._Scores(data, dtype, rows, cols, ld, begin))
+
+
+BAD_VIEWS = [
+    (dict(data=None), INV), (dict(dtype=3), INV), (dict(dtype=-1), INV), (dict(rows=-1), INV),
+    (dict(cols=-1), INV), (dict(begin=-1), INV), (dict(ld=99), INV), (dict(data=P + 2), INV),
+    (dict(data=P + 1, dtype=1), INV), (dict(rows=2**31), OVF), (dict(cols=2**31, ld=2**31), OVF),
+    (dict(begin=2**31 - 50), OVF), (dict(ld=2**62), OVF),
+]
+
+
+@pytest.mark.parametrize("kw,want", BAD_VIEWS)
+def test_bad_views(lib, kw, want):
+    assert lib.sps_select_chunk(view(**kw), None, 4, 1, P, P, P, 1 << 30, None) == want
+    assert lib.sps_beam_select(view(**kw), None, 1, 4, P, P, P, P, 1 << 30, None) == want
+    assert lib.sps_last_error_message()
+
+
+@pytest.mark.parametrize("k", [0, -1, 257])
+def test_bad_k(lib, k):
+    n = ctypes.c_size_t()
+    assert lib.sps_select_workspace_size(8, 100, k, ctypes.byref(n)) == INV
+    assert lib.sps_beam_workspace_size(8, 100, k, ctypes.byref(n)) == INV
+    assert lib.sps_select_chunk(view(), None, k, 1, P, P, P, 1 << 30, None) == INV
+    assert lib.sps_beam_select(view(), None, 1, k, P, P, P, P, 1 << 30, None) == INV
+    assert lib.sps_beam_join(P, P, 8, k, 1, 4, P, P, P, None) == INV
+    assert lib.sps_beam_join(P, P, 8, 4, 1, k, P, P, P, None) == INV
+
+
+def test_select_refusals(lib):
+    n = ctypes.c_size_t()
+    assert lib.sps_select_workspace_size(8, 100, 4, None) == INV
+    assert lib.sps_beam_workspace_size(8, 100, 4, None) == INV
+    assert lib.sps_select_workspace_size(-1, 100, 4, ctypes.byref(n)) == INV
+    assert lib.sps_select_workspace_size(2**31, 100, 4, ctypes.byref(n)) == OVF
+    assert lib.sps_select_chunk(None, None, 4, 1, P, P, None, 0, None) == INV
+    assert lib.sps_select_chunk(view(), None, 4, 1, None, P, None, 0, None) == INV
+    assert lib.sps_select_chunk(view(), None, 4, 1, P, None, None, 0, None) == INV
+    # few long rows need a workspace
+    wide = dict(rows=2, cols=100000, ld=100000)
+    assert lib.sps_select_workspace_size(2, 100000, 4, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.sps_select_chunk(view(**wide), None, 4, 1, P, P, None, 0, None) == INV
+    assert lib.sps_select_chunk(view(**wide), None, 4, 1, P, P, P, n.value - 1, None) == WS
+    assert lib.sps_select_chunk(view(**wide), None, 4, 1, P, P, P + 8, n.value, None) == INV
+
+
+def test_beam_refusals(lib):
+    n = ctypes.c_size_t()
+    assert lib.sps_beam_workspace_size(8, 100, 4, ctypes.byref(n)) == 0 and n.value == 8 * 4 * 8
+    for beams in (0, -1, 3):
+        assert lib.sps_beam_select(view(), None, beams, 4, P, P, P, P, n.value, None) == INV
+        assert lib.sps_beam_join(P, P, 8, 4, beams, 4, P, P, P, None) == INV
+    assert lib.sps_beam_select(view(), None, 2, 4, None, P, P, P, n.value, None) == INV
+    assert lib.sps_beam_select(view(), None, 2, 4, P, P, P, None, 0, None) == INV
+    assert lib.sps_beam_select(view(), None, 2, 4, P, P, P, P, n.value - 1, None) == WS
+    assert lib.sps_beam_join(None, P, 8, 4, 2, 4, P, P, P, None) == INV
+    assert lib.sps_beam_join(P, P, -8, 4, 2, 4, P, P, P, None) == INV
+    assert lib.sps_beam_join(P, P, 2**31, 4, 2, 4, P, P, P, None) == OVF
+    # more candidates in a group than a place can number
+    assert lib.sps_beam_join(P, P, 2**30, 256, 2**30, 4, P, P, P, None) == OVF
+
+
+def state(src=P, dst=2 * P, row=64, ss=64, ds=64):
+    return sps._State(src, dst, row, ss, ds)
+
+
+@pytest.mark.parametrize("st,want", [
+    (state(src=None), INV), (state(dst=None), INV), (state(row=-1), INV), (state(ss=63), INV),
+    (state(ds=63), INV), (state(ss=2**62), OVF), (state(ds=2**62), OVF),
+    (state(dst=P), INV), (state(dst=P + 7 * 64 + 63), INV), (state(dst=P - 7 * 64 - 63), INV),
+])
+def test_reorder_refusals(lib, st, want):
+    assert lib.sps_reorder_states(ctypes.byref(st), 1, P, 8, 8, None) == want
+
+
+def test_reorder_counts(lib):
+    st = state()
+    assert lib.sps_reorder_states(None, 1, P, 8, 8, None) == INV
+    assert lib.sps_reorder_states(ctypes.byref(st), 1, None, 8, 8, None) == INV
+    assert lib.sps_reorder_states(ctypes.byref(st), -1, P, 8, 8, None) == INV
+    assert lib.sps_reorder_states(ctypes.byref(st), 1, P, -8, 8, None) == INV
+    assert lib.sps_reorder_states(ctypes.byref(st), 1, P, 2**31, 8, None) == OVF
+    # nothing to do: no launch
+    assert lib.sps_reorder_states(ctypes.byref(st), 0, P, 8, 8, None) == 0
+    assert lib.sps_reorder_states(ctypes.byref(st), 1, P, 0, 8, None) == 0
+    # an output that overlaps another state's source
+    two = (sps._State * 2)(state(), state(src=8 * P, dst=P + 64))
+    assert lib.sps_reorder_states(two, 2, P, 8, 8, None) == INV
+
+
+def test_nothing_to_do(lib):
+    assert lib.sps_select_chunk(view(rows=0, data=None), None, 4, 1, None, None, None, 0,
+                                None) == 0
+    assert lib.sps_beam_select(view(rows=0, data=None), None, 2, 4, None, None, None, None, 0,
+                               None) == 0
+    assert lib.sps_beam_join(None, None, 0, 4, 2, 4, None, None, None, None) == 0
