@@ -447,6 +447,86 @@ sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const i
                               int64_t n_out, int64_t n_rows, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Rows of scores: distillation                                        */
+/* ------------------------------------------------------------------ */
+
+/* Distillation from a teacher's top list, for embeddings that are trained:
+ * the loss of every row of scores s over n_cols columns against the teacher's
+ * k best (id, logit) of that row, and its gradient. With z = s / temperature
+ * and q = softmax(z) over all columns, T the listed columns:
+ *   without teacher_lse: p = softmax over the list of (logit / temperature),
+ *     loss = sum over T of p (log p - log q)
+ *     d loss / d s_j = (q_j - [j in T] p_j) / temperature
+ *   with teacher_lse (the teacher's log-sum-exp of logit / temperature over
+ *   all columns): p = exp(logit / temperature - teacher_lse), the mass
+ *   p_rest = max(0, 1 - sum p) belongs to the columns outside the list as one
+ *   class, whose student mass is q_rest:
+ *     loss = sum over T of p (log p - log q) + p_rest (log p_rest - log q_rest)
+ *     d loss / d s_j = (m q_j - p_j) / temperature                   j in T
+ *                    = (m - p_rest / q_rest) q_j / temperature       otherwise
+ *     with m = sum p + p_rest (1 unless the list's mass exceeds 1).
+ * (0 log 0 = 0.) Listed entries that take no part: an id outside [0, n_cols)
+ * (pad with -1), a logit of -inf, an id that an earlier entry which takes part
+ * has.
+ * A row without any entry left, or whose scores are all -inf, has loss 0 and
+ * gradient 0. A score of -inf has q = 0 and gradient 0 outside the list; a
+ * listed one with p > 0 makes the loss +inf. NaN (and +inf scores) make their
+ * own row's loss and gradient NaN. Sums and the statistics of the softmax are
+ * kept in float32 per thread and float64 beyond; gradients are rounded once to
+ * their type. Results are bitwise reproducible. */
+
+/* Opaque host handle of a batch's lists and running statistics. */
+typedef struct sps_distill sps_distill;
+
+/* Bytes of the workspace of a batch of n_rows lists of k (1..1024). Pure host. */
+sps_status sps_distill_workspace_size(int64_t n_rows, int32_t k, size_t *bytes);
+
+/* Prepare the teacher's lists (asynchronous): ids DEVICE int32[n_rows * k],
+ * logits DEVICE float[n_rows * k], teacher_lse DEVICE float[n_rows] or NULL;
+ * they may be released once this stream work has completed. temperature: 1e-6
+ * to 1e6. workspace: DEVICE, 256-byte aligned, caller-owned, kept
+ * alive while the handle is used. On success *out receives a new handle (free
+ * with sps_distill_destroy). */
+sps_status sps_distill_prepare(const int32_t *ids, const float *logits, const float *teacher_lse,
+                               int64_t n_rows, int32_t k, int64_t n_cols, float temperature,
+                               void *workspace, size_t workspace_bytes, void *stream,
+                               sps_distill **out);
+
+/* Take in a chunk of the columns (asynchronous), in any order, each column
+ * once between two calls with first != 0 (which forget what came before).
+ * scores->n_rows is the batch's, col_begin + n_cols at most its n_cols. Calls
+ * on one handle must be ordered on one stream. */
+sps_status sps_distill_chunk(sps_distill *h, const sps_scores *scores, int32_t first,
+                             void *stream);
+
+/* The rows' losses once all columns are in (asynchronous): loss DEVICE
+ * float[n_rows] (not averaged). lse (nullable): DEVICE float[n_rows], the
+ * student's log-sum-exp of s / temperature. */
+sps_status sps_distill_loss(sps_distill *h, float *loss, float *lse, void *stream);
+
+/* The gradient about a chunk of scores (asynchronous, after sps_distill_loss
+ * of the same columns): grad[r * ld_grad + j] = row_weights[r] * d loss_r / d
+ * s[r, j], of type grad_dtype: the scores' or SPS_F32. row_weights (nullable:
+ * 1): DEVICE float[n_rows], the gradient of what is minimised about each row's
+ * loss. grad may be the scores themselves (same address, type and ld). */
+sps_status sps_distill_chunk_grad(sps_distill *h, const sps_scores *scores,
+                                  const float *row_weights, void *grad, int32_t grad_dtype,
+                                  int64_t ld_grad, void *stream);
+
+/* Free the host handle (never the caller's workspace). NULL is ignored. */
+void sps_distill_destroy(sps_distill *h);
+
+/* All of the above for rows that are whole (asynchronous): scores->col_begin
+ * is 0 and its n_cols the whole. loss and grad as above (grad nullable: the
+ * losses alone). workspace: as for sps_distill_prepare, free again once the
+ * stream work has completed. */
+sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const float *logits,
+                            const float *teacher_lse, int32_t k, float temperature,
+                            const float *row_weights, float *loss, void *grad, int32_t grad_dtype,
+                            int64_t ld_grad, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Block-Sparse CSR codec                                              */
 /* ------------------------------------------------------------------ */
 

@@ -111,6 +111,15 @@ SIGNATURES = {
     "sps_beam_select": (_I32, [ctypes.POINTER(_Scores), _P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     "sps_beam_join": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),
     "sps_reorder_states": (_I32, [ctypes.POINTER(_State), _I32, _P, _I64, _I64, _P]),
+    "sps_distill_workspace_size": (_I32, [_I64, _I32, ctypes.POINTER(_SZ)]),
+    "sps_distill_prepare": (_I32, [_P, _P, _P, _I64, _I32, _I64, ctypes.c_float, _P, _SZ, _P,
+                                   ctypes.POINTER(_P)]),
+    "sps_distill_chunk": (_I32, [_P, ctypes.POINTER(_Scores), _I32, _P]),
+    "sps_distill_loss": (_I32, [_P, _P, _P, _P]),
+    "sps_distill_chunk_grad": (_I32, [_P, ctypes.POINTER(_Scores), _P, _P, _I32, _I64, _P]),
+    "sps_distill_destroy": (None, [_P]),
+    "sps_distill_rows": (_I32, [ctypes.POINTER(_Scores), _P, _P, _P, _I32, ctypes.c_float, _P, _P,
+                                _P, _I32, _I64, _P, _SZ, _P]),
     "sps_row_inv_norms": (_I32, [ctypes.POINTER(_Csr), _P, _P]),
     "sps_bsc_offsets_bytes": (_I32, [_I64, ctypes.POINTER(_SZ)]),
     "sps_bsc_encode_sizes": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P, ctypes.POINTER(_I64)]),
@@ -759,6 +768,125 @@ def bulk_select(queries: CSR, items: CSR, k: int, chunk_size: int = 8192) -> Top
         cosine_chunk(q, it, c, buf)
         select_chunk(buf[:, :it.chunk_len(c)], top, c * chunk_size, first=c == 0)
     return top
+
+
+# ---------------------------------------------------------------------------
+# rows of scores: distillation
+
+class Distill:
+    """A batch's teacher lists and the running statistics of its rows (owns its workspace)."""
+
+    def __init__(self, handle, ws, n_rows: int, n_cols: int, device):
+        self._h = handle
+        self._ws = ws
+        self.n_rows, self.n_cols, self.device = n_rows, n_cols, device
+
+    def __del__(self):
+        h, self._h = getattr(self, "_h", None), None
+        if h and _lib is not None:
+            _lib.sps_distill_destroy(h)
+
+
+def _teacher(ids: torch.Tensor, logits: torch.Tensor, teacher_lse):
+    assert ids.dim() == 2 and ids.dtype == torch.int32 and ids.is_contiguous(), \
+        "teacher ids must be contiguous int32 (rows, k)"
+    assert logits.shape == ids.shape and logits.dtype == torch.float32 and logits.is_contiguous(), \
+        "teacher logits must be contiguous float32 (rows, k)"
+    n, k = ids.shape
+    return n, k, _rows_f32(teacher_lse, n, "teacher_lse")
+
+
+def distill_prepare(teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, n_cols: int,
+                    temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+                    stream=None) -> Distill:
+    """The teacher's best k of every row, for rows of n_cols scores that come in chunks:
+    distill_chunk for every chunk, distill_loss, distill_chunk_grad for every chunk. ids
+    outside [0, n_cols) (pad with -1), an id's repetitions in its row and logits of -inf take
+    no part. With teacher_lse (the teacher's log-sum-exp of logits / temperature over all
+    columns) its mass outside the list is one more class; without, the list's is all."""
+    load_library()
+    _here(teacher_ids, teacher_logits, teacher_lse)
+    n, k, lse = _teacher(teacher_ids, teacher_logits, teacher_lse)
+    nb = _sized("sps_distill_workspace_size", n, k)
+    dev = teacher_ids.device
+    with _on(stream):
+        buf, ptr = _workspace(nb, dev)
+        h = _P()
+        _check(_lib.sps_distill_prepare(teacher_ids.data_ptr(), teacher_logits.data_ptr(), lse, n, k,
+                                        n_cols, float(temperature), ptr, nb, _stream_ptr(stream),
+                                        ctypes.byref(h)))
+    return Distill(h.value, buf, n, n_cols, dev)
+
+
+def distill_chunk(d: Distill, scores: torch.Tensor, col_begin: int = 0, first: bool = False,
+                  stream=None) -> None:
+    """Take in the student's scores of columns [col_begin, col_begin + scores.shape[1]); every
+    column once, in any order of the chunks. first=True forgets what came before."""
+    _here(scores)
+    v = _view(scores, col_begin)
+    _check(_lib.sps_distill_chunk(d._h, ctypes.byref(v), int(first), _stream_ptr(stream)))
+
+
+def distill_loss(d: Distill, return_lse: bool = False, stream=None):
+    """The loss of every row, float32 (n_rows,), once all chunks are in; with return_lse also
+    the student's log-sum-exp of scores / temperature."""
+    with _on(stream):
+        loss = torch.empty(d.n_rows, dtype=torch.float32, device=d.device)
+        lse = torch.empty_like(loss) if return_lse else None
+        _here(loss)
+        _check(_lib.sps_distill_loss(d._h, loss.data_ptr(),
+                                     lse.data_ptr() if return_lse else None, _stream_ptr(stream)))
+    return (loss, lse) if return_lse else loss
+
+
+def _grad_out(scores: torch.Tensor, out):
+    if out is None:
+        out = torch.empty(scores.shape, dtype=scores.dtype, device=scores.device)
+    assert out.shape == scores.shape and (out.stride(1) == 1 or out.shape[1] <= 1)
+    assert out.dtype in (scores.dtype, torch.float32), "gradients have the scores' type or float32"
+    return out, out.stride(0) if out.shape[0] > 1 else out.shape[1]
+
+
+def distill_chunk_grad(d: Distill, scores: torch.Tensor, col_begin: int = 0,
+                       row_weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """row_weights[r] * d loss_r / d scores[r, j] of a chunk, after distill_loss of the same
+    scores. out: of the scores' type or float32, may be `scores` itself."""
+    _here(scores, row_weights, out)
+    v = _view(scores, col_begin)
+    w = _rows_f32(row_weights, v.n_rows, "row_weights")
+    with _on(stream):
+        out, ld = _grad_out(scores, out)
+        _check(_lib.sps_distill_chunk_grad(d._h, ctypes.byref(v), w, out.data_ptr(),
+                                           _SCORE_TYPES[out.dtype], ld, _stream_ptr(stream)))
+    return out
+
+
+def distill(scores: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor,
+            temperature: float = 1.0, teacher_lse: torch.Tensor | None = None,
+            row_weights: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            need_grad: bool = True, stream=None):
+    """(loss of every row, gradient about the scores) of whole rows against the teacher's best
+    k (distill_prepare says which entries count); the gradient is None without need_grad."""
+    load_library()
+    _here(scores, teacher_ids, teacher_logits, teacher_lse, row_weights, out)
+    v = _view(scores)
+    n, k, lse = _teacher(teacher_ids, teacher_logits, teacher_lse)
+    assert n == v.n_rows, "one list a row"
+    w = _rows_f32(row_weights, n, "row_weights")
+    nb = _sized("sps_distill_workspace_size", n, k)
+    with _on(stream):
+        loss = torch.empty(n, dtype=torch.float32, device=scores.device)
+        ld = 0
+        if need_grad:
+            out, ld = _grad_out(scores, out)
+        buf, ptr = _workspace(nb, scores.device)
+        _check(_lib.sps_distill_rows(ctypes.byref(v), teacher_ids.data_ptr(),
+                                     teacher_logits.data_ptr(), lse, k, float(temperature), w,
+                                     loss.data_ptr(), out.data_ptr() if need_grad else None,
+                                     _SCORE_TYPES[out.dtype] if need_grad else 0, ld, ptr, nb,
+                                     _stream_ptr(stream)))
+    return loss, out if need_grad else None
 
 
 def row_inv_norms(m: CSR, stream=None) -> torch.Tensor:

@@ -1,0 +1,679 @@
+// sps_distill.hip -- distillation of rows of scores from a teacher's top list
+// on gfx950: the loss of every row and its gradient, over whole rows or over
+// chunks of columns as they stream by.
+//
+// Mathematics. With c = log2(e) / temperature every exponential is 2^((x - M)
+// c) for a running maximum M: the difference is taken first, so that rows of
+// the type's lowest value keep a finite softmax. The columns of the teacher's
+// list stay out of the running sum (a bit per column, set in LDS) and are
+// added at the end from their own scores: the mass outside the list, which
+// the loss with a remaining class divides by, is then a sum of its own terms
+// and not a difference. From M, that sum and the listed scores a row's loss
+// follows, and two factors a and b with which the gradient is b e (columns
+// outside the list) and a e - p (listed), e = 2^((x - M) c).
+//
+// What bounds it: reading the scores for the sums, reading them again and
+// writing the gradient; a score costs about ten operations.
+#include <cmath>
+#include <new>
+
+#include "sps_rows.h"
+
+namespace sps {
+
+constexpr int kDistMaxK = 1024;   // listed entries of a row: the public limit
+constexpr int kDistThreads = 256;
+constexpr int kDistVpt = 32;      // scores a thread holds: one bit each of a word
+constexpr int kDistTile = kDistThreads * kDistVpt;
+constexpr int kSuperTiles = 8;    // tiles whose bits LDS holds at a time
+constexpr int kDistFill = 1024;   // workgroups that fill the card
+constexpr int kMaxSlots = 256;
+
+struct Stat {  // sum of 2^((x - m) c) over a part of a row's unlisted columns
+  double s;
+  float m;
+  float pad;
+};
+
+struct RowTeach {  // of a row's list
+  double entropy;  // sum p log p, the remaining class's term included
+  double mass;     // sum p + p_rest
+  double rest;     // p_rest
+  int32_t has;     // an entry takes part
+  int32_t pad;
+};
+
+struct RowCoef {  // for the gradient
+  double a, b;
+  float m;
+  int32_t live;  // 0: loss and gradient are 0
+};
+
+struct DistillDev {
+  int64_t n_rows, n_cols;
+  int32_t k, slots;
+  float c;        // log2(e) / temperature
+  double inv_tau;
+  bool rest;      // the teacher's mass outside its list is known
+  int32_t *sid;   // [rows][k]: column, -1 where the entry takes no part
+  float *p;       // [rows][k]
+  float *x;       // [rows][k]: the student's score of the entry
+  RowTeach *teach;
+  RowCoef *coef;
+  Stat *stat;     // [rows][slots]
+};
+
+__device__ __forceinline__ float exp2_from(float x, float m, float c) {
+  return __builtin_amdgcn_exp2f((x - m) * c);
+}
+// what a maximum of -inf (nothing but -inf yet) is subtracted as
+__device__ __forceinline__ float finite_max(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+// ---- the teacher's lists ----
+template <int NT>
+__device__ __forceinline__ double block_sum_f64(double v, double *ws) {
+  v = wave_sum(v);
+  if (NT == 64) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double r = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) r += ws[i];
+  return r;
+}
+template <int NT>
+__device__ __forceinline__ float block_max(float v, float *ws) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  if (NT == 64) return v;
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float r = ws[0];
+#pragma unroll
+  for (int i = 1; i < NT / 64; ++i) r = fmaxf(r, ws[i]);
+  return r;
+}
+
+// One workgroup a row: which entries take part (an id's first occurrence in
+// the row, inside the columns, with a logit), and their masses.
+template <int NT>
+__global__ __launch_bounds__(NT) void distill_prepare_kernel(DistillDev d,
+                                                             const int32_t *__restrict__ ids,
+                                                             const float *__restrict__ logits,
+                                                             const float *__restrict__ lse) {
+  __shared__ int32_t id[kDistMaxK];
+  __shared__ double wd[NT / 64];
+  __shared__ float wf[NT / 64];
+  const int64_t row = blockIdx.x, at = row * d.k;
+  for (int i = threadIdx.x; i < d.k; i += NT) {
+    const int32_t v = ids[at + i];
+    const bool ok = v >= 0 && v < d.n_cols && logits[at + i] != -__builtin_inff();
+    id[i] = ok ? v : -1;
+  }
+  __syncthreads();
+  float mx = -__builtin_inff();
+  int has = 0;
+  for (int i = threadIdx.x; i < d.k; i += NT) {
+    int32_t v = id[i];
+    // an earlier entry of the same id has the place, whether or not it counts itself:
+    // entries that do not take part are -1 here
+    for (int j = 0; j < i && v >= 0; ++j)
+      if (id[j] == v) v = -1;
+    d.sid[at + i] = v;
+    if (v >= 0) {
+      has = 1;
+      mx = fmaxf(mx, logits[at + i]);
+    }
+  }
+  has = __syncthreads_or(has);
+  mx = block_max<NT>(mx, wf);
+  double sum = 0;
+  const double shift = d.rest ? (double)lse[row] : (double)finite_max(mx) * d.inv_tau;
+  for (int i = threadIdx.x; i < d.k; i += NT)
+    if (d.sid[at + i] >= 0) sum += exp((double)logits[at + i] * d.inv_tau - shift);
+  sum = block_sum_f64<NT>(sum, wd);
+  const double scale = d.rest ? 1.0 : 1.0 / sum;
+  double ent = 0;
+  for (int i = threadIdx.x; i < d.k; i += NT) {
+    double p = 0;
+    if (d.sid[at + i] >= 0) {
+      p = exp((double)logits[at + i] * d.inv_tau - shift) * scale;
+      ent += p == 0 ? 0.0 : p * log(p);
+    }
+    d.p[at + i] = (float)p;
+  }
+  ent = block_sum_f64<NT>(ent, wd);
+  if (threadIdx.x == 0) {
+    double rest = 0;
+    if (d.rest) rest = sum < 1 ? 1 - sum : sum >= 1 ? 0.0 : sum;  // NaN stays
+    RowTeach t;
+    t.entropy = ent + (rest == 0 ? 0.0 : rest * log(rest));
+    t.mass = d.rest ? sum + rest : 1.0 + (sum - sum);  // 1, or NaN where the logits are
+    t.rest = rest;
+    t.has = has;
+    t.pad = 0;
+    d.teach[row] = t;
+  }
+}
+
+// ---- the sums ----
+struct ChunkArgs {
+  DistillDev d;
+  const void *x;
+  int64_t ld, n_cols, col_begin, seg;
+  int32_t splits, first;
+};
+
+// the word and bit of a column `o` columns into its tile of scores of type T
+template <typename T>
+__device__ __forceinline__ void bit_of(int o, int &word, int &bit) {
+  constexpr int V = kVec<T>;
+  const int v = o / V;
+  word = v % kDistThreads;
+  bit = v / kDistThreads * V + o % V;
+}
+
+// a tile's scores of this thread; columns past the end are -inf
+template <typename T>
+__device__ __forceinline__ void load_tile(const T *x, int64_t base, int64_t end,
+                                          float (&f)[kDistVpt]) {
+  constexpr int V = kVec<T>;
+#pragma unroll
+  for (int v = 0; v < kDistVpt / V; ++v) {
+    const int64_t c = base + ((int64_t)v * kDistThreads + threadIdx.x) * V;
+    if (c + V <= end) {
+      const Vec<T> w = *reinterpret_cast<const Vec<T> *>(x + c);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[v * V + e] = to_f32(w.e[e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        f[v * V + e] = c + e < end ? to_f32(x[c + e]) : -__builtin_inff();
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kDistThreads) void distill_chunk_kernel(ChunkArgs a) {
+  __shared__ uint32_t bits[kSuperTiles][kDistThreads];
+  __shared__ double wd[kDistThreads / 64];
+  __shared__ float wf[kDistThreads / 64];
+  const DistillDev &d = a.d;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x / (uint32_t)a.splits;
+  const int32_t split = (int32_t)(blockIdx.x % (uint32_t)a.splits);
+  const int64_t c0 = split * a.seg, c1 = c0 + a.seg < a.n_cols ? c0 + a.seg : a.n_cols;
+  const T *x = static_cast<const T *>(a.x) + row * a.ld;
+  const int32_t *sid = d.sid + row * d.k;
+  // the listed scores of this part; on the first chunk, the first part clears those elsewhere
+  for (int i = t; i < d.k; i += kDistThreads) {
+    const int64_t o = (int64_t)sid[i] - a.col_begin;
+    if (sid[i] >= 0 && o >= c0 && o < c1) d.x[row * d.k + i] = to_f32(x[o]);
+    else if (a.first && split == 0 && (sid[i] < 0 || o < 0 || o >= a.n_cols))
+      d.x[row * d.k + i] = -__builtin_inff();
+  }
+  float m = -__builtin_inff();
+  double s = 0;
+  for (int64_t s0 = c0; s0 < c1; s0 += (int64_t)kSuperTiles * kDistTile) {
+    const int64_t s1 =
+        s0 + (int64_t)kSuperTiles * kDistTile < c1 ? s0 + (int64_t)kSuperTiles * kDistTile : c1;
+    const int tiles = (int)((s1 - s0 + kDistTile - 1) / kDistTile);
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) bits[i][t] = 0;
+    __syncthreads();
+    for (int i = t; i < d.k; i += kDistThreads) {
+      const int64_t o = (int64_t)sid[i] - a.col_begin - s0;
+      if (sid[i] >= 0 && o >= 0 && o < s1 - s0) {
+        int word, bit;
+        bit_of<T>((int)(o % kDistTile), word, bit);
+        atomicOr(&bits[o / kDistTile][word], 1u << bit);
+      }
+    }
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      float f[kDistVpt];
+      load_tile<T>(x, s0 + (int64_t)i * kDistTile, s1, f);
+      const uint32_t listed = bits[i][t];
+      if (listed) {
+#pragma unroll
+        for (int e = 0; e < kDistVpt; ++e)
+          if (listed >> e & 1u) f[e] = -__builtin_inff();
+      }
+      float mt = m;
+#pragma unroll
+      for (int e = 0; e < kDistVpt; ++e) mt = fmaxf(mt, f[e]);
+      const float mf = finite_max(mt);
+      float part = 0;
+#pragma unroll
+      for (int e = 0; e < kDistVpt; ++e) part += exp2_from(f[e], mf, d.c);
+      s = s * (double)exp2_from(m, mf, d.c) + (double)part;
+      m = mt;
+    }
+  }
+  const float mb = block_max<kDistThreads>(m, wf);
+  const double sb = block_sum_f64<kDistThreads>(s * (double)exp2_from(m, finite_max(mb), d.c), wd);
+  if (t == 0) {
+    Stat *st = d.stat + row * d.slots;
+    Stat r{sb, mb, 0};
+    if (!a.first) {
+      const Stat o = st[split];
+      r.m = fmaxf(o.m, mb);
+      const float mf = finite_max(r.m);
+      r.s = o.s * (double)exp2_from(o.m, mf, d.c) + sb * (double)exp2_from(mb, mf, d.c);
+    }
+    st[split] = r;
+    if (a.first && split == 0)
+      for (int i = a.splits; i < d.slots; ++i) st[i] = Stat{0, -__builtin_inff(), 0};
+  }
+}
+
+// ---- the losses ----
+// One wave a row.
+__global__ __launch_bounds__(256) void distill_loss_kernel(DistillDev d, float *__restrict__ loss,
+                                                           float *__restrict__ lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= d.n_rows) return;  // uniform per wave
+  const int32_t *sid = d.sid + row * d.k;
+  const float *x = d.x + row * d.k, *p = d.p + row * d.k;
+  const Stat *st = d.stat + row * d.slots;
+  const RowTeach te = d.teach[row];
+  float m = -__builtin_inff();
+  for (int i = lane; i < d.slots; i += 64) m = fmaxf(m, st[i].m);
+  for (int i = lane; i < d.k; i += 64)
+    if (sid[i] >= 0) m = fmaxf(m, x[i]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+  const float mf = finite_max(m);
+  const double c = (double)d.c, ln2 = 0.693147180559945309417;
+  double z_rest = 0, z_list = 0;
+  for (int i = lane; i < d.slots; i += 64) {
+    const Stat s = st[i];
+    if (s.s != 0) z_rest += s.s * exp2(((double)s.m - (double)mf) * c);
+  }
+  for (int i = lane; i < d.k; i += 64)
+    if (sid[i] >= 0) z_list += exp2(((double)x[i] - (double)mf) * c);
+  z_rest = wave_sum(z_rest);
+  z_list = wave_sum(z_list);
+  const double z = z_rest + z_list, log_z = log(z);
+  double l = 0;
+  for (int i = lane; i < d.k; i += 64)
+    if (sid[i] >= 0 && p[i] != 0)
+      l += (double)p[i] * (log_z - ((double)x[i] - (double)mf) * c * ln2);
+  l = wave_sum(l) + te.entropy;
+  if (te.rest != 0) l += te.rest * (log_z - log(z_rest));
+  const int32_t live = te.has && z != 0;  // a NaN is no 0
+  if (lane == 0) {
+    RowCoef r;
+    r.a = te.mass / z;
+    r.b = te.rest != 0 && z_rest != 0 ? te.mass / z - te.rest / z_rest : r.a;
+    r.m = mf;
+    r.live = live;
+    d.coef[row] = r;
+    loss[row] = live ? (float)l : 0.0f;
+    if (lse) lse[row] = (float)((double)mf * c * ln2 + log_z);
+  }
+}
+
+// ---- the gradient ----
+struct GradArgs {
+  DistillDev d;
+  const void *x;
+  void *g;
+  const float *weights;  // nullable: 1
+  int64_t ld, ldg, n_cols, col_begin, seg;
+  int32_t splits;
+};
+
+template <typename T, typename G>
+__device__ __forceinline__ void store_tile(G *g, int64_t base, int64_t end,
+                                           const float (&f)[kDistVpt]) {
+  constexpr int V = kVec<T>, W = kVec<G>;
+#pragma unroll
+  for (int v = 0; v < kDistVpt / V; ++v) {
+    const int64_t c = base + ((int64_t)v * kDistThreads + threadIdx.x) * V;
+    if (c + V <= end) {
+#pragma unroll
+      for (int w = 0; w < V; w += W) {
+        Vec<G> o;
+#pragma unroll
+        for (int e = 0; e < W; ++e) o.e[e] = from_f32<G>(f[v * V + w + e]);
+        *reinterpret_cast<Vec<G> *>(g + c + w) = o;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (c + e < end) g[c + e] = from_f32<G>(f[v * V + e]);
+    }
+  }
+}
+
+template <typename T, typename G>
+__global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(GradArgs a) {
+  const DistillDev &d = a.d;
+  const int64_t row = blockIdx.x / (uint32_t)a.splits;
+  const int32_t split = (int32_t)(blockIdx.x % (uint32_t)a.splits);
+  const int64_t c0 = split * a.seg, c1 = c0 + a.seg < a.n_cols ? c0 + a.seg : a.n_cols;
+  const T *x = static_cast<const T *>(a.x) + row * a.ld;
+  G *g = static_cast<G *>(a.g) + row * a.ldg;
+  const RowCoef r = d.coef[row];
+  const double w = (a.weights ? (double)a.weights[row] : 1.0) * d.inv_tau;
+  const float b = (float)(r.b * w);
+  for (int64_t base = c0; base < c1; base += kDistTile) {
+    float f[kDistVpt];
+    load_tile<T>(x, base, c1, f);
+#pragma unroll
+    for (int e = 0; e < kDistVpt; ++e) f[e] = r.live ? exp2_from(f[e], r.m, d.c) * b : 0.0f;
+    store_tile<T, G>(g, base, c1, f);
+  }
+  if (!r.live) return;  // uniform
+  __syncthreads();      // the listed columns are written over what stands there
+  for (int i = threadIdx.x; i < d.k; i += kDistThreads) {
+    const int32_t id = d.sid[row * d.k + i];
+    const int64_t o = (int64_t)id - a.col_begin;
+    if (id >= 0 && o >= c0 && o < c1) {
+      const double e = exp2(((double)d.x[row * d.k + i] - (double)r.m) * (double)d.c);
+      g[o] = from_f32<G>((float)((e * r.a - (double)d.p[row * d.k + i]) * w));
+    }
+  }
+}
+
+}  // namespace sps
+
+struct sps_distill {
+  sps::DistillDev d;
+};
+
+namespace {
+
+using sps::DistillDev;
+using sps::set_error;
+
+constexpr int64_t kMax31 = 2147483647ll;
+
+int32_t slots_of(int64_t n_rows) {
+  if (n_rows <= 0 || n_rows >= sps::kDistFill) return 1;
+  const int64_t s = (sps::kDistFill + n_rows - 1) / n_rows;
+  return (int32_t)(s < sps::kMaxSlots ? s : sps::kMaxSlots);
+}
+
+// parts of a chunk's rows: as many as fill the card, none below a tile
+void split_of(int64_t n_rows, int64_t n_cols, int32_t *splits, int64_t *seg) {
+  int64_t s = slots_of(n_rows);
+  const int64_t most = (n_cols + sps::kDistTile - 1) / sps::kDistTile;
+  s = s < most ? s : most;
+  s = s > 1 ? s : 1;
+  int64_t g = ((n_cols + s - 1) / s + 7) / 8 * 8;
+  if (g < 8) g = 8;
+  s = (n_cols + g - 1) / g;
+  *splits = (int32_t)(s > 1 ? s : 1);
+  *seg = g;
+}
+
+struct Layout {
+  size_t sid, p, x, teach, coef, stat, total;
+};
+Layout layout_of(int64_t n, int32_t k) {
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  Layout L;
+  size_t at = 0;
+  L.sid = at;
+  at = up(at + (size_t)n * k * 4);
+  L.p = at;
+  at = up(at + (size_t)n * k * 4);
+  L.x = at;
+  at = up(at + (size_t)n * k * 4);
+  L.teach = at;
+  at = up(at + (size_t)n * sizeof(sps::RowTeach));
+  L.coef = at;
+  at = up(at + (size_t)n * sizeof(sps::RowCoef));
+  L.stat = at;
+  at = up(at + (size_t)n * slots_of(n) * sizeof(sps::Stat));
+  L.total = at;
+  return L;
+}
+
+sps_status check_sizes(int64_t n_rows, int32_t k, const char *what) {
+  if (n_rows < 0) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: negative size", what);
+  if (k < 1 || k > sps::kDistMaxK)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: k must be in [1, %d]", what, sps::kDistMaxK);
+  if (n_rows >= kMax31) return set_error(SPS_ERR_OVERFLOW, "%s: rows must be below 2^31", what);
+  return SPS_OK;
+}
+
+// the checks of a list and its workspace; fills d
+sps_status make_dev(const int32_t *ids, const float *logits, const float *lse, int64_t n_rows,
+                    int32_t k, int64_t n_cols, float tau, void *ws, size_t bytes, const char *what,
+                    DistillDev *d) {
+  sps_status st = check_sizes(n_rows, k, what);
+  if (st != SPS_OK) return st;
+  if (n_cols < 0) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: negative size", what);
+  if (n_cols >= kMax31) return set_error(SPS_ERR_OVERFLOW, "%s: columns must be below 2^31", what);
+  if (!(tau >= 1e-6f && tau <= 1e6f))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: temperature must be in [1e-6, 1e6]", what);
+  if (n_rows > 0 && (!ids || !logits))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL list", what);
+  const Layout L = layout_of(n_rows, k);
+  if (n_rows > 0 && !ws) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL workspace", what);
+  if (bytes < L.total)
+    return set_error(SPS_ERR_WORKSPACE_TOO_SMALL, "%s: need %zu bytes, got %zu", what, L.total,
+                     bytes);
+  if (reinterpret_cast<uintptr_t>(ws) & 255)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", what);
+  char *b = static_cast<char *>(ws);
+  d->n_rows = n_rows;
+  d->n_cols = n_cols;
+  d->k = k;
+  d->slots = slots_of(n_rows);
+  d->c = (float)(1.44269504088896340736 / (double)tau);
+  d->inv_tau = 1.0 / (double)tau;
+  d->rest = lse != nullptr;
+  d->sid = reinterpret_cast<int32_t *>(b + L.sid);
+  d->p = reinterpret_cast<float *>(b + L.p);
+  d->x = reinterpret_cast<float *>(b + L.x);
+  d->teach = reinterpret_cast<sps::RowTeach *>(b + L.teach);
+  d->coef = reinterpret_cast<sps::RowCoef *>(b + L.coef);
+  d->stat = reinterpret_cast<sps::Stat *>(b + L.stat);
+  return SPS_OK;
+}
+
+void launch_prepare(const DistillDev &d, const int32_t *ids, const float *logits, const float *lse,
+                    hipStream_t s) {
+  if (d.k <= 128)
+    hipLaunchKernelGGL((sps::distill_prepare_kernel<64>), dim3((uint32_t)d.n_rows), dim3(64), 0, s,
+                       d, ids, logits, lse);
+  else
+    hipLaunchKernelGGL((sps::distill_prepare_kernel<256>), dim3((uint32_t)d.n_rows), dim3(256), 0,
+                       s, d, ids, logits, lse);
+}
+
+void launch_chunk(const DistillDev &d, const sps_scores *x, int32_t first, hipStream_t s) {
+  sps::ChunkArgs a{};
+  a.d = d;
+  a.x = x->data;
+  a.ld = x->ld;
+  a.n_cols = x->n_cols;
+  a.col_begin = x->col_begin;
+  a.first = first != 0;
+  split_of(d.n_rows, x->n_cols, &a.splits, &a.seg);
+  const dim3 grid((uint32_t)(d.n_rows * a.splits)), block(sps::kDistThreads);
+  if (x->dtype == SPS_F32)
+    hipLaunchKernelGGL((sps::distill_chunk_kernel<float>), grid, block, 0, s, a);
+  else if (x->dtype == SPS_F16)
+    hipLaunchKernelGGL((sps::distill_chunk_kernel<sps::f16_t>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::distill_chunk_kernel<sps::bf16_t>), grid, block, 0, s, a);
+}
+
+void launch_loss(const DistillDev &d, float *loss, float *lse, hipStream_t s) {
+  hipLaunchKernelGGL(sps::distill_loss_kernel, dim3((uint32_t)((d.n_rows + 3) / 4)), dim3(256), 0,
+                     s, d, loss, lse);
+}
+
+sps_status check_grad(const sps_scores *x, const void *grad, int32_t dtype, int64_t ld,
+                      const char *what) {
+  if (dtype != x->dtype && dtype != SPS_F32)
+    return set_error(SPS_ERR_INVALID_ARGUMENT,
+                     "%s: the gradient's type is the scores' or float32", what);
+  if (ld < x->n_cols)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: ld_grad below the columns", what);
+  if (x->n_rows > 0 && (uint64_t)ld > (uint64_t)INT64_MAX / 4 / (uint64_t)x->n_rows)
+    return set_error(SPS_ERR_OVERFLOW, "%s: n_rows * ld_grad overflows", what);
+  if (x->n_rows > 0 && x->n_cols > 0 && !grad)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL gradient", what);
+  if (reinterpret_cast<uintptr_t>(grad) % (uintptr_t)sps::dtype_size(dtype))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: gradient not aligned to its elements", what);
+  if (x->n_rows > 0 && x->n_cols > 0) {
+    // in place, or apart: a gradient that overlaps other scores would overwrite them unread
+    const uintptr_t s0 = reinterpret_cast<uintptr_t>(x->data), g0 = reinterpret_cast<uintptr_t>(grad);
+    const uintptr_t s1 = s0 + ((uintptr_t)(x->n_rows - 1) * x->ld + x->n_cols) *
+                                  (uintptr_t)sps::dtype_size(x->dtype);
+    const uintptr_t g1 =
+        g0 + ((uintptr_t)(x->n_rows - 1) * ld + x->n_cols) * (uintptr_t)sps::dtype_size(dtype);
+    const bool same = s0 == g0 && dtype == x->dtype && (ld == x->ld || x->n_rows == 1);
+    if (!same && g0 < s1 && s0 < g1)
+      return set_error(SPS_ERR_INVALID_ARGUMENT,
+                       "%s: the gradient overlaps the scores without being them", what);
+  }
+  return SPS_OK;
+}
+
+void launch_grad(const DistillDev &d, const sps_scores *x, const float *weights, void *grad,
+                 int32_t dtype, int64_t ldg, hipStream_t s) {
+  if (x->n_cols == 0) return;
+  sps::GradArgs a{};
+  a.d = d;
+  a.x = x->data;
+  a.g = grad;
+  a.weights = weights;
+  a.ld = x->ld;
+  a.ldg = ldg;
+  a.n_cols = x->n_cols;
+  a.col_begin = x->col_begin;
+  split_of(d.n_rows, x->n_cols, &a.splits, &a.seg);
+  const dim3 grid((uint32_t)(d.n_rows * a.splits)), block(sps::kDistThreads);
+  using sps::bf16_t;
+  using sps::f16_t;
+  if (x->dtype == SPS_F32)
+    hipLaunchKernelGGL((sps::distill_grad_kernel<float, float>), grid, block, 0, s, a);
+  else if (x->dtype == SPS_F16 && dtype == SPS_F16)
+    hipLaunchKernelGGL((sps::distill_grad_kernel<f16_t, f16_t>), grid, block, 0, s, a);
+  else if (x->dtype == SPS_F16)
+    hipLaunchKernelGGL((sps::distill_grad_kernel<f16_t, float>), grid, block, 0, s, a);
+  else if (dtype == SPS_BF16)
+    hipLaunchKernelGGL((sps::distill_grad_kernel<bf16_t, bf16_t>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::distill_grad_kernel<bf16_t, float>), grid, block, 0, s, a);
+}
+
+// a chunk of the batch's columns
+sps_status check_chunk(const sps_distill *h, const sps_scores *x, const char *what) {
+  if (!h) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL handle", what);
+  const sps_status st = sps::check_scores(x, what);
+  if (st != SPS_OK) return st;
+  if (x->n_rows != h->d.n_rows)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: %lld rows of scores, %lld lists", what,
+                     (long long)x->n_rows, (long long)h->d.n_rows);
+  if (x->col_begin + x->n_cols > h->d.n_cols)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: columns past the batch's %lld", what,
+                     (long long)h->d.n_cols);
+  return SPS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sps_status sps_distill_workspace_size(int64_t n_rows, int32_t k, size_t *bytes) {
+  if (!bytes) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output pointer");
+  const sps_status st = check_sizes(n_rows, k, "sps_distill_workspace_size");
+  if (st != SPS_OK) return st;
+  *bytes = layout_of(n_rows, k).total;
+  return SPS_OK;
+}
+
+sps_status sps_distill_prepare(const int32_t *ids, const float *logits, const float *teacher_lse,
+                               int64_t n_rows, int32_t k, int64_t n_cols, float temperature,
+                               void *workspace, size_t workspace_bytes, void *stream,
+                               sps_distill **out) {
+  if (!out) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output handle pointer");
+  *out = nullptr;
+  DistillDev d{};
+  sps_status st = make_dev(ids, logits, teacher_lse, n_rows, k, n_cols, temperature, workspace,
+                           workspace_bytes, "sps_distill_prepare", &d);
+  if (st != SPS_OK) return st;
+  sps_distill *h = new (std::nothrow) sps_distill;
+  if (!h) return set_error(SPS_ERR_INVALID_ARGUMENT, "out of host memory");
+  h->d = d;
+  if (n_rows > 0) {
+    launch_prepare(d, ids, logits, teacher_lse, reinterpret_cast<hipStream_t>(stream));
+    st = sps::launch_status("sps_distill_prepare");
+    if (st != SPS_OK) {
+      delete h;
+      return st;
+    }
+  }
+  *out = h;
+  return SPS_OK;
+}
+
+sps_status sps_distill_chunk(sps_distill *h, const sps_scores *scores, int32_t first,
+                             void *stream) {
+  const sps_status st = check_chunk(h, scores, "sps_distill_chunk");
+  if (st != SPS_OK) return st;
+  if (h->d.n_rows == 0) return SPS_OK;
+  launch_chunk(h->d, scores, first, reinterpret_cast<hipStream_t>(stream));
+  return sps::launch_status("sps_distill_chunk");
+}
+
+sps_status sps_distill_loss(sps_distill *h, float *loss, float *lse, void *stream) {
+  if (!h) return set_error(SPS_ERR_INVALID_ARGUMENT, "sps_distill_loss: NULL handle");
+  if (h->d.n_rows == 0) return SPS_OK;
+  if (!loss) return set_error(SPS_ERR_INVALID_ARGUMENT, "sps_distill_loss: NULL output");
+  launch_loss(h->d, loss, lse, reinterpret_cast<hipStream_t>(stream));
+  return sps::launch_status("sps_distill_loss");
+}
+
+sps_status sps_distill_chunk_grad(sps_distill *h, const sps_scores *scores,
+                                  const float *row_weights, void *grad, int32_t grad_dtype,
+                                  int64_t ld_grad, void *stream) {
+  sps_status st = check_chunk(h, scores, "sps_distill_chunk_grad");
+  if (st == SPS_OK) st = check_grad(scores, grad, grad_dtype, ld_grad, "sps_distill_chunk_grad");
+  if (st != SPS_OK) return st;
+  if (h->d.n_rows == 0) return SPS_OK;
+  launch_grad(h->d, scores, row_weights, grad, grad_dtype, ld_grad,
+              reinterpret_cast<hipStream_t>(stream));
+  return sps::launch_status("sps_distill_chunk_grad");
+}
+
+void sps_distill_destroy(sps_distill *h) { delete h; }
+
+sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const float *logits,
+                            const float *teacher_lse, int32_t k, float temperature,
+                            const float *row_weights, float *loss, void *grad, int32_t grad_dtype,
+                            int64_t ld_grad, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+  const char *what = "sps_distill_rows";
+  sps_status st = sps::check_scores(scores, what);
+  if (st != SPS_OK) return st;
+  if (scores->col_begin != 0)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: rows must be whole (col_begin 0)", what);
+  DistillDev d{};
+  st = make_dev(ids, logits, teacher_lse, scores->n_rows, k, scores->n_cols, temperature,
+                workspace, workspace_bytes, what, &d);
+  if (st != SPS_OK) return st;
+  if (grad) st = check_grad(scores, grad, grad_dtype, ld_grad, what);
+  if (st != SPS_OK) return st;
+  if (d.n_rows == 0) return SPS_OK;
+  if (!loss) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL loss", what);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  launch_prepare(d, ids, logits, teacher_lse, s);
+  launch_chunk(d, scores, 1, s);
+  launch_loss(d, loss, nullptr, s);
+  if (grad) launch_grad(d, scores, row_weights, grad, grad_dtype, ld_grad, s);
+  return sps::launch_status(what);
+}
+
+}  // extern "C"

@@ -112,3 +112,79 @@ def test_nothing_to_do(lib):
     assert lib.sps_beam_select(view(rows=0, data=None), None, 2, 4, None, None, None, None, 0,
                                None) == 0
     assert lib.sps_beam_join(None, None, 0, 4, 2, 4, None, None, None, None) == 0
+
+
+def size(lib, n, k):
+    b = ctypes.c_size_t()
+    assert lib.sps_distill_workspace_size(n, k, ctypes.byref(b)) == 0
+    return b.value
+
+
+def test_distill_sizes(lib):
+    b = ctypes.c_size_t()
+    assert size(lib, 8, 16) >= 8 * 16 * 12
+    for k in (0, -1, 1025):
+        assert lib.sps_distill_workspace_size(8, k, ctypes.byref(b)) == INV
+    assert lib.sps_distill_workspace_size(8, 16, None) == INV
+    assert lib.sps_distill_workspace_size(-1, 16, ctypes.byref(b)) == INV
+    assert lib.sps_distill_workspace_size(2**31, 16, ctypes.byref(b)) == OVF
+
+
+def prepare(lib, ids=P, logits=P, lse=None, n=8, k=16, cols=100, tau=1.0, ws=P, bytes_=None):
+    out = ctypes.c_void_p()
+    bytes_ = 1 << 30 if bytes_ is None else bytes_
+    st = lib.sps_distill_prepare(ids, logits, lse, n, k, cols, tau, ws, bytes_, None,
+                                 ctypes.byref(out))
+    assert out.value is None or st == 0
+    if out.value is not None:
+        lib.sps_distill_destroy(out)
+    return st
+
+
+BAD_LISTS = [
+    (dict(ids=None), INV), (dict(logits=None), INV), (dict(n=-1), INV), (dict(k=0), INV),
+    (dict(k=1025), INV), (dict(tau=0.0), INV), (dict(tau=-1.0), INV), (dict(tau=float("nan")), INV),
+    (dict(tau=float("inf")), INV), (dict(tau=9e-7), INV), (dict(ws=None), INV),
+    (dict(ws=P + 16), INV), (dict(bytes_=100), WS), (dict(n=2**31), OVF),
+]
+
+
+@pytest.mark.parametrize("kw,want", BAD_LISTS + [(dict(cols=-1), INV), (dict(cols=2**31), OVF)])
+def test_distill_prepare_refusals(lib, kw, want):
+    assert prepare(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", BAD_LISTS)
+def test_distill_rows_refusals(lib, kw, want):
+    a = dict(ids=P, logits=P, lse=None, n=8, k=16, tau=1.0, ws=P, bytes_=1 << 30)
+    a.update(kw)
+    assert lib.sps_distill_rows(view(rows=a["n"]), a["ids"], a["logits"], a["lse"], a["k"], a["tau"],
+                                None, P, None, 0, 0, a["ws"], a["bytes_"], None) == want
+
+
+def rows_call(lib, v, loss=P, grad=None, gtype=0, ld=100):
+    return lib.sps_distill_rows(v, P, P, None, 16, 1.0, None, loss, grad, gtype, ld, P, 1 << 30, None)
+
+
+def test_distill_rows_outputs(lib):
+    for kw, want in BAD_VIEWS:
+        if kw not in (dict(begin=2**31 - 50),):
+            assert rows_call(lib, view(**kw)) == want, kw
+    assert rows_call(lib, view(begin=1)) == INV
+    assert rows_call(lib, view(), loss=None) == INV
+    g = 64 * P
+    assert rows_call(lib, view(), grad=g, gtype=1) == INV            # fp16 about fp32 scores
+    assert rows_call(lib, view(dtype=1), grad=g, gtype=2) == INV
+    assert rows_call(lib, view(), grad=g, ld=99) == INV
+    assert rows_call(lib, view(), grad=g + 2) == INV
+    assert rows_call(lib, view(), grad=P + 4) == INV                 # overlaps the scores
+    assert rows_call(lib, view(), grad=P, ld=101) == INV
+    assert rows_call(lib, view(dtype=1), grad=P, gtype=0) == INV     # in place, wider type
+    assert rows_call(lib, view(), grad=g, ld=2**62) == OVF
+
+
+def test_distill_null_handles(lib):
+    assert lib.sps_distill_chunk(None, view(), 1, None) == INV
+    assert lib.sps_distill_loss(None, P, None, None) == INV
+    assert lib.sps_distill_chunk_grad(None, view(), None, P, 0, 100, None) == INV
+    lib.sps_distill_destroy(None)
