@@ -527,6 +527,41 @@ sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const 
                             void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Gradient of the scores                                              */
+/* ------------------------------------------------------------------ */
+
+/* The gradient of the cosines (§3.1) with respect to the stored values of the
+ * sparse rows on one side, from the gradient G of the score matrix. With u =
+ * v / |v| for every row and S = u . w, entry e = (row r, dim d) of the rows has
+ *     du_e = sum over rows i of the other side of G[r, i] w_i[d]
+ *     dv_e = (du_e - u_e * sum over r's entries of u du) / |v_r|.
+ * The other side is a prepared corpus (its inverted lists hold w): the items
+ * for the queries' gradient; for the items', the queries prepared as a corpus
+ * of their own. A row of norm 0 has gradient 0. The stored structure is fixed:
+ * dims that a row does not store get no gradient. */
+
+/* Bytes of the workspace for sps_cosine_grad over rows of a CSR with nnz
+ * entries (0 where a chunk of `other` is one slice). Pure host. */
+sps_status sps_cosine_grad_workspace_size(int64_t nnz, const sps_items *other, size_t *bytes);
+
+/* du over chunk `chunk` of `other` (asynchronous) for the rows of a canonical
+ * CSR: du[e] = (first != 0 ? 0 : du[e]) + the chunk's sum. grad is a view of
+ * the chunk's part of G with one row a row and one column an item of the
+ * chunk, or, with transposed != 0, one row an item of the chunk and one
+ * column a row (col_begin is not used). du: DEVICE float[rows->nnz].
+ * workspace: DEVICE, 16-byte aligned, used until the call's stream work is
+ * done. Sums are float32 in a fixed order: bitwise reproducible. Errors:
+ * SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH, SPS_ERR_CHUNK_RANGE,
+ * SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW. */
+sps_status sps_cosine_grad(const sps_csr *rows, const sps_items *other, int32_t chunk,
+                           const sps_scores *grad, int32_t transposed, int32_t first, float *du,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* dv from du through the rows' norms (asynchronous), for all rows of the CSR.
+ * dv: DEVICE float[nnz], may be du itself. Sums in float64. */
+sps_status sps_cosine_grad_values(const sps_csr *rows, const float *du, float *dv, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Block-Sparse CSR codec                                              */
 /* ------------------------------------------------------------------ */
 

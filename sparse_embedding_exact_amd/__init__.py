@@ -120,6 +120,10 @@ SIGNATURES = {
     "sps_distill_destroy": (None, [_P]),
     "sps_distill_rows": (_I32, [ctypes.POINTER(_Scores), _P, _P, _P, _I32, ctypes.c_float, _P, _P,
                                 _P, _I32, _I64, _P, _SZ, _P]),
+    "sps_cosine_grad_workspace_size": (_I32, [_I64, _P, ctypes.POINTER(_SZ)]),
+    "sps_cosine_grad": (_I32, [ctypes.POINTER(_Csr), _P, _I32, ctypes.POINTER(_Scores), _I32, _I32,
+                               _P, _P, _SZ, _P]),
+    "sps_cosine_grad_values": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P]),
     "sps_row_inv_norms": (_I32, [ctypes.POINTER(_Csr), _P, _P]),
     "sps_bsc_offsets_bytes": (_I32, [_I64, ctypes.POINTER(_SZ)]),
     "sps_bsc_encode_sizes": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P, ctypes.POINTER(_I64)]),
@@ -887,6 +891,109 @@ def distill(scores: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: tor
                                      _SCORE_TYPES[out.dtype] if need_grad else 0, ld, ptr, nb,
                                      _stream_ptr(stream)))
     return loss, out if need_grad else None
+
+
+# ---------------------------------------------------------------------------
+# the gradient of the scores
+
+def cosine_chunk_grad(rows: CSR, other: Items, chunk: int, grad: torch.Tensor, du: torch.Tensor,
+                      transposed: bool = False, first: bool = False, stream=None) -> None:
+    """du[e] (+)= the gradient about the unit values of the rows of a CSR from chunk `chunk`
+    of the other side, `grad` being that of the scores: (rows, chunk's items), or with
+    transposed (chunk's items, rows). For the items' gradient, `rows` are items and `other`
+    the queries prepared as a corpus. first=True starts the sums; cosine_grad_values ends
+    them."""
+    load_library()
+    _here(rows.values, grad, du)
+    assert du.dtype == torch.float32 and du.is_contiguous() and du.numel() == rows.nnz
+    v = _view(grad)
+    c = rows._c()
+    nb = _SZ()
+    _check(_lib.sps_cosine_grad_workspace_size(rows.nnz, other._h, ctypes.byref(nb)))
+    with _on(stream):
+        ws = torch.empty(nb.value, dtype=torch.uint8, device=grad.device) if nb.value else None
+        _check(_lib.sps_cosine_grad(ctypes.byref(c), other._h, chunk, ctypes.byref(v),
+                                    int(transposed), int(first), du.data_ptr(),
+                                    ws.data_ptr() if nb.value else None, nb.value,
+                                    _stream_ptr(stream)))
+
+
+def cosine_grad_values(rows: CSR, du: torch.Tensor, out: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """The gradient about the stored values from that about the unit values (the norm's
+    part taken off); out may be du itself."""
+    load_library()
+    _here(rows.values, du, out)
+    assert du.dtype == torch.float32 and du.is_contiguous() and du.numel() == rows.nnz
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(du)
+        assert out.dtype == torch.float32 and out.is_contiguous() and out.numel() == rows.nnz
+        c = rows._c()
+        _check(_lib.sps_cosine_grad_values(ctypes.byref(c), du.data_ptr(), out.data_ptr(),
+                                           _stream_ptr(stream)))
+    return out
+
+
+def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, chunk_size: int = 65536):
+    """(gradient of the queries' values, gradient of the items' values), float32 (nnz,) each,
+    from the gradient of their whole score matrix (n_query, n_item): float32, float16 or
+    bfloat16. The stored structure of both is fixed."""
+    assert grad.shape == (queries.n_rows, items.n_rows)
+
+    def side(rows, other, transposed):
+        du = torch.empty(rows.nnz, dtype=torch.float32, device=grad.device)
+        it = prepare(other, max(min(chunk_size, other.n_rows), 1))
+        if it.num_chunks == 0:
+            du.zero_()
+        for c in range(it.num_chunks):
+            b = c * it.chunk_size
+            part = grad[b:b + it.chunk_size] if transposed else grad[:, b:b + it.chunk_size]
+            cosine_chunk_grad(rows, it, c, part, du, transposed=transposed, first=c == 0)
+        return cosine_grad_values(rows, du, du)
+
+    return side(queries, items, False), side(items, queries, True)
+
+
+def bulk_distill(queries: CSR, items: CSR, teacher_ids: torch.Tensor,
+                 teacher_logits: torch.Tensor, temperature: float = 1.0,
+                 teacher_lse: torch.Tensor | None = None,
+                 row_weights: torch.Tensor | None = None, chunk_size: int = 8192):
+    """One step of distilling sparse embeddings over a whole corpus: (loss of every query,
+    gradient of the queries' values, gradient of the items' values) of the softmax over all
+    cosines / temperature against the teacher's best k of every query (bulk_select's lists of
+    another scorer, say). bulk_similarity's loop, twice: once for the sums, once for the
+    gradients, with one chunk of scores kept."""
+    it = prepare(items, chunk_size)
+    q = prepare_queries(queries, it)
+    qt = prepare(queries, max(min(chunk_size, queries.n_rows), 1))
+    dev = queries.indptr.device
+    d = distill_prepare(teacher_ids, teacher_logits, it.n_items, temperature, teacher_lse)
+    buf = torch.empty(queries.n_rows, min(chunk_size, it.n_items), dtype=torch.float32, device=dev)
+    gq = torch.zeros(queries.nnz, dtype=torch.float32, device=dev)
+    gi = torch.zeros(items.nnz, dtype=torch.float32, device=dev)
+    if it.num_chunks == 0:
+        distill_chunk(d, buf, 0, first=True)
+    for c in range(it.num_chunks):
+        cosine_chunk(q, it, c, buf)
+        distill_chunk(d, buf[:, :it.chunk_len(c)], c * chunk_size, first=c == 0)
+    loss = distill_loss(d)
+    # entries of each chunk of items: one copy to the host
+    begins = list(range(0, it.n_items, chunk_size)) + [it.n_items]
+    cuts = items.indptr[torch.tensor(begins, device=dev)].tolist()
+    for c in range(it.num_chunks):
+        cosine_chunk(q, it, c, buf)
+        g = buf[:, :it.chunk_len(c)]
+        distill_chunk_grad(d, g, c * chunk_size, row_weights, out=g)
+        cosine_chunk_grad(queries, it, c, g, gq, first=c == 0)
+        lo, hi = cuts[c], cuts[c + 1]
+        part = CSR(items.indptr[begins[c]:begins[c + 1] + 1] - lo, items.indices[lo:hi],
+                   items.values[lo:hi], it.chunk_len(c), items.n_cols)
+        for j in range(qt.num_chunks):
+            b = j * qt.chunk_size
+            cosine_chunk_grad(part, qt, j, g[b:b + qt.chunk_len(j)], gi[lo:hi], transposed=True,
+                              first=j == 0)
+    return loss, cosine_grad_values(queries, gq, gq), cosine_grad_values(items, gi, gi)
 
 
 def row_inv_norms(m: CSR, stream=None) -> torch.Tensor:

@@ -10,7 +10,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("sps_prepare.hip", "sps_score.hip", "sps_bsc.hip",
                                               "sps_select.hip", "sps_distill.hip",
-                                              "sps_api.hip")]
+                                              "sps_grad.hip", "sps_api.hip")]
 HEADERS = [os.path.join(ROOT, "include", "sps.h"), os.path.join(CSRC, "sps_internal.h"),
            os.path.join(CSRC, "sps_device.h"), os.path.join(CSRC, "sps_rows.h")]
 LIB = os.path.join(PKG, "libsps.so")

@@ -192,24 +192,6 @@ QueriesLayout queries_layout(int64_t n, int64_t nnz, int32_t n_sub, bool dense, 
 
 }  // namespace
 
-struct sps_items {
-  sps::Geom g;
-  int64_t dim, nnz;
-  int device;
-  bool dense;
-  int32_t pitch;         // slab row pitch (items), dense only
-  int32_t heavy_blocks;  // heavy-dim blocks the slab holds (dense only)
-  int64_t slab_bstride;  // halves from one block's slab to the next's
-  float *inv_norm;
-  int4 *dinfo;
-  uint4 *dtab;
-  uint2 *post;
-  int32_t *slice_base;
-  int32_t *heavy;
-  uint16_t *slab;
-  uint32_t *post4;  // reduced-precision postings (null until sps_items_enable_half)
-};
-
 struct sps_queries {
   int64_t n_rows, dim, nnz;
   int32_t n_groups;

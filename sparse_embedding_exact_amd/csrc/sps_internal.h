@@ -318,3 +318,22 @@ size_t score_lds_bytes(int32_t S);
 hipError_t launch_score(const ScoreArgs &a, hipStream_t s);
 
 }  // namespace sps
+
+// A prepared corpus (the opaque handle of include/sps.h).
+struct sps_items {
+  sps::Geom g;
+  int64_t dim, nnz;
+  int device;
+  bool dense;
+  int32_t pitch;         // slab row pitch (items), dense only
+  int32_t heavy_blocks;  // heavy-dim blocks the slab holds (dense only)
+  int64_t slab_bstride;  // halves from one block's slab to the next's
+  float *inv_norm;
+  int4 *dinfo;
+  uint4 *dtab;
+  uint2 *post;
+  int32_t *slice_base;
+  int32_t *heavy;
+  uint16_t *slab;
+  uint32_t *post4;  // reduced-precision postings (null until sps_items_enable_half)
+};

@@ -188,3 +188,32 @@ def test_distill_null_handles(lib):
     assert lib.sps_distill_loss(None, P, None, None) == INV
     assert lib.sps_distill_chunk_grad(None, view(), None, P, 0, 100, None) == INV
     lib.sps_distill_destroy(None)
+
+
+def csr(n=4, cols=50, nnz=9, indptr=P, indices=P, values=P):
+    return ctypes.byref(sps._Csr(n, cols, nnz, indptr, indices, values))
+
+
+BAD_CSR = [(dict(n=-1), INV), (dict(cols=0), INV), (dict(nnz=-1), INV), (dict(indptr=None), INV),
+           (dict(indices=None), INV), (dict(values=None), INV), (dict(n=2**31), OVF),
+           (dict(nnz=2**31), OVF), (dict(cols=2**31), OVF)]
+
+
+@pytest.mark.parametrize("kw,want", BAD_CSR)
+def test_grad_bad_csr(lib, kw, want):
+    # the CSR is looked at before the other side's handle
+    assert lib.sps_cosine_grad(csr(**kw), None, 0, view(), 0, 1, P, None, 0, None) == want
+    assert lib.sps_cosine_grad_values(csr(**kw), P, P, None) == want
+
+
+def test_grad_refusals(lib):
+    n = ctypes.c_size_t()
+    assert lib.sps_cosine_grad_workspace_size(5, None, ctypes.byref(n)) == INV
+    assert lib.sps_cosine_grad_workspace_size(5, None, None) == INV
+    assert lib.sps_cosine_grad(None, None, 0, view(), 0, 1, P, None, 0, None) == INV
+    assert lib.sps_cosine_grad(csr(), None, 0, view(), 0, 1, P, None, 0, None) == INV
+    assert lib.sps_cosine_grad_values(None, P, P, None) == INV
+    assert lib.sps_cosine_grad_values(csr(), None, P, None) == INV
+    assert lib.sps_cosine_grad_values(csr(), P, None, None) == INV
+    assert lib.sps_cosine_grad_values(csr(n=0, nnz=0, indices=None, values=None), None, None,
+                                      None) == 0
