@@ -561,6 +561,22 @@ sps_status sps_cosine_grad(const sps_csr *rows, const sps_items *other, int32_t 
  * dv: DEVICE float[nnz], may be du itself. Sums in float64. */
 sps_status sps_cosine_grad_values(const sps_csr *rows, const float *du, float *dv, void *stream);
 
+/* Bytes of the workspace of sps_cosine_grad_both. Pure host. */
+sps_status sps_cosine_grad_both_workspace_size(int64_t nnz_queries, int64_t nnz_items,
+                                               size_t *bytes);
+
+/* dv of both sides at once, from the two canonical CSRs and the gradient of
+ * their whole score matrix (asynchronous; nothing is prepared): what a
+ * training step on a batch needs. grad: n_query x n_item (col_begin is not
+ * used). grad_queries, grad_items: DEVICE float[nnz] of each side. workspace:
+ * DEVICE, 256-byte aligned, used until the call's stream work is done. Sums
+ * are float32 in a fixed order, those of the norms float64: bitwise
+ * reproducible. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,
+ * SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW. */
+sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
+                                const sps_scores *grad, float *grad_queries, float *grad_items,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
 /* ------------------------------------------------------------------ */
 /* Block-Sparse CSR codec                                              */
 /* ------------------------------------------------------------------ */

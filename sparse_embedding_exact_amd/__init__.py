@@ -123,6 +123,9 @@ SIGNATURES = {
     "sps_cosine_grad_workspace_size": (_I32, [_I64, _P, ctypes.POINTER(_SZ)]),
     "sps_cosine_grad": (_I32, [ctypes.POINTER(_Csr), _P, _I32, ctypes.POINTER(_Scores), _I32, _I32,
                                _P, _P, _SZ, _P]),
+    "sps_cosine_grad_both_workspace_size": (_I32, [_I64, _I64, ctypes.POINTER(_SZ)]),
+    "sps_cosine_grad_both": (_I32, [ctypes.POINTER(_Csr), ctypes.POINTER(_Csr),
+                                    ctypes.POINTER(_Scores), _P, _P, _P, _SZ, _P]),
     "sps_cosine_grad_values": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P]),
     "sps_row_inv_norms": (_I32, [ctypes.POINTER(_Csr), _P, _P]),
     "sps_bsc_offsets_bytes": (_I32, [_I64, ctypes.POINTER(_SZ)]),
@@ -591,8 +594,8 @@ def _view(x: torch.Tensor, col_begin: int = 0) -> _Scores:
     assert x.dim() == 2 and x.dtype in _SCORE_TYPES, \
         "scores must be (rows, columns) of float32, float16 or bfloat16"
     n, m = x.shape
-    assert x.stride(1) == 1 or m <= 1, "rows must be contiguous"
-    ld = x.stride(0) if n > 1 else m
+    assert n == 0 or m <= 1 or x.stride(1) == 1, "rows must be contiguous"
+    ld = x.stride(0) if n > 1 and m else m
     return _Scores(x.data_ptr() if n and m else None, _SCORE_TYPES[x.dtype], n, m, ld, col_begin)
 
 
@@ -935,24 +938,24 @@ def cosine_grad_values(rows: CSR, du: torch.Tensor, out: torch.Tensor | None = N
     return out
 
 
-def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, chunk_size: int = 65536):
+def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, stream=None):
     """(gradient of the queries' values, gradient of the items' values), float32 (nnz,) each,
     from the gradient of their whole score matrix (n_query, n_item): float32, float16 or
-    bfloat16. The stored structure of both is fixed."""
-    assert grad.shape == (queries.n_rows, items.n_rows)
-
-    def side(rows, other, transposed):
-        du = torch.empty(rows.nnz, dtype=torch.float32, device=grad.device)
-        it = prepare(other, max(min(chunk_size, other.n_rows), 1))
-        if it.num_chunks == 0:
-            du.zero_()
-        for c in range(it.num_chunks):
-            b = c * it.chunk_size
-            part = grad[b:b + it.chunk_size] if transposed else grad[:, b:b + it.chunk_size]
-            cosine_chunk_grad(rows, it, c, part, du, transposed=transposed, first=c == 0)
-        return cosine_grad_values(rows, du, du)
-
-    return side(queries, items, False), side(items, queries, True)
+    bfloat16. The stored structure of both is fixed. Nothing is prepared: a training step's
+    batch has new values each time."""
+    load_library()
+    _here(queries.values, items.values, grad)
+    v = _view(grad)
+    q, i = queries._c(), items._c()
+    nb = _sized("sps_cosine_grad_both_workspace_size", q.nnz, i.nnz)
+    with _on(stream):
+        gq = torch.empty(q.nnz, dtype=torch.float32, device=grad.device)
+        gi = torch.empty(i.nnz, dtype=torch.float32, device=grad.device)
+        buf, ptr = _workspace(nb, grad.device)
+        _check(_lib.sps_cosine_grad_both(ctypes.byref(q), ctypes.byref(i), ctypes.byref(v),
+                                         gq.data_ptr(), gi.data_ptr(), ptr, nb,
+                                         _stream_ptr(stream)))
+    return gq, gi
 
 
 def bulk_distill(queries: CSR, items: CSR, teacher_ids: torch.Tensor,

@@ -132,15 +132,9 @@ __global__ __launch_bounds__(256) void grad_fold_kernel(WalkArgs a) {
   }
 }
 
-// One wave a row.
-__global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_t nnz,
-                                                          const int32_t *__restrict__ indptr,
-                                                          const float *__restrict__ values,
-                                                          const float *du, float *dv) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= n_rows) return;  // uniform per wave
-  const int64_t e0 = clamp64(indptr[row], 0, nnz), e1 = clamp64(indptr[row + 1], e0, nnz);
+// dv of the entries [e0, e1) of a row from its du, by one wave; sums in float64.
+__device__ __forceinline__ void through_norm(const float *__restrict__ values, const float *du,
+                                             float *dv, int64_t e0, int64_t e1, int lane) {
   double nn = 0, dot = 0;
   for (int64_t e = e0 + lane; e < e1; e += 64) {
     const double v = values[e];
@@ -152,6 +146,406 @@ __global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_
   const double inv = nn > 0 ? 1.0 / sqrt(nn) : 0.0, along = nn > 0 ? dot / nn : 0.0;
   for (int64_t e = e0 + lane; e < e1; e += 64)
     dv[e] = nn > 0 ? (float)(((double)du[e] - (double)values[e] * along) * inv) : 0.0f;
+}
+
+// One wave a row.
+__global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_t nnz,
+                                                          const int32_t *__restrict__ indptr,
+                                                          const float *__restrict__ values,
+                                                          const float *du, float *dv) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= n_rows) return;  // uniform per wave
+  const int64_t e0 = clamp64(indptr[row], 0, nnz), e1 = clamp64(indptr[row + 1], e0, nnz);
+  through_norm(values, du, dv, e0, e1, threadIdx.x & 63);
+}
+
+// ---------------------------------------------------------------------------
+// Both sides of a whole score matrix, from the two CSRs alone.
+//
+// The lists that a side walks are the other side's entries by dim. They are
+// made here by a stable radix sort of both CSRs at once (dim as the key, row
+// and unit value as the load), not taken from a prepared corpus: a training
+// step has new values every time, its batches are small, and a corpus'
+// per-slice sorts and dim index would keep 8 to 16 workgroups busy for longer
+// than all that follows. Five launches (two passes of up to 11 bits for dims
+// up to 2^22): unit values and the first histogram, scatter, histogram,
+// scatter, walk.
+//
+// The walk keeps up to 8192 values of G in LDS (one row of 8192 items, or R
+// rows of 8192 / R) and gives each entry of its rows a lane: the lane finds
+// the entry's list by bisection. Lists of up to 4 entries are the lane's own,
+// of up to 128 a group of 16 lanes', longer ones the wave's, 512 entries in
+// flight. The norm's part is taken off at the end of the same launch.
+// ---------------------------------------------------------------------------
+
+constexpr int kSortThreads = 512;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxBits = 11;
+constexpr int kMaxBins = 1 << kMaxBits;
+constexpr int kSortMinEntries = 8192;  // of a workgroup, at least
+constexpr int kSortBlocks = 120;       // about: every scatter block adds all histograms itself
+constexpr int kTile = 8192;            // values of G in LDS
+constexpr int kBatch = 512;            // entries walked at a time
+constexpr int kLaneList = 4, kGroupList = 128;
+
+struct BothSide {
+  const int32_t *indptr, *indices;
+  const float *values;
+  float *dv;
+  int64_t n_rows, nnz;
+  int64_t base;       // of its entries in the joint arrays
+  int32_t block0, blocks;  // of the sort
+  int32_t rows, cols; // rows of a workgroup, columns of its tile
+  int64_t groups;
+};
+
+struct BothArgs {
+  BothSide s[2];  // queries, items
+  float *unit;    // [entries of both]: value / norm
+  int32_t *row;   // row of the entry
+  int32_t *key[2];
+  uint2 *load[2]; // (row, bits of the unit value)
+  int32_t *hist;  // [sort blocks][bins]
+  int64_t per_block;
+  int32_t pass, passes, bits, last;  // `last`: which of the buffers holds the lists
+  const void *grad;
+  int64_t ld;
+};
+
+__device__ __forceinline__ int digit_of(int32_t key, const BothArgs &a) {
+  return (int)((uint32_t)key >> (a.pass * a.bits)) & ((1 << a.bits) - 1);
+}
+
+// the entries of sort block b: side, and joint positions [lo, hi)
+__device__ __forceinline__ int sort_range(const BothArgs &a, int b, int64_t &lo, int64_t &hi) {
+  const int side = b >= a.s[1].block0;
+  const BothSide &s = a.s[side];
+  lo = s.base + (int64_t)(b - s.block0) * a.per_block;
+  hi = lo + a.per_block < s.base + s.nnz ? lo + a.per_block : s.base + s.nnz;
+  return side;
+}
+__device__ __forceinline__ int32_t key_at(const BothArgs &a, int side, int64_t e) {
+  return a.pass == 0 ? a.s[side].indices[e - a.s[side].base] : a.key[(a.pass - 1) & 1][e];
+}
+
+__device__ __forceinline__ void histogram(const BothArgs &a, int b, int32_t *cnt) {
+  const int bins = 1 << a.bits;
+  for (int i = threadIdx.x; i < bins; i += kSortThreads) cnt[i] = 0;
+  __syncthreads();
+  int64_t lo, hi;
+  const int side = sort_range(a, b, lo, hi);
+  for (int64_t e = lo + threadIdx.x; e < hi; e += kSortThreads)
+    atomicAdd(&cnt[digit_of(key_at(a, side, e), a)], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < bins; i += kSortThreads) a.hist[(int64_t)b * bins + i] = cnt[i];
+}
+
+// Unit values and row numbers, one wave a row; the first workgroups make the
+// first histogram, which needs neither.
+__global__ __launch_bounds__(kSortThreads) void both_unit_kernel(BothArgs a) {
+  __shared__ int32_t cnt[kMaxBins];
+  const int blocks = a.s[0].blocks + a.s[1].blocks;
+  if ((int)blockIdx.x < blocks) {
+    histogram(a, blockIdx.x, cnt);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t row = (int64_t)(blockIdx.x - blocks) * kSortWaves + (threadIdx.x >> 6);
+  int side = 0;
+  if (row >= a.s[0].n_rows) {
+    row -= a.s[0].n_rows;
+    side = 1;
+  }
+  const BothSide &s = a.s[side];
+  if (row >= s.n_rows) return;
+  const int64_t e0 = clamp64(s.indptr[row], 0, s.nnz), e1 = clamp64(s.indptr[row + 1], e0, s.nnz);
+  double nn = 0;
+  for (int64_t e = e0 + lane; e < e1; e += 64) nn += (double)s.values[e] * (double)s.values[e];
+  nn = wave_sum(nn);
+  const double inv = nn > 0 ? 1.0 / sqrt(nn) : 0.0;
+  for (int64_t e = e0 + lane; e < e1; e += 64) {
+    a.unit[s.base + e] = (float)((double)s.values[e] * inv);
+    a.row[s.base + e] = (int32_t)row;
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void both_hist_kernel(BothArgs a) {
+  __shared__ int32_t cnt[kMaxBins];
+  histogram(a, blockIdx.x, cnt);
+}
+
+// Stable: a block's entries are cut among its waves in order, a wave takes 64
+// at a time, and equal digits among them are ranked by lane.
+__global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) {
+  __shared__ int32_t cnt[kSortWaves][kMaxBins];
+  __shared__ int32_t ws[kSortWaves];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, b = blockIdx.x;
+  const int bins = 1 << a.bits;
+  int64_t lo, hi;
+  const int side = sort_range(a, b, lo, hi);
+  const BothSide &s = a.s[side];
+  const int64_t part = ((a.per_block / kSortWaves) + 63) / 64 * 64;
+  const int64_t e0 = lo + w * part < hi ? lo + w * part : hi;
+  const int64_t e1 = w + 1 < kSortWaves && e0 + part < hi ? e0 + part : hi;
+  for (int i = lane; i < bins; i += 64) cnt[w][i] = 0;
+  for (int64_t e = e0 + lane; e < e1; e += 64)
+    atomicAdd(&cnt[w][digit_of(key_at(a, side, e), a)], 1);
+  __syncthreads();
+  // thread t places digits 4 t .. 4 t + 3
+  int32_t total[4] = {}, before[4] = {};
+  if (4 * t < bins)
+    for (int j = 0; j < s.blocks; ++j) {
+      const int4 h = *reinterpret_cast<const int4 *>(a.hist + (int64_t)(s.block0 + j) * bins + 4 * t);
+      const int32_t v[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        total[i] += v[i];
+        if (j < b - s.block0) before[i] += v[i];
+      }
+    }
+  int32_t all;
+  const int32_t sum = total[0] + total[1] + total[2] + total[3];
+  int32_t at = block_incl_scan<kSortThreads, int32_t>(sum, ws, &all) - sum + (int32_t)s.base;
+  if (4 * t < bins)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int32_t o = at + before[i];
+#pragma unroll
+      for (int j = 0; j < kSortWaves; ++j) {
+        const int32_t c = cnt[j][4 * t + i];
+        cnt[j][4 * t + i] = o;
+        o += c;
+      }
+      at += total[i];
+    }
+  __syncthreads();
+  int32_t *key = a.key[a.pass & 1];
+  uint2 *load = a.load[a.pass & 1];
+  const uint2 *from = a.load[(a.pass + 1) & 1];
+  for (int64_t w0 = e0; w0 < e1; w0 += 64) {
+    const int64_t e = w0 + lane;
+    const bool valid = e < e1;
+    const int32_t k = valid ? key_at(a, side, e) : 0;
+    uint2 v = make_uint2(0, 0);
+    if (valid)
+      v = a.pass == 0 ? make_uint2((uint32_t)a.row[e], __builtin_bit_cast(uint32_t, a.unit[e]))
+                      : from[e];
+    const int d = digit_of(k, a);
+    uint64_t same = __ballot(valid);
+    for (int i = 0; i < a.bits; ++i) {
+      const bool bit = d >> i & 1;
+      const uint64_t m = __ballot(bit);
+      same &= bit ? m : ~m;
+    }
+    if (valid) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      const int32_t p = cnt[w][d] + rank;
+      __builtin_amdgcn_wave_barrier();
+      if (rank == 0) cnt[w][d] = p + __popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      key[p] = k;
+      load[p] = v;
+    }
+  }
+}
+
+// Sum of a float over the row of 16 lanes (in its last lane), and over the
+// wave (in lane 63); every lane must be active.
+template <int CTRL, int ROW_MASK, bool BOUND>
+__device__ __forceinline__ float dpp_f32(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL,
+                                                               ROW_MASK, 0xf, BOUND));
+}
+__device__ __forceinline__ float row16_total(float x) {
+  x += dpp_f32<0x111, 0xf, true>(x);   // row_shr:1
+  x += dpp_f32<0x112, 0xf, true>(x);   // row_shr:2
+  x += dpp_f32<0x114, 0xf, true>(x);   // row_shr:4
+  x += dpp_f32<0x118, 0xf, true>(x);   // row_shr:8
+  return x;
+}
+__device__ __forceinline__ float wave_total(float x) {
+  x = row16_total(x);
+  x += dpp_f32<0x142, 0xa, false>(x);  // row_bcast:15
+  x += dpp_f32<0x143, 0xc, false>(x);  // row_bcast:31
+  return x;
+}
+
+struct BothShared {
+  float tile[kTile];
+  int32_t lo[kBatch], hi[kBatch];
+  float acc[kBatch];
+  uint16_t row[kBatch];
+};
+
+// `load` entries [i, i + 2) with the second masked: 16 bytes, 8-byte aligned
+struct __attribute__((packed, aligned(8))) Pair {
+  uint2 a, b;
+};
+
+template <typename T, bool TRANSPOSED>
+__device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group, BothShared &sh) {
+  const BothSide &s = a.s[side], &o = a.s[1 - side];
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const int64_t r0 = group * s.rows;
+  const int nr = s.n_rows - r0 < s.rows ? (int)(s.n_rows - r0) : s.rows;
+  const int64_t e0 = clamp64(s.indptr[r0], 0, s.nnz), e1 = clamp64(s.indptr[r0 + nr], e0, s.nnz);
+  const int32_t *key = a.key[a.last];
+  const uint2 *load = a.load[a.last];
+  const T *g = static_cast<const T *>(a.grad);
+  for (int64_t eb = e0; eb < e1; eb += kBatch) {
+    const int ne = e1 - eb < kBatch ? (int)(e1 - eb) : kBatch;
+    __syncthreads();  // the batch before is done with
+    // entry i belongs to thread (i % 4) * 64 + i / 4 % 64: every wave gets some of a short row
+    for (int i = lane * 4 + w; i < ne; i += kGradThreads) {
+      const uint32_t d = (uint32_t)s.indices[eb + i];
+      int32_t l0 = (int32_t)o.base, l1 = (int32_t)(o.base + o.nnz), h0 = l0, h1 = l1;
+      while (l0 < l1 || h0 < h1) {  // first key >= d and first key > d, side by side
+        if (l0 < l1) {
+          const int32_t m = l0 + ((l1 - l0) >> 1);
+          if ((uint32_t)key[m] < d) l0 = m + 1;
+          else l1 = m;
+        }
+        if (h0 < h1) {
+          const int32_t m = h0 + ((h1 - h0) >> 1);
+          if ((uint32_t)key[m] <= d) h0 = m + 1;
+          else h1 = m;
+        }
+      }
+      sh.lo[i] = l0;
+      sh.hi[i] = h0;
+      sh.acc[i] = 0;
+      const int64_t r = (int64_t)a.row[s.base + eb + i] - r0;
+      sh.row[i] = (uint16_t)(r >= 0 && r < nr ? r : 0);
+    }
+    for (int64_t c0 = 0; c0 < o.n_rows; c0 += s.cols) {
+      const int nc = o.n_rows - c0 < s.cols ? (int)(o.n_rows - c0) : s.cols;
+      __syncthreads();
+      if (!TRANSPOSED) {
+        constexpr int V = kVec<T>;
+        for (int r = 0; r < nr; ++r) {
+          const T *p = g + (r0 + r) * a.ld + c0;
+          float *q = sh.tile + r * s.cols;
+          for (int j = t * V; j < nc; j += kGradThreads * V) {
+            if (j + V <= nc) {
+              const Vec<T> v = *reinterpret_cast<const Vec<T> *>(p + j);
+#pragma unroll
+              for (int e = 0; e < V; ++e) q[j + e] = to_f32(v.e[e]);
+            } else {
+              for (int e = 0; j + e < nc; ++e) q[j + e] = to_f32(p[j + e]);
+            }
+          }
+        }
+      } else {
+        const int r = t % s.rows, step = kGradThreads / s.rows;
+        if (r < nr)
+          for (int j = t / s.rows; j < nc; j += step)
+            sh.tile[r * s.cols + j] = to_f32(g[(c0 + j) * a.ld + r0 + r]);
+      }
+      __syncthreads();
+      const bool whole = nc == o.n_rows;
+      for (int i0 = 0; i0 < ne; i0 += kGradThreads) {
+        const int i = i0 + lane * 4 + w;
+        int32_t l = 0, h = 0;
+        int at = 0;
+        if (i < ne) {
+          l = sh.lo[i];
+          h = sh.hi[i];
+          at = (int)sh.row[i] * s.cols;
+          if (!whole && h - l > kLaneList) {
+            // the list's part in this tile starts where the last tile's ended
+            int32_t m0 = l, m1 = h;
+            while (m0 < m1) {
+              const int32_t m = m0 + ((m1 - m0) >> 1);
+              if ((int64_t)load[m].x < c0 + nc) m0 = m + 1;
+              else m1 = m;
+            }
+            h = m0;
+            sh.lo[i] = h;
+          }
+        }
+        float acc = 0;
+        const int n = h - l;
+        if (n <= kLaneList)
+          for (int j = 0; j < n; ++j) {
+            const uint2 v = load[l + j];
+            const uint32_t c = v.x - (uint32_t)c0;
+            if (c < (uint32_t)nc) acc += sh.tile[at + c] * __builtin_bit_cast(float, v.y);
+          }
+        if (i < ne) sh.acc[i] += acc;
+        __builtin_amdgcn_wave_barrier();  // other lanes add to it below
+        // four lists at a time, 16 lanes each
+        uint64_t mid = __ballot(n > kLaneList && n <= kGroupList);
+        while (mid) {
+          int src = -1, q = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int f = mid ? __builtin_ctzll(mid) : -1;
+            if (k == lane >> 4) src = f;
+            mid &= mid ? mid - 1 : 0;
+          }
+          const int from = src < 0 ? 0 : src;
+          // every lane shuffles: a source lane must be active
+          const int32_t l2 = __shfl(l, from, 64), n1 = __shfl(n, from, 64);
+          const int at2 = __shfl(at, from, 64);
+          const int32_t n2 = src < 0 ? 0 : n1;
+          float part = 0;
+          for (q = lane & 15; q < n2; q += 16) {
+            const uint2 v = load[l2 + q];
+            const uint32_t c = v.x - (uint32_t)c0;
+            if (c < (uint32_t)nc) part += sh.tile[at2 + c] * __builtin_bit_cast(float, v.y);
+          }
+          part = row16_total(part);
+          if ((lane & 15) == 15 && src >= 0) sh.acc[i0 + src * 4 + w] += part;
+        }
+        // the whole wave's
+        uint64_t big = __ballot(n > kGroupList);
+        while (big) {
+          const int f = __builtin_ctzll(big);
+          big &= big - 1;
+          const int32_t l2 = __builtin_amdgcn_readlane(l, f), h2 = __builtin_amdgcn_readlane(h, f);
+          const int at2 = __builtin_amdgcn_readlane(at, f);
+          const float *tile = sh.tile + at2;
+          float p0 = 0, p1 = 0;
+          int32_t q = l2 + lane * 2;
+          for (; q - lane * 2 + 512 <= h2; q += 512) {
+            Pair v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const Pair *>(load + q + k * 128);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t ca = v[k].a.x - (uint32_t)c0, cb = v[k].b.x - (uint32_t)c0;
+              if (ca < (uint32_t)nc) p0 += tile[ca] * __builtin_bit_cast(float, v[k].a.y);
+              if (cb < (uint32_t)nc) p1 += tile[cb] * __builtin_bit_cast(float, v[k].b.y);
+            }
+          }
+          for (; q < h2; q += 128) {
+            const uint2 va = load[q];
+            const uint2 vb = q + 1 < h2 ? load[q + 1] : make_uint2((uint32_t)c0, 0);
+            const uint32_t ca = va.x - (uint32_t)c0, cb = vb.x - (uint32_t)c0;
+            if (ca < (uint32_t)nc) p0 += tile[ca] * __builtin_bit_cast(float, va.y);
+            if (cb < (uint32_t)nc) p1 += tile[cb] * __builtin_bit_cast(float, vb.y);
+          }
+          const float part = wave_total(p0 + p1);
+          if (lane == 63) sh.acc[i0 + f * 4 + w] += part;
+        }
+      }
+    }
+    __syncthreads();
+    for (int i = t; i < ne; i += kGradThreads) s.dv[eb + i] = sh.acc[i];
+  }
+  __syncthreads();
+  for (int r = w; r < nr; r += kGradThreads / 64) {
+    const int64_t b0 = clamp64(s.indptr[r0 + r], 0, s.nnz), b1 = clamp64(s.indptr[r0 + r + 1], b0, s.nnz);
+    through_norm(s.values, s.dv, s.dv, b0, b1, lane);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kGradThreads) void both_walk_kernel(BothArgs a) {
+  __shared__ BothShared sh;
+  const int64_t id = xcd_tile(blockIdx.x, gridDim.x);
+  if (id < a.s[0].groups) walk<T, false>(a, 0, id, sh);
+  else walk<T, true>(a, 1, id - a.s[0].groups, sh);
 }
 
 }  // namespace sps
@@ -171,6 +565,43 @@ sps_status check_csr(const sps_csr *m, const char *what) {
   if (m->nnz > 0 && (!m->indices || !m->values))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL indices or values", what);
   return SPS_OK;
+}
+
+struct BothLayout {
+  size_t unit, row, key[2], load[2], hist, total;
+  int64_t per_block;
+};
+BothLayout both_layout(int64_t n) {
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  BothLayout L;
+  size_t at = 0;
+  L.unit = at;
+  at = up(at + (size_t)n * 4);
+  L.row = at;
+  at = up(at + (size_t)n * 4);
+  for (int i = 0; i < 2; ++i) {
+    L.key[i] = at;
+    at = up(at + (size_t)n * 4);
+    L.load[i] = at;
+    at = up(at + (size_t)n * 8);
+  }
+  L.per_block = (n + sps::kSortBlocks - 1) / sps::kSortBlocks;
+  if (L.per_block < sps::kSortMinEntries) L.per_block = sps::kSortMinEntries;
+  L.hist = at;
+  // one block more on each side than full blocks of the whole
+  at = up(at + ((size_t)(n / L.per_block) + 2) * sps::kMaxBins * 4);
+  L.total = at;
+  return L;
+}
+
+// Rows of a workgroup of the walk. Along rows of G: as many as fit the tile,
+// while there are rows for 1024 workgroups. Across them (the items' side):
+// 16 bytes of a row of G at a time, more where the queries are few.
+int32_t walk_rows(int64_t n_rows, int64_t n_cols, bool transposed, int32_t size) {
+  int32_t r = transposed ? 16 / size : 1;
+  const int32_t most = transposed ? 16 : 8;
+  while (r < most && sps::kTile / (2 * r) >= n_cols && n_rows / (2 * r) >= 1024) r *= 2;
+  return r;
 }
 
 }  // namespace
@@ -266,6 +697,107 @@ sps_status sps_cosine_grad_values(const sps_csr *rows, const float *du, float *d
   hipLaunchKernelGGL(sps::grad_values_kernel, dim3((uint32_t)((rows->n_rows + 3) / 4)), dim3(256),
                      0, reinterpret_cast<hipStream_t>(stream), rows->n_rows, rows->nnz,
                      rows->indptr, rows->values, du, dv);
+  return sps::launch_status(what);
+}
+
+sps_status sps_cosine_grad_both_workspace_size(int64_t nnz_queries, int64_t nnz_items,
+                                               size_t *bytes) {
+  if (!bytes) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output pointer");
+  if (nnz_queries < 0 || nnz_items < 0)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "negative size");
+  if (nnz_queries >= kMax31 || nnz_items >= kMax31 || nnz_queries + nnz_items >= kMax31)
+    return set_error(SPS_ERR_OVERFLOW, "entries of both sides must be below 2^31");
+  *bytes = both_layout(nnz_queries + nnz_items).total;
+  return SPS_OK;
+}
+
+sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
+                                const sps_scores *grad, float *grad_queries, float *grad_items,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+  const char *what = "sps_cosine_grad_both";
+  sps_status st = check_csr(queries, what);
+  if (st == SPS_OK) st = check_csr(items, what);
+  if (st == SPS_OK) st = sps::check_scores(grad, what);
+  if (st != SPS_OK) return st;
+  if (queries->n_cols != items->n_cols)
+    return set_error(SPS_ERR_DIM_MISMATCH, "%s: dims of the two sides differ: %lld and %lld", what,
+                     (long long)queries->n_cols, (long long)items->n_cols);
+  if (grad->n_rows != queries->n_rows || grad->n_cols != items->n_rows)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the gradient is not %lld x %lld", what,
+                     (long long)queries->n_rows, (long long)items->n_rows);
+  size_t need = 0;
+  st = sps_cosine_grad_both_workspace_size(queries->nnz, items->nnz, &need);
+  if (st != SPS_OK) return st;
+  if ((queries->nnz > 0 && !grad_queries) || (items->nnz > 0 && !grad_items))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL output", what);
+  const int64_t n = queries->nnz + items->nnz;
+  if (n == 0) return SPS_OK;
+  if (!workspace) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL workspace", what);
+  if (workspace_bytes < need)
+    return set_error(SPS_ERR_WORKSPACE_TOO_SMALL, "%s: need %zu bytes, got %zu", what, need,
+                     workspace_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", what);
+  const BothLayout L = both_layout(n);
+  char *b = static_cast<char *>(workspace);
+  sps::BothArgs a{};
+  a.unit = reinterpret_cast<float *>(b + L.unit);
+  a.row = reinterpret_cast<int32_t *>(b + L.row);
+  for (int i = 0; i < 2; ++i) {
+    a.key[i] = reinterpret_cast<int32_t *>(b + L.key[i]);
+    a.load[i] = reinterpret_cast<uint2 *>(b + L.load[i]);
+  }
+  a.hist = reinterpret_cast<int32_t *>(b + L.hist);
+  a.per_block = L.per_block;
+  int bits = 1;
+  while (bits < 31 && (queries->n_cols - 1) >> bits) ++bits;
+  a.passes = (bits + sps::kMaxBits - 1) / sps::kMaxBits;
+  a.bits = (bits + a.passes - 1) / a.passes;
+  if (a.bits < 2) a.bits = 2;  // histograms are read four bins at a time
+  a.last = (a.passes - 1) & 1;
+  a.grad = grad->data;
+  a.ld = grad->ld;
+  const sps_csr *m[2] = {queries, items};
+  float *dv[2] = {grad_queries, grad_items};
+  int64_t base = 0, groups = 0;
+  int32_t blocks = 0;
+  for (int i = 0; i < 2; ++i) {
+    sps::BothSide &s = a.s[i];
+    s.indptr = m[i]->indptr;
+    s.indices = m[i]->indices;
+    s.values = m[i]->values;
+    s.dv = dv[i];
+    s.n_rows = m[i]->n_rows;
+    s.nnz = m[i]->nnz;
+    s.base = base;
+    base += s.nnz;
+    s.block0 = blocks;
+    s.blocks = (int32_t)((s.nnz + a.per_block - 1) / a.per_block);
+    blocks += s.blocks;
+    s.rows = walk_rows(s.n_rows, m[1 - i]->n_rows, i == 1, sps::dtype_size(grad->dtype));
+    s.cols = sps::kTile / s.rows;
+    s.groups = (s.n_rows + s.rows - 1) / s.rows;
+    groups += s.groups;
+  }
+  const int64_t rows = queries->n_rows + items->n_rows;
+  const int64_t unit_blocks = blocks + (rows + sps::kSortWaves - 1) / sps::kSortWaves;
+  if (groups > kMax31 || unit_blocks > kMax31)
+    return set_error(SPS_ERR_OVERFLOW, "%s: too many rows for a launch", what);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const dim3 sort(sps::kSortThreads);
+  hipLaunchKernelGGL(sps::both_unit_kernel, dim3((uint32_t)unit_blocks), sort, 0, s, a);
+  for (a.pass = 0; a.pass < a.passes; ++a.pass) {
+    if (a.pass > 0)
+      hipLaunchKernelGGL(sps::both_hist_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
+    hipLaunchKernelGGL(sps::both_scatter_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
+  }
+  const dim3 grid((uint32_t)groups), block(sps::kGradThreads);
+  if (grad->dtype == SPS_F32)
+    hipLaunchKernelGGL((sps::both_walk_kernel<float>), grid, block, 0, s, a);
+  else if (grad->dtype == SPS_F16)
+    hipLaunchKernelGGL((sps::both_walk_kernel<sps::f16_t>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::both_walk_kernel<sps::bf16_t>), grid, block, 0, s, a);
   return sps::launch_status(what);
 }
 

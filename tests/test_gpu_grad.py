@@ -37,8 +37,8 @@ def corpus(r, n, dim, per_row, zeros=True):
         v.append(w)
         indptr.append(indptr[-1] + k)
     cat = np.concatenate
-    return synth.HostCSR(np.array(indptr, np.int32), cat(ix).astype(np.int32) if ix else
-                         np.zeros(0, np.int32), cat(v).astype(np.float32) if v else
+    return synth.HostCSR(np.array(indptr, np.int32), cat(ix).astype(np.int32) if indptr[-1] else
+                         np.zeros(0, np.int32), cat(v).astype(np.float32) if indptr[-1] else
                          np.zeros(0, np.float32), n, dim)
 
 
@@ -74,8 +74,20 @@ def close(got, want, bar):
     assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], bar[bad][:5])
 
 
+def by_chunks(env, rows, other, g, transposed, chunk_size):
+    torch, sps, dev = env
+    h = sps.prepare(other, min(chunk_size, max(other.n_rows, 1)))
+    # a corpus without chunks starts no sums
+    du = torch.full((rows.nnz,), float("nan") if h.num_chunks else 0.0, device=dev)
+    for c in range(h.num_chunks):
+        b = c * h.chunk_size
+        part = g[b:b + h.chunk_size] if transposed else g[:, b:b + h.chunk_size]
+        sps.cosine_chunk_grad(rows, h, c, part, du, transposed=transposed, first=c == 0)
+    return sps.cosine_grad_values(rows, du)
+
+
 SHAPES = [(1, 1, 5), (3, 7, 40), (17, 1023, 60), (8, 1025, 3000), (40, 3000, 20), (1030, 33, 90),
-          (2100, 1100, 400)]
+          (2100, 1100, 400), (3, 17000, 50), (9000, 5, 30), (0, 4, 9), (4, 0, 9)]
 
 
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
@@ -88,10 +100,13 @@ def test_both_sides(env, dtype, nq, ni, dim):
     g = torch.from_numpy(r.randn(nq, ni).astype(np.float32)).to(getattr(torch, dtype)).to(dev)
     g64 = g.double().cpu().numpy()
     qc, ic = sps.CSR.from_host(q, dev), sps.CSR.from_host(it, dev)
-    for cs in (65536, 1500, 700):
-        gq, gi = sps.cosine_grad(qc, ic, g, chunk_size=cs)
-        close(gq, *oracle(q, it, g64, ni // 256 + 4))
-        close(gi, *oracle(it, q, g64.T, nq // 256 + 4))
+    want_q, want_i = oracle(q, it, g64, ni // 256 + 4), oracle(it, q, g64.T, nq // 256 + 4)
+    gq, gi = sps.cosine_grad(qc, ic, g)
+    close(gq, *want_q)
+    close(gi, *want_i)
+    for cs in (4096, 1500, 700):  # by chunks of a prepared corpus
+        close(by_chunks(env, qc, ic, g, False, cs), *want_q)
+        close(by_chunks(env, ic, qc, g, True, cs), *want_i)
 
 
 def test_shared_dims_and_long_rows(env):
@@ -101,10 +116,32 @@ def test_shared_dims_and_long_rows(env):
     r = np.random.RandomState(0)
     q, it = corpus(r, 30, 150, lambda i: 150), corpus(r, 2500, 150, lambda i: 100 + i % 51)
     g = torch.randn(30, 2500, device=dev)
-    gq, gi = sps.cosine_grad(sps.CSR.from_host(q, dev), sps.CSR.from_host(it, dev), g)
+    qc, ic = sps.CSR.from_host(q, dev), sps.CSR.from_host(it, dev)
+    gq, gi = sps.cosine_grad(qc, ic, g)
     g64 = g.double().cpu().numpy()
-    close(gq, *oracle(q, it, g64, 3))
-    close(gi, *oracle(it, q, g64.T, 3))
+    want_q, want_i = oracle(q, it, g64, 3), oracle(it, q, g64.T, 3)
+    close(gq, *want_q)
+    close(gi, *want_i)
+    close(by_chunks(env, qc, ic, g, False, 2500), *want_q)
+    close(by_chunks(env, ic, qc, g, True, 30), *want_i)
+
+
+def test_rows_of_many_entries(env):
+    """Rows of more entries than are walked at a time, over more columns than a tile, dims up
+    to the largest key."""
+    torch, sps, dev = env
+    r = np.random.RandomState(8)
+    q, it = corpus(r, 4, 2000, lambda i: [1200, 0, 700, 3][i]), corpus(r, 9000, 2000, lambda i: i % 9)
+    g = torch.randn(4, 9000, device=dev)
+    g64 = g.double().cpu().numpy()
+    want_q, want_i = oracle(q, it, g64, 40), oracle(it, q, g64.T, 40)
+    for shift in (0, 2**31 - 2 - 2000):  # the same rows at the upper end of the dims
+        for m in (q, it):
+            m.indices += np.int32(shift)
+            m.n_cols = 2000 + shift
+        gq, gi = sps.cosine_grad(sps.CSR.from_host(q, dev), sps.CSR.from_host(it, dev), g)
+        close(gq, *want_q)
+        close(gi, *want_i)
 
 
 def test_workload(env):
@@ -177,16 +214,25 @@ def test_reproducible_streams_and_graphs(env):
         step(b, s)
         torch.cuda.synchronize()
         assert torch.equal(a, b)
+    ic = sps.CSR.from_host(it, dev)
+    both = sps.cosine_grad(qc, ic, g)
+    for s in [torch.cuda.Stream() for _ in range(2)]:
+        again = sps.cosine_grad(qc, ic, g, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(both[0], again[0]) and torch.equal(both[1], again[1])
     out = torch.empty(q.nnz, device=dev)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
         step(out)
+        both = sps.cosine_grad(qc, ic, g)
     for i in range(4):
         g.copy_(torch.randn(50, 3000, device=dev))
         graph.replay()
         e = step(torch.empty(q.nnz, device=dev))
+        fresh = sps.cosine_grad(qc, ic, g)
         torch.cuda.synchronize()
         assert torch.equal(out, e)
+        assert torch.equal(both[0], fresh[0]) and torch.equal(both[1], fresh[1])
 
 
 def test_faulty_other_side_scores_nothing(env):
@@ -215,13 +261,14 @@ def test_refusals(env):
                         (lambda: sps.cosine_chunk_grad(qc, h, 1, g, du), -1),
                         (lambda: sps.cosine_chunk_grad(qc, h, 0, g, du, transposed=True), -1),
                         (lambda: sps.cosine_chunk_grad(qc, h, 0, g[:4], du), -1),
+                        (lambda: sps.cosine_grad(qc, qc, g), -1), (lambda: sps.cosine_grad(qc, other, g[:, :5]), -3),
                         (lambda: sps.cosine_chunk_grad(other, h, 0, g, torch.zeros(other.nnz, device=dev)), -3)):
         with pytest.raises(sps.SpsError) as e:
             bad()
         assert e.value.status == status
     for bad in (lambda: sps.cosine_chunk_grad(qc, h, 0, g, du[1:]),
                 lambda: sps.cosine_chunk_grad(qc, h, 0, g, du.double()),
-                lambda: sps.cosine_grad(qc, qc, g), lambda: sps.cosine_grad_values(qc, du, du[1:])):
+                lambda: sps.cosine_grad(qc, qc, g.double()), lambda: sps.cosine_grad_values(qc, du, du[1:])):
         with pytest.raises(AssertionError):
             bad()
 

@@ -217,3 +217,31 @@ def test_grad_refusals(lib):
     assert lib.sps_cosine_grad_values(csr(), P, None, None) == INV
     assert lib.sps_cosine_grad_values(csr(n=0, nnz=0, indices=None, values=None), None, None,
                                       None) == 0
+
+
+@pytest.mark.parametrize("kw,want", BAD_CSR)
+def test_both_bad_csr(lib, kw, want):
+    both = lib.sps_cosine_grad_both
+    assert both(csr(**kw), csr(), view(rows=4, cols=4), P, P, P, 1 << 30, None) == want
+    assert both(csr(), csr(**kw), view(rows=4, cols=4), P, P, P, 1 << 30, None) == want
+
+
+def test_both_refusals(lib):
+    n = ctypes.c_size_t()
+    sizes = lib.sps_cosine_grad_both_workspace_size
+    assert sizes(5, 5, None) == INV and sizes(-1, 5, ctypes.byref(n)) == INV
+    assert sizes(2**31 - 10, 9, ctypes.byref(n)) == OVF and sizes(2**31, 9, ctypes.byref(n)) == OVF
+    assert sizes(9, 9, ctypes.byref(n)) == 0
+    v = view(rows=4, cols=4)
+    both = lib.sps_cosine_grad_both
+    assert both(None, csr(), v, P, P, P, n.value, None) == INV
+    assert both(csr(), csr(), None, P, P, P, n.value, None) == INV
+    assert both(csr(), csr(cols=51), v, P, P, P, n.value, None) == -3
+    assert both(csr(), csr(n=5), v, P, P, P, n.value, None) == INV
+    assert both(csr(), csr(), v, None, P, P, n.value, None) == INV
+    assert both(csr(), csr(), v, P, None, P, n.value, None) == INV
+    assert both(csr(), csr(), v, P, P, None, n.value, None) == INV
+    assert both(csr(), csr(), v, P, P, P, n.value - 1, None) == WS
+    assert both(csr(), csr(), v, P, P, P + 16, n.value, None) == INV
+    empty = dict(nnz=0, indices=None, values=None)
+    assert both(csr(**empty), csr(**empty), v, None, None, None, 0, None) == 0
