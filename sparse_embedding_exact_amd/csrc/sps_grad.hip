@@ -184,8 +184,10 @@ constexpr int kMaxBits = 11;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortMinEntries = 8192;  // of a workgroup, at least
 constexpr int kSortBlocks = 120;       // about: every scatter block adds all histograms itself
+constexpr int kSortAhead = 16;         // entries of a lane in flight
 constexpr int kTile = 8192;            // values of G in LDS
 constexpr int kBatch = 512;            // entries walked at a time
+constexpr int kSamples = 2048;         // keys of the other side in LDS for the bisections
 constexpr int kLaneList = 4, kGroupList = 128;
 
 struct BothSide {
@@ -234,8 +236,17 @@ __device__ __forceinline__ void histogram(const BothArgs &a, int b, int32_t *cnt
   __syncthreads();
   int64_t lo, hi;
   const int side = sort_range(a, b, lo, hi);
-  for (int64_t e = lo + threadIdx.x; e < hi; e += kSortThreads)
-    atomicAdd(&cnt[digit_of(key_at(a, side, e), a)], 1);
+  for (int64_t e0 = lo + threadIdx.x; e0 < hi; e0 += kSortThreads * kSortAhead) {
+    int32_t k[kSortAhead];
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      const int64_t e = e0 + (int64_t)i * kSortThreads;
+      k[i] = key_at(a, side, e < hi ? e : e0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i)
+      if (e0 + (int64_t)i * kSortThreads < hi) atomicAdd(&cnt[digit_of(k[i], a)], 1);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < bins; i += kSortThreads) a.hist[(int64_t)b * bins + i] = cnt[i];
 }
@@ -288,12 +299,19 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
   const int64_t e0 = lo + w * part < hi ? lo + w * part : hi;
   const int64_t e1 = w + 1 < kSortWaves && e0 + part < hi ? e0 + part : hi;
   for (int i = lane; i < bins; i += 64) cnt[w][i] = 0;
-  for (int64_t e = e0 + lane; e < e1; e += 64)
-    atomicAdd(&cnt[w][digit_of(key_at(a, side, e), a)], 1);
+  for (int64_t w0 = e0 + lane; w0 < e1; w0 += 64 * kSortAhead) {
+    int32_t k[kSortAhead];
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) k[i] = key_at(a, side, w0 + 64 * i < e1 ? w0 + 64 * i : w0);
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i)
+      if (w0 + 64 * i < e1) atomicAdd(&cnt[w][digit_of(k[i], a)], 1);
+  }
   __syncthreads();
   // thread t places digits 4 t .. 4 t + 3
   int32_t total[4] = {}, before[4] = {};
   if (4 * t < bins)
+#pragma unroll 8
     for (int j = 0; j < s.blocks; ++j) {
       const int4 h = *reinterpret_cast<const int4 *>(a.hist + (int64_t)(s.block0 + j) * bins + 4 * t);
       const int32_t v[4] = {h.x, h.y, h.z, h.w};
@@ -322,29 +340,36 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
   int32_t *key = a.key[a.pass & 1];
   uint2 *load = a.load[a.pass & 1];
   const uint2 *from = a.load[(a.pass + 1) & 1];
-  for (int64_t w0 = e0; w0 < e1; w0 += 64) {
-    const int64_t e = w0 + lane;
-    const bool valid = e < e1;
-    const int32_t k = valid ? key_at(a, side, e) : 0;
-    uint2 v = make_uint2(0, 0);
-    if (valid)
-      v = a.pass == 0 ? make_uint2((uint32_t)a.row[e], __builtin_bit_cast(uint32_t, a.unit[e]))
-                      : from[e];
-    const int d = digit_of(k, a);
-    uint64_t same = __ballot(valid);
-    for (int i = 0; i < a.bits; ++i) {
-      const bool bit = d >> i & 1;
-      const uint64_t m = __ballot(bit);
-      same &= bit ? m : ~m;
+  for (int64_t w0 = e0; w0 < e1; w0 += 64 * kSortAhead) {
+    int32_t k[kSortAhead];
+    uint2 v[kSortAhead];
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      const int64_t x = w0 + 64 * i + lane, e = x < e1 ? x : e0;
+      k[i] = key_at(a, side, e);
+      v[i] = a.pass == 0 ? make_uint2((uint32_t)a.row[e], __builtin_bit_cast(uint32_t, a.unit[e]))
+                         : from[e];
     }
-    if (valid) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      const int32_t p = cnt[w][d] + rank;
-      __builtin_amdgcn_wave_barrier();
-      if (rank == 0) cnt[w][d] = p + __popcll(same);
-      __builtin_amdgcn_wave_barrier();
-      key[p] = k;
-      load[p] = v;
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i) {
+      if (w0 + 64 * i >= e1) break;  // uniform
+      const bool valid = w0 + 64 * i + lane < e1;
+      const int d = digit_of(k[i], a);
+      uint64_t same = __ballot(valid);
+      for (int j = 0; j < a.bits; ++j) {
+        const bool bit = d >> j & 1;
+        const uint64_t m = __ballot(bit);
+        same &= bit ? m : ~m;
+      }
+      if (valid) {
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        const int32_t p = cnt[w][d] + rank;
+        __builtin_amdgcn_wave_barrier();
+        if (rank == 0) cnt[w][d] = p + __popcll(same);
+        __builtin_amdgcn_wave_barrier();
+        key[p] = k[i];
+        load[p] = v[i];
+      }
     }
   }
 }
@@ -371,7 +396,7 @@ __device__ __forceinline__ float wave_total(float x) {
 }
 
 struct BothShared {
-  float tile[kTile];
+  float tile[kTile];  // indexes are masked: in range whatever a CSR holds
   int32_t lo[kBatch], hi[kBatch];
   float acc[kBatch];
   uint16_t row[kBatch];
@@ -395,20 +420,49 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
   for (int64_t eb = e0; eb < e1; eb += kBatch) {
     const int ne = e1 - eb < kBatch ? (int)(e1 - eb) : kBatch;
     __syncthreads();  // the batch before is done with
+    // every step-th key of the other side, where G will stand: the first eleven steps of each
+    // bisection in LDS
+    const int32_t o0 = (int32_t)o.base, on = (int32_t)o.nnz;
+    const int32_t step = (on + kSamples - 1) / kSamples;
+    const int samples = step > 0 ? (on + step - 1) / step : 0;
+    uint32_t *top = reinterpret_cast<uint32_t *>(sh.tile);
+    for (int i = t; i < samples; i += kGradThreads) top[i] = (uint32_t)key[o0 + (int64_t)i * step];
+    __syncthreads();
     // entry i belongs to thread (i % 4) * 64 + i / 4 % 64: every wave gets some of a short row
     for (int i = lane * 4 + w; i < ne; i += kGradThreads) {
       const uint32_t d = (uint32_t)s.indices[eb + i];
-      int32_t l0 = (int32_t)o.base, l1 = (int32_t)(o.base + o.nnz), h0 = l0, h1 = l1;
-      while (l0 < l1 || h0 < h1) {  // first key >= d and first key > d, side by side
+      // first key >= d and first key > d, side by side; sample j is key j * step
+      int32_t l0 = 0, l1 = samples, h0 = 0, h1 = samples;
+      while (l0 < l1 || h0 < h1) {
+        const int32_t ml = (l0 + l1) >> 1, mh = (h0 + h1) >> 1;
         if (l0 < l1) {
-          const int32_t m = l0 + ((l1 - l0) >> 1);
-          if ((uint32_t)key[m] < d) l0 = m + 1;
-          else l1 = m;
+          if (top[ml] < d) l0 = ml + 1;
+          else l1 = ml;
         }
         if (h0 < h1) {
-          const int32_t m = h0 + ((h1 - h0) >> 1);
-          if ((uint32_t)key[m] <= d) h0 = m + 1;
-          else h1 = m;
+          if (top[mh] <= d) h0 = mh + 1;
+          else h1 = mh;
+        }
+      }
+      // behind the last sample below, up to the sample found
+      l1 = l0 < samples ? l0 * step : on;
+      h1 = h0 < samples ? h0 * step : on;
+      l0 = l0 > 0 ? (l0 - 1) * step + 1 : 0;
+      h0 = h0 > 0 ? (h0 - 1) * step + 1 : 0;
+      l0 += o0;
+      l1 += o0;
+      h0 += o0;
+      h1 += o0;
+      while (l0 < l1 || h0 < h1) {
+        const int32_t ml = l0 + ((l1 - l0) >> 1), mh = h0 + ((h1 - h0) >> 1);
+        const uint32_t kl = l0 < l1 ? (uint32_t)key[ml] : 0u, kh = h0 < h1 ? (uint32_t)key[mh] : 0u;
+        if (l0 < l1) {
+          if (kl < d) l0 = ml + 1;
+          else l1 = ml;
+        }
+        if (h0 < h1) {
+          if (kh <= d) h0 = mh + 1;
+          else h1 = mh;
         }
       }
       sh.lo[i] = l0;
@@ -465,12 +519,17 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
         }
         float acc = 0;
         const int n = h - l;
-        if (n <= kLaneList)
-          for (int j = 0; j < n; ++j) {
-            const uint2 v = load[l + j];
-            const uint32_t c = v.x - (uint32_t)c0;
-            if (c < (uint32_t)nc) acc += sh.tile[at + c] * __builtin_bit_cast(float, v.y);
+        if (n > 0 && n <= kLaneList) {
+          uint2 v[kLaneList];
+#pragma unroll
+          for (int j = 0; j < kLaneList; ++j) v[j] = load[l + (j < n ? j : 0)];
+#pragma unroll
+          for (int j = 0; j < kLaneList; ++j) {
+            const uint32_t c = v[j].x - (uint32_t)c0;  // may lie in another tile
+            const float x = sh.tile[(at + c) & (kTile - 1)];
+            acc += j < n && c < (uint32_t)nc ? x * __builtin_bit_cast(float, v[j].y) : 0.0f;
           }
+        }
         if (i < ne) sh.acc[i] += acc;
         __builtin_amdgcn_wave_barrier();  // other lanes add to it below
         // four lists at a time, 16 lanes each
@@ -486,13 +545,18 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
           const int from = src < 0 ? 0 : src;
           // every lane shuffles: a source lane must be active
           const int32_t l2 = __shfl(l, from, 64), n1 = __shfl(n, from, 64);
-          const int at2 = __shfl(at, from, 64);
+          const uint32_t base2 = (uint32_t)(__shfl(at, from, 64) - (int)c0);
           const int32_t n2 = src < 0 ? 0 : n1;
           float part = 0;
-          for (q = lane & 15; q < n2; q += 16) {
-            const uint2 v = load[l2 + q];
-            const uint32_t c = v.x - (uint32_t)c0;
-            if (c < (uint32_t)nc) part += sh.tile[at2 + c] * __builtin_bit_cast(float, v.y);
+          for (q = lane & 15; q < n2; q += 64) {
+            uint2 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = load[l2 + (q + 16 * k < n2 ? q + 16 * k : q)];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x = sh.tile[(base2 + v[k].x) & (kTile - 1)];
+              part += q + 16 * k < n2 ? x * __builtin_bit_cast(float, v[k].y) : 0.0f;
+            }
           }
           part = row16_total(part);
           if ((lane & 15) == 15 && src >= 0) sh.acc[i0 + src * 4 + w] += part;
@@ -503,8 +567,7 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
           const int f = __builtin_ctzll(big);
           big &= big - 1;
           const int32_t l2 = __builtin_amdgcn_readlane(l, f), h2 = __builtin_amdgcn_readlane(h, f);
-          const int at2 = __builtin_amdgcn_readlane(at, f);
-          const float *tile = sh.tile + at2;
+          const uint32_t base2 = (uint32_t)(__builtin_amdgcn_readlane(at, f) - (int)c0);
           float p0 = 0, p1 = 0;
           int32_t q = l2 + lane * 2;
           for (; q - lane * 2 + 512 <= h2; q += 512) {
@@ -513,17 +576,23 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
             for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const Pair *>(load + q + k * 128);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const uint32_t ca = v[k].a.x - (uint32_t)c0, cb = v[k].b.x - (uint32_t)c0;
-              if (ca < (uint32_t)nc) p0 += tile[ca] * __builtin_bit_cast(float, v[k].a.y);
-              if (cb < (uint32_t)nc) p1 += tile[cb] * __builtin_bit_cast(float, v[k].b.y);
+              p0 += sh.tile[(base2 + v[k].a.x) & (kTile - 1)] * __builtin_bit_cast(float, v[k].a.y);
+              p1 += sh.tile[(base2 + v[k].b.x) & (kTile - 1)] * __builtin_bit_cast(float, v[k].b.y);
             }
           }
-          for (; q < h2; q += 128) {
-            const uint2 va = load[q];
-            const uint2 vb = q + 1 < h2 ? load[q + 1] : make_uint2((uint32_t)c0, 0);
-            const uint32_t ca = va.x - (uint32_t)c0, cb = vb.x - (uint32_t)c0;
-            if (ca < (uint32_t)nc) p0 += tile[ca] * __builtin_bit_cast(float, va.y);
-            if (cb < (uint32_t)nc) p1 += tile[cb] * __builtin_bit_cast(float, vb.y);
+          if (q - lane * 2 < h2) {  // the last 512, in part
+            uint2 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int32_t j = q + (k >> 1) * 128 + (k & 1);
+              v[k] = load[j < h2 ? j : l2];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int32_t j = q + (k >> 1) * 128 + (k & 1);
+              const float x = sh.tile[(base2 + v[k].x) & (kTile - 1)];
+              p0 += j < h2 ? x * __builtin_bit_cast(float, v[k].y) : 0.0f;
+            }
           }
           const float part = wave_total(p0 + p1);
           if (lane == 63) sh.acc[i0 + f * 4 + w] += part;
