@@ -12,9 +12,9 @@
 // What bounds it: reading the scores once. A workgroup holds a tile of a row
 // in registers and the best k so far in LDS; after the first tile almost no
 // element passes the k-th best, and the tile costs one compare an element.
-// The first tile has no such bound yet: it takes the k-th largest of its
-// threads' own maxima, which at least k elements reach, so that little more
-// than k elements are ever written to LDS and ranked.
+// The first tile has no such bound yet: it takes a bound just below the k-th
+// largest of its threads' own maxima, which at least k elements reach, so that
+// little more than k elements are ever written to LDS and ranked.
 #include "sps_rows.h"
 
 namespace sps {
@@ -22,16 +22,19 @@ namespace sps {
 constexpr int kSelMaxK = 256;     // entries of a list: the public limit of k
 constexpr int kSelThreads = 256;  // >= kSelMaxK: the threads' maxima bound the k-th best
 constexpr int kSelBuf = 1024;     // candidates ranked at a time
+constexpr int kBoundBits = 20;    // upper bits of a key that the first bound resolves
+constexpr int kOneMax = 96;       // up to this k one maximum a thread bounds well, else two
 // a list that grows by 64-candidate steps must leave room for one
 static_assert(kSelBuf >= 64 && kSelThreads >= kSelMaxK, "selection buffers");
 
 struct SelShared {
   uint64_t buf[kSelBuf];
   uint64_t list[2][kSelMaxK];
-  uint64_t best[kSelThreads];
+  uint64_t best[kSelThreads];  // also 2 x kSelThreads upper halves
   // of three rounds: a wave may still read one round's while another pushes
   // the next one's, so the third is the one that can be cleared
   uint32_t cnt[3], full_at[3];
+  uint32_t bound;
 };
 
 // k-th largest of the workgroup's `best` keys (0 where fewer than k of them
@@ -75,6 +78,25 @@ __device__ __forceinline__ uint64_t kth_of_best(const SelShared &sh, int k) {
   return ((uint64_t)th << 32) | tl;
 }
 
+// The largest multiple of 2^(32 - kBoundBits) that at least k of N x 64 keys'
+// upper halves reach (0 where fewer than k are set), by one wave.
+template <int N>
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t *best, int k) {
+  const int lane = threadIdx.x & 63;
+  uint32_t h[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) h[i] = best[i * 64 + lane];
+  uint32_t th = 0;
+  for (int b = 31; b >= 32 - kBoundBits; --b) {
+    const uint32_t t = th | (1u << b);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) c += __popcll(__ballot(h[i] >= t));
+    if (c >= k) th = t;
+  }
+  return th;
+}
+
 // Puts the m candidates of `buf` into the sorted list (n of at most k): a
 // key's place is the number of larger keys. Every key is compared with the m
 // new ones, a new one with the list by bisection. Returns the list's length;
@@ -85,6 +107,7 @@ __device__ __forceinline__ int merge_buf(SelShared &sh, int cur, int n, int m, i
   for (int i = threadIdx.x; i < n; i += kSelThreads) {
     const uint64_t v = list[i];
     int r = i;
+#pragma unroll 8
     for (int j = 0; j < m; ++j) r += sh.buf[j] > v;
     if (r < k) to[r] = v;
   }
@@ -97,59 +120,69 @@ __device__ __forceinline__ int merge_buf(SelShared &sh, int cur, int n, int m, i
       else hi = mid;
     }
     int r = lo;
+#pragma unroll 8
     for (int j = 0; j < m; ++j) r += sh.buf[j] > v;
     if (r < k) to[r] = v;
   }
   return n + m < k ? n + m : k;
 }
 
-// One tile: thread t offers u[i] (an ordered key, 0 for none) with place
+// One tile: thread t offers keys f[i] (-inf or NaN for none) with place
 // place(i), ascending in i. Updates the list list[cur][0, n); all threads must
 // call it. `rnd` is the round (0, 1, 2, 0, ...), the same in all threads.
 template <int VPT, typename Place>
-__device__ __forceinline__ void offer_tile(SelShared &sh, const uint32_t (&u)[VPT], Place place,
-                                           int k, int &cur, int &n, int &rnd) {
+__device__ __forceinline__ void offer_tile(SelShared &sh, const float (&f)[VPT], Place place, int k,
+                                           int &cur, int &n, int &rnd) {
   static_assert(VPT <= 32, "one bit an element");
-  const int lane = threadIdx.x & 63;
-  bool bound = n < k;  // no k-th best yet: bound it by the threads' maxima
-  uint64_t thr = n < k ? 0 : sh.list[cur][k - 1];
-  uint32_t pend = 0;
+  const int t = threadIdx.x, lane = t & 63;
+  float m0 = -__builtin_inff(), m1 = -__builtin_inff();
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const uint64_t v = ((uint64_t)u[i] << 32) | (uint32_t)~place(i);
-    pend |= (u[i] != 0 && v > thr) ? 1u << i : 0u;
+  for (int i = 0; i < VPT / 2; ++i) {
+    m0 = fmaxf(m0, f[i]);
+    m1 = fmaxf(m1, f[VPT / 2 + i]);
   }
-  for (;;) {
-    if (bound) {
-      uint64_t mx = 0;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const uint64_t v = ((uint64_t)u[i] << 32) | (uint32_t)~place(i);
-        if ((pend >> i & 1u) && v > mx) mx = v;
-      }
-      sh.best[threadIdx.x] = mx;
-      __syncthreads();
-      const uint64_t t = kth_of_best(sh, k);
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const uint64_t v = ((uint64_t)u[i] << 32) | (uint32_t)~place(i);
-        if (v < t) pend &= ~(1u << i);
-      }
+  uint64_t thr;  // candidates are above it
+  if (n < k) {   // no k-th best yet: bound it by the threads' maxima
+    uint32_t *best = reinterpret_cast<uint32_t *>(sh.best);
+    if (k <= kOneMax) {
+      best[t] = order_bits(fmaxf(m0, m1));
+    } else {
+      best[2 * t] = order_bits(m0);
+      best[2 * t + 1] = order_bits(m1);
     }
+    __syncthreads();
+    if (t < 64) {
+      const uint32_t b = k <= kOneMax ? kth_bound<kSelThreads / 64>(best, k)
+                                      : kth_bound<2 * kSelThreads / 64>(best, k);
+      if (t == 0) sh.bound = b;
+    }
+    __syncthreads();
+    const uint32_t b = sh.bound;
+    thr = b ? ((uint64_t)b << 32) - 1 : 0;
+  } else {
+    thr = sh.list[cur][k - 1];
+  }
+  float tf = unorder_bits((uint32_t)((thr + 1) >> 32));  // no key below it is a candidate
+  if (thr == 0) tf = -__builtin_inff();
+  uint32_t pend = ~0u;
+  for (;;) {
     // candidates into the buffer, a wave's i-th elements at a time, while they fit
-    if (__ballot(pend != 0)) {
+    if (__ballot(fmaxf(m0, m1) >= tf)) {
       bool full = false;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const uint64_t mask = __ballot(pend >> i & 1u);
+        if (!__ballot(f[i] >= tf)) continue;
+        const uint32_t u = order_bits(f[i]);
+        const uint64_t v = ((uint64_t)u << 32) | (uint32_t)~place(i);
+        const bool c = u != 0 && v > thr && (pend >> i & 1u);
+        const uint64_t mask = __ballot(c);
         if (mask != 0 && !full) {
           uint32_t at = 0;
           if (lane == 0) at = atomicAdd(&sh.cnt[rnd], (uint32_t)__popcll(mask));
           at = __builtin_amdgcn_readfirstlane(at);
           if (at + (uint32_t)__popcll(mask) <= (uint32_t)kSelBuf) {
-            if (pend >> i & 1u) {
-              const uint32_t o = at + (uint32_t)__popcll(mask & ((1ull << lane) - 1));
-              sh.buf[o] = ((uint64_t)u[i] << 32) | (uint32_t)~place(i);
+            if (c) {
+              sh.buf[at + (uint32_t)__popcll(mask & ((1ull << lane) - 1))] = v;
               pend &= ~(1u << i);
             }
           } else {
@@ -163,7 +196,7 @@ __device__ __forceinline__ void offer_tile(SelShared &sh, const uint32_t (&u)[VP
     __syncthreads();
     const uint32_t cnt = sh.cnt[rnd], full_at = sh.full_at[rnd];
     rnd = rnd == 2 ? 0 : rnd + 1;
-    if (threadIdx.x == 0) {  // the round after the next: read before the barrier above
+    if (t == 0) {  // the round after the next: read before the barrier above
       const int later = rnd == 2 ? 0 : rnd + 1;
       sh.cnt[later] = 0;
       sh.full_at[later] = ~0u;
@@ -175,14 +208,21 @@ __device__ __forceinline__ void offer_tile(SelShared &sh, const uint32_t (&u)[VP
     cur ^= 1;
     n = n2;
     if (full_at == ~0u) return;
-    // what did not fit: drop what the list now excludes, bound the rest again
+    // what did not fit, as with many equal keys: the list's k-th best and the k-th largest
+    // of the threads' best, now to the last bit
     thr = n < k ? 0 : sh.list[cur][k - 1];
+    uint64_t mx = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const uint64_t v = ((uint64_t)u[i] << 32) | (uint32_t)~place(i);
-      if (v <= thr) pend &= ~(1u << i);
+      const uint32_t u = order_bits(f[i]);
+      const uint64_t v = ((uint64_t)u << 32) | (uint32_t)~place(i);
+      if (u != 0 && v > thr && (pend >> i & 1u) && v > mx) mx = v;
     }
-    bound = true;
+    sh.best[t] = mx;
+    __syncthreads();
+    const uint64_t b = kth_of_best(sh, k);
+    if (b > thr) thr = b - 1;
+    tf = thr == 0 ? -__builtin_inff() : unorder_bits((uint32_t)((thr + 1) >> 32));
   }
 }
 
@@ -233,23 +273,32 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelArgs a) {
   }
   __syncthreads();
   for (int64_t base = c0; base < c1; base += kSelThreads * VPT) {
-    uint32_t u[VPT];
+    float f[VPT];
+    if (base + kSelThreads * VPT <= c1) {  // a whole tile: all loads in flight
+      Vec<T> w[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int64_t c = base + ((int64_t)v * kSelThreads + t) * V;
-      if (c + V <= c1) {
-        const Vec<T> w = *reinterpret_cast<const Vec<T> *>(x + c);
+      for (int v = 0; v < NV; ++v)
+        w[v] = *reinterpret_cast<const Vec<T> *>(x + base + ((int64_t)v * kSelThreads + t) * V);
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[v * V + e] = order_bits(to_f32(w.e[e]) + off);
-      } else {
+      for (int i = 0; i < VPT; ++i) f[i] = to_f32(w[i / V].e[i % V]) + off;
+    } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          u[v * V + e] = c + e < c1 ? order_bits(to_f32(x[c + e]) + off) : 0u;
+      for (int v = 0; v < NV; ++v) {
+        const int64_t c = base + ((int64_t)v * kSelThreads + t) * V;
+        if (c + V <= c1) {
+          const Vec<T> w = *reinterpret_cast<const Vec<T> *>(x + c);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[v * V + e] = to_f32(w.e[e]) + off;
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            f[v * V + e] = c + e < c1 ? to_f32(x[c + e]) + off : -__builtin_inff();
+        }
       }
     }
     const uint32_t g = (uint32_t)(a.col_begin + base);
     offer_tile<VPT>(
-        sh, u,
+        sh, f,
         [&](int i) { return g + (uint32_t)((i / V * kSelThreads + t) * V + i % V); }, a.k, cur, n, rnd);
   }
   if (t < a.k) {
@@ -293,15 +342,16 @@ __global__ __launch_bounds__(kSelThreads) void select_fold_kernel(FoldArgs a) {
   const int64_t total = (int64_t)a.lists * a.k;
   const uint64_t *p = a.parts + row * total;
   for (int64_t base = 0; base < total; base += kSelThreads * kJoinVpt) {
-    uint32_t u[kJoinVpt], c[kJoinVpt];
+    float f[kJoinVpt];
+    uint32_t c[kJoinVpt];
 #pragma unroll
     for (int i = 0; i < kJoinVpt; ++i) {
       const int64_t at = base + (int64_t)i * kSelThreads + t;
       const uint64_t v = at < total ? p[at] : 0;
-      u[i] = (uint32_t)(v >> 32);
+      f[i] = v ? unorder_bits((uint32_t)(v >> 32)) : -__builtin_inff();
       c[i] = ~(uint32_t)v;
     }
-    offer_tile<kJoinVpt>(sh, u, [&](int i) { return c[i]; }, a.k, cur, n, rnd);
+    offer_tile<kJoinVpt>(sh, f, [&](int i) { return c[i]; }, a.k, cur, n, rnd);
   }
   if (t < a.k) {
     const uint64_t v = t < n ? sh.list[cur][t] : 0;
@@ -333,19 +383,23 @@ __global__ __launch_bounds__(kSelThreads) void beam_join_kernel(JoinArgs a) {
   sel_init(sh);
   __syncthreads();
   for (int64_t base = 0; base < total; base += kSelThreads * kJoinVpt) {
-    uint32_t u[kJoinVpt];
+    float f[kJoinVpt];
 #pragma unroll
     for (int i = 0; i < kJoinVpt; ++i) {
       const int64_t at = base + (int64_t)i * kSelThreads + t;
-      u[i] = 0;
+      f[i] = -__builtin_inff();
       if (at < total) {
-        if (a.parts) u[i] = (uint32_t)(a.parts[at0 + at] >> 32);
-        else if (a.in_cols[at0 + at] >= 0) u[i] = order_bits(a.in_scores[at0 + at]);
+        if (a.parts) {
+          const uint32_t u = (uint32_t)(a.parts[at0 + at] >> 32);
+          if (u) f[i] = unorder_bits(u);
+        } else if (a.in_cols[at0 + at] >= 0) {
+          f[i] = a.in_scores[at0 + at];
+        }
       }
     }
     const uint32_t g = (uint32_t)base;
     offer_tile<kJoinVpt>(
-        sh, u, [&](int i) { return g + (uint32_t)(i * kSelThreads + t); }, a.k, cur, n, rnd);
+        sh, f, [&](int i) { return g + (uint32_t)(i * kSelThreads + t); }, a.k, cur, n, rnd);
   }
   if (t < a.k) {
     const uint64_t v = t < n ? sh.list[cur][t] : 0;
@@ -420,10 +474,18 @@ struct Split {
 Split split_of(int64_t n_rows, int64_t n_cols) {
   int64_t s = 1;
   if (n_rows > 0 && n_rows < kFill) {
-    s = (kFill + n_rows - 1) / n_rows;
-    const int64_t most = (n_cols + kMinSeg - 1) / kMinSeg;
-    s = s < most ? s : most;
-    s = s > 1 ? s : 1;
+    const int64_t least = (kFill + n_rows - 1) / n_rows, most = (n_cols + kMinSeg - 1) / kMinSeg;
+    s = least < most ? least : most > 1 ? most : 1;
+    if (s == least) {  // of up to half as many again, the one that leaves the last round fullest
+      double best = 0;
+      for (int64_t c = least; c <= least + least / 2 && c <= most; ++c) {
+        const double part = (double)(n_rows * c), fill = part / (double)((n_rows * c + 255) / 256 * 256);
+        if (fill > best + 0.02) {
+          best = fill;
+          s = c;
+        }
+      }
+    }
   }
   int64_t seg = (n_cols + s - 1) / s;
   seg = (seg + 7) / 8 * 8;  // whole vectors
