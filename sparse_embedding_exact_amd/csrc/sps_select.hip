@@ -37,6 +37,11 @@ struct SelShared {
   uint32_t bound;
 };
 
+__device__ __forceinline__ uint64_t key_of(float f, uint32_t place) {
+  const uint32_t u = order_bits(f);
+  return u ? ((uint64_t)u << 32) | (uint32_t)~place : 0;
+}
+
 // k-th largest of the workgroup's `best` keys (0 where fewer than k of them
 // are set), found bit by bit: every wave holds all keys and counts by ballot.
 __device__ __forceinline__ uint64_t kth_of_best(const SelShared &sh, int k) {
@@ -127,11 +132,14 @@ __device__ __forceinline__ int merge_buf(SelShared &sh, int cur, int n, int m, i
   return n + m < k ? n + m : k;
 }
 
-// One tile: thread t offers keys f[i] (-inf or NaN for none) with place
-// place(i), ascending in i. Updates the list list[cur][0, n); all threads must
-// call it. `rnd` is the round (0, 1, 2, 0, ...), the same in all threads.
-template <int VPT, typename Place>
-__device__ __forceinline__ void offer_tile(SelShared &sh, const float (&f)[VPT], Place place, int k,
+// One tile: thread t offers keys f[i] (-inf or NaN for none). key(i) gives the
+// 64-bit integer of the thread's i-th element, with places ascending in i; it
+// loads the element once more, which the few candidates of a tile are cheaper
+// with than every element with an integer key of its own. Updates the list
+// list[cur][0, n); all threads must call it. `rnd` is the round (0, 1, 2, 0,
+// ...), the same in all threads.
+template <int VPT, typename Key>
+__device__ __forceinline__ void offer_tile(SelShared &sh, const float (&f)[VPT], Key key, int k,
                                            int &cur, int &n, int &rnd) {
   static_assert(VPT <= 32, "one bit an element");
   const int t = threadIdx.x, lane = t & 63;
@@ -141,8 +149,9 @@ __device__ __forceinline__ void offer_tile(SelShared &sh, const float (&f)[VPT],
     m0 = fmaxf(m0, f[i]);
     m1 = fmaxf(m1, f[VPT / 2 + i]);
   }
-  uint64_t thr;  // candidates are above it
-  if (n < k) {   // no k-th best yet: bound it by the threads' maxima
+  uint64_t thr = 0;  // candidates are above it
+  float tf = -3.4028234663852886e38f;  // none is below it: every key above -inf so far
+  if (n < k) {  // no k-th best yet: bound it by the threads' maxima
     uint32_t *best = reinterpret_cast<uint32_t *>(sh.best);
     if (k <= kOneMax) {
       best[t] = order_bits(fmaxf(m0, m1));
@@ -157,41 +166,43 @@ __device__ __forceinline__ void offer_tile(SelShared &sh, const float (&f)[VPT],
       if (t == 0) sh.bound = b;
     }
     __syncthreads();
-    const uint32_t b = sh.bound;
-    thr = b ? ((uint64_t)b << 32) - 1 : 0;
+    if (sh.bound) {
+      tf = unorder_bits(sh.bound);
+      thr = ((uint64_t)sh.bound << 32) - 1;
+    }
   } else {
     thr = sh.list[cur][k - 1];
+    tf = unorder_bits((uint32_t)(thr >> 32));
   }
-  float tf = unorder_bits((uint32_t)((thr + 1) >> 32));  // no key below it is a candidate
-  if (thr == 0) tf = -__builtin_inff();
-  uint32_t pend = ~0u;
-  for (;;) {
-    // candidates into the buffer, a wave's i-th elements at a time, while they fit
-    if (__ballot(fmaxf(m0, m1) >= tf)) {
-      bool full = false;
+  uint32_t pend = 0;  // element i in bit VPT - 1 - i
+  if (__ballot(fmaxf(m0, m1) >= tf)) {
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        if (!__ballot(f[i] >= tf)) continue;
-        const uint32_t u = order_bits(f[i]);
-        const uint64_t v = ((uint64_t)u << 32) | (uint32_t)~place(i);
-        const bool c = u != 0 && v > thr && (pend >> i & 1u);
-        const uint64_t mask = __ballot(c);
-        if (mask != 0 && !full) {
-          uint32_t at = 0;
-          if (lane == 0) at = atomicAdd(&sh.cnt[rnd], (uint32_t)__popcll(mask));
-          at = __builtin_amdgcn_readfirstlane(at);
-          if (at + (uint32_t)__popcll(mask) <= (uint32_t)kSelBuf) {
-            if (c) {
-              sh.buf[at + (uint32_t)__popcll(mask & ((1ull << lane) - 1))] = v;
-              pend &= ~(1u << i);
-            }
-          } else {
-            // every later request fails too: places only grow
-            if (lane == 0) atomicMin(&sh.full_at[rnd], at);
-            full = true;
-          }
+    for (int i = 0; i < VPT; ++i) {
+      pend = pend << 1 | (f[i] >= tf ? 1u : 0u);
+      if (i % 4 == 3) asm volatile("" : "+v"(pend));  // not all terms first
+    }
+  }
+  for (;;) {
+    // candidates into the buffer, one of each lane at a time, while they fit
+    bool full = false;
+    while (!full && __ballot(pend != 0)) {
+      const int bit = 31 - __builtin_clz(pend | 1u);
+      const uint64_t v = pend ? key(VPT - 1 - bit) : 0;
+      const bool c = v > thr;
+      const uint64_t mask = __ballot(c);
+      uint32_t at = 0;
+      if (mask != 0) {
+        if (lane == 0) at = atomicAdd(&sh.cnt[rnd], (uint32_t)__popcll(mask));
+        at = __builtin_amdgcn_readfirstlane(at);
+        if (at + (uint32_t)__popcll(mask) > (uint32_t)kSelBuf) {
+          // every later request fails too: places only grow
+          if (lane == 0) atomicMin(&sh.full_at[rnd], at);
+          full = true;
+        } else if (c) {
+          sh.buf[at + (uint32_t)__popcll(mask & ((1ull << lane) - 1))] = v;
         }
       }
+      if (!full) pend &= ~(1u << bit);
     }
     __syncthreads();
     const uint32_t cnt = sh.cnt[rnd], full_at = sh.full_at[rnd];
@@ -208,21 +219,23 @@ __device__ __forceinline__ void offer_tile(SelShared &sh, const float (&f)[VPT],
     cur ^= 1;
     n = n2;
     if (full_at == ~0u) return;
-    // what did not fit, as with many equal keys: the list's k-th best and the k-th largest
-    // of the threads' best, now to the last bit
+    // what did not fit, as with many equal keys: bounded by the list's k-th best and by the
+    // k-th largest of the threads' best, now to the last bit
     thr = n < k ? 0 : sh.list[cur][k - 1];
     uint64_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const uint32_t u = order_bits(f[i]);
-      const uint64_t v = ((uint64_t)u << 32) | (uint32_t)~place(i);
-      if (u != 0 && v > thr && (pend >> i & 1u) && v > mx) mx = v;
+    uint32_t left = 0;
+    while (pend) {
+      const int bit = 31 - __builtin_clz(pend);
+      pend &= ~(1u << bit);
+      const uint64_t v = key(VPT - 1 - bit);
+      if (v > thr) left |= 1u << bit;
+      if (v > thr && v > mx) mx = v;
     }
+    pend = left;
     sh.best[t] = mx;
     __syncthreads();
     const uint64_t b = kth_of_best(sh, k);
     if (b > thr) thr = b - 1;
-    tf = thr == 0 ? -__builtin_inff() : unorder_bits((uint32_t)((thr + 1) >> 32));
   }
 }
 
@@ -248,7 +261,7 @@ struct SelArgs {
 // Best k of columns [split * seg, ...) of one row. With parts, they are
 // written there as keys (0 behind the last); without, they join the row's list.
 template <typename T, int VPT>
-__global__ __launch_bounds__(kSelThreads) void select_kernel(SelArgs a) {
+__global__ __launch_bounds__(kSelThreads, 6) void select_kernel(SelArgs a) {
   __shared__ SelShared sh;
   constexpr int V = kVec<T>, NV = VPT / V;
   const int64_t row = blockIdx.x / (uint32_t)a.splits;
@@ -296,10 +309,13 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(SelArgs a) {
         }
       }
     }
-    const uint32_t g = (uint32_t)(a.col_begin + base);
     offer_tile<VPT>(
         sh, f,
-        [&](int i) { return g + (uint32_t)((i / V * kSelThreads + t) * V + i % V); }, a.k, cur, n, rnd);
+        [&](int i) {
+          const int64_t c = base + ((int64_t)(i / V) * kSelThreads + t) * V + i % V;
+          return c < c1 ? key_of(to_f32(x[c]) + off, (uint32_t)(a.col_begin + c)) : (uint64_t)0;
+        },
+        a.k, cur, n, rnd);
   }
   if (t < a.k) {
     const uint64_t v = t < n ? sh.list[cur][t] : 0;
@@ -343,15 +359,19 @@ __global__ __launch_bounds__(kSelThreads) void select_fold_kernel(FoldArgs a) {
   const uint64_t *p = a.parts + row * total;
   for (int64_t base = 0; base < total; base += kSelThreads * kJoinVpt) {
     float f[kJoinVpt];
-    uint32_t c[kJoinVpt];
 #pragma unroll
     for (int i = 0; i < kJoinVpt; ++i) {
       const int64_t at = base + (int64_t)i * kSelThreads + t;
       const uint64_t v = at < total ? p[at] : 0;
       f[i] = v ? unorder_bits((uint32_t)(v >> 32)) : -__builtin_inff();
-      c[i] = ~(uint32_t)v;
     }
-    offer_tile<kJoinVpt>(sh, f, [&](int i) { return c[i]; }, a.k, cur, n, rnd);
+    offer_tile<kJoinVpt>(
+        sh, f,
+        [&](int i) {
+          const int64_t at = base + (int64_t)i * kSelThreads + t;
+          return at < total ? p[at] : (uint64_t)0;
+        },
+        a.k, cur, n, rnd);
   }
   if (t < a.k) {
     const uint64_t v = t < n ? sh.list[cur][t] : 0;
@@ -397,9 +417,16 @@ __global__ __launch_bounds__(kSelThreads) void beam_join_kernel(JoinArgs a) {
         }
       }
     }
-    const uint32_t g = (uint32_t)base;
     offer_tile<kJoinVpt>(
-        sh, f, [&](int i) { return g + (uint32_t)(i * kSelThreads + t); }, a.k, cur, n, rnd);
+        sh, f,
+        [&](int i) {
+          const int64_t at = base + (int64_t)i * kSelThreads + t;
+          if (at >= total || (!a.parts && a.in_cols[at0 + at] < 0)) return (uint64_t)0;
+          const float x = a.parts ? unorder_bits((uint32_t)(a.parts[at0 + at] >> 32))
+                                  : a.in_scores[at0 + at];
+          return key_of(x, (uint32_t)at);
+        },
+        a.k, cur, n, rnd);
   }
   if (t < a.k) {
     const uint64_t v = t < n ? sh.list[cur][t] : 0;
