@@ -69,93 +69,123 @@ __device__ __forceinline__ float exp2_from(float x, float m, float c) {
 // what a maximum of -inf (nothing but -inf yet) is subtracted as
 __device__ __forceinline__ float finite_max(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
-// ---- the teacher's lists ----
-template <int NT>
-__device__ __forceinline__ double block_sum_f64(double v, double *ws) {
-  v = wave_sum(v);
-  if (NT == 64) return v;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double r = 0;
+// ---- reductions over a workgroup ----
+// Sum of ws[0, n), n <= 16, in every lane (at = lane % 16), in a fixed order.
+__device__ __forceinline__ double row16_sum(int at, int n, const double *ws) {
+  double s = at < n ? ws[at] : 0.0;
+  s += dpp_f64<0x111, 0xf, true>(s);  // row_shr:1
+  s += dpp_f64<0x112, 0xf, true>(s);  // row_shr:2
+  s += dpp_f64<0x114, 0xf, true>(s);  // row_shr:4
+  s += dpp_f64<0x118, 0xf, true>(s);  // row_shr:8
+  return __shfl(s, 15, 64);
+}
+// Sums of N doubles over NT threads, in every thread; `ws` is N x 16 doubles.
+template <int NT, int N>
+__device__ __forceinline__ void block_sums(double (&v)[N], double (*ws)[16]) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
-  for (int i = 0; i < NT / 64; ++i) r += ws[i];
-  return r;
+  for (int i = 0; i < N; ++i) {
+    const double s = wave_total_f64(v[i]);
+    if (lane == 63) ws[i][threadIdx.x >> 6] = s;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = row16_sum(lane & 15, NT / 64, ws[i]);
+  __syncthreads();
 }
 template <int NT>
 __device__ __forceinline__ float block_max(float v, float *ws) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  if (NT == 64) return v;
+  const int lane = threadIdx.x & 63;
+  if (lane == 0) ws[threadIdx.x >> 6] = v;
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float r = ws[0];
+  v = ws[lane & (NT / 64 - 1)];
 #pragma unroll
-  for (int i = 1; i < NT / 64; ++i) r = fmaxf(r, ws[i]);
+  for (int o = NT / 128; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  __syncthreads();
+  return v;
+}
+
+// ---- the teacher's lists ----
+struct TeachShared {
+  int32_t id[kDistMaxK];   // as given, -1 where unusable
+  int32_t sid[kDistMaxK];  // -1 where the entry takes no part
+  float p[kDistMaxK];
+  double wd[3][16];
+  float wf[16];
+};
+
+// By one workgroup: which entries of a row take part (an id's first
+// occurrence, inside the columns, with a logit), and their masses.
+template <int NT>
+__device__ __forceinline__ RowTeach teach_row(const int32_t *__restrict__ ids,
+                                              const float *__restrict__ logits, const float *lse,
+                                              int k, int64_t n_cols, double inv_tau,
+                                              TeachShared &sh) {
+  const int t = threadIdx.x;
+  const double given = lse ? (double)*lse : 0.0;
+  for (int i = t; i < k; i += NT) {
+    const int32_t v = ids[i];
+    const float l = logits[i];
+    sh.id[i] = v >= 0 && v < n_cols && l != -__builtin_inff() ? v : -1;
+    sh.p[i] = l;
+  }
+  __syncthreads();
+  float mx = -__builtin_inff();
+  int has = 0;
+  for (int i = t; i < k; i += NT) {
+    const int32_t v = sh.id[i];
+    int dup = v < 0;
+#pragma unroll 8
+    for (int j = 0; j < i; ++j) dup |= sh.id[j] == v;
+    sh.sid[i] = dup ? -1 : v;
+    if (!dup) {
+      has = 1;
+      mx = fmaxf(mx, sh.p[i]);
+    }
+  }
+  if (!lse) mx = block_max<NT>(mx, sh.wf);
+  const double shift = lse ? given : (double)finite_max(mx) * inv_tau;
+  double v[3] = {0, 0, (double)has};  // sum e, sum e log e, entries
+  for (int i = t; i < k; i += NT)
+    if (sh.sid[i] >= 0) {
+      const double x = (double)sh.p[i] * inv_tau - shift, e = exp(x);
+      v[0] += e;
+      v[1] += e == 0 ? 0.0 : e * x;
+    }
+  block_sums<NT>(v, sh.wd);
+  const double sum = v[0], scale = lse ? 1.0 : 1.0 / sum;
+  for (int i = t; i < k; i += NT) {
+    const bool ok = sh.sid[i] >= 0;
+    sh.p[i] = ok ? (float)(exp((double)sh.p[i] * inv_tau - shift) * scale) : 0.0f;
+  }
+  RowTeach r;
+  r.has = v[2] != 0;
+  r.rest = 0;
+  if (lse) r.rest = sum < 1 ? 1 - sum : sum >= 1 ? 0.0 : sum;  // NaN stays
+  // sum p log p: p = e scale, log p = x + log scale
+  r.entropy = v[1] * scale + (lse || !r.has ? 0.0 : log(scale)) +
+              (r.rest == 0 ? 0.0 : r.rest * log(r.rest));
+  r.mass = lse ? sum + r.rest : 1.0 + (sum - sum);  // 1, or NaN where the logits are
+  r.pad = 0;
   return r;
 }
 
-// One workgroup a row: which entries take part (an id's first occurrence in
-// the row, inside the columns, with a logit), and their masses.
 template <int NT>
 __global__ __launch_bounds__(NT) void distill_prepare_kernel(DistillDev d,
                                                              const int32_t *__restrict__ ids,
                                                              const float *__restrict__ logits,
                                                              const float *__restrict__ lse) {
-  __shared__ int32_t id[kDistMaxK];
-  __shared__ double wd[NT / 64];
-  __shared__ float wf[NT / 64];
+  __shared__ TeachShared sh;
   const int64_t row = blockIdx.x, at = row * d.k;
+  const RowTeach r = teach_row<NT>(ids + at, logits + at, lse ? lse + row : nullptr, d.k, d.n_cols,
+                                   d.inv_tau, sh);
   for (int i = threadIdx.x; i < d.k; i += NT) {
-    const int32_t v = ids[at + i];
-    const bool ok = v >= 0 && v < d.n_cols && logits[at + i] != -__builtin_inff();
-    id[i] = ok ? v : -1;
+    d.sid[at + i] = sh.sid[i];
+    d.p[at + i] = sh.p[i];
   }
-  __syncthreads();
-  float mx = -__builtin_inff();
-  int has = 0;
-  for (int i = threadIdx.x; i < d.k; i += NT) {
-    int32_t v = id[i];
-    // an earlier entry of the same id has the place, whether or not it counts itself:
-    // entries that do not take part are -1 here
-    for (int j = 0; j < i && v >= 0; ++j)
-      if (id[j] == v) v = -1;
-    d.sid[at + i] = v;
-    if (v >= 0) {
-      has = 1;
-      mx = fmaxf(mx, logits[at + i]);
-    }
-  }
-  has = __syncthreads_or(has);
-  mx = block_max<NT>(mx, wf);
-  double sum = 0;
-  const double shift = d.rest ? (double)lse[row] : (double)finite_max(mx) * d.inv_tau;
-  for (int i = threadIdx.x; i < d.k; i += NT)
-    if (d.sid[at + i] >= 0) sum += exp((double)logits[at + i] * d.inv_tau - shift);
-  sum = block_sum_f64<NT>(sum, wd);
-  const double scale = d.rest ? 1.0 : 1.0 / sum;
-  double ent = 0;
-  for (int i = threadIdx.x; i < d.k; i += NT) {
-    double p = 0;
-    if (d.sid[at + i] >= 0) {
-      p = exp((double)logits[at + i] * d.inv_tau - shift) * scale;
-      ent += p == 0 ? 0.0 : p * log(p);
-    }
-    d.p[at + i] = (float)p;
-  }
-  ent = block_sum_f64<NT>(ent, wd);
-  if (threadIdx.x == 0) {
-    double rest = 0;
-    if (d.rest) rest = sum < 1 ? 1 - sum : sum >= 1 ? 0.0 : sum;  // NaN stays
-    RowTeach t;
-    t.entropy = ent + (rest == 0 ? 0.0 : rest * log(rest));
-    t.mass = d.rest ? sum + rest : 1.0 + (sum - sum);  // 1, or NaN where the logits are
-    t.rest = rest;
-    t.has = has;
-    t.pad = 0;
-    d.teach[row] = t;
-  }
+  if (threadIdx.x == 0) d.teach[row] = r;
 }
 
 // ---- the sums ----
@@ -167,22 +197,30 @@ struct ChunkArgs {
 };
 
 // the word and bit of a column `o` columns into its tile of scores of type T
-template <typename T>
+template <typename T, int NT>
 __device__ __forceinline__ void bit_of(int o, int &word, int &bit) {
   constexpr int V = kVec<T>;
   const int v = o / V;
-  word = v % kDistThreads;
-  bit = v / kDistThreads * V + o % V;
+  word = v % NT;
+  bit = v / NT * V + o % V;
 }
 
 // a tile's scores of this thread; columns past the end are -inf
-template <typename T>
-__device__ __forceinline__ void load_tile(const T *x, int64_t base, int64_t end,
-                                          float (&f)[kDistVpt]) {
+template <typename T, int NT, int VPT>
+__device__ __forceinline__ void load_tile(const T *x, int64_t base, int64_t end, float (&f)[VPT]) {
   constexpr int V = kVec<T>;
+  if (base + NT * VPT <= end) {  // a whole tile: all loads in flight
+    Vec<T> w[VPT / V];
 #pragma unroll
-  for (int v = 0; v < kDistVpt / V; ++v) {
-    const int64_t c = base + ((int64_t)v * kDistThreads + threadIdx.x) * V;
+    for (int v = 0; v < VPT / V; ++v)
+      w[v] = *reinterpret_cast<const Vec<T> *>(x + base + ((int64_t)v * NT + threadIdx.x) * V);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) f[i] = to_f32(w[i / V].e[i % V]);
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < VPT / V; ++v) {
+    const int64_t c = base + ((int64_t)v * NT + threadIdx.x) * V;
     if (c + V <= end) {
       const Vec<T> w = *reinterpret_cast<const Vec<T> *>(x + c);
 #pragma unroll
@@ -198,8 +236,8 @@ __device__ __forceinline__ void load_tile(const T *x, int64_t base, int64_t end,
 template <typename T>
 __global__ __launch_bounds__(kDistThreads) void distill_chunk_kernel(ChunkArgs a) {
   __shared__ uint32_t bits[kSuperTiles][kDistThreads];
-  __shared__ double wd[kDistThreads / 64];
-  __shared__ float wf[kDistThreads / 64];
+  __shared__ double wd[1][16];
+  __shared__ float wf[16];
   const DistillDev &d = a.d;
   const int t = threadIdx.x;
   const int64_t row = blockIdx.x / (uint32_t)a.splits;
@@ -227,14 +265,14 @@ __global__ __launch_bounds__(kDistThreads) void distill_chunk_kernel(ChunkArgs a
       const int64_t o = (int64_t)sid[i] - a.col_begin - s0;
       if (sid[i] >= 0 && o >= 0 && o < s1 - s0) {
         int word, bit;
-        bit_of<T>((int)(o % kDistTile), word, bit);
+        bit_of<T, kDistThreads>((int)(o % kDistTile), word, bit);
         atomicOr(&bits[o / kDistTile][word], 1u << bit);
       }
     }
     __syncthreads();
     for (int i = 0; i < tiles; ++i) {
       float f[kDistVpt];
-      load_tile<T>(x, s0 + (int64_t)i * kDistTile, s1, f);
+      load_tile<T, kDistThreads>(x, s0 + (int64_t)i * kDistTile, s1, f);
       const uint32_t listed = bits[i][t];
       if (listed) {
 #pragma unroll
@@ -253,7 +291,9 @@ __global__ __launch_bounds__(kDistThreads) void distill_chunk_kernel(ChunkArgs a
     }
   }
   const float mb = block_max<kDistThreads>(m, wf);
-  const double sb = block_sum_f64<kDistThreads>(s * (double)exp2_from(m, finite_max(mb), d.c), wd);
+  double sums[1] = {s * (double)exp2_from(m, finite_max(mb), d.c)};
+  block_sums<kDistThreads>(sums, wd);
+  const double sb = sums[0];
   if (t == 0) {
     Stat *st = d.stat + row * d.slots;
     Stat r{sb, mb, 0};
@@ -327,13 +367,12 @@ struct GradArgs {
   int32_t splits;
 };
 
-template <typename T, typename G>
-__device__ __forceinline__ void store_tile(G *g, int64_t base, int64_t end,
-                                           const float (&f)[kDistVpt]) {
+template <typename T, typename G, int NT, int VPT>
+__device__ __forceinline__ void store_tile(G *g, int64_t base, int64_t end, const float (&f)[VPT]) {
   constexpr int V = kVec<T>, W = kVec<G>;
 #pragma unroll
-  for (int v = 0; v < kDistVpt / V; ++v) {
-    const int64_t c = base + ((int64_t)v * kDistThreads + threadIdx.x) * V;
+  for (int v = 0; v < VPT / V; ++v) {
+    const int64_t c = base + ((int64_t)v * NT + threadIdx.x) * V;
     if (c + V <= end) {
 #pragma unroll
       for (int w = 0; w < V; w += W) {
@@ -363,10 +402,10 @@ __global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(GradArgs a) 
   const float b = (float)(r.b * w);
   for (int64_t base = c0; base < c1; base += kDistTile) {
     float f[kDistVpt];
-    load_tile<T>(x, base, c1, f);
+    load_tile<T, kDistThreads>(x, base, c1, f);
 #pragma unroll
     for (int e = 0; e < kDistVpt; ++e) f[e] = r.live ? exp2_from(f[e], r.m, d.c) * b : 0.0f;
-    store_tile<T, G>(g, base, c1, f);
+    store_tile<T, G, kDistThreads>(g, base, c1, f);
   }
   if (!r.live) return;  // uniform
   __syncthreads();      // the listed columns are written over what stands there
@@ -380,6 +419,307 @@ __global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(GradArgs a) 
   }
 }
 
+// ---- whole rows in one launch ----
+// One workgroup a row. A row that fits NT x VPT scores stays in registers from
+// the load to the gradient: read once, written once, one exponential a score.
+// A longer one is read a second time for the gradient, soon enough after the
+// first that much of it still comes from the caches.
+struct RowsArgs {
+  const void *x;
+  void *g;  // nullable
+  const int32_t *ids;
+  const float *logits, *lse, *weights;
+  float *loss;
+  int64_t ld, ldg, n_cols;
+  int32_t k;
+  float c;
+  double inv_tau;
+};
+
+// A thread's scores of a tile as they were loaded, four bytes a register: for
+// 16-bit scores half the registers of their float32 values. Past the end of
+// the row stands -inf.
+template <typename T, int NT, int VPT>
+struct RawTile {
+  static constexpr int V = kVec<T>, E = 4 / (int)sizeof(T);
+  uint32_t r[VPT / E];
+
+  struct __attribute__((packed, aligned(sizeof(T)))) Quad {
+    uint32_t w[4];
+  };
+  static __device__ __forceinline__ uint32_t bits(T v) {
+    if constexpr (E == 1) return __builtin_bit_cast(uint32_t, v);
+    else return v.u;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (E == 1) {
+      return __builtin_bit_cast(float, r[i]);
+    } else {
+      T v;
+      v.u = (uint16_t)(r[i / 2] >> (i % 2 * 16));
+      return to_f32(v);
+    }
+  }
+  __device__ __forceinline__ void strike(int i) {
+    const uint32_t inf = bits(from_f32<T>(-__builtin_inff()));
+    if constexpr (E == 1) r[i] = inf;
+    else r[i / 2] = i % 2 ? (r[i / 2] & 0xFFFFu) | inf << 16 : (r[i / 2] & 0xFFFF0000u) | inf;
+  }
+  // columns [base, base + NT * VPT) of a row that ends at `end`
+  __device__ __forceinline__ void load(const T *x, int64_t base, int64_t end) {
+    if (base + NT * VPT <= end) {  // a whole tile: all loads in flight
+#pragma unroll
+      for (int v = 0; v < VPT / V; ++v) {
+        const Quad q = *reinterpret_cast<const Quad *>(x + base + ((int64_t)v * NT + threadIdx.x) * V);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[v * 4 + e] = q.w[e];
+      }
+      return;
+    }
+    const uint32_t inf = bits(from_f32<T>(-__builtin_inff()));
+#pragma unroll
+    for (int v = 0; v < VPT / V; ++v) {
+      const int64_t c = base + ((int64_t)v * NT + threadIdx.x) * V;
+      if (c + V <= end) {
+        const Quad q = *reinterpret_cast<const Quad *>(x + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[v * 4 + e] = q.w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t word = 0;
+#pragma unroll
+          for (int h = 0; h < E; ++h)
+            word |= (c + e * E + h < end ? bits(x[c + e * E + h]) : inf) << (16 * h);
+          r[v * 4 + e] = word;
+        }
+      }
+    }
+  }
+  // g[...] = 2^((x - m) c) b of the tile's columns, or 0
+  template <typename G>
+  __device__ __forceinline__ void store(G *g, int64_t base, int64_t end, bool live, float m, float c,
+                                        float b) const {
+    constexpr int W = kVec<G>;
+#pragma unroll
+    for (int v = 0; v < VPT / V; ++v) {
+      const int64_t o = base + ((int64_t)v * NT + threadIdx.x) * V;
+      if (o + V <= end) {
+#pragma unroll
+        for (int w = 0; w < V; w += W) {
+          Vec<G> q;
+#pragma unroll
+          for (int e = 0; e < W; ++e)
+            q.e[e] = from_f32<G>(live ? exp2_from(get(v * V + w + e), m, c) * b : 0.0f);
+          *reinterpret_cast<Vec<G> *>(g + o + w) = q;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (o + e < end)
+            g[o + e] = from_f32<G>(live ? exp2_from(get(v * V + e), m, c) * b : 0.0f);
+      }
+    }
+  }
+};
+
+template <int NT>
+struct RowsShared {
+  int32_t id[kDistMaxK];   // as given, -1 where unusable
+  float x[kDistMaxK];      // the student's score of the entry
+  double e[kDistMaxK];     // the entry's logit; then its mass before the common factor
+  uint32_t bits[NT];  // the listed ones of a thread's scores
+  double ws[6][16];
+  float wf[2][16];
+};
+
+// The waves a SIMD holds: as many as the registers of a thread's scores (REGS)
+// and about 40 more allow, since the other rows of a CU are what hides a row's
+// chain of loads, barriers and reductions.
+constexpr int rows_waves(int regs) { return regs <= 16 ? 8 : regs <= 32 ? 5 : 4; }
+
+template <typename T, typename G, int NT, int VPT, bool LONG>
+__global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void distill_rows_kernel(
+    RowsArgs a) {
+  __shared__ RowsShared<NT> sh;
+  constexpr int64_t kTileCols = (int64_t)NT * VPT;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int64_t row = blockIdx.x;
+  const T *x = static_cast<const T *>(a.x) + row * a.ld;
+  const int32_t *ids = a.ids + row * a.k;
+  const float *logits = a.logits + row * a.k;
+  RawTile<T, NT, VPT> f;
+  if (!LONG) f.load(x, 0, a.n_cols);  // on its way while the list is worked on
+  const double given = a.lse ? (double)a.lse[row] : 0.0;
+  sh.bits[t] = 0;
+#pragma unroll 1
+  for (int i = t; i < a.k; i += NT) {
+    const int32_t v = ids[i];
+    const float l = logits[i];
+    const bool ok = v >= 0 && v < a.n_cols && l != -__builtin_inff();
+    sh.id[i] = ok ? v : -1;
+    sh.x[i] = ok ? to_f32(x[v]) : -__builtin_inff();
+    sh.e[i] = (double)l;
+  }
+  __syncthreads();
+  // an entry takes part if no earlier one has its id; its column's bit is set
+  uint32_t part = 0;  // of this thread's entries (k <= 1024: four at most)
+  float mt = -__builtin_inff(), m = -__builtin_inff();
+#pragma unroll 1
+  for (int i = t, j = 0; i < a.k; i += NT, ++j) {
+    const int32_t v = sh.id[i];
+    int dup = v < 0;
+#pragma unroll 8
+    for (int q = 0; q < i; ++q) dup |= sh.id[q] == v;
+    if (!dup) {
+      part |= 1u << j;
+      mt = fmaxf(mt, (float)sh.e[i]);
+      m = fmaxf(m, sh.x[i]);
+      if (!LONG) {
+        int word, bit;
+        bit_of<T, NT>(v, word, bit);
+        atomicOr(&sh.bits[word], 1u << bit);
+      }
+    }
+  }
+  __syncthreads();
+  double z_rest = 0;
+  if (LONG) {
+    for (int64_t b0 = 0; b0 < a.n_cols; b0 += kTileCols) {
+      for (int i = t, j = 0; i < a.k; i += NT, ++j) {
+        const int64_t o = (int64_t)sh.id[i] - b0;
+        if ((part >> j & 1u) && o >= 0 && o < kTileCols) {
+          int word, bit;
+          bit_of<T, NT>((int)o, word, bit);
+          atomicOr(&sh.bits[word], 1u << bit);
+        }
+      }
+      f.load(x, b0, a.n_cols);
+      __syncthreads();
+      const uint32_t listed = sh.bits[t];
+      if (listed) {
+        sh.bits[t] = 0;  // for the next tile: set behind the barrier below
+#pragma unroll
+        for (int e = 0; e < VPT; ++e)
+          if (listed >> e & 1u) f.strike(e);
+      }
+      // a maximum of the thread's own; the workgroup's follows
+      float mn = m;
+#pragma unroll
+      for (int e = 0; e < VPT; ++e) mn = fmaxf(mn, f.get(e));
+      const float mf = finite_max(mn);
+      float sum = 0;
+#pragma unroll
+      for (int e = 0; e < VPT; ++e) sum += exp2_from(f.get(e), mf, a.c);
+      z_rest = z_rest * (double)exp2_from(m, mf, a.c) + (double)sum;
+      m = mn;
+      __syncthreads();
+    }
+  } else {
+    const uint32_t listed = sh.bits[t];
+    if (listed) {
+#pragma unroll
+      for (int e = 0; e < VPT; ++e)
+        if (listed >> e & 1u) f.strike(e);
+    }
+#pragma unroll
+    for (int e = 0; e < VPT; ++e) m = fmaxf(m, f.get(e));
+  }
+  const float mine = m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    mt = fmaxf(mt, __shfl_xor(mt, o, 64));
+  }
+  if (lane == 0) {
+    sh.wf[0][wave] = m;
+    sh.wf[1][wave] = mt;
+  }
+  __syncthreads();
+  m = sh.wf[0][lane & (NT / 64 - 1)];
+  mt = sh.wf[1][lane & (NT / 64 - 1)];
+#pragma unroll
+  for (int o = NT / 128; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    mt = fmaxf(mt, __shfl_xor(mt, o, 64));
+  }
+  const float mf = finite_max(m);
+  if (LONG) {
+    z_rest *= (double)exp2_from(mine, mf, a.c);
+  } else {
+    float sum = 0;
+#pragma unroll
+    for (int e = 0; e < VPT; ++e) sum += exp2_from(f.get(e), mf, a.c);
+    z_rest = (double)sum;
+  }
+  // sums: student's mass outside the list and inside; teacher's e, e log e and e (x - m), where
+  // a listed entry's mass is e over their sum (or e itself); entries
+  const double c = (double)a.c, ln2 = 0.693147180559945309417;
+  {
+    const double shift = a.lse ? given : (double)finite_max(mt) * a.inv_tau;
+    double v[6] = {z_rest, 0, 0, 0, 0, 0};
+#pragma unroll 1
+    for (int i = t, j = 0; i < a.k; i += NT, ++j)
+      if (part >> j & 1u) {
+        const double d = ((double)sh.x[i] - (double)mf) * c;
+        double s = exp2(d);
+        asm volatile("" : "+v"(s));  // one function's temporaries at a time
+        v[1] += s;
+        const double y = sh.e[i] * a.inv_tau - shift, e = exp(y);
+        v[2] += e;
+        if (e != 0) {
+          v[3] += e * y;
+          v[4] += e * d;
+        }
+        v[5] += 1;
+        sh.e[i] = e;
+      }
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      const double s = wave_total_f64(v[i]);
+      if (lane == 63) sh.ws[i][wave] = s;
+    }
+  }
+  __syncthreads();
+  double v[6];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) v[i] = row16_sum(lane & 15, NT / 64, sh.ws[i]);
+  z_rest = v[0];
+  const double z = z_rest + v[1];
+  const double scale = a.lse ? 1.0 : 1.0 / v[2];
+  const double rest = !a.lse ? 0.0 : v[2] < 1 ? 1 - v[2] : v[2] >= 1 ? 0.0 : v[2];  // NaN stays
+  const double listed_mass = a.lse ? v[2] : 1.0 + (v[2] - v[2]);  // 1, or NaN where the logits are
+  const bool live = v[5] != 0 && z != 0;  // a NaN is no 0
+  if (wave == NT / 64 - 1 && lane == 0) {
+    // sum p log p, p = e scale; sum p (log z - (x - m)); the remaining class
+    const double log_z = log(z);
+    double l = v[3] * scale + (a.lse ? 0.0 : log(scale)) + listed_mass * log_z - v[4] * scale * ln2;
+    if (rest != 0) l += rest * (log(rest) + log_z - log(z_rest));
+    a.loss[row] = live ? (float)l : 0.0f;
+  }
+  if (!a.g) return;
+  const double w = (a.weights ? (double)a.weights[row] : 1.0) * a.inv_tau;
+  const double fa = (listed_mass + rest) / z;
+  const float b = (float)((rest != 0 && z_rest != 0 ? fa - rest / z_rest : fa) * w);
+  G *g = static_cast<G *>(a.g) + row * a.ldg;
+  if (LONG) {  // backwards: the last tiles are still in the nearest cache
+    for (int64_t b0 = (a.n_cols - 1) / kTileCols * kTileCols; b0 >= 0; b0 -= kTileCols) {
+      f.load(x, b0, a.n_cols);
+      f.store(g, b0, a.n_cols, live, mf, a.c, b);
+    }
+  } else {
+    f.store(g, 0, a.n_cols, live, mf, a.c, b);
+  }
+  if (!live) return;  // uniform
+  __syncthreads();    // the listed columns are written over what stands there
+#pragma unroll 1
+  for (int i = t, j = 0; i < a.k; i += NT, ++j)
+    if (part >> j & 1u) {
+      const double e = exp2(((double)sh.x[i] - (double)mf) * c);
+      g[sh.id[i]] = from_f32<G>((float)((e * fa - sh.e[i] * scale) * w));
+    }
+}
+
 }  // namespace sps
 
 struct sps_distill {
@@ -390,6 +730,11 @@ namespace {
 
 using sps::DistillDev;
 using sps::set_error;
+
+// Whole rows go to one launch, a workgroup each, where a row fits a
+// workgroup's registers or where there are rows enough to fill half the card;
+// few long rows are cut among workgroups instead, in four launches.
+constexpr int64_t kOneTile = 32768, kManyRows = 128;
 
 constexpr int64_t kMax31 = 2147483647ll;
 
@@ -568,6 +913,21 @@ void launch_grad(const DistillDev &d, const sps_scores *x, const float *weights,
     hipLaunchKernelGGL((sps::distill_grad_kernel<bf16_t, float>), grid, block, 0, s, a);
 }
 
+template <typename T, typename G>
+void launch_rows(const sps::RowsArgs &a, int64_t rows, hipStream_t s) {
+  const dim3 grid((uint32_t)rows);
+  if (a.n_cols <= 256 * 8)
+    hipLaunchKernelGGL((sps::distill_rows_kernel<T, G, 256, 8, false>), grid, dim3(256), 0, s, a);
+  else if (a.n_cols <= 256 * 32)
+    hipLaunchKernelGGL((sps::distill_rows_kernel<T, G, 256, 32, false>), grid, dim3(256), 0, s, a);
+  else if (a.n_cols <= 512 * 32)
+    hipLaunchKernelGGL((sps::distill_rows_kernel<T, G, 512, 32, false>), grid, dim3(512), 0, s, a);
+  else if (a.n_cols <= 1024 * 32)
+    hipLaunchKernelGGL((sps::distill_rows_kernel<T, G, 1024, 32, false>), grid, dim3(1024), 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::distill_rows_kernel<T, G, 1024, 32, true>), grid, dim3(1024), 0, s, a);
+}
+
 // a chunk of the batch's columns
 sps_status check_chunk(const sps_distill *h, const sps_scores *x, const char *what) {
   if (!h) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL handle", what);
@@ -669,6 +1029,31 @@ sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const 
   if (d.n_rows == 0) return SPS_OK;
   if (!loss) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL loss", what);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (scores->n_cols <= kOneTile || scores->n_rows >= kManyRows) {
+    sps::RowsArgs a{};
+    a.x = scores->data;
+    a.g = scores->n_cols > 0 ? grad : nullptr;
+    a.ids = ids;
+    a.logits = logits;
+    a.lse = teacher_lse;
+    a.weights = row_weights;
+    a.loss = loss;
+    a.ld = scores->ld;
+    a.ldg = ld_grad;
+    a.n_cols = scores->n_cols;
+    a.k = k;
+    a.c = d.c;
+    a.inv_tau = d.inv_tau;
+    using sps::bf16_t;
+    using sps::f16_t;
+    if (scores->dtype == SPS_F32) launch_rows<float, float>(a, d.n_rows, s);
+    else if (scores->dtype == SPS_F16 && (grad_dtype == SPS_F16 || !grad))
+      launch_rows<f16_t, f16_t>(a, d.n_rows, s);
+    else if (scores->dtype == SPS_F16) launch_rows<f16_t, float>(a, d.n_rows, s);
+    else if (grad_dtype == SPS_BF16 || !grad) launch_rows<bf16_t, bf16_t>(a, d.n_rows, s);
+    else launch_rows<bf16_t, float>(a, d.n_rows, s);
+    return sps::launch_status(what);
+  }
   launch_prepare(d, ids, logits, teacher_lse, s);
   launch_chunk(d, scores, 1, s);
   launch_loss(d, loss, nullptr, s);
