@@ -403,8 +403,9 @@ sps_status sps_select_chunk(const sps_scores *scores, const float *offsets, int3
                             int32_t first, float *top_scores, int32_t *top_cols, void *workspace,
                             size_t workspace_bytes, void *stream);
 
-/* Bytes of the workspace of sps_beam_select. Pure host. */
-sps_status sps_beam_workspace_size(int64_t n_rows, int64_t n_cols, int32_t k, size_t *bytes);
+/* Bytes of the workspace of sps_beam_select (0 for small groups). Pure host. */
+sps_status sps_beam_workspace_size(int64_t n_rows, int64_t n_cols, int32_t beams, int32_t k,
+                                   size_t *bytes);
 
 /* One step of a beam search (asynchronous): rows [g * beams, (g + 1) * beams)
  * are the beams of group g, and the best k of (beam, column) of each group are

@@ -69,11 +69,6 @@ class _Scores(ctypes.Structure):
                 ("n_cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("col_begin", ctypes.c_int64)]
 
 
-class _State(ctypes.Structure):
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("row_bytes", ctypes.c_int64),
-                ("src_stride", ctypes.c_int64), ("dst_stride", ctypes.c_int64)]
-
-
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -107,10 +102,10 @@ SIGNATURES = {
     "sps_cosine_chunk_half": (_I32, [_P, _P, _I32, _P, _I64, _P, _P]),
     "sps_select_workspace_size": (_I32, [_I64, _I64, _I32, ctypes.POINTER(_SZ)]),
     "sps_select_chunk": (_I32, [ctypes.POINTER(_Scores), _P, _I32, _I32, _P, _P, _P, _SZ, _P]),
-    "sps_beam_workspace_size": (_I32, [_I64, _I64, _I32, ctypes.POINTER(_SZ)]),
+    "sps_beam_workspace_size": (_I32, [_I64, _I64, _I32, _I32, ctypes.POINTER(_SZ)]),
     "sps_beam_select": (_I32, [ctypes.POINTER(_Scores), _P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     "sps_beam_join": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),
-    "sps_reorder_states": (_I32, [ctypes.POINTER(_State), _I32, _P, _I64, _I64, _P]),
+    "sps_reorder_states": (_I32, [_P, _I32, _P, _I64, _I64, _P]),
     "sps_distill_workspace_size": (_I32, [_I64, _I32, ctypes.POINTER(_SZ)]),
     "sps_distill_prepare": (_I32, [_P, _P, _P, _I64, _I32, _I64, ctypes.c_float, _P, _SZ, _P,
                                    ctypes.POINTER(_P)]),
@@ -579,13 +574,28 @@ def cosine_stream_host(q: Queries, items: Items, chunk_begin: int, chunk_end: in
 _SCORE_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
-def _here(*tensors) -> None:
-    """Device tensors of the current device: a launch goes to that device's streams."""
+def _here(*tensors) -> int:
+    """The current device's index; device tensors must be on it, since a launch goes to its
+    streams."""
     cur = torch.cuda.current_device()
     for t in tensors:
         if t is not None:
             assert t.is_cuda and t.get_device() == cur, \
                 "tensors must be on the current device (torch.cuda.set_device)"
+    return cur
+
+
+# torch's own way to the current stream's handle, without a Stream object a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device: int, stream) -> int:
+    """The handle of `stream`, or of the device's current stream for None."""
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(device)
+    return int(torch.cuda.current_stream(device).cuda_stream)
 
 
 def _view(x: torch.Tensor, col_begin: int = 0) -> _Scores:
@@ -665,7 +675,7 @@ def select_chunk(scores: torch.Tensor, top: TopRows, col_begin: int = 0,
     best k of every row, by fl32(offsets[row] + score), ties to the lower column. NaN and
     -inf are no candidates. first=True starts the lists; chunks may come in any order."""
     load_library()
-    _here(scores, top.scores, top.cols, offsets)
+    dev = _here(scores, top.scores, top.cols, offsets)
     v = _view(scores, col_begin)
     n, k = v.n_rows, top.scores.shape[1]
     assert top.scores.shape == (n, k) and top.cols.shape == (n, k)
@@ -676,12 +686,13 @@ def select_chunk(scores: torch.Tensor, top: TopRows, col_begin: int = 0,
         ws = torch.empty(nb, dtype=torch.uint8, device=scores.device) if nb else None
         _check(_lib.sps_select_chunk(ctypes.byref(v), _rows_f32(offsets, n, "offsets"), k,
                                      int(first), top.scores.data_ptr(), top.cols.data_ptr(),
-                                     ws.data_ptr() if nb else None, nb, _stream_ptr(stream)))
+                                     ws.data_ptr() if nb else None, nb, _stream_of(dev, stream)))
 
 
 def _beam_step(groups: int, k: int, device) -> BeamStep:
-    i = torch.empty(2, groups, k, dtype=torch.int32, device=device)
-    return BeamStep(torch.empty(groups, k, dtype=torch.float32, device=device), i[0], i[1])
+    return BeamStep(torch.empty((groups, k), dtype=torch.float32, device=device),
+                    torch.empty((groups, k), dtype=torch.int32, device=device),
+                    torch.empty((groups, k), dtype=torch.int32, device=device))
 
 
 def beam_select(scores: torch.Tensor, beam_scores: torch.Tensor | None, beams: int,
@@ -690,18 +701,18 @@ def beam_select(scores: torch.Tensor, beam_scores: torch.Tensor | None, beams: i
     the best k (default: beams) of (beam, column) by fl32(beam_scores[row] + score), ties to
     the lower row, then the lower column. A beam whose score is -inf takes no part."""
     load_library()
-    _here(scores, beam_scores)
+    dev = _here(scores, beam_scores)
     v = _view(scores, col_begin)
     k = beams if k is None else k
     assert beams >= 1 and v.n_rows % beams == 0, "rows must be groups of %d beams" % beams
     bs = _rows_f32(beam_scores, v.n_rows, "beam_scores")
-    nb = _sized("sps_beam_workspace_size", v.n_rows, v.n_cols, k)
+    nb = _sized("sps_beam_workspace_size", v.n_rows, v.n_cols, beams, k)
     with _on(stream):
         out = _beam_step(v.n_rows // beams, k, scores.device)
-        ws = torch.empty(nb, dtype=torch.uint8, device=scores.device)
+        ws = torch.empty(nb, dtype=torch.uint8, device=scores.device) if nb else None
         _check(_lib.sps_beam_select(ctypes.byref(v), bs, beams, k, out.scores.data_ptr(),
-                                    out.parents.data_ptr(), out.cols.data_ptr(), ws.data_ptr(), nb,
-                                    _stream_ptr(stream)))
+                                    out.parents.data_ptr(), out.cols.data_ptr(),
+                                    ws.data_ptr() if nb else None, nb, _stream_of(dev, stream)))
     return out
 
 
@@ -709,7 +720,7 @@ def beam_join(top: TopRows, beams: int, k: int | None = None, stream=None) -> Be
     """beam_select's step from the running lists that select_chunk kept over chunks of
     columns with the beams' scores as its offsets (equal to it where top.k >= k)."""
     load_library()
-    _here(top.scores, top.cols)
+    dev = _here(top.scores, top.cols)
     n, k_in = top.scores.shape
     assert top.cols.shape == (n, k_in)
     assert top.scores.dtype == torch.float32 and top.cols.dtype == torch.int32
@@ -720,7 +731,7 @@ def beam_join(top: TopRows, beams: int, k: int | None = None, stream=None) -> Be
         out = _beam_step(n // beams, k, top.scores.device)
         _check(_lib.sps_beam_join(top.scores.data_ptr(), top.cols.data_ptr(), n, k_in, beams, k,
                                   out.scores.data_ptr(), out.parents.data_ptr(),
-                                  out.cols.data_ptr(), _stream_ptr(stream)))
+                                  out.cols.data_ptr(), _stream_of(dev, stream)))
     return out
 
 
@@ -731,33 +742,30 @@ def reorder_states(states, parents: torch.Tensor, outs=None, stream=None) -> lis
     not given; they may not overlap any state)."""
     load_library()
     states = list(states)
-    _here(parents, *states)
+    dev = _here(parents, *states)
     assert parents.dtype == torch.int32 and parents.is_contiguous()
     n = parents.numel()
     rows = states[0].shape[0] if states else 0
     with _on(stream):
         if outs is None:
-            outs = [torch.empty((n,) + tuple(t.shape[1:]), dtype=t.dtype, device=t.device)
-                    for t in states]
+            outs = [t.new_empty((n,) + t.shape[1:]) for t in states]
         else:
             outs = list(outs)
             _here(*outs)
         assert len(outs) == len(states)
-        arr = (_State * max(len(states), 1))()
-        for i, (t, o) in enumerate(zip(states, outs)):
-            assert t.dim() >= 1 and t.shape[0] == rows, "states must have the same rows"
+        args = []
+        for t, o in zip(states, outs):
+            assert t.shape[0] == rows, "states must have the same rows"
             assert o.dtype == t.dtype and o.shape[0] == n and o.shape[1:] == t.shape[1:]
             size = t.element_size()
-            width = size
-            for d in t.shape[1:]:
-                width *= d
+            width = t.numel() // rows * size if rows else o.numel() // n * size if n else 0
             for x in (t, o):  # a row is one run of bytes
                 assert x.is_contiguous() or x[:1].is_contiguous(), "rows must be contiguous"
-            arr[i] = _State(t.data_ptr(), o.data_ptr(), width,
-                            t.stride(0) * size if rows > 1 else width,
-                            o.stride(0) * size if n > 1 else width)
-        _check(_lib.sps_reorder_states(arr, len(states), parents.data_ptr(), n, rows,
-                                       _stream_ptr(stream)))
+            args += (t.data_ptr(), o.data_ptr(), width, t.stride(0) * size if rows > 1 else width,
+                     o.stride(0) * size if n > 1 else width)
+        # sps_state is five 8-byte words: the two addresses and the three sizes
+        _check(_lib.sps_reorder_states((_I64 * len(args))(*args), len(states), parents.data_ptr(), n,
+                                       rows, _stream_of(dev, stream)))
     return outs
 
 
@@ -812,7 +820,7 @@ def distill_prepare(teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, n_c
     no part. With teacher_lse (the teacher's log-sum-exp of logits / temperature over all
     columns) its mass outside the list is one more class; without, the list's is all."""
     load_library()
-    _here(teacher_ids, teacher_logits, teacher_lse)
+    cur = _here(teacher_ids, teacher_logits, teacher_lse)
     n, k, lse = _teacher(teacher_ids, teacher_logits, teacher_lse)
     nb = _sized("sps_distill_workspace_size", n, k)
     dev = teacher_ids.device
@@ -820,7 +828,8 @@ def distill_prepare(teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, n_c
         buf, ptr = _workspace(nb, dev)
         h = _P()
         _check(_lib.sps_distill_prepare(teacher_ids.data_ptr(), teacher_logits.data_ptr(), lse, n, k,
-                                        n_cols, float(temperature), ptr, nb, _stream_ptr(stream),
+                                        n_cols, float(temperature), ptr, nb,
+                                        _stream_of(cur, stream),
                                         ctypes.byref(h)))
     return Distill(h.value, buf, n, n_cols, dev)
 
@@ -829,9 +838,9 @@ def distill_chunk(d: Distill, scores: torch.Tensor, col_begin: int = 0, first: b
                   stream=None) -> None:
     """Take in the student's scores of columns [col_begin, col_begin + scores.shape[1]); every
     column once, in any order of the chunks. first=True forgets what came before."""
-    _here(scores)
+    dev = _here(scores)
     v = _view(scores, col_begin)
-    _check(_lib.sps_distill_chunk(d._h, ctypes.byref(v), int(first), _stream_ptr(stream)))
+    _check(_lib.sps_distill_chunk(d._h, ctypes.byref(v), int(first), _stream_of(dev, stream)))
 
 
 def distill_loss(d: Distill, return_lse: bool = False, stream=None):
@@ -840,9 +849,8 @@ def distill_loss(d: Distill, return_lse: bool = False, stream=None):
     with _on(stream):
         loss = torch.empty(d.n_rows, dtype=torch.float32, device=d.device)
         lse = torch.empty_like(loss) if return_lse else None
-        _here(loss)
-        _check(_lib.sps_distill_loss(d._h, loss.data_ptr(),
-                                     lse.data_ptr() if return_lse else None, _stream_ptr(stream)))
+        _check(_lib.sps_distill_loss(d._h, loss.data_ptr(), lse.data_ptr() if return_lse else None,
+                                     _stream_of(_here(loss), stream)))
     return (loss, lse) if return_lse else loss
 
 
@@ -859,13 +867,13 @@ def distill_chunk_grad(d: Distill, scores: torch.Tensor, col_begin: int = 0,
                        stream=None) -> torch.Tensor:
     """row_weights[r] * d loss_r / d scores[r, j] of a chunk, after distill_loss of the same
     scores. out: of the scores' type or float32, may be `scores` itself."""
-    _here(scores, row_weights, out)
+    dev = _here(scores, row_weights, out)
     v = _view(scores, col_begin)
     w = _rows_f32(row_weights, v.n_rows, "row_weights")
     with _on(stream):
         out, ld = _grad_out(scores, out)
         _check(_lib.sps_distill_chunk_grad(d._h, ctypes.byref(v), w, out.data_ptr(),
-                                           _SCORE_TYPES[out.dtype], ld, _stream_ptr(stream)))
+                                           _SCORE_TYPES[out.dtype], ld, _stream_of(dev, stream)))
     return out
 
 
@@ -876,7 +884,7 @@ def distill(scores: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: tor
     """(loss of every row, gradient about the scores) of whole rows against the teacher's best
     k (distill_prepare says which entries count); the gradient is None without need_grad."""
     load_library()
-    _here(scores, teacher_ids, teacher_logits, teacher_lse, row_weights, out)
+    dev = _here(scores, teacher_ids, teacher_logits, teacher_lse, row_weights, out)
     v = _view(scores)
     n, k, lse = _teacher(teacher_ids, teacher_logits, teacher_lse)
     assert n == v.n_rows, "one list a row"
@@ -892,7 +900,7 @@ def distill(scores: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: tor
                                      teacher_logits.data_ptr(), lse, k, float(temperature), w,
                                      loss.data_ptr(), out.data_ptr() if need_grad else None,
                                      _SCORE_TYPES[out.dtype] if need_grad else 0, ld, ptr, nb,
-                                     _stream_ptr(stream)))
+                                     _stream_of(dev, stream)))
     return loss, out if need_grad else None
 
 
@@ -907,7 +915,7 @@ def cosine_chunk_grad(rows: CSR, other: Items, chunk: int, grad: torch.Tensor, d
     the queries prepared as a corpus. first=True starts the sums; cosine_grad_values ends
     them."""
     load_library()
-    _here(rows.values, grad, du)
+    dev = _here(rows.values, grad, du)
     assert du.dtype == torch.float32 and du.is_contiguous() and du.numel() == rows.nnz
     v = _view(grad)
     c = rows._c()
@@ -918,7 +926,7 @@ def cosine_chunk_grad(rows: CSR, other: Items, chunk: int, grad: torch.Tensor, d
         _check(_lib.sps_cosine_grad(ctypes.byref(c), other._h, chunk, ctypes.byref(v),
                                     int(transposed), int(first), du.data_ptr(),
                                     ws.data_ptr() if nb.value else None, nb.value,
-                                    _stream_ptr(stream)))
+                                    _stream_of(dev, stream)))
 
 
 def cosine_grad_values(rows: CSR, du: torch.Tensor, out: torch.Tensor | None = None,
@@ -926,7 +934,7 @@ def cosine_grad_values(rows: CSR, du: torch.Tensor, out: torch.Tensor | None = N
     """The gradient about the stored values from that about the unit values (the norm's
     part taken off); out may be du itself."""
     load_library()
-    _here(rows.values, du, out)
+    dev = _here(rows.values, du, out)
     assert du.dtype == torch.float32 and du.is_contiguous() and du.numel() == rows.nnz
     with _on(stream):
         if out is None:
@@ -934,7 +942,7 @@ def cosine_grad_values(rows: CSR, du: torch.Tensor, out: torch.Tensor | None = N
         assert out.dtype == torch.float32 and out.is_contiguous() and out.numel() == rows.nnz
         c = rows._c()
         _check(_lib.sps_cosine_grad_values(ctypes.byref(c), du.data_ptr(), out.data_ptr(),
-                                           _stream_ptr(stream)))
+                                           _stream_of(dev, stream)))
     return out
 
 
@@ -944,7 +952,7 @@ def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, stream=None):
     bfloat16. The stored structure of both is fixed. Nothing is prepared: a training step's
     batch has new values each time."""
     load_library()
-    _here(queries.values, items.values, grad)
+    dev = _here(queries.values, items.values, grad)
     v = _view(grad)
     q, i = queries._c(), items._c()
     nb = _sized("sps_cosine_grad_both_workspace_size", q.nnz, i.nnz)
@@ -954,7 +962,7 @@ def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, stream=None):
         buf, ptr = _workspace(nb, grad.device)
         _check(_lib.sps_cosine_grad_both(ctypes.byref(q), ctypes.byref(i), ctypes.byref(v),
                                          gq.data_ptr(), gi.data_ptr(), ptr, nb,
-                                         _stream_ptr(stream)))
+                                         _stream_of(dev, stream)))
     return gq, gi
 
 

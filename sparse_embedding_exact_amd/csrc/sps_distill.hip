@@ -44,9 +44,11 @@ struct RowTeach {  // of a row's list
 };
 
 struct RowCoef {  // for the gradient
-  double a, b;
-  float m;
+  double a;      // of a listed score's 2^((x - m_all) c)
+  double b;      // of another score's 2^((x - m) c)
+  float m_all, m;
   int32_t live;  // 0: loss and gradient are 0
+  int32_t pad;
 };
 
 struct DistillDev {
@@ -65,6 +67,11 @@ struct DistillDev {
 
 __device__ __forceinline__ float exp2_from(float x, float m, float c) {
   return __builtin_amdgcn_exp2f((x - m) * c);
+}
+// x, or -inf where bit e of `listed` is set (two operations, no branch)
+__device__ __forceinline__ float strike_if(float x, uint32_t listed, int e) {
+  const uint32_t mask = (uint32_t)((int32_t)(listed << (31 - e)) >> 31);
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & ~mask) | (0xFF800000u & mask));
 }
 // what a maximum of -inf (nothing but -inf yet) is subtracted as
 __device__ __forceinline__ float finite_max(float m) { return m == -__builtin_inff() ? 0.0f : m; }
@@ -108,21 +115,22 @@ __device__ __forceinline__ float block_max(float v, float *ws) {
 }
 
 // ---- the teacher's lists ----
+template <int KMAX>
 struct TeachShared {
-  int32_t id[kDistMaxK];   // as given, -1 where unusable
-  int32_t sid[kDistMaxK];  // -1 where the entry takes no part
-  float p[kDistMaxK];
+  int32_t id[KMAX];   // as given, -1 where unusable
+  int32_t sid[KMAX];  // -1 where the entry takes no part
+  float p[KMAX];
   double wd[3][16];
   float wf[16];
 };
 
 // By one workgroup: which entries of a row take part (an id's first
 // occurrence, inside the columns, with a logit), and their masses.
-template <int NT>
+template <int NT, int KMAX>
 __device__ __forceinline__ RowTeach teach_row(const int32_t *__restrict__ ids,
                                               const float *__restrict__ logits, const float *lse,
                                               int k, int64_t n_cols, double inv_tau,
-                                              TeachShared &sh) {
+                                              TeachShared<KMAX> &sh) {
   const int t = threadIdx.x;
   const double given = lse ? (double)*lse : 0.0;
   for (int i = t; i < k; i += NT) {
@@ -172,14 +180,14 @@ __device__ __forceinline__ RowTeach teach_row(const int32_t *__restrict__ ids,
   return r;
 }
 
-template <int NT>
+template <int NT, int KMAX>
 __global__ __launch_bounds__(NT) void distill_prepare_kernel(DistillDev d,
                                                              const int32_t *__restrict__ ids,
                                                              const float *__restrict__ logits,
                                                              const float *__restrict__ lse) {
-  __shared__ TeachShared sh;
+  __shared__ TeachShared<KMAX> sh;
   const int64_t row = blockIdx.x, at = row * d.k;
-  const RowTeach r = teach_row<NT>(ids + at, logits + at, lse ? lse + row : nullptr, d.k, d.n_cols,
+  const RowTeach r = teach_row<NT, KMAX>(ids + at, logits + at, lse ? lse + row : nullptr, d.k, d.n_cols,
                                    d.inv_tau, sh);
   for (int i = threadIdx.x; i < d.k; i += NT) {
     d.sid[at + i] = sh.sid[i];
@@ -232,209 +240,6 @@ __device__ __forceinline__ void load_tile(const T *x, int64_t base, int64_t end,
     }
   }
 }
-
-template <typename T>
-__global__ __launch_bounds__(kDistThreads) void distill_chunk_kernel(ChunkArgs a) {
-  __shared__ uint32_t bits[kSuperTiles][kDistThreads];
-  __shared__ double wd[1][16];
-  __shared__ float wf[16];
-  const DistillDev &d = a.d;
-  const int t = threadIdx.x;
-  const int64_t row = blockIdx.x / (uint32_t)a.splits;
-  const int32_t split = (int32_t)(blockIdx.x % (uint32_t)a.splits);
-  const int64_t c0 = split * a.seg, c1 = c0 + a.seg < a.n_cols ? c0 + a.seg : a.n_cols;
-  const T *x = static_cast<const T *>(a.x) + row * a.ld;
-  const int32_t *sid = d.sid + row * d.k;
-  // the listed scores of this part; on the first chunk, the first part clears those elsewhere
-  for (int i = t; i < d.k; i += kDistThreads) {
-    const int64_t o = (int64_t)sid[i] - a.col_begin;
-    if (sid[i] >= 0 && o >= c0 && o < c1) d.x[row * d.k + i] = to_f32(x[o]);
-    else if (a.first && split == 0 && (sid[i] < 0 || o < 0 || o >= a.n_cols))
-      d.x[row * d.k + i] = -__builtin_inff();
-  }
-  float m = -__builtin_inff();
-  double s = 0;
-  for (int64_t s0 = c0; s0 < c1; s0 += (int64_t)kSuperTiles * kDistTile) {
-    const int64_t s1 =
-        s0 + (int64_t)kSuperTiles * kDistTile < c1 ? s0 + (int64_t)kSuperTiles * kDistTile : c1;
-    const int tiles = (int)((s1 - s0 + kDistTile - 1) / kDistTile);
-    __syncthreads();
-    for (int i = 0; i < tiles; ++i) bits[i][t] = 0;
-    __syncthreads();
-    for (int i = t; i < d.k; i += kDistThreads) {
-      const int64_t o = (int64_t)sid[i] - a.col_begin - s0;
-      if (sid[i] >= 0 && o >= 0 && o < s1 - s0) {
-        int word, bit;
-        bit_of<T, kDistThreads>((int)(o % kDistTile), word, bit);
-        atomicOr(&bits[o / kDistTile][word], 1u << bit);
-      }
-    }
-    __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
-      float f[kDistVpt];
-      load_tile<T, kDistThreads>(x, s0 + (int64_t)i * kDistTile, s1, f);
-      const uint32_t listed = bits[i][t];
-      if (listed) {
-#pragma unroll
-        for (int e = 0; e < kDistVpt; ++e)
-          if (listed >> e & 1u) f[e] = -__builtin_inff();
-      }
-      float mt = m;
-#pragma unroll
-      for (int e = 0; e < kDistVpt; ++e) mt = fmaxf(mt, f[e]);
-      const float mf = finite_max(mt);
-      float part = 0;
-#pragma unroll
-      for (int e = 0; e < kDistVpt; ++e) part += exp2_from(f[e], mf, d.c);
-      s = s * (double)exp2_from(m, mf, d.c) + (double)part;
-      m = mt;
-    }
-  }
-  const float mb = block_max<kDistThreads>(m, wf);
-  double sums[1] = {s * (double)exp2_from(m, finite_max(mb), d.c)};
-  block_sums<kDistThreads>(sums, wd);
-  const double sb = sums[0];
-  if (t == 0) {
-    Stat *st = d.stat + row * d.slots;
-    Stat r{sb, mb, 0};
-    if (!a.first) {
-      const Stat o = st[split];
-      r.m = fmaxf(o.m, mb);
-      const float mf = finite_max(r.m);
-      r.s = o.s * (double)exp2_from(o.m, mf, d.c) + sb * (double)exp2_from(mb, mf, d.c);
-    }
-    st[split] = r;
-    if (a.first && split == 0)
-      for (int i = a.splits; i < d.slots; ++i) st[i] = Stat{0, -__builtin_inff(), 0};
-  }
-}
-
-// ---- the losses ----
-// One wave a row.
-__global__ __launch_bounds__(256) void distill_loss_kernel(DistillDev d, float *__restrict__ loss,
-                                                           float *__restrict__ lse) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= d.n_rows) return;  // uniform per wave
-  const int32_t *sid = d.sid + row * d.k;
-  const float *x = d.x + row * d.k, *p = d.p + row * d.k;
-  const Stat *st = d.stat + row * d.slots;
-  const RowTeach te = d.teach[row];
-  float m = -__builtin_inff();
-  for (int i = lane; i < d.slots; i += 64) m = fmaxf(m, st[i].m);
-  for (int i = lane; i < d.k; i += 64)
-    if (sid[i] >= 0) m = fmaxf(m, x[i]);
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  const float mf = finite_max(m);
-  const double c = (double)d.c, ln2 = 0.693147180559945309417;
-  double z_rest = 0, z_list = 0;
-  for (int i = lane; i < d.slots; i += 64) {
-    const Stat s = st[i];
-    if (s.s != 0) z_rest += s.s * exp2(((double)s.m - (double)mf) * c);
-  }
-  for (int i = lane; i < d.k; i += 64)
-    if (sid[i] >= 0) z_list += exp2(((double)x[i] - (double)mf) * c);
-  z_rest = wave_sum(z_rest);
-  z_list = wave_sum(z_list);
-  const double z = z_rest + z_list, log_z = log(z);
-  double l = 0;
-  for (int i = lane; i < d.k; i += 64)
-    if (sid[i] >= 0 && p[i] != 0)
-      l += (double)p[i] * (log_z - ((double)x[i] - (double)mf) * c * ln2);
-  l = wave_sum(l) + te.entropy;
-  if (te.rest != 0) l += te.rest * (log_z - log(z_rest));
-  const int32_t live = te.has && z != 0;  // a NaN is no 0
-  if (lane == 0) {
-    RowCoef r;
-    r.a = te.mass / z;
-    r.b = te.rest != 0 && z_rest != 0 ? te.mass / z - te.rest / z_rest : r.a;
-    r.m = mf;
-    r.live = live;
-    d.coef[row] = r;
-    loss[row] = live ? (float)l : 0.0f;
-    if (lse) lse[row] = (float)((double)mf * c * ln2 + log_z);
-  }
-}
-
-// ---- the gradient ----
-struct GradArgs {
-  DistillDev d;
-  const void *x;
-  void *g;
-  const float *weights;  // nullable: 1
-  int64_t ld, ldg, n_cols, col_begin, seg;
-  int32_t splits;
-};
-
-template <typename T, typename G, int NT, int VPT>
-__device__ __forceinline__ void store_tile(G *g, int64_t base, int64_t end, const float (&f)[VPT]) {
-  constexpr int V = kVec<T>, W = kVec<G>;
-#pragma unroll
-  for (int v = 0; v < VPT / V; ++v) {
-    const int64_t c = base + ((int64_t)v * NT + threadIdx.x) * V;
-    if (c + V <= end) {
-#pragma unroll
-      for (int w = 0; w < V; w += W) {
-        Vec<G> o;
-#pragma unroll
-        for (int e = 0; e < W; ++e) o.e[e] = from_f32<G>(f[v * V + w + e]);
-        *reinterpret_cast<Vec<G> *>(g + c + w) = o;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-        if (c + e < end) g[c + e] = from_f32<G>(f[v * V + e]);
-    }
-  }
-}
-
-template <typename T, typename G>
-__global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(GradArgs a) {
-  const DistillDev &d = a.d;
-  const int64_t row = blockIdx.x / (uint32_t)a.splits;
-  const int32_t split = (int32_t)(blockIdx.x % (uint32_t)a.splits);
-  const int64_t c0 = split * a.seg, c1 = c0 + a.seg < a.n_cols ? c0 + a.seg : a.n_cols;
-  const T *x = static_cast<const T *>(a.x) + row * a.ld;
-  G *g = static_cast<G *>(a.g) + row * a.ldg;
-  const RowCoef r = d.coef[row];
-  const double w = (a.weights ? (double)a.weights[row] : 1.0) * d.inv_tau;
-  const float b = (float)(r.b * w);
-  for (int64_t base = c0; base < c1; base += kDistTile) {
-    float f[kDistVpt];
-    load_tile<T, kDistThreads>(x, base, c1, f);
-#pragma unroll
-    for (int e = 0; e < kDistVpt; ++e) f[e] = r.live ? exp2_from(f[e], r.m, d.c) * b : 0.0f;
-    store_tile<T, G, kDistThreads>(g, base, c1, f);
-  }
-  if (!r.live) return;  // uniform
-  __syncthreads();      // the listed columns are written over what stands there
-  for (int i = threadIdx.x; i < d.k; i += kDistThreads) {
-    const int32_t id = d.sid[row * d.k + i];
-    const int64_t o = (int64_t)id - a.col_begin;
-    if (id >= 0 && o >= c0 && o < c1) {
-      const double e = exp2(((double)d.x[row * d.k + i] - (double)r.m) * (double)d.c);
-      g[o] = from_f32<G>((float)((e * r.a - (double)d.p[row * d.k + i]) * w));
-    }
-  }
-}
-
-// ---- whole rows in one launch ----
-// One workgroup a row. A row that fits NT x VPT scores stays in registers from
-// the load to the gradient: read once, written once, one exponential a score.
-// A longer one is read a second time for the gradient, soon enough after the
-// first that much of it still comes from the caches.
-struct RowsArgs {
-  const void *x;
-  void *g;  // nullable
-  const int32_t *ids;
-  const float *logits, *lse, *weights;
-  float *loss;
-  int64_t ld, ldg, n_cols;
-  int32_t k;
-  float c;
-  double inv_tau;
-};
 
 // A thread's scores of a tile as they were loaded, four bytes a register: for
 // 16-bit scores half the registers of their float32 values. Past the end of
@@ -496,6 +301,12 @@ struct RawTile {
       }
     }
   }
+  // Nothing derived from the scores so far is kept: a second use converts them
+  // again, where the compiler would hold VPT values more across the barriers.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < VPT / E; ++i) asm volatile("" : "+v"(r[i]));
+  }
   // g[...] = 2^((x - m) c) b of the tile's columns, or 0
   template <typename G>
   __device__ __forceinline__ void store(G *g, int64_t base, int64_t end, bool live, float m, float c,
@@ -523,6 +334,247 @@ struct RawTile {
   }
 };
 
+template <typename T>
+__global__ __launch_bounds__(kDistThreads) void distill_chunk_kernel(ChunkArgs a) {
+  __shared__ uint32_t bits[kSuperTiles][kDistThreads];
+  __shared__ double ws[kDistThreads / 64];
+  __shared__ float wm[kDistThreads / 64];
+  const DistillDev &d = a.d;
+  const int t = threadIdx.x;
+  const int64_t row = blockIdx.x / (uint32_t)a.splits;
+  const int32_t split = (int32_t)(blockIdx.x % (uint32_t)a.splits);
+  const int64_t c0 = split * a.seg, c1 = c0 + a.seg < a.n_cols ? c0 + a.seg : a.n_cols;
+  const T *x = static_cast<const T *>(a.x) + row * a.ld;
+  const int32_t *sid = d.sid + row * d.k;
+  Stat *st = d.stat + row * d.slots;
+  // the first tile, the list and what came before are on their way together
+  float f[kDistVpt];
+  load_tile<T, kDistThreads>(x, c0, c1, f);
+  Stat old{0, -__builtin_inff(), 0};
+  if (!a.first) old = st[split];
+  float m = -__builtin_inff();
+  double s = 0;
+  for (int64_t s0 = c0; s0 < c1; s0 += (int64_t)kSuperTiles * kDistTile) {
+    const int64_t s1 =
+        s0 + (int64_t)kSuperTiles * kDistTile < c1 ? s0 + (int64_t)kSuperTiles * kDistTile : c1;
+    const int tiles = (int)((s1 - s0 + kDistTile - 1) / kDistTile);
+    if (s0 > c0) __syncthreads();
+    for (int i = 0; i < tiles; ++i) bits[i][t] = 0;
+    __syncthreads();
+    for (int i = t; i < d.k; i += kDistThreads) {
+      const int32_t id = sid[i];
+      const int64_t o = (int64_t)id - a.col_begin;
+      if (id >= 0 && o >= s0 && o < s1) {
+        int word, bit;
+        bit_of<T, kDistThreads>((int)((o - s0) % kDistTile), word, bit);
+        atomicOr(&bits[(o - s0) / kDistTile][word], 1u << bit);
+        d.x[row * d.k + i] = to_f32(x[o]);
+      }
+    }
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+      if (i > 0 || s0 > c0) load_tile<T, kDistThreads>(x, s0 + (int64_t)i * kDistTile, s1, f);
+      const uint32_t listed = bits[i][t];
+      if (__ballot(listed != 0)) {
+#pragma unroll
+        for (int e = 0; e < kDistVpt; ++e) f[e] = strike_if(f[e], listed, e);
+      }
+      float mt = m;
+#pragma unroll
+      for (int e = 0; e < kDistVpt; ++e) mt = fmaxf(mt, f[e]);
+      const float mf = finite_max(mt);
+      float part = 0;
+#pragma unroll
+      for (int e = 0; e < kDistVpt; ++e) part += exp2_from(f[e], mf, d.c);
+      s = s * (double)exp2_from(m, mf, d.c) + (double)part;
+      m = mt;
+    }
+  }
+  // on the first chunk, the first part clears the scores of entries that lie elsewhere
+  if (a.first && split == 0)
+    for (int i = t; i < d.k; i += kDistThreads) {
+      const int64_t o = (int64_t)sid[i] - a.col_begin;
+      if (sid[i] < 0 || o < 0 || o >= a.n_cols) d.x[row * d.k + i] = -__builtin_inff();
+    }
+  // a maximum and a sum of each wave, joined by one thread
+  float mw = m;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) mw = fmaxf(mw, __shfl_xor(mw, o, 64));
+  s = wave_total_f64(s * (double)exp2_from(m, finite_max(mw), d.c));
+  if ((t & 63) == 63) {
+    ws[t >> 6] = s;
+    wm[t >> 6] = mw;
+  }
+  __syncthreads();
+  if (t == 0) {
+    float mb = old.m;
+#pragma unroll
+    for (int i = 0; i < kDistThreads / 64; ++i) mb = fmaxf(mb, wm[i]);
+    const float mf = finite_max(mb);
+    double sb = old.s * (double)exp2_from(old.m, mf, d.c);
+#pragma unroll
+    for (int i = 0; i < kDistThreads / 64; ++i) sb += ws[i] * (double)exp2_from(wm[i], mf, d.c);
+    st[split] = Stat{sb, mb, 0};
+    if (a.first && split == 0)
+      for (int i = a.splits; i < d.slots; ++i) st[i] = Stat{0, -__builtin_inff(), 0};
+  }
+}
+
+// ---- the losses ----
+// A row's sums joined. z_rest: of 2^((x - m) c) outside the list; z_list: of
+// 2^((x - m_all) c) inside it, m_all >= m.
+struct Whole {
+  double z, log_z;   // of all columns, about m_all
+  double rest_term;  // log z - log z_rest: -log of the mass outside the list
+  double a, b;       // the gradient's factors (RowCoef)
+};
+__device__ __forceinline__ Whole whole(double z_rest, double z_list, float m, float m_all, double c,
+                                       double mass, double rest) {
+  Whole r;
+  const double d = ((double)m - (double)m_all) * c;
+  // nothing outside the list: m stands for no score
+  r.z = z_list + (z_rest == 0 ? 0.0 : z_rest * exp2(d));
+  r.log_z = log(r.z);
+  r.rest_term = r.log_z - log(z_rest) - d * 0.693147180559945309417;
+  r.a = mass / r.z;
+  // with nothing outside the list b meets zeros alone: 0, or NaN where the row is
+  r.b = z_rest == 0 ? (r.z - r.z) : r.a * exp2(d) - rest / z_rest;
+  return r;
+}
+
+// One wave a row.
+__global__ __launch_bounds__(256) void distill_loss_kernel(DistillDev d, float *__restrict__ loss,
+                                                           float *__restrict__ lse) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= d.n_rows) return;  // uniform per wave
+  const int32_t *sid = d.sid + row * d.k;
+  const float *x = d.x + row * d.k, *p = d.p + row * d.k;
+  const Stat *st = d.stat + row * d.slots;
+  const RowTeach te = d.teach[row];
+  // the columns outside the list by their own largest score: their mass, which the remaining
+  // class divides by, must not vanish next to the list's
+  float m = -__builtin_inff(), ml = -__builtin_inff();
+  for (int i = lane; i < d.slots; i += 64) m = fmaxf(m, st[i].m);
+  for (int i = lane; i < d.k; i += 64)
+    if (sid[i] >= 0) ml = fmaxf(ml, x[i]);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o, 64));
+    ml = fmaxf(ml, __shfl_xor(ml, o, 64));
+  }
+  const float mf = finite_max(m), ma = finite_max(fmaxf(m, ml));
+  const double c = (double)d.c, ln2 = 0.693147180559945309417;
+  double z_rest = 0, z_list = 0;
+  for (int i = lane; i < d.slots; i += 64) {
+    const Stat s = st[i];
+    if (s.s != 0) z_rest += s.s * exp2(((double)s.m - (double)mf) * c);
+  }
+  for (int i = lane; i < d.k; i += 64)
+    if (sid[i] >= 0) z_list += exp2(((double)x[i] - (double)ma) * c);
+  z_rest = __shfl(wave_total_f64(z_rest), 63, 64);
+  z_list = __shfl(wave_total_f64(z_list), 63, 64);
+  const Whole z = whole(z_rest, z_list, mf, ma, c, te.mass, te.rest);
+  double l = 0;
+  for (int i = lane; i < d.k; i += 64)
+    if (sid[i] >= 0 && p[i] != 0)
+      l += (double)p[i] * (z.log_z - ((double)x[i] - (double)ma) * c * ln2);
+  l = __shfl(wave_total_f64(l), 63, 64) + te.entropy;
+  if (te.rest != 0) l += te.rest * z.rest_term;
+  const int32_t live = te.has && z.z != 0;  // a NaN is no 0
+  if (lane == 0) {
+    RowCoef r;
+    r.a = z.a;
+    r.b = z.b;
+    r.m_all = ma;
+    r.m = mf;
+    r.live = live;
+    r.pad = 0;
+    d.coef[row] = r;
+    loss[row] = live ? (float)l : 0.0f;
+    if (lse) lse[row] = (float)((double)ma * c * ln2 + z.log_z);
+  }
+}
+
+// ---- the gradient ----
+struct GradArgs {
+  DistillDev d;
+  const void *x;
+  void *g;
+  const float *weights;  // nullable: 1
+  int64_t ld, ldg, n_cols, col_begin, seg;
+  int32_t splits;
+};
+
+template <typename T, typename G, int NT, int VPT>
+__device__ __forceinline__ void store_tile(G *g, int64_t base, int64_t end, const float (&f)[VPT]) {
+  constexpr int V = kVec<T>, W = kVec<G>;
+#pragma unroll
+  for (int v = 0; v < VPT / V; ++v) {
+    const int64_t c = base + ((int64_t)v * NT + threadIdx.x) * V;
+    if (c + V <= end) {
+#pragma unroll
+      for (int w = 0; w < V; w += W) {
+        Vec<G> o;
+#pragma unroll
+        for (int e = 0; e < W; ++e) o.e[e] = from_f32<G>(f[v * V + w + e]);
+        *reinterpret_cast<Vec<G> *>(g + c + w) = o;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (c + e < end) g[c + e] = from_f32<G>(f[v * V + e]);
+    }
+  }
+}
+
+template <typename T, typename G>
+__global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(GradArgs a) {
+  const DistillDev &d = a.d;
+  const int64_t row = blockIdx.x / (uint32_t)a.splits;
+  const int32_t split = (int32_t)(blockIdx.x % (uint32_t)a.splits);
+  const int64_t c0 = split * a.seg, c1 = c0 + a.seg < a.n_cols ? c0 + a.seg : a.n_cols;
+  const T *x = static_cast<const T *>(a.x) + row * a.ld;
+  G *g = static_cast<G *>(a.g) + row * a.ldg;
+  const RowCoef r = d.coef[row];
+  const double w = (a.weights ? (double)a.weights[row] : 1.0) * d.inv_tau;
+  const float b = (float)(r.b * w);
+  for (int64_t base = c0; base < c1; base += kDistTile) {
+    float f[kDistVpt];
+    load_tile<T, kDistThreads>(x, base, c1, f);
+#pragma unroll
+    for (int e = 0; e < kDistVpt; ++e) f[e] = r.live ? exp2_from(f[e], r.m, d.c) * b : 0.0f;
+    store_tile<T, G, kDistThreads>(g, base, c1, f);
+  }
+  if (!r.live) return;  // uniform
+  __syncthreads();      // the listed columns are written over what stands there
+  for (int i = threadIdx.x; i < d.k; i += kDistThreads) {
+    const int32_t id = d.sid[row * d.k + i];
+    const int64_t o = (int64_t)id - a.col_begin;
+    if (id >= 0 && o >= c0 && o < c1) {
+      const double e = exp2(((double)d.x[row * d.k + i] - (double)r.m_all) * (double)d.c);
+      g[o] = from_f32<G>((float)((e * r.a - (double)d.p[row * d.k + i]) * w));
+    }
+  }
+}
+
+// ---- whole rows in one launch ----
+// One workgroup a row. A row that fits NT x VPT scores stays in registers from
+// the load to the gradient: read once, written once, one exponential a score.
+// A longer one is read a second time for the gradient, soon enough after the
+// first that much of it still comes from the caches.
+struct RowsArgs {
+  const void *x;
+  void *g;  // nullable
+  const int32_t *ids;
+  const float *logits, *lse, *weights;
+  float *loss;
+  int64_t ld, ldg, n_cols;
+  int32_t k;
+  float c;
+  double inv_tau;
+};
+
 template <int NT>
 struct RowsShared {
   int32_t id[kDistMaxK];   // as given, -1 where unusable
@@ -530,16 +582,23 @@ struct RowsShared {
   double e[kDistMaxK];     // the entry's logit; then its mass before the common factor
   uint32_t bits[NT];  // the listed ones of a thread's scores
   double ws[6][16];
-  float wf[2][16];
+  float wf[3][16];
+  double fa, fp;  // the factors of a listed score's exponential and of its entry's mass
+  float b;        // of another score's exponential
+  bool live;      // false: loss and gradient are 0
 };
 
-// The waves a SIMD holds: as many as the registers of a thread's scores (REGS)
-// and about 40 more allow, since the other rows of a CU are what hides a row's
-// chain of loads, barriers and reductions.
-constexpr int rows_waves(int regs) { return regs <= 16 ? 8 : regs <= 32 ? 5 : 4; }
+// The waves a SIMD holds: the other rows of a CU are what hides a row's chain
+// of loads, barriers and reductions. Two workgroups of 1024 need 64 registers
+// a thread (a few values spill; one workgroup without spills is slower, 220
+// against 149 us at 4095 x 30522); smaller workgroups fit the registers of a
+// thread's scores (`regs`) and about 60 more.
+constexpr int rows_waves(int nt, int regs) {
+  return nt == 1024 ? (regs <= 16 ? 8 : 4) : (regs <= 16 ? 6 : 5);
+}
 
 template <typename T, typename G, int NT, int VPT, bool LONG>
-__global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void distill_rows_kernel(
+__global__ __launch_bounds__(NT, rows_waves(NT, VPT * (int)sizeof(T) / 4)) void distill_rows_kernel(
     RowsArgs a) {
   __shared__ RowsShared<NT> sh;
   constexpr int64_t kTileCols = (int64_t)NT * VPT;
@@ -564,7 +623,7 @@ __global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void dist
   __syncthreads();
   // an entry takes part if no earlier one has its id; its column's bit is set
   uint32_t part = 0;  // of this thread's entries (k <= 1024: four at most)
-  float mt = -__builtin_inff(), m = -__builtin_inff();
+  float mt = -__builtin_inff(), ml = -__builtin_inff(), m = -__builtin_inff();
 #pragma unroll 1
   for (int i = t, j = 0; i < a.k; i += NT, ++j) {
     const int32_t v = sh.id[i];
@@ -574,7 +633,7 @@ __global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void dist
     if (!dup) {
       part |= 1u << j;
       mt = fmaxf(mt, (float)sh.e[i]);
-      m = fmaxf(m, sh.x[i]);
+      ml = fmaxf(ml, sh.x[i]);
       if (!LONG) {
         int word, bit;
         bit_of<T, NT>(v, word, bit);
@@ -629,28 +688,34 @@ __global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void dist
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     m = fmaxf(m, __shfl_xor(m, o, 64));
+    ml = fmaxf(ml, __shfl_xor(ml, o, 64));
     mt = fmaxf(mt, __shfl_xor(mt, o, 64));
   }
   if (lane == 0) {
     sh.wf[0][wave] = m;
     sh.wf[1][wave] = mt;
+    sh.wf[2][wave] = ml;
   }
   __syncthreads();
   m = sh.wf[0][lane & (NT / 64 - 1)];
   mt = sh.wf[1][lane & (NT / 64 - 1)];
+  ml = sh.wf[2][lane & (NT / 64 - 1)];
 #pragma unroll
   for (int o = NT / 128; o > 0; o >>= 1) {
     m = fmaxf(m, __shfl_xor(m, o, 64));
+    ml = fmaxf(ml, __shfl_xor(ml, o, 64));
     mt = fmaxf(mt, __shfl_xor(mt, o, 64));
   }
-  const float mf = finite_max(m);
+  const float mf = finite_max(m), ma = finite_max(fmaxf(m, ml));
   if (LONG) {
     z_rest *= (double)exp2_from(mine, mf, a.c);
   } else {
+    f.forget();
     float sum = 0;
 #pragma unroll
     for (int e = 0; e < VPT; ++e) sum += exp2_from(f.get(e), mf, a.c);
     z_rest = (double)sum;
+    f.forget();
   }
   // sums: student's mass outside the list and inside; teacher's e, e log e and e (x - m), where
   // a listed entry's mass is e over their sum (or e itself); entries
@@ -661,7 +726,7 @@ __global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void dist
 #pragma unroll 1
     for (int i = t, j = 0; i < a.k; i += NT, ++j)
       if (part >> j & 1u) {
-        const double d = ((double)sh.x[i] - (double)mf) * c;
+        const double d = ((double)sh.x[i] - (double)ma) * c;
         double s = exp2(d);
         asm volatile("" : "+v"(s));  // one function's temporaries at a time
         v[1] += s;
@@ -681,26 +746,33 @@ __global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void dist
     }
   }
   __syncthreads();
-  double v[6];
+  if (wave == 0) {
+    double v[6];
 #pragma unroll
-  for (int i = 0; i < 6; ++i) v[i] = row16_sum(lane & 15, NT / 64, sh.ws[i]);
-  z_rest = v[0];
-  const double z = z_rest + v[1];
-  const double scale = a.lse ? 1.0 : 1.0 / v[2];
-  const double rest = !a.lse ? 0.0 : v[2] < 1 ? 1 - v[2] : v[2] >= 1 ? 0.0 : v[2];  // NaN stays
-  const double listed_mass = a.lse ? v[2] : 1.0 + (v[2] - v[2]);  // 1, or NaN where the logits are
-  const bool live = v[5] != 0 && z != 0;  // a NaN is no 0
-  if (wave == NT / 64 - 1 && lane == 0) {
-    // sum p log p, p = e scale; sum p (log z - (x - m)); the remaining class
-    const double log_z = log(z);
-    double l = v[3] * scale + (a.lse ? 0.0 : log(scale)) + listed_mass * log_z - v[4] * scale * ln2;
-    if (rest != 0) l += rest * (log(rest) + log_z - log(z_rest));
-    a.loss[row] = live ? (float)l : 0.0f;
+    for (int i = 0; i < 6; ++i) v[i] = row16_sum(lane & 15, NT / 64, sh.ws[i]);
+    const double scale = a.lse ? 1.0 : 1.0 / v[2];
+    const double rest = !a.lse ? 0.0 : v[2] < 1 ? 1 - v[2] : v[2] >= 1 ? 0.0 : v[2];  // NaN stays
+    // the list's mass: 1, or NaN where the logits are
+    const double listed_mass = a.lse ? v[2] : 1.0 + (v[2] - v[2]);
+    const Whole z = whole(v[0], v[1], mf, ma, c, listed_mass + rest, rest);
+    const bool live = v[5] != 0 && z.z != 0;  // a NaN is no 0
+    if (lane == 0) {
+      // sum p log p, p = e scale; sum p (log z - (x - m)); the remaining class
+      double l =
+          v[3] * scale + (a.lse ? 0.0 : log(scale)) + listed_mass * z.log_z - v[4] * scale * ln2;
+      if (rest != 0) l += rest * (log(rest) + z.rest_term);
+      a.loss[row] = live ? (float)l : 0.0f;
+      const double w = (a.weights ? (double)a.weights[row] : 1.0) * a.inv_tau;
+      sh.fa = z.a * w;
+      sh.fp = scale * w;
+      sh.b = (float)(z.b * w);
+      sh.live = live;
+    }
   }
   if (!a.g) return;
-  const double w = (a.weights ? (double)a.weights[row] : 1.0) * a.inv_tau;
-  const double fa = (listed_mass + rest) / z;
-  const float b = (float)((rest != 0 && z_rest != 0 ? fa - rest / z_rest : fa) * w);
+  __syncthreads();
+  const float b = sh.b;
+  const bool live = sh.live;
   G *g = static_cast<G *>(a.g) + row * a.ldg;
   if (LONG) {  // backwards: the last tiles are still in the nearest cache
     for (int64_t b0 = (a.n_cols - 1) / kTileCols * kTileCols; b0 >= 0; b0 -= kTileCols) {
@@ -715,8 +787,8 @@ __global__ __launch_bounds__(NT, rows_waves(VPT * (int)sizeof(T) / 4)) void dist
 #pragma unroll 1
   for (int i = t, j = 0; i < a.k; i += NT, ++j)
     if (part >> j & 1u) {
-      const double e = exp2(((double)sh.x[i] - (double)mf) * c);
-      g[sh.id[i]] = from_f32<G>((float)((e * fa - sh.e[i] * scale) * w));
+      const double e = exp2(((double)sh.x[i] - (double)ma) * c);
+      g[sh.id[i]] = from_f32<G>((float)(e * sh.fa - sh.e[i] * sh.fp));
     }
 }
 
@@ -734,6 +806,7 @@ using sps::set_error;
 // Whole rows go to one launch, a workgroup each, where a row fits a
 // workgroup's registers or where there are rows enough to fill half the card;
 // few long rows are cut among workgroups instead, in four launches.
+constexpr int kShortList = 128;  // of lists up to this a wave prepares one: little LDS, many at once
 constexpr int64_t kOneTile = 32768, kManyRows = 128;
 
 constexpr int64_t kMax31 = 2147483647ll;
@@ -826,11 +899,11 @@ sps_status make_dev(const int32_t *ids, const float *logits, const float *lse, i
 
 void launch_prepare(const DistillDev &d, const int32_t *ids, const float *logits, const float *lse,
                     hipStream_t s) {
-  if (d.k <= 128)
-    hipLaunchKernelGGL((sps::distill_prepare_kernel<64>), dim3((uint32_t)d.n_rows), dim3(64), 0, s,
+  if (d.k <= kShortList)
+    hipLaunchKernelGGL((sps::distill_prepare_kernel<64, kShortList>), dim3((uint32_t)d.n_rows), dim3(64), 0, s,
                        d, ids, logits, lse);
   else
-    hipLaunchKernelGGL((sps::distill_prepare_kernel<256>), dim3((uint32_t)d.n_rows), dim3(256), 0,
+    hipLaunchKernelGGL((sps::distill_prepare_kernel<256, sps::kDistMaxK>), dim3((uint32_t)d.n_rows), dim3(256), 0,
                        s, d, ids, logits, lse);
 }
 

@@ -445,6 +445,68 @@ __global__ __launch_bounds__(kSelThreads) void beam_join_kernel(JoinArgs a) {
   }
 }
 
+// A whole group by one workgroup: its beams' rows as one run of places b *
+// n_cols + column. For the small groups of a latency-bound step, where a
+// second launch would cost more than the scores.
+struct GroupArgs {
+  const void *x;
+  int64_t ld, n_cols, col_begin;
+  const float *offsets;  // nullable
+  int32_t beams, k;
+  float *scores;
+  int32_t *parents, *cols;
+};
+
+template <typename T, int VPT>
+__global__ __launch_bounds__(kSelThreads) void beam_group_kernel(GroupArgs a) {
+  __shared__ SelShared sh;
+  constexpr int V = kVec<T>, NV = VPT / V;
+  const int t = threadIdx.x;
+  const int64_t row0 = (int64_t)blockIdx.x * a.beams;
+  const T *x = static_cast<const T *>(a.x) + row0 * a.ld;
+  const float *off = a.offsets ? a.offsets + row0 : nullptr;
+  const uint32_t cols = (uint32_t)a.n_cols, total = cols * (uint32_t)a.beams;  // below 2^32
+  auto at = [&](uint32_t p) {
+    const uint32_t b = p / cols;
+    return to_f32(x[b * a.ld + (p - b * cols)]) + (off ? off[b] : 0.0f);
+  };
+  int cur = 0, n = 0, rnd = 0;
+  sel_init(sh);
+  __syncthreads();
+  for (uint32_t base = 0; base < total; base += kSelThreads * VPT) {
+    float f[VPT];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const uint32_t p = base + (uint32_t)(v * kSelThreads + t) * V;
+      const uint32_t b = p < total ? p / cols : 0, c = p - b * cols;
+      if (p + V <= total && c + V <= cols) {
+        const Vec<T> w = *reinterpret_cast<const Vec<T> *>(x + b * a.ld + c);
+        const float o = off ? off[b] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[v * V + e] = to_f32(w.e[e]) + o;
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[v * V + e] = p + e < total ? at(p + e) : -__builtin_inff();
+      }
+    }
+    offer_tile<VPT>(
+        sh, f,
+        [&](int i) {
+          const uint32_t p = base + (uint32_t)(i / V * kSelThreads + t) * V + (uint32_t)(i % V);
+          return p < total ? key_of(at(p), p) : (uint64_t)0;
+        },
+        a.k, cur, n, rnd);
+  }
+  if (t < a.k) {
+    const uint64_t v = t < n ? sh.list[cur][t] : 0;
+    const int64_t o = (int64_t)blockIdx.x * a.k + t;
+    const uint32_t p = ~(uint32_t)v, b = v ? p / cols : 0;
+    a.scores[o] = v ? unorder_bits((uint32_t)(v >> 32)) : -__builtin_inff();
+    a.parents[o] = v ? (int32_t)(row0 + b) : -1;
+    a.cols[o] = v ? (int32_t)(a.col_begin + (p - b * cols)) : -1;
+  }
+}
+
 // ---- states ----
 constexpr int kMaxStates = 8;      // states of one launch
 constexpr int kPieceBytes = 16384; // of a row, copied by one workgroup
@@ -519,6 +581,19 @@ Split split_of(int64_t n_rows, int64_t n_cols) {
   if (seg < 8) seg = 8;
   s = (n_cols + seg - 1) / seg;
   return {(int32_t)(s > 1 ? s : 1), seg};
+}
+
+// Groups of up to this many scores go to one workgroup each, in one launch.
+constexpr int64_t kOneGroup = 16384;
+bool one_launch(int64_t n_cols, int32_t beams) { return n_cols <= kOneGroup / beams; }
+
+template <typename T>
+void launch_group(const sps::GroupArgs &a, int64_t groups, hipStream_t s) {
+  const dim3 grid((uint32_t)groups), block(sps::kSelThreads);
+  if (a.n_cols * a.beams <= sps::kSelThreads * 8)
+    hipLaunchKernelGGL((sps::beam_group_kernel<T, 8>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::beam_group_kernel<T, 32>), grid, block, 0, s, a);
 }
 
 template <typename T>
@@ -615,15 +690,6 @@ sps_status sps_select_chunk(const sps_scores *scores, const float *offsets, int3
   return sps::launch_status("sps_select_chunk");
 }
 
-sps_status sps_beam_workspace_size(int64_t n_rows, int64_t n_cols, int32_t k, size_t *bytes) {
-  size_t unused = 0;
-  const sps_status st = sps_select_workspace_size(n_rows, n_cols, k, &unused);
-  if (st != SPS_OK) return st;
-  if (!bytes) return sps::set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output pointer");
-  *bytes = parts_bytes(n_rows, split_of(n_rows, n_cols), k);
-  return SPS_OK;
-}
-
 static sps_status check_beams(int64_t n_rows, int32_t beams, int64_t lists, int32_t k_in,
                               const char *what) {
   if (beams < 1 || n_rows % beams)
@@ -631,6 +697,19 @@ static sps_status check_beams(int64_t n_rows, int32_t beams, int64_t lists, int3
                           what, (long long)n_rows, beams);
   if ((int64_t)beams * lists > kMax31 / k_in)
     return sps::set_error(SPS_ERR_OVERFLOW, "%s: beams x lists x k reaches 2^31", what);
+  return SPS_OK;
+}
+
+sps_status sps_beam_workspace_size(int64_t n_rows, int64_t n_cols, int32_t beams, int32_t k,
+                                   size_t *bytes) {
+  size_t unused = 0;
+  sps_status st = sps_select_workspace_size(n_rows, n_cols, k, &unused);
+  if (st != SPS_OK) return st;
+  if (!bytes) return sps::set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output pointer");
+  const Split sp = split_of(n_rows, n_cols);
+  st = check_beams(n_rows, beams, sp.splits, k, "sps_beam_workspace_size");
+  if (st != SPS_OK) return st;
+  *bytes = one_launch(n_cols, beams) ? 0 : parts_bytes(n_rows, sp, k);
   return SPS_OK;
 }
 
@@ -648,11 +727,28 @@ sps_status sps_beam_select(const sps_scores *scores, const float *beam_scores, i
   if (rows == 0) return SPS_OK;
   if (!out_scores || !out_parents || !out_cols)
     return sps::set_error(SPS_ERR_INVALID_ARGUMENT, "sps_beam_select: NULL output");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (one_launch(scores->n_cols, beams)) {
+    sps::GroupArgs g{};
+    g.x = scores->data;
+    g.ld = scores->ld;
+    g.n_cols = scores->n_cols;
+    g.col_begin = scores->col_begin;
+    g.offsets = beam_scores;
+    g.beams = beams;
+    g.k = k;
+    g.scores = out_scores;
+    g.parents = out_parents;
+    g.cols = out_cols;
+    if (scores->dtype == SPS_F32) launch_group<float>(g, rows / beams, s);
+    else if (scores->dtype == SPS_F16) launch_group<sps::f16_t>(g, rows / beams, s);
+    else launch_group<sps::bf16_t>(g, rows / beams, s);
+    return sps::launch_status("sps_beam_select");
+  }
   st = check_ws(workspace, workspace_bytes, parts_bytes(rows, sp, k), "sps_beam_select");
   if (st != SPS_OK) return st;
   if (rows * sp.splits > kMax31)
     return sps::set_error(SPS_ERR_OVERFLOW, "sps_beam_select: too many rows for a launch");
-  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   sps::SelArgs a{};
   a.x = scores->data;
   a.ld = scores->ld;

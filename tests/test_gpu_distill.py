@@ -177,6 +177,35 @@ def test_masks_and_odd_lists(env, dtype, rest):
         assert torch.isinf(loss[4]) and loss[4] > 0 and torch.isfinite(grad[4]).all()
 
 
+@pytest.mark.parametrize("chunked", [False, True])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("cols", [700, 40000])
+def test_list_far_above_the_rest(env, chunked, rest, cols):
+    """A sharp student: what lies outside the list is e^-150 to e^-400 of the whole, below
+    float32's range, and still a class of its own with a finite loss; and far below the list
+    in the other direction."""
+    torch, sps, dev = env
+    x, ids, t, w = make(env, 6, cols, 4, "float32", 9, 0.01)
+    ids[:] = np.arange(4) * 31
+    tau = 0.01
+    for i, gap in enumerate((1.5, 2.5, 4.0, -1.5, -4.0, 0.0)):
+        x[i, ids[i]] += gap
+    t *= 0.01
+    lse = teacher_lse(ids, t, tau, cols, 0.6, 1) if rest else None
+    a = (dev_of(env, ids), dev_of(env, t))
+    if chunked:
+        d = sps.distill_prepare(*a, cols, tau, dev_of(env, lse))
+        sps.distill_chunk(d, x[:, :300], 0, first=True)
+        sps.distill_chunk(d, x[:, 300:], 300)
+        loss = sps.distill_loss(d)
+        grad = torch.cat([sps.distill_chunk_grad(d, x[:, :300], 0, dev_of(env, w)),
+                          sps.distill_chunk_grad(d, x[:, 300:], 300, dev_of(env, w))], 1)
+    else:
+        loss, grad = sps.distill(x, *a, tau, dev_of(env, lse), row_weights=dev_of(env, w))
+    assert torch.isfinite(loss).all() and torch.isfinite(grad).all()
+    compare(env, loss, grad, x, ids, t, tau, lse, w)
+
+
 def test_strides(env):
     torch, sps, dev = env
     for dtype in TYPES:

@@ -142,7 +142,8 @@ def test_columns_to_the_largest(env):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("groups,beams,cols,k", [(1, 4, 1000, 4), (3, 5, 9001, 10), (2, 3, 70000, 256),
-                                                 (300, 4, 500, 8), (2, 1, 40, 60), (2, 40, 3, 7)])
+                                                 (300, 4, 500, 8), (2, 1, 40, 60), (2, 40, 3, 7),
+                                                 (3, 3, 5461, 20), (1, 7, 2341, 256)])
 def test_beams(env, dtype, kind, groups, beams, cols, k):
     torch, sps, dev = env
     rows = groups * beams

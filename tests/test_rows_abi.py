@@ -38,7 +38,7 @@ def test_bad_views(lib, kw, want):
 def test_bad_k(lib, k):
     n = ctypes.c_size_t()
     assert lib.sps_select_workspace_size(8, 100, k, ctypes.byref(n)) == INV
-    assert lib.sps_beam_workspace_size(8, 100, k, ctypes.byref(n)) == INV
+    assert lib.sps_beam_workspace_size(8, 100, 1, k, ctypes.byref(n)) == INV
     assert lib.sps_select_chunk(view(), None, k, 1, P, P, P, 1 << 30, None) == INV
     assert lib.sps_beam_select(view(), None, 1, k, P, P, P, P, 1 << 30, None) == INV
     assert lib.sps_beam_join(P, P, 8, k, 1, 4, P, P, P, None) == INV
@@ -48,7 +48,7 @@ def test_bad_k(lib, k):
 def test_select_refusals(lib):
     n = ctypes.c_size_t()
     assert lib.sps_select_workspace_size(8, 100, 4, None) == INV
-    assert lib.sps_beam_workspace_size(8, 100, 4, None) == INV
+    assert lib.sps_beam_workspace_size(8, 100, 1, 4, None) == INV
     assert lib.sps_select_workspace_size(-1, 100, 4, ctypes.byref(n)) == INV
     assert lib.sps_select_workspace_size(2**31, 100, 4, ctypes.byref(n)) == OVF
     assert lib.sps_select_chunk(None, None, 4, 1, P, P, None, 0, None) == INV
@@ -64,13 +64,18 @@ def test_select_refusals(lib):
 
 def test_beam_refusals(lib):
     n = ctypes.c_size_t()
-    assert lib.sps_beam_workspace_size(8, 100, 4, ctypes.byref(n)) == 0 and n.value == 8 * 4 * 8
+    assert lib.sps_beam_workspace_size(8, 100, 2, 4, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.sps_beam_workspace_size(8, 8192, 4, 4, ctypes.byref(n)) == 0 and n.value == 8 * 4 * 8
     for beams in (0, -1, 3):
+        assert lib.sps_beam_workspace_size(8, 100, beams, 4, ctypes.byref(n)) == INV
         assert lib.sps_beam_select(view(), None, beams, 4, P, P, P, P, n.value, None) == INV
         assert lib.sps_beam_join(P, P, 8, 4, beams, 4, P, P, P, None) == INV
     assert lib.sps_beam_select(view(), None, 2, 4, None, P, P, P, n.value, None) == INV
-    assert lib.sps_beam_select(view(), None, 2, 4, P, P, P, None, 0, None) == INV
-    assert lib.sps_beam_select(view(), None, 2, 4, P, P, P, P, n.value - 1, None) == WS
+    assert lib.sps_beam_select(view(), None, 2, 4, P, None, P, P, 0, None) == INV
+    assert lib.sps_beam_select(view(), None, 2, 4, P, P, None, P, 0, None) == INV
+    big = dict(cols=8192, ld=8192)
+    assert lib.sps_beam_select(view(**big), None, 4, 4, P, P, P, P, 8 * 4 * 8 - 1, None) == WS
+    assert lib.sps_beam_select(view(**big), None, 4, 4, P, P, P, None, 8 * 4 * 8, None) == INV
     assert lib.sps_beam_join(None, P, 8, 4, 2, 4, P, P, P, None) == INV
     assert lib.sps_beam_join(P, P, -8, 4, 2, 4, P, P, P, None) == INV
     assert lib.sps_beam_join(P, P, 2**31, 4, 2, 4, P, P, P, None) == OVF
@@ -79,7 +84,7 @@ def test_beam_refusals(lib):
 
 
 def state(src=P, dst=2 * P, row=64, ss=64, ds=64):
-    return sps._State(src, dst, row, ss, ds)
+    return (ctypes.c_int64 * 5)(src or 0, dst or 0, row, ss, ds)
 
 
 @pytest.mark.parametrize("st,want", [
@@ -102,7 +107,7 @@ def test_reorder_counts(lib):
     assert lib.sps_reorder_states(ctypes.byref(st), 0, P, 8, 8, None) == 0
     assert lib.sps_reorder_states(ctypes.byref(st), 1, P, 0, 8, None) == 0
     # an output that overlaps another state's source
-    two = (sps._State * 2)(state(), state(src=8 * P, dst=P + 64))
+    two = (ctypes.c_int64 * 10)(*state(), *state(src=8 * P, dst=P + 64))
     assert lib.sps_reorder_states(two, 2, P, 8, 8, None) == INV
 
 
