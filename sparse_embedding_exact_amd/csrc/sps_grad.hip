@@ -171,11 +171,14 @@ __global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_
 // up to 2^22): unit values and the first histogram, scatter, histogram,
 // scatter, walk.
 //
-// The walk keeps up to 8192 values of G in LDS (one row of 8192 items, or R
-// rows of 8192 / R) and gives each entry of its rows a lane: the lane finds
+// The walk keeps four rows of G over 4096 columns in LDS, the four values of a
+// column side by side, and gives each entry of its rows a lane: the lane finds
 // the entry's list by bisection. Lists of up to 4 entries are the lane's own,
-// of up to 128 a group of 16 lanes', longer ones the wave's, 512 entries in
-// flight. The norm's part is taken off at the end of the same launch.
+// of up to 128 a group of 16 lanes'. A longer one is a wave's, 512 entries in
+// flight, and serves every row of the four that holds the dim: such dims are
+// the ones that most rows share, one load of an entry and one 16-byte read of
+// LDS then make four products. The norm's part is taken off at the end of the
+// same launch.
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 512;
@@ -185,8 +188,11 @@ constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortMinEntries = 8192;  // of a workgroup, at least
 constexpr int kSortBlocks = 120;       // about: every scatter block adds all histograms itself
 constexpr int kSortAhead = 16;         // entries of a lane in flight
-constexpr int kTile = 8192;            // values of G in LDS
-constexpr int kBatch = 512;            // entries walked at a time
+constexpr int kWalkThreads = 512;
+constexpr int kWalkWaves = kWalkThreads / 64;
+constexpr int kWalkRows = 4;           // rows of G side by side in LDS
+constexpr int kWalkCols = 4096;        // and their columns: 64 KB, two workgroups a CU
+constexpr int kBatch = kWalkThreads;   // entries walked at a time, one a thread
 constexpr int kSamples = 2048;         // keys of the other side in LDS for the bisections
 constexpr int kLaneList = 4, kGroupList = 128;
 
@@ -197,7 +203,7 @@ struct BothSide {
   int64_t n_rows, nnz;
   int64_t base;       // of its entries in the joint arrays
   int32_t block0, blocks;  // of the sort
-  int32_t rows, cols; // rows of a workgroup, columns of its tile
+  int32_t rows;       // of a workgroup, at most kWalkRows
   int64_t groups;
 };
 
@@ -396,16 +402,51 @@ __device__ __forceinline__ float wave_total(float x) {
 }
 
 struct BothShared {
-  float tile[kTile];  // indexes are masked: in range whatever a CSR holds
+  float4 tile[kWalkCols];  // indexes are masked: in range whatever a CSR holds
   int32_t lo[kBatch], hi[kBatch];
   float acc[kBatch];
-  uint16_t row[kBatch];
+  int32_t begin[kWalkRows + 1];  // of the rows' entries in the batch
 };
+static_assert(kWalkRows == 4, "the rows of G are a float4");
 
-// `load` entries [i, i + 2) with the second masked: 16 bytes, 8-byte aligned
+// two entries, 8-byte aligned
 struct __attribute__((packed, aligned(8))) Pair {
   uint2 a, b;
 };
+
+// Up to 128 N entries of a list from q on (this lane: q, q + 1, and every 128
+// further), times the four rows' values of their columns; none at or past h.
+template <int N, bool WHOLE>
+__device__ __forceinline__ void four_rows(const uint2 *load, int32_t q, int32_t h, uint32_t c0,
+                                          const float4 *tile, float4 &s) {
+  Pair v[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (WHOLE) {
+      v[k] = *reinterpret_cast<const Pair *>(load + q + k * 128);
+    } else {
+      const int32_t j = q + k * 128;
+      v[k].a = load[j < h ? j : h - 1];
+      v[k].b = load[j + 1 < h ? j + 1 : h - 1];
+      if (j >= h) v[k].a.y = 0;
+      if (j + 1 >= h) v[k].b.y = 0;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float4 ga = tile[(v[k].a.x - c0) & (kWalkCols - 1)];
+    const float4 gb = tile[(v[k].b.x - c0) & (kWalkCols - 1)];
+    const float wa = __builtin_bit_cast(float, v[k].a.y), wb = __builtin_bit_cast(float, v[k].b.y);
+    s.x += ga.x * wa;
+    s.y += ga.y * wa;
+    s.z += ga.z * wa;
+    s.w += ga.w * wa;
+    s.x += gb.x * wb;
+    s.y += gb.y * wb;
+    s.z += gb.z * wb;
+    s.w += gb.w * wb;
+  }
+}
 
 template <typename T, bool TRANSPOSED>
 __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group, BothShared &sh) {
@@ -417,6 +458,7 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
   const int32_t *key = a.key[a.last];
   const uint2 *load = a.load[a.last];
   const T *g = static_cast<const T *>(a.grad);
+  const float *tile1 = reinterpret_cast<const float *>(sh.tile);
   for (int64_t eb = e0; eb < e1; eb += kBatch) {
     const int ne = e1 - eb < kBatch ? (int)(e1 - eb) : kBatch;
     __syncthreads();  // the batch before is done with
@@ -426,195 +468,209 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
     const int32_t step = (on + kSamples - 1) / kSamples;
     const int samples = step > 0 ? (on + step - 1) / step : 0;
     uint32_t *top = reinterpret_cast<uint32_t *>(sh.tile);
-    for (int i = t; i < samples; i += kGradThreads) top[i] = (uint32_t)key[o0 + (int64_t)i * step];
+    for (int i = t; i < samples; i += kWalkThreads) top[i] = (uint32_t)key[o0 + (int64_t)i * step];
+    if (t <= nr) {
+      const int64_t b = clamp64(s.indptr[r0 + t], e0, e1) - eb;
+      sh.begin[t] = (int32_t)clamp64(b, 0, ne);
+    }
     __syncthreads();
-    // entry i belongs to thread (i % 4) * 64 + i / 4 % 64: every wave gets some of a short row
-    for (int i = lane * 4 + w; i < ne; i += kGradThreads) {
+    // entry i is thread (i % 8) * 64 + i / 8's: every wave gets some of a short row
+    const int i = lane * kWalkWaves + w;
+    int32_t l = 0, h = 0, row = 0;
+    if (i < ne) {
       const uint32_t d = (uint32_t)s.indices[eb + i];
       // first key >= d and first key > d, side by side; sample j is key j * step
-      int32_t l0 = 0, l1 = samples, h0 = 0, h1 = samples;
-      while (l0 < l1 || h0 < h1) {
-        const int32_t ml = (l0 + l1) >> 1, mh = (h0 + h1) >> 1;
-        if (l0 < l1) {
-          if (top[ml] < d) l0 = ml + 1;
+      int32_t l1 = samples, h1 = samples;
+      while (l < l1 || h < h1) {
+        const int32_t ml = (l + l1) >> 1, mh = (h + h1) >> 1;
+        if (l < l1) {
+          if (top[ml] < d) l = ml + 1;
           else l1 = ml;
         }
-        if (h0 < h1) {
-          if (top[mh] <= d) h0 = mh + 1;
+        if (h < h1) {
+          if (top[mh] <= d) h = mh + 1;
           else h1 = mh;
         }
       }
       // behind the last sample below, up to the sample found
-      l1 = l0 < samples ? l0 * step : on;
-      h1 = h0 < samples ? h0 * step : on;
-      l0 = l0 > 0 ? (l0 - 1) * step + 1 : 0;
-      h0 = h0 > 0 ? (h0 - 1) * step + 1 : 0;
-      l0 += o0;
-      l1 += o0;
-      h0 += o0;
-      h1 += o0;
-      while (l0 < l1 || h0 < h1) {
-        const int32_t ml = l0 + ((l1 - l0) >> 1), mh = h0 + ((h1 - h0) >> 1);
-        const uint32_t kl = l0 < l1 ? (uint32_t)key[ml] : 0u, kh = h0 < h1 ? (uint32_t)key[mh] : 0u;
-        if (l0 < l1) {
-          if (kl < d) l0 = ml + 1;
+      l1 = o0 + (l < samples ? l * step : on);
+      h1 = o0 + (h < samples ? h * step : on);
+      l = o0 + (l > 0 ? (l - 1) * step + 1 : 0);
+      h = o0 + (h > 0 ? (h - 1) * step + 1 : 0);
+      while (l < l1 || h < h1) {
+        const int32_t ml = l + ((l1 - l) >> 1), mh = h + ((h1 - h) >> 1);
+        const uint32_t kl = l < l1 ? (uint32_t)key[ml] : 0u, kh = h < h1 ? (uint32_t)key[mh] : 0u;
+        if (l < l1) {
+          if (kl < d) l = ml + 1;
           else l1 = ml;
         }
-        if (h0 < h1) {
-          if (kh <= d) h0 = mh + 1;
+        if (h < h1) {
+          if (kh <= d) h = mh + 1;
           else h1 = mh;
         }
       }
-      sh.lo[i] = l0;
-      sh.hi[i] = h0;
+      sh.lo[i] = l;
+      sh.hi[i] = h;
       sh.acc[i] = 0;
-      const int64_t r = (int64_t)a.row[s.base + eb + i] - r0;
-      sh.row[i] = (uint16_t)(r >= 0 && r < nr ? r : 0);
-    }
-    for (int64_t c0 = 0; c0 < o.n_rows; c0 += s.cols) {
-      const int nc = o.n_rows - c0 < s.cols ? (int)(o.n_rows - c0) : s.cols;
-      __syncthreads();
-      if (!TRANSPOSED) {
-        constexpr int V = kVec<T>;
-        for (int r = 0; r < nr; ++r) {
-          const T *p = g + (r0 + r) * a.ld + c0;
-          float *q = sh.tile + r * s.cols;
-          for (int j = t * V; j < nc; j += kGradThreads * V) {
-            if (j + V <= nc) {
-              const Vec<T> v = *reinterpret_cast<const Vec<T> *>(p + j);
-#pragma unroll
-              for (int e = 0; e < V; ++e) q[j + e] = to_f32(v.e[e]);
-            } else {
-              for (int e = 0; j + e < nc; ++e) q[j + e] = to_f32(p[j + e]);
-            }
-          }
-        }
-      } else {
-        const int r = t % s.rows, step = kGradThreads / s.rows;
-        if (r < nr)
-          for (int j = t / s.rows; j < nc; j += step)
-            sh.tile[r * s.cols + j] = to_f32(g[(c0 + j) * a.ld + r0 + r]);
-      }
-      __syncthreads();
-      const bool whole = nc == o.n_rows;
-      for (int i0 = 0; i0 < ne; i0 += kGradThreads) {
-        const int i = i0 + lane * 4 + w;
-        int32_t l = 0, h = 0;
-        int at = 0;
-        if (i < ne) {
-          l = sh.lo[i];
-          h = sh.hi[i];
-          at = (int)sh.row[i] * s.cols;
-          if (!whole && h - l > kLaneList) {
-            // the list's part in this tile starts where the last tile's ended
-            int32_t m0 = l, m1 = h;
-            while (m0 < m1) {
-              const int32_t m = m0 + ((m1 - m0) >> 1);
-              if ((int64_t)load[m].x < c0 + nc) m0 = m + 1;
-              else m1 = m;
-            }
-            h = m0;
-            sh.lo[i] = h;
-          }
-        }
-        float acc = 0;
-        const int n = h - l;
-        if (n > 0 && n <= kLaneList) {
-          uint2 v[kLaneList];
-#pragma unroll
-          for (int j = 0; j < kLaneList; ++j) v[j] = load[l + (j < n ? j : 0)];
-#pragma unroll
-          for (int j = 0; j < kLaneList; ++j) {
-            const uint32_t c = v[j].x - (uint32_t)c0;  // may lie in another tile
-            const float x = sh.tile[(at + c) & (kTile - 1)];
-            acc += j < n && c < (uint32_t)nc ? x * __builtin_bit_cast(float, v[j].y) : 0.0f;
-          }
-        }
-        if (i < ne) sh.acc[i] += acc;
-        __builtin_amdgcn_wave_barrier();  // other lanes add to it below
-        // four lists at a time, 16 lanes each
-        uint64_t mid = __ballot(n > kLaneList && n <= kGroupList);
-        while (mid) {
-          int src = -1, q = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int f = mid ? __builtin_ctzll(mid) : -1;
-            if (k == lane >> 4) src = f;
-            mid &= mid ? mid - 1 : 0;
-          }
-          const int from = src < 0 ? 0 : src;
-          // every lane shuffles: a source lane must be active
-          const int32_t l2 = __shfl(l, from, 64), n1 = __shfl(n, from, 64);
-          const uint32_t base2 = (uint32_t)(__shfl(at, from, 64) - (int)c0);
-          const int32_t n2 = src < 0 ? 0 : n1;
-          float part = 0;
-          for (q = lane & 15; q < n2; q += 64) {
-            uint2 v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = load[l2 + (q + 16 * k < n2 ? q + 16 * k : q)];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float x = sh.tile[(base2 + v[k].x) & (kTile - 1)];
-              part += q + 16 * k < n2 ? x * __builtin_bit_cast(float, v[k].y) : 0.0f;
-            }
-          }
-          part = row16_total(part);
-          if ((lane & 15) == 15 && src >= 0) sh.acc[i0 + src * 4 + w] += part;
-        }
-        // the whole wave's
-        uint64_t big = __ballot(n > kGroupList);
-        while (big) {
-          const int f = __builtin_ctzll(big);
-          big &= big - 1;
-          const int32_t l2 = __builtin_amdgcn_readlane(l, f), h2 = __builtin_amdgcn_readlane(h, f);
-          const uint32_t base2 = (uint32_t)(__builtin_amdgcn_readlane(at, f) - (int)c0);
-          float p0 = 0, p1 = 0;
-          int32_t q = l2 + lane * 2;
-          for (; q - lane * 2 + 512 <= h2; q += 512) {
-            Pair v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = *reinterpret_cast<const Pair *>(load + q + k * 128);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              p0 += sh.tile[(base2 + v[k].a.x) & (kTile - 1)] * __builtin_bit_cast(float, v[k].a.y);
-              p1 += sh.tile[(base2 + v[k].b.x) & (kTile - 1)] * __builtin_bit_cast(float, v[k].b.y);
-            }
-          }
-          if (q - lane * 2 < h2) {  // the last 512, in part
-            uint2 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int32_t j = q + (k >> 1) * 128 + (k & 1);
-              v[k] = load[j < h2 ? j : l2];
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int32_t j = q + (k >> 1) * 128 + (k & 1);
-              const float x = sh.tile[(base2 + v[k].x) & (kTile - 1)];
-              p0 += j < h2 ? x * __builtin_bit_cast(float, v[k].y) : 0.0f;
-            }
-          }
-          const float part = wave_total(p0 + p1);
-          if (lane == 63) sh.acc[i0 + f * 4 + w] += part;
-        }
-      }
+      for (int r = 1; r < nr; ++r) row += i >= sh.begin[r];
     }
     __syncthreads();
-    for (int i = t; i < ne; i += kGradThreads) s.dv[eb + i] = sh.acc[i];
+    // a long list: the first row that has it walks it, for the others too. A row's entries have
+    // ascending dims, so their lists' starts ascend; the last start at or before l is the dim's
+    // own if the row has it (absent dims before it may share the start).
+    uint32_t mate01 = ~0u, mate23 = ~0u;  // each row's entry, 16 bits each, all ones for none
+    bool leads = false;
+    if (i < ne && h - l > kGroupList) {
+      leads = true;
+#pragma unroll
+      for (int r = 0; r < kWalkRows; ++r) {
+        uint32_t m = 0xFFFFu;
+        if (r < nr) {
+          int32_t x0 = sh.begin[r], x1 = sh.begin[r + 1];
+          while (x0 < x1) {
+            const int32_t x = (x0 + x1) >> 1;
+            if (sh.lo[x] <= l) x0 = x + 1;
+            else x1 = x;
+          }
+          if (x0 > sh.begin[r] && sh.lo[x0 - 1] == l && sh.hi[x0 - 1] == h) {
+            m = (uint32_t)(x0 - 1);
+            if (r < row) leads = false;
+          }
+        }
+        if (r < 2) mate01 = (mate01 & ~(0xFFFFu << (r * 16))) | m << (r * 16);
+        else mate23 = (mate23 & ~(0xFFFFu << (r * 16 - 32))) | m << (r * 16 - 32);
+      }
+      if (!leads) h = l;
+    }
+    for (int64_t c0 = 0; c0 < o.n_rows; c0 += kWalkCols) {
+      const int nc = o.n_rows - c0 < kWalkCols ? (int)(o.n_rows - c0) : kWalkCols;
+      __syncthreads();
+#pragma unroll 4
+      for (int c = t; c < nc; c += kWalkThreads) {
+        float v[kWalkRows];
+        if (!TRANSPOSED) {
+          const T *p = g + r0 * a.ld + c0 + c;
+#pragma unroll
+          for (int r = 0; r < kWalkRows; ++r) v[r] = r < nr ? to_f32(p[r * a.ld]) : 0.0f;
+        } else {
+          const T *p = g + (c0 + c) * a.ld + r0;
+          if (nr == kWalkRows) {
+            struct __attribute__((packed, aligned(sizeof(T)))) Four {
+              T e[kWalkRows];
+            };
+            const Four q = *reinterpret_cast<const Four *>(p);
+#pragma unroll
+            for (int r = 0; r < kWalkRows; ++r) v[r] = to_f32(q.e[r]);
+          } else {
+#pragma unroll
+            for (int r = 0; r < kWalkRows; ++r) v[r] = r < nr ? to_f32(p[r]) : 0.0f;
+          }
+        }
+        sh.tile[c] = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      __syncthreads();
+      // the list's part in this tile starts where the last tile's ended
+      const bool cut = nc < o.n_rows && h - l > kLaneList;
+      int32_t next = h;
+      if (cut) {
+        int32_t m0 = l, m1 = h;
+        while (m0 < m1) {
+          const int32_t m = m0 + ((m1 - m0) >> 1);
+          if ((int64_t)load[m].x < c0 + nc) m0 = m + 1;
+          else m1 = m;
+        }
+        next = m0;
+      }
+      const int n = next - l;
+      float acc = 0;
+      if (!leads && n > 0 && n <= kLaneList) {
+        uint2 v[kLaneList];
+#pragma unroll
+        for (int j = 0; j < kLaneList; ++j) v[j] = load[l + (j < n ? j : 0)];
+#pragma unroll
+        for (int j = 0; j < kLaneList; ++j) {
+          const uint32_t c = v[j].x - (uint32_t)c0;  // may lie in another tile
+          const float x = tile1[(c & (kWalkCols - 1)) * kWalkRows + row];
+          acc += j < n && c < (uint32_t)nc ? x * __builtin_bit_cast(float, v[j].y) : 0.0f;
+        }
+        sh.acc[i] += acc;
+      }
+      // four lists at a time, 16 lanes each
+      uint64_t mid = __ballot(!leads && n > kLaneList);
+      while (mid) {
+        int src = -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int f = mid ? __builtin_ctzll(mid) : -1;
+          if (k == lane >> 4) src = f;
+          mid &= mid ? mid - 1 : 0;
+        }
+        const int from = src < 0 ? 0 : src;
+        // every lane shuffles: a source lane must be active
+        const int32_t l2 = __shfl(l, from, 64), n1 = __shfl(n, from, 64);
+        const int row2 = __shfl(row, from, 64);
+        const int32_t n2 = src < 0 ? 0 : n1;
+        float part = 0;
+        for (int q = lane & 15; q < n2; q += 64) {
+          uint2 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = load[l2 + (q + 16 * k < n2 ? q + 16 * k : q)];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x =
+                tile1[((v[k].x - (uint32_t)c0) & (kWalkCols - 1)) * kWalkRows + row2];
+            part += q + 16 * k < n2 ? x * __builtin_bit_cast(float, v[k].y) : 0.0f;
+          }
+        }
+        part = row16_total(part);
+        if ((lane & 15) == 15 && src >= 0) sh.acc[src * kWalkWaves + w] += part;
+      }
+      // the whole wave's, for up to four rows
+      uint64_t big = __ballot(leads && n > 0);
+      while (big) {
+        const int f = __builtin_ctzll(big);
+        big &= big - 1;
+        const int32_t l2 = __builtin_amdgcn_readlane(l, f), h2 = __builtin_amdgcn_readlane(next, f);
+        const uint32_t m01 = (uint32_t)__builtin_amdgcn_readlane((int)mate01, f);
+        const uint32_t m23 = (uint32_t)__builtin_amdgcn_readlane((int)mate23, f);
+        float4 p = make_float4(0, 0, 0, 0);
+        int32_t q = l2;
+        for (; q + 512 <= h2; q += 512)
+          four_rows<4, true>(load, q + lane * 2, h2, (uint32_t)c0, sh.tile, p);
+        if (h2 - q > 256) four_rows<4, false>(load, q + lane * 2, h2, (uint32_t)c0, sh.tile, p);
+        else if (h2 - q > 128) four_rows<2, false>(load, q + lane * 2, h2, (uint32_t)c0, sh.tile, p);
+        else if (h2 > q) four_rows<1, false>(load, q + lane * 2, h2, (uint32_t)c0, sh.tile, p);
+        p.x = wave_total(p.x);
+        p.y = wave_total(p.y);
+        p.z = wave_total(p.z);
+        p.w = wave_total(p.w);
+        if (lane == 63) {
+          const uint32_t m[kWalkRows] = {m01 & 0xFFFFu, m01 >> 16, m23 & 0xFFFFu, m23 >> 16};
+          const float x[kWalkRows] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+          for (int r = 0; r < kWalkRows; ++r)
+            if (m[r] != 0xFFFFu) sh.acc[m[r]] += x[r];
+        }
+      }
+      if (cut) l = next;
+    }
+    __syncthreads();
+    if (i < ne) s.dv[eb + i] = sh.acc[i];
   }
   __syncthreads();
-  for (int r = w; r < nr; r += kGradThreads / 64) {
+  for (int r = w; r < nr; r += kWalkWaves) {
     const int64_t b0 = clamp64(s.indptr[r0 + r], 0, s.nnz), b1 = clamp64(s.indptr[r0 + r + 1], b0, s.nnz);
     through_norm(s.values, s.dv, s.dv, b0, b1, lane);
   }
 }
 
+// Each XCD takes a run of the queries' groups, then one of the items'.
 template <typename T>
-__global__ __launch_bounds__(kGradThreads) void both_walk_kernel(BothArgs a) {
+__global__ __launch_bounds__(kWalkThreads) void both_walk_kernel(BothArgs a) {
   __shared__ BothShared sh;
-  const int64_t id = xcd_tile(blockIdx.x, gridDim.x);
-  if (id < a.s[0].groups) walk<T, false>(a, 0, id, sh);
-  else walk<T, true>(a, 1, id - a.s[0].groups, sh);
+  const int64_t b = blockIdx.x, first = (a.s[0].groups + 7) / 8 * 8;
+  if (b < a.s[0].groups) walk<T, false>(a, 0, xcd_tile(b, a.s[0].groups), sh);
+  else if (b >= first) walk<T, true>(a, 1, xcd_tile(b - first, a.s[1].groups), sh);
 }
 
 }  // namespace sps
@@ -663,15 +719,8 @@ BothLayout both_layout(int64_t n) {
   return L;
 }
 
-// Rows of a workgroup of the walk. Along rows of G: as many as fit the tile,
-// while there are rows for 1024 workgroups. Across them (the items' side):
-// 16 bytes of a row of G at a time, more where the queries are few.
-int32_t walk_rows(int64_t n_rows, int64_t n_cols, bool transposed, int32_t size) {
-  int32_t r = transposed ? 16 / size : 1;
-  const int32_t most = transposed ? 16 : 8;
-  while (r < most && sps::kTile / (2 * r) >= n_cols && n_rows / (2 * r) >= 1024) r *= 2;
-  return r;
-}
+// Rows of a workgroup of the walk: four, while that leaves 512 workgroups.
+int32_t walk_rows(int64_t n_rows) { return n_rows >= 2048 ? 4 : n_rows >= 1024 ? 2 : 1; }
 
 }  // namespace
 
@@ -843,10 +892,9 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
     s.block0 = blocks;
     s.blocks = (int32_t)((s.nnz + a.per_block - 1) / a.per_block);
     blocks += s.blocks;
-    s.rows = walk_rows(s.n_rows, m[1 - i]->n_rows, i == 1, sps::dtype_size(grad->dtype));
-    s.cols = sps::kTile / s.rows;
+    s.rows = walk_rows(s.n_rows);
     s.groups = (s.n_rows + s.rows - 1) / s.rows;
-    groups += s.groups;
+    groups = (groups + 7) / 8 * 8 + s.groups;
   }
   const int64_t rows = queries->n_rows + items->n_rows;
   const int64_t unit_blocks = blocks + (rows + sps::kSortWaves - 1) / sps::kSortWaves;
@@ -860,7 +908,7 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
       hipLaunchKernelGGL(sps::both_hist_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
     hipLaunchKernelGGL(sps::both_scatter_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
   }
-  const dim3 grid((uint32_t)groups), block(sps::kGradThreads);
+  const dim3 grid((uint32_t)groups), block(sps::kWalkThreads);
   if (grad->dtype == SPS_F32)
     hipLaunchKernelGGL((sps::both_walk_kernel<float>), grid, block, 0, s, a);
   else if (grad->dtype == SPS_F16)

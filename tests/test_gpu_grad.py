@@ -126,6 +126,31 @@ def test_shared_dims_and_long_rows(env):
     close(by_chunks(env, ic, qc, g, True, 30), *want_i)
 
 
+@pytest.mark.parametrize("nq,ni", [(1030, 9000), (2050, 4100), (5000, 300)])
+def test_lists_over_several_tiles(env, nq, ni):
+    """Rows of a workgroup that share some long lists, not others, over several tiles of
+    columns; a dim held only by items of the first columns."""
+    torch, sps, dev = env
+    r = np.random.RandomState(nq)
+
+    def some(n, first):
+        rows = []
+        for i in range(n):
+            d = np.nonzero(r.rand(40) < np.linspace(0.95, 0.02, 40))[0]
+            if i % 7 == 3:
+                d = d[d > 4]
+            rows.append(np.concatenate([d, [40] if i < first else [], [41 + i % 50]]).astype(np.int32))
+        ptr = np.concatenate([[0], np.cumsum([len(x) for x in rows])]).astype(np.int32)
+        ix = np.concatenate(rows)
+        return synth.HostCSR(ptr, ix, r.randn(len(ix)).astype(np.float32), n, 91)
+    q, it = some(nq, nq), some(ni, 200)
+    g = torch.from_numpy(r.randn(nq, ni).astype(np.float32)).to(dev)
+    gq, gi = sps.cosine_grad(sps.CSR.from_host(q, dev), sps.CSR.from_host(it, dev), g)
+    g64 = g.double().cpu().numpy()
+    close(gq, *oracle(q, it, g64, ni // 256 + 4))
+    close(gi, *oracle(it, q, g64.T, nq // 256 + 4))
+
+
 def test_rows_of_many_entries(env):
     """Rows of more entries than are walked at a time, over more columns than a tile, dims up
     to the largest key."""
