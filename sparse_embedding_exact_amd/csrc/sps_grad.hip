@@ -185,7 +185,7 @@ constexpr int kSortThreads = 512;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxBits = 11;
 constexpr int kMaxBins = 1 << kMaxBits;
-constexpr int kSortMinEntries = 8192;  // of a workgroup, at least
+constexpr int kSortMinEntries = 2048;  // of a workgroup, at least
 constexpr int kSortBlocks = 120;       // about: every scatter block adds all histograms itself
 constexpr int kSortAhead = 16;         // entries of a lane in flight
 constexpr int kWalkThreads = 512;
@@ -203,7 +203,6 @@ struct BothSide {
   int64_t n_rows, nnz;
   int64_t base;       // of its entries in the joint arrays
   int32_t block0, blocks;  // of the sort
-  int32_t rows;       // of a workgroup, at most kWalkRows
   int64_t groups;
 };
 
@@ -452,8 +451,8 @@ template <typename T, bool TRANSPOSED>
 __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group, BothShared &sh) {
   const BothSide &s = a.s[side], &o = a.s[1 - side];
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-  const int64_t r0 = group * s.rows;
-  const int nr = s.n_rows - r0 < s.rows ? (int)(s.n_rows - r0) : s.rows;
+  const int64_t r0 = group * kWalkRows;
+  const int nr = s.n_rows - r0 < kWalkRows ? (int)(s.n_rows - r0) : kWalkRows;
   const int64_t e0 = clamp64(s.indptr[r0], 0, s.nnz), e1 = clamp64(s.indptr[r0 + nr], e0, s.nnz);
   const int32_t *key = a.key[a.last];
   const uint2 *load = a.load[a.last];
@@ -719,9 +718,6 @@ BothLayout both_layout(int64_t n) {
   return L;
 }
 
-// Rows of a workgroup of the walk: four, while that leaves 512 workgroups.
-int32_t walk_rows(int64_t n_rows) { return n_rows >= 2048 ? 4 : n_rows >= 1024 ? 2 : 1; }
-
 }  // namespace
 
 extern "C" {
@@ -892,8 +888,7 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
     s.block0 = blocks;
     s.blocks = (int32_t)((s.nnz + a.per_block - 1) / a.per_block);
     blocks += s.blocks;
-    s.rows = walk_rows(s.n_rows);
-    s.groups = (s.n_rows + s.rows - 1) / s.rows;
+    s.groups = (s.n_rows + sps::kWalkRows - 1) / sps::kWalkRows;
     groups = (groups + 7) / 8 * 8 + s.groups;
   }
   const int64_t rows = queries->n_rows + items->n_rows;
