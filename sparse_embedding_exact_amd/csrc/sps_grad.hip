@@ -186,7 +186,7 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kMaxBits = 11;
 constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kSortMinEntries = 2048;  // of a workgroup, at least
-constexpr int kSortBlocks = 120;       // about: every scatter block adds all histograms itself
+constexpr int kSortBlocks = 250;       // about: one a CU
 constexpr int kSortAhead = 16;         // entries of a lane in flight
 constexpr int kWalkThreads = 512;
 constexpr int kWalkWaves = kWalkThreads / 64;
@@ -213,6 +213,7 @@ struct BothArgs {
   int32_t *key[2];
   uint2 *load[2]; // (row, bits of the unit value)
   int32_t *hist;  // [sort blocks][bins]
+  int32_t *total; // [sides][kMaxBins]
   int64_t per_block;
   int32_t pass, passes, bits, last;  // `last`: which of the buffers holds the lists
   const void *grad;
@@ -290,6 +291,41 @@ __global__ __launch_bounds__(kSortThreads) void both_hist_kernel(BothArgs a) {
   histogram(a, blockIdx.x, cnt);
 }
 
+// Per side and digit: the blocks' counts become the counts of the blocks
+// before them, and their sum goes to `total`. A workgroup takes 64 digits, a
+// quarter of the blocks each wave. (Every scatter block adding up all
+// histograms by itself took 14 of its 26 us at 440,000 entries: the counts
+// have just been written by other XCDs.)
+__global__ __launch_bounds__(256) void both_prefix_kernel(BothArgs a) {
+  __shared__ int32_t part[4][64];
+  const int bins = 1 << a.bits, lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int per_side = (bins + 63) / 64;
+  const int side = (int)blockIdx.x / per_side;
+  const int d = (int)blockIdx.x % per_side * 64 + lane;
+  const BothSide &s = a.s[side];
+  const int each = (s.blocks + 3) / 4, j0 = q * each,
+            j1 = j0 + each < s.blocks ? j0 + each : s.blocks;
+  int32_t *h = a.hist + (int64_t)s.block0 * bins + (d < bins ? d : 0);
+  int32_t sum = 0;
+#pragma unroll 8
+  for (int j = j0; j < j1; ++j) sum += h[(int64_t)j * bins];
+  part[q][lane] = sum;
+  __syncthreads();
+  int32_t at = 0, total = 0;
+  for (int i = 0; i < 4; ++i) {
+    if (i < q) at += part[i][lane];
+    total += part[i][lane];
+  }
+  if (d >= bins) return;
+#pragma unroll 8
+  for (int j = j0; j < j1; ++j) {
+    const int32_t c = h[(int64_t)j * bins];
+    h[(int64_t)j * bins] = at;
+    at += c;
+  }
+  if (q == 0) a.total[side * kMaxBins + d] = total;
+}
+
 // Stable: a block's entries are cut among its waves in order, a wave takes 64
 // at a time, and equal digits among them are ranked by lane.
 __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) {
@@ -315,17 +351,12 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
   __syncthreads();
   // thread t places digits 4 t .. 4 t + 3
   int32_t total[4] = {}, before[4] = {};
-  if (4 * t < bins)
-#pragma unroll 8
-    for (int j = 0; j < s.blocks; ++j) {
-      const int4 h = *reinterpret_cast<const int4 *>(a.hist + (int64_t)(s.block0 + j) * bins + 4 * t);
-      const int32_t v[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        total[i] += v[i];
-        if (j < b - s.block0) before[i] += v[i];
-      }
-    }
+  if (4 * t < bins) {
+    const int4 v = *reinterpret_cast<const int4 *>(a.total + side * kMaxBins + 4 * t);
+    const int4 h = *reinterpret_cast<const int4 *>(a.hist + (int64_t)b * bins + 4 * t);
+    total[0] = v.x, total[1] = v.y, total[2] = v.z, total[3] = v.w;
+    before[0] = h.x, before[1] = h.y, before[2] = h.z, before[3] = h.w;
+  }
   int32_t all;
   const int32_t sum = total[0] + total[1] + total[2] + total[3];
   int32_t at = block_incl_scan<kSortThreads, int32_t>(sum, ws, &all) - sum + (int32_t)s.base;
@@ -692,7 +723,7 @@ sps_status check_csr(const sps_csr *m, const char *what) {
 }
 
 struct BothLayout {
-  size_t unit, row, key[2], load[2], hist, total;
+  size_t unit, row, key[2], load[2], sums, hist, total;
   int64_t per_block;
 };
 BothLayout both_layout(int64_t n) {
@@ -711,6 +742,8 @@ BothLayout both_layout(int64_t n) {
   }
   L.per_block = (n + sps::kSortBlocks - 1) / sps::kSortBlocks;
   if (L.per_block < sps::kSortMinEntries) L.per_block = sps::kSortMinEntries;
+  L.sums = at;
+  at = up(at + 2 * sps::kMaxBins * 4);
   L.hist = at;
   // one block more on each side than full blocks of the whole
   at = up(at + ((size_t)(n / L.per_block) + 2) * sps::kMaxBins * 4);
@@ -862,6 +895,7 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
     a.load[i] = reinterpret_cast<uint2 *>(b + L.load[i]);
   }
   a.hist = reinterpret_cast<int32_t *>(b + L.hist);
+  a.total = reinterpret_cast<int32_t *>(b + L.sums);
   a.per_block = L.per_block;
   int bits = 1;
   while (bits < 31 && (queries->n_cols - 1) >> bits) ++bits;
@@ -901,6 +935,8 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
   for (a.pass = 0; a.pass < a.passes; ++a.pass) {
     if (a.pass > 0)
       hipLaunchKernelGGL(sps::both_hist_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
+    hipLaunchKernelGGL(sps::both_prefix_kernel, dim3(2u * (uint32_t)(((1 << a.bits) + 63) / 64)),
+                       dim3(256), 0, s, a);
     hipLaunchKernelGGL(sps::both_scatter_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
   }
   const dim3 grid((uint32_t)groups), block(sps::kWalkThreads);
