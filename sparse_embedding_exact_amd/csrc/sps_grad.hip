@@ -167,13 +167,13 @@ __global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_
 // and unit value as the load), not taken from a prepared corpus: a training
 // step has new values every time, its batches are small, and a corpus'
 // per-slice sorts and dim index would keep 8 to 16 workgroups busy for longer
-// than all that follows. Five launches (two passes of up to 11 bits for dims
-// up to 2^22): unit values and the first histogram, scatter, histogram,
-// scatter, walk.
+// than all that follows. Unit values; a histogram, its prefix and a scatter a
+// pass of up to 11 bits (two for dims up to 2^22); the table of the lists; the
+// walk: eight launches.
 //
 // The walk keeps four rows of G over 4096 columns in LDS, the four values of a
-// column side by side, and gives each entry of its rows a lane: the lane finds
-// the entry's list by bisection. Lists of up to 4 entries are the lane's own,
+// column side by side, and gives each entry of its rows a lane, which looks the
+// entry's list up. Lists of up to 4 entries are the lane's own,
 // of up to 128 a group of 16 lanes'. A longer one is a wave's, 512 entries in
 // flight, and serves every row of the four that holds the dim: such dims are
 // the ones that most rows share, one load of an entry and one 16-byte read of
@@ -193,7 +193,7 @@ constexpr int kWalkWaves = kWalkThreads / 64;
 constexpr int kWalkRows = 4;           // rows of G side by side in LDS
 constexpr int kWalkCols = 4096;        // and their columns: 64 KB, two workgroups a CU
 constexpr int kBatch = kWalkThreads;   // entries walked at a time, one a thread
-constexpr int kSamples = 2048;         // keys of the other side in LDS for the bisections
+constexpr int kFillEach = 8;           // slots of a thread that empties them
 constexpr int kLaneList = 4, kGroupList = 128;
 
 struct BothSide {
@@ -203,6 +203,8 @@ struct BothSide {
   int64_t n_rows, nnz;
   int64_t base;       // of its entries in the joint arrays
   int32_t block0, blocks;  // of the sort
+  uint4 *lists;            // slots of its dims: (dim, first place, place behind the last, -)
+  uint32_t slots;
   int64_t groups;
 };
 
@@ -258,7 +260,7 @@ __device__ __forceinline__ void histogram(const BothArgs &a, int b, int32_t *cnt
 }
 
 // Unit values and row numbers, one wave a row; the first workgroups make the
-// first histogram, which needs neither.
+// first histogram and the last ones empty the slots, which need neither.
 __global__ __launch_bounds__(kSortThreads) void both_unit_kernel(BothArgs a) {
   __shared__ int32_t cnt[kMaxBins];
   const int blocks = a.s[0].blocks + a.s[1].blocks;
@@ -267,7 +269,17 @@ __global__ __launch_bounds__(kSortThreads) void both_unit_kernel(BothArgs a) {
     return;
   }
   const int lane = threadIdx.x & 63;
+  const int64_t row_blocks = (a.s[0].n_rows + a.s[1].n_rows + kSortWaves - 1) / kSortWaves;
   int64_t row = (int64_t)(blockIdx.x - blocks) * kSortWaves + (threadIdx.x >> 6);
+  if ((int64_t)blockIdx.x - blocks >= row_blocks) {  // both sides' slots are one array
+    const int64_t first = (int64_t)blockIdx.x - blocks - row_blocks;
+    const int64_t n = (int64_t)a.s[0].slots + a.s[1].slots;
+    for (int i = 0; i < kFillEach; ++i) {
+      const int64_t j = (first * kFillEach + i) * kSortThreads + threadIdx.x;
+      if (j < n) a.s[0].lists[j] = make_uint4(kDimEmpty, 0, 0, 0);
+    }
+    return;
+  }
   int side = 0;
   if (row >= a.s[0].n_rows) {
     row -= a.s[0].n_rows;
@@ -410,6 +422,52 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
   }
 }
 
+// Where a dim's entries stand among a side's sorted ones: an open-addressing
+// table, filled by the threads of each run's first and last entry (whichever
+// comes first takes the slot). Slots outnumber the entries, so that a chain
+// ends; where a dim lies in the table depends on the order of insertion and is
+// never observed. A lookup is one or two loads, where a bisection of the keys
+// is eighteen dependent ones.
+__device__ __forceinline__ uint32_t slot_of(uint32_t d, uint32_t slots) {
+  return (uint32_t)(((uint64_t)(d * 0x9E3779B1u) * slots) >> 32);
+}
+__global__ __launch_bounds__(256) void both_lists_kernel(BothArgs a) {
+  const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int side = p >= a.s[1].base;
+  const BothSide &s = a.s[side];
+  const int64_t e = s.base + s.nnz;
+  if (p >= e) return;
+  const int32_t *key = a.key[a.last];
+  const uint32_t d = (uint32_t)key[p];
+  const bool first = p == s.base || (uint32_t)key[p - 1] != d;
+  const bool last = p + 1 == e || (uint32_t)key[p + 1] != d;
+  if (!first && !last) return;
+  uint32_t *slot = reinterpret_cast<uint32_t *>(s.lists);
+  uint32_t i = slot_of(d, s.slots);
+  for (uint32_t n = 0; n < s.slots; ++n) {
+    const uint32_t was = atomicCAS(slot + 4 * (int64_t)i, kDimEmpty, d);
+    if (was == kDimEmpty || was == d) {
+      if (first) slot[4 * (int64_t)i + 1] = (uint32_t)p;
+      if (last) slot[4 * (int64_t)i + 2] = (uint32_t)(p + 1);
+      return;
+    }
+    i = i + 1 == s.slots ? 0 : i + 1;
+  }
+}
+__device__ __forceinline__ void find_list(const BothSide &s, uint32_t d, int32_t &l, int32_t &h) {
+  uint32_t i = slot_of(d, s.slots);
+  for (uint32_t n = 0; n < s.slots; ++n) {
+    const uint4 v = s.lists[i];
+    if (v.x == d) {
+      l = (int32_t)v.y;
+      h = (int32_t)v.z;
+      return;
+    }
+    if (v.x == kDimEmpty) return;
+    i = i + 1 == s.slots ? 0 : i + 1;
+  }
+}
+
 // Sum of a float over the row of 16 lanes (in its last lane), and over the
 // wave (in lane 63); every lane must be active.
 template <int CTRL, int ROW_MASK, bool BOUND>
@@ -433,8 +491,8 @@ __device__ __forceinline__ float wave_total(float x) {
 
 struct BothShared {
   float4 tile[kWalkCols];  // indexes are masked: in range whatever a CSR holds
-  int32_t lo[kBatch], hi[kBatch];
-  float acc[kBatch];
+  int32_t dim[kBatch];
+  float acc[kBatch], value[kBatch];
   int32_t begin[kWalkRows + 1];  // of the rows' entries in the batch
 };
 static_assert(kWalkRows == 4, "the rows of G are a float4");
@@ -485,91 +543,62 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
   const int64_t r0 = group * kWalkRows;
   const int nr = s.n_rows - r0 < kWalkRows ? (int)(s.n_rows - r0) : kWalkRows;
   const int64_t e0 = clamp64(s.indptr[r0], 0, s.nnz), e1 = clamp64(s.indptr[r0 + nr], e0, s.nnz);
-  const int32_t *key = a.key[a.last];
   const uint2 *load = a.load[a.last];
   const T *g = static_cast<const T *>(a.grad);
   const float *tile1 = reinterpret_cast<const float *>(sh.tile);
   for (int64_t eb = e0; eb < e1; eb += kBatch) {
     const int ne = e1 - eb < kBatch ? (int)(e1 - eb) : kBatch;
     __syncthreads();  // the batch before is done with
-    // every step-th key of the other side, where G will stand: the first eleven steps of each
-    // bisection in LDS
-    const int32_t o0 = (int32_t)o.base, on = (int32_t)o.nnz;
-    const int32_t step = (on + kSamples - 1) / kSamples;
-    const int samples = step > 0 ? (on + step - 1) / step : 0;
-    uint32_t *top = reinterpret_cast<uint32_t *>(sh.tile);
-    for (int i = t; i < samples; i += kWalkThreads) top[i] = (uint32_t)key[o0 + (int64_t)i * step];
     if (t <= nr) {
       const int64_t b = clamp64(s.indptr[r0 + t], e0, e1) - eb;
       sh.begin[t] = (int32_t)clamp64(b, 0, ne);
     }
-    __syncthreads();
     // entry i is thread (i % 8) * 64 + i / 8's: every wave gets some of a short row
     const int i = lane * kWalkWaves + w;
     int32_t l = 0, h = 0, row = 0;
     if (i < ne) {
-      const uint32_t d = (uint32_t)s.indices[eb + i];
-      // first key >= d and first key > d, side by side; sample j is key j * step
-      int32_t l1 = samples, h1 = samples;
-      while (l < l1 || h < h1) {
-        const int32_t ml = (l + l1) >> 1, mh = (h + h1) >> 1;
-        if (l < l1) {
-          if (top[ml] < d) l = ml + 1;
-          else l1 = ml;
-        }
-        if (h < h1) {
-          if (top[mh] <= d) h = mh + 1;
-          else h1 = mh;
-        }
-      }
-      // behind the last sample below, up to the sample found
-      l1 = o0 + (l < samples ? l * step : on);
-      h1 = o0 + (h < samples ? h * step : on);
-      l = o0 + (l > 0 ? (l - 1) * step + 1 : 0);
-      h = o0 + (h > 0 ? (h - 1) * step + 1 : 0);
-      while (l < l1 || h < h1) {
-        const int32_t ml = l + ((l1 - l) >> 1), mh = h + ((h1 - h) >> 1);
-        const uint32_t kl = l < l1 ? (uint32_t)key[ml] : 0u, kh = h < h1 ? (uint32_t)key[mh] : 0u;
-        if (l < l1) {
-          if (kl < d) l = ml + 1;
-          else l1 = ml;
-        }
-        if (h < h1) {
-          if (kh <= d) h = mh + 1;
-          else h1 = mh;
-        }
-      }
-      sh.lo[i] = l;
-      sh.hi[i] = h;
+      const int32_t d = s.indices[eb + i];
+      sh.value[i] = s.values[eb + i];
+      find_list(o, (uint32_t)d, l, h);
+      sh.dim[i] = d;
       sh.acc[i] = 0;
-      for (int r = 1; r < nr; ++r) row += i >= sh.begin[r];
     }
     __syncthreads();
-    // a long list: the first row that has it walks it, for the others too. A row's entries have
-    // ascending dims, so their lists' starts ascend; the last start at or before l is the dim's
-    // own if the row has it (absent dims before it may share the start).
+    if (i < ne)
+      for (int r = 1; r < nr; ++r) row += i >= sh.begin[r];
+    // a long list: the first row that has the dim walks it, for the others too
     uint32_t mate01 = ~0u, mate23 = ~0u;  // each row's entry, 16 bits each, all ones for none
     bool leads = false;
     if (i < ne && h - l > kGroupList) {
-      leads = true;
+      const int32_t d = sh.dim[i];
+      int32_t x0[kWalkRows], x1[kWalkRows];  // bisections of the rows' ascending dims
 #pragma unroll
       for (int r = 0; r < kWalkRows; ++r) {
-        uint32_t m = 0xFFFFu;
-        if (r < nr) {
-          int32_t x0 = sh.begin[r], x1 = sh.begin[r + 1];
-          while (x0 < x1) {
-            const int32_t x = (x0 + x1) >> 1;
-            if (sh.lo[x] <= l) x0 = x + 1;
-            else x1 = x;
-          }
-          if (x0 > sh.begin[r] && sh.lo[x0 - 1] == l && sh.hi[x0 - 1] == h) {
-            m = (uint32_t)(x0 - 1);
-            if (r < row) leads = false;
-          }
-        }
-        if (r < 2) mate01 = (mate01 & ~(0xFFFFu << (r * 16))) | m << (r * 16);
-        else mate23 = (mate23 & ~(0xFFFFu << (r * 16 - 32))) | m << (r * 16 - 32);
+        x0[r] = r < nr ? sh.begin[r] : 0;
+        x1[r] = r < nr ? sh.begin[r + 1] : 0;
       }
+      bool more = true;
+      while (more) {
+        more = false;
+#pragma unroll
+        for (int r = 0; r < kWalkRows; ++r)
+          if (x0[r] < x1[r]) {
+            const int32_t x = (x0[r] + x1[r]) >> 1;
+            if (sh.dim[x] < d) x0[r] = x + 1;
+            else x1[r] = x;
+            more = true;
+          }
+      }
+      leads = true;
+      uint32_t m[kWalkRows];
+#pragma unroll
+      for (int r = 0; r < kWalkRows; ++r) {
+        const bool has = r < nr && x0[r] < sh.begin[r + 1] && sh.dim[x0[r]] == d;
+        m[r] = has ? (uint32_t)x0[r] : 0xFFFFu;
+        if (has && r < row) leads = false;
+      }
+      mate01 = m[0] | m[1] << 16;
+      mate23 = m[2] | m[3] << 16;
       if (!leads) h = l;
     }
     for (int64_t c0 = 0; c0 < o.n_rows; c0 += kWalkCols) {
@@ -685,6 +714,11 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
       if (cut) l = next;
     }
     __syncthreads();
+    if (e1 - e0 <= kBatch) {  // the rows are whole: the norm's part from LDS
+      for (int r = w; r < nr; r += kWalkWaves)
+        through_norm(sh.value, sh.acc, s.dv + eb, sh.begin[r], sh.begin[r + 1], lane);
+      return;
+    }
     if (i < ne) s.dv[eb + i] = sh.acc[i];
   }
   __syncthreads();
@@ -722,8 +756,18 @@ sps_status check_csr(const sps_csr *m, const char *what) {
   return SPS_OK;
 }
 
+// Slots of a side's table: more than its entries; for small sides many more,
+// where the longest chain of a wave, not the table's size, is what costs (1.5
+// slots an entry at 82,000 entries of 47,000 dims: 20 us to fill, 8: 6 us).
+constexpr size_t kMoreSlots = 1 << 19;
+uint32_t slots_of(int64_t nnz) {
+  const int64_t least = nnz + nnz / 2, most = 8 * nnz;
+  const int64_t more = most < (int64_t)kMoreSlots ? most : (int64_t)kMoreSlots;
+  return (uint32_t)((least > more ? least : more) + 64);
+}
+
 struct BothLayout {
-  size_t unit, row, key[2], load[2], sums, hist, total;
+  size_t unit, row, key[2], load[2], sums, lists, hist, total;
   int64_t per_block;
 };
 BothLayout both_layout(int64_t n) {
@@ -742,6 +786,8 @@ BothLayout both_layout(int64_t n) {
   }
   L.per_block = (n + sps::kSortBlocks - 1) / sps::kSortBlocks;
   if (L.per_block < sps::kSortMinEntries) L.per_block = sps::kSortMinEntries;
+  L.lists = at;
+  at = up(at + ((size_t)n + (size_t)n / 2 + 2 * kMoreSlots + 128) * 16);
   L.sums = at;
   at = up(at + 2 * sps::kMaxBins * 4);
   L.hist = at;
@@ -922,11 +968,16 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
     s.block0 = blocks;
     s.blocks = (int32_t)((s.nnz + a.per_block - 1) / a.per_block);
     blocks += s.blocks;
+    s.slots = slots_of(s.nnz);
+    s.lists = reinterpret_cast<uint4 *>(b + L.lists) + (i ? a.s[0].slots : 0);
     s.groups = (s.n_rows + sps::kWalkRows - 1) / sps::kWalkRows;
     groups = (groups + 7) / 8 * 8 + s.groups;
   }
   const int64_t rows = queries->n_rows + items->n_rows;
-  const int64_t unit_blocks = blocks + (rows + sps::kSortWaves - 1) / sps::kSortWaves;
+  const int64_t slots = (int64_t)a.s[0].slots + a.s[1].slots;
+  const int64_t unit_blocks =
+      blocks + (rows + sps::kSortWaves - 1) / sps::kSortWaves +
+      (slots + sps::kSortThreads * sps::kFillEach - 1) / (sps::kSortThreads * sps::kFillEach);
   if (groups > kMax31 || unit_blocks > kMax31)
     return set_error(SPS_ERR_OVERFLOW, "%s: too many rows for a launch", what);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -939,6 +990,7 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
                        dim3(256), 0, s, a);
     hipLaunchKernelGGL(sps::both_scatter_kernel, dim3((uint32_t)blocks), sort, 0, s, a);
   }
+  hipLaunchKernelGGL(sps::both_lists_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, a);
   const dim3 grid((uint32_t)groups), block(sps::kWalkThreads);
   if (grad->dtype == SPS_F32)
     hipLaunchKernelGGL((sps::both_walk_kernel<float>), grid, block, 0, s, a);
