@@ -21,7 +21,7 @@ namespace sps {
 constexpr int kGradRows = 8;      // rows of a workgroup: 8 x 1028 floats are 33 KB of LDS
 constexpr int kGradThreads = 256;
 constexpr int kGradPitch = kSliceMax + 4;  // rows start 4 banks apart
-constexpr int kGradShort = 8;     // a list of at most this many postings is one lane's
+constexpr int kGradShort = 4;     // a list of at most this many postings is one lane's
 
 struct WalkArgs {
   const int32_t *indptr, *indices;
@@ -44,6 +44,27 @@ struct WalkArgs {
 __device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t total) {
   const int64_t q = total / 8, r = total % 8, x = b % 8;
   return x * q + (x < r ? x : r) + b / 8;
+}
+
+// Sum of a float over the row of 16 lanes (in its last lane), and over the
+// wave (in lane 63); every lane must be active.
+template <int CTRL, int ROW_MASK, bool BOUND>
+__device__ __forceinline__ float dpp_f32(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL,
+                                                               ROW_MASK, 0xf, BOUND));
+}
+__device__ __forceinline__ float row16_total(float x) {
+  x += dpp_f32<0x111, 0xf, true>(x);   // row_shr:1
+  x += dpp_f32<0x112, 0xf, true>(x);   // row_shr:2
+  x += dpp_f32<0x114, 0xf, true>(x);   // row_shr:4
+  x += dpp_f32<0x118, 0xf, true>(x);   // row_shr:8
+  return x;
+}
+__device__ __forceinline__ float wave_total(float x) {
+  x = row16_total(x);
+  x += dpp_f32<0x142, 0xa, false>(x);  // row_bcast:15
+  x += dpp_f32<0x143, 0xc, false>(x);  // row_bcast:31
+  return x;
 }
 
 template <typename T>
@@ -95,11 +116,16 @@ __global__ __launch_bounds__(kGradThreads) void grad_walk_kernel(WalkArgs a) {
         if (start < 0 || n > snnz - start) n = 0;
       }
       float acc = 0;
-      if (n <= kGradShort)
-        for (int i = 0; i < n; ++i) {
-          const uint2 p = post[start + i];
-          acc += g[p.x & (kSliceMax - 1)] * __builtin_bit_cast(float, p.y);
+      if (n > 0 && n <= kGradShort) {
+        uint2 p[kGradShort];
+#pragma unroll
+        for (int i = 0; i < kGradShort; ++i) p[i] = post[start + (i < n ? i : 0)];
+#pragma unroll
+        for (int i = 0; i < kGradShort; ++i) {
+          const float x = g[p[i].x & (kSliceMax - 1)];
+          acc += i < n ? x * __builtin_bit_cast(float, p[i].y) : 0.0f;
         }
+      }
       uint64_t rest = __ballot(n > kGradShort);
       while (rest) {
         const int l = __builtin_ctzll(rest);
@@ -107,11 +133,18 @@ __global__ __launch_bounds__(kGradThreads) void grad_walk_kernel(WalkArgs a) {
         const int32_t s = __builtin_amdgcn_readlane(start, l);
         const int32_t m = __builtin_amdgcn_readlane(n, l);
         float part = 0;
-        for (int i = lane; i < m; i += 64) {
-          const uint2 p = post[s + i];
-          part += g[p.x & (kSliceMax - 1)] * __builtin_bit_cast(float, p.y);
+        for (int i = lane; i < m; i += 256) {
+          uint2 p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = post[s + (i + 64 * j < m ? i + 64 * j : i)];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = g[p[j].x & (kSliceMax - 1)];
+            part += i + 64 * j < m ? x * __builtin_bit_cast(float, p[j].y) : 0.0f;
+          }
         }
-        part = wave_sum(part);
+        part = __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wave_total(part)), 63));
         if (lane == l) acc = part;
       }
       if (e < e1) {
@@ -466,27 +499,6 @@ __device__ __forceinline__ void find_list(const BothSide &s, uint32_t d, int32_t
     if (v.x == kDimEmpty) return;
     i = i + 1 == s.slots ? 0 : i + 1;
   }
-}
-
-// Sum of a float over the row of 16 lanes (in its last lane), and over the
-// wave (in lane 63); every lane must be active.
-template <int CTRL, int ROW_MASK, bool BOUND>
-__device__ __forceinline__ float dpp_f32(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL,
-                                                               ROW_MASK, 0xf, BOUND));
-}
-__device__ __forceinline__ float row16_total(float x) {
-  x += dpp_f32<0x111, 0xf, true>(x);   // row_shr:1
-  x += dpp_f32<0x112, 0xf, true>(x);   // row_shr:2
-  x += dpp_f32<0x114, 0xf, true>(x);   // row_shr:4
-  x += dpp_f32<0x118, 0xf, true>(x);   // row_shr:8
-  return x;
-}
-__device__ __forceinline__ float wave_total(float x) {
-  x = row16_total(x);
-  x += dpp_f32<0x142, 0xa, false>(x);  // row_bcast:15
-  x += dpp_f32<0x143, 0xc, false>(x);  // row_bcast:31
-  return x;
 }
 
 struct BothShared {
