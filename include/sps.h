@@ -368,7 +368,8 @@ enum { SPS_F32 = 0, SPS_F16 = 1, SPS_BF16 = 2 };
  * whole (for chunk c of a prepared corpus, col_begin = c * chunk_size).
  * data: DEVICE, aligned to its element only; ld >= n_cols, so a view may be a
  * part of a wider matrix. Rows, col_begin and col_begin + n_cols are below
- * 2^31 - 1. */
+ * 2^31 - 1, and rows few enough for a launch (about 4 million workgroups of
+ * 1024 threads, 16 million of 256; SPS_ERR_OVERFLOW otherwise). */
 typedef struct {
   const void *data;
   int32_t dtype; /* SPS_F32, SPS_F16 (what sps_cosine_chunk_half writes) or SPS_BF16 */
@@ -569,7 +570,8 @@ sps_status sps_cosine_grad_both_workspace_size(int64_t nnz_queries, int64_t nnz_
 /* dv of both sides at once, from the two canonical CSRs and the gradient of
  * their whole score matrix (asynchronous; nothing is prepared): what a
  * training step on a batch needs. grad: n_query x n_item (col_begin is not
- * used). grad_queries, grad_items: DEVICE float[nnz] of each side. workspace:
+ * used). grad_queries, grad_items: DEVICE float[nnz] of each side; together
+ * fewer than 2^31 - 2^16 entries. workspace:
  * DEVICE, 256-byte aligned, used until the call's stream work is done. Sums
  * are float32 in a fixed order, those of the norms float64: bitwise
  * reproducible. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,

@@ -858,7 +858,8 @@ sps_status check_sizes(int64_t n_rows, int32_t k, const char *what) {
   if (k < 1 || k > sps::kDistMaxK)
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: k must be in [1, %d]", what, sps::kDistMaxK);
   if (n_rows >= kMax31) return set_error(SPS_ERR_OVERFLOW, "%s: rows must be below 2^31", what);
-  return SPS_OK;
+  // a workgroup a row at the most; more than one only of fewer than kDistFill rows
+  return sps::check_grid(n_rows, 1024, what);
 }
 
 // the checks of a list and its workspace; fills d

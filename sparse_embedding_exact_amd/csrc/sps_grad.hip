@@ -875,8 +875,8 @@ sps_status sps_cosine_grad(const sps_csr *rows, const sps_items *other, int32_t 
     a.parts = static_cast<float *>(workspace);
   }
   const int64_t blocks = a.n_groups * other->g.n_sub;
-  if (blocks > kMax31)
-    return set_error(SPS_ERR_OVERFLOW, "%s: too many rows and slices for a launch", what);
+  st = sps::check_grid(blocks, sps::kGradThreads, what);
+  if (st != SPS_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((uint32_t)blocks), block(sps::kGradThreads);
   if (grad->dtype == SPS_F32)
@@ -899,6 +899,8 @@ sps_status sps_cosine_grad_values(const sps_csr *rows, const float *du, float *d
   if (st != SPS_OK) return st;
   if (rows->n_rows == 0 || rows->nnz == 0) return SPS_OK;
   if (!du || !dv) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL gradient", what);
+  const sps_status fits = sps::check_grid((rows->n_rows + 3) / 4, 256, what);
+  if (fits != SPS_OK) return fits;
   hipLaunchKernelGGL(sps::grad_values_kernel, dim3((uint32_t)((rows->n_rows + 3) / 4)), dim3(256),
                      0, reinterpret_cast<hipStream_t>(stream), rows->n_rows, rows->nnz,
                      rows->indptr, rows->values, du, dv);
@@ -910,8 +912,10 @@ sps_status sps_cosine_grad_both_workspace_size(int64_t nnz_queries, int64_t nnz_
   if (!bytes) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output pointer");
   if (nnz_queries < 0 || nnz_items < 0)
     return set_error(SPS_ERR_INVALID_ARGUMENT, "negative size");
-  if (nnz_queries >= kMax31 || nnz_items >= kMax31 || nnz_queries + nnz_items >= kMax31)
-    return set_error(SPS_ERR_OVERFLOW, "entries of both sides must be below 2^31");
+  // places are 32-bit, and a wave looks up to 512 past one
+  const int64_t most = kMax31 - 65536;
+  if (nnz_queries >= most || nnz_items >= most || nnz_queries + nnz_items >= most)
+    return set_error(SPS_ERR_OVERFLOW, "entries of both sides must be below 2^31 - 2^16");
   *bytes = both_layout(nnz_queries + nnz_items).total;
   return SPS_OK;
 }
@@ -990,8 +994,9 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
   const int64_t unit_blocks =
       blocks + (rows + sps::kSortWaves - 1) / sps::kSortWaves +
       (slots + sps::kSortThreads * sps::kFillEach - 1) / (sps::kSortThreads * sps::kFillEach);
-  if (groups > kMax31 || unit_blocks > kMax31)
-    return set_error(SPS_ERR_OVERFLOW, "%s: too many rows for a launch", what);
+  st = sps::check_grid(groups, sps::kWalkThreads, what);
+  if (st == SPS_OK) st = sps::check_grid(unit_blocks, sps::kSortThreads, what);
+  if (st != SPS_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   const dim3 sort(sps::kSortThreads);
   hipLaunchKernelGGL(sps::both_unit_kernel, dim3((uint32_t)unit_blocks), sort, 0, s, a);

@@ -80,6 +80,13 @@ inline sps_status check_scores(const sps_scores *s, const char *what) {
   return SPS_OK;
 }
 
+// A launch's threads are counted in 32 bits.
+inline sps_status check_grid(int64_t blocks, int64_t threads, const char *what) {
+  if (blocks > 4294967295ll / threads)
+    return set_error(SPS_ERR_OVERFLOW, "%s: too many rows for a launch", what);
+  return SPS_OK;
+}
+
 inline sps_status launch_status(const char *what) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return set_error(SPS_ERR_HIP, "%s: %s", what, hipGetErrorString(e));

@@ -552,6 +552,7 @@ __global__ __launch_bounds__(256) void reorder_kernel(StateArgs a) {
 namespace {
 
 constexpr int64_t kMax31 = 2147483647ll;
+constexpr int64_t kMaxPieces = 4294967295ll / 256;  // pieces of states in a launch
 
 // Workgroups that fill the card, and the fewest columns worth one of them.
 constexpr int64_t kFill = 1024, kMinSeg = 8192;
@@ -665,8 +666,8 @@ sps_status sps_select_chunk(const sps_scores *scores, const float *offsets, int3
   const size_t need = sp.splits > 1 ? parts_bytes(rows, sp, k) : 0;
   st = check_ws(workspace, workspace_bytes, need, "sps_select_chunk");
   if (st != SPS_OK) return st;
-  if (rows * sp.splits > kMax31)
-    return sps::set_error(SPS_ERR_OVERFLOW, "sps_select_chunk: too many rows for a launch");
+  st = sps::check_grid(rows * sp.splits, sps::kSelThreads, "sps_select_chunk");
+  if (st != SPS_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   sps::SelArgs a{};
   a.x = scores->data;
@@ -727,6 +728,8 @@ sps_status sps_beam_select(const sps_scores *scores, const float *beam_scores, i
   if (rows == 0) return SPS_OK;
   if (!out_scores || !out_parents || !out_cols)
     return sps::set_error(SPS_ERR_INVALID_ARGUMENT, "sps_beam_select: NULL output");
+  st = sps::check_grid(rows * sp.splits, sps::kSelThreads, "sps_beam_select");
+  if (st != SPS_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (one_launch(scores->n_cols, beams)) {
     sps::GroupArgs g{};
@@ -747,8 +750,6 @@ sps_status sps_beam_select(const sps_scores *scores, const float *beam_scores, i
   }
   st = check_ws(workspace, workspace_bytes, parts_bytes(rows, sp, k), "sps_beam_select");
   if (st != SPS_OK) return st;
-  if (rows * sp.splits > kMax31)
-    return sps::set_error(SPS_ERR_OVERFLOW, "sps_beam_select: too many rows for a launch");
   sps::SelArgs a{};
   a.x = scores->data;
   a.ld = scores->ld;
@@ -787,6 +788,8 @@ sps_status sps_beam_join(const float *top_scores, const int32_t *top_cols, int64
   if (n_rows == 0) return SPS_OK;
   if (!top_scores || !top_cols || !out_scores || !out_parents || !out_cols)
     return sps::set_error(SPS_ERR_INVALID_ARGUMENT, "sps_beam_join: NULL list or output");
+  st = sps::check_grid(n_rows / beams, sps::kSelThreads, "sps_beam_join");
+  if (st != SPS_OK) return st;
   sps::JoinArgs j{};
   j.in_scores = top_scores;
   j.in_cols = top_cols;
@@ -821,7 +824,7 @@ sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const i
     if (x.row_bytes == 0) continue;
     if ((!x.src && n_rows > 0) || !x.dst)
       return sps::set_error(SPS_ERR_INVALID_ARGUMENT, "sps_reorder_states: state %d is NULL", i);
-    if ((x.row_bytes + sps::kPieceBytes - 1) / sps::kPieceBytes > kMax31 / n_out)
+    if ((x.row_bytes + sps::kPieceBytes - 1) / sps::kPieceBytes > kMaxPieces / n_out)
       return sps::set_error(SPS_ERR_OVERFLOW, "sps_reorder_states: state %d exceeds a launch", i);
   }
   // sources are read while the destinations are written
@@ -850,7 +853,7 @@ sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const i
       const sps_state &x = states[i];
       if (x.row_bytes == 0) continue;
       const int64_t pieces = (x.row_bytes + sps::kPieceBytes - 1) / sps::kPieceBytes;
-      if (blocks + pieces * n_out > kMax31) break;
+      if (blocks + pieces * n_out > kMaxPieces) break;
       const int32_t k = a.n++;
       a.src[k] = static_cast<const uint8_t *>(x.src);
       a.dst[k] = static_cast<uint8_t *>(x.dst);

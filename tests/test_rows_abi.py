@@ -235,7 +235,7 @@ def test_both_refusals(lib):
     n = ctypes.c_size_t()
     sizes = lib.sps_cosine_grad_both_workspace_size
     assert sizes(5, 5, None) == INV and sizes(-1, 5, ctypes.byref(n)) == INV
-    assert sizes(2**31 - 10, 9, ctypes.byref(n)) == OVF and sizes(2**31, 9, ctypes.byref(n)) == OVF
+    assert sizes(2**31 - 70000, 9000, ctypes.byref(n)) == OVF and sizes(2**31, 9, ctypes.byref(n)) == OVF
     assert sizes(9, 9, ctypes.byref(n)) == 0
     v = view(rows=4, cols=4)
     both = lib.sps_cosine_grad_both
@@ -250,3 +250,18 @@ def test_both_refusals(lib):
     assert both(csr(), csr(), v, P, P, P + 16, n.value, None) == INV
     empty = dict(nnz=0, indices=None, values=None)
     assert both(csr(**empty), csr(**empty), v, None, None, None, 0, None) == 0
+
+
+def test_launch_limits(lib):
+    """Sizes within 31 bits whose launches would count their threads past 32: refused."""
+    n = ctypes.c_size_t()
+    many = dict(rows=2**25, cols=1, ld=1)
+    assert lib.sps_select_chunk(view(**many), None, 1, 1, P, P, None, 0, None) == OVF
+    assert lib.sps_beam_select(view(**many), None, 1, 1, P, P, P, None, 0, None) == OVF
+    assert lib.sps_beam_join(P, P, 2**25, 1, 1, 1, P, P, P, None) == OVF
+    assert lib.sps_distill_workspace_size(2**23, 1, ctypes.byref(n)) == OVF
+    st = state(row=1, ss=1, ds=1, src=P, dst=2**40)
+    assert lib.sps_reorder_states(ctypes.byref(st), 1, P, 2**30, 8, None) == OVF
+    assert lib.sps_cosine_grad_values(csr(n=2**27), P, P, None) == OVF
+    wide = view(rows=4, cols=2**29, ld=2**29)
+    assert lib.sps_cosine_grad_both(csr(), csr(n=2**29), wide, P, P, P, 1 << 40, None) == OVF
