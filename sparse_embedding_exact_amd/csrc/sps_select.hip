@@ -23,7 +23,10 @@ constexpr int kSelMaxK = 256;     // entries of a list: the public limit of k
 constexpr int kSelThreads = 256;  // >= kSelMaxK: the threads' maxima bound the k-th best
 constexpr int kSelBuf = 1024;     // candidates ranked at a time
 constexpr int kBoundBits = 20;    // upper bits of a key that the first bound resolves
-constexpr int kOneMax = 96;       // up to this k one maximum a thread bounds well, else two
+// Up to this k one maximum a thread bounds the k-th best, beyond two (8192 x
+// 8192: k = 16 42.4 us with one, 44.0 with two; k = 96 56.9 and 56.7; k = 256
+// 977, as the bound then is the least of 256 maxima, and 142).
+constexpr int kOneMax = 96;
 // a list that grows by 64-candidate steps must leave room for one
 static_assert(kSelBuf >= 64 && kSelThreads >= kSelMaxK, "selection buffers");
 
@@ -260,6 +263,10 @@ struct SelArgs {
 
 // Best k of columns [split * seg, ...) of one row. With parts, they are
 // written there as keys (0 behind the last); without, they join the row's list.
+// Tiles of 256 threads x 32 scores: with 16 a thread the first chunk's lists
+// are merged twice as often (808 against 696 us for two chunks of 50,000 x
+// 8192), and 72 registers leave six workgroups a CU. Reads at 4.8 TB/s there
+// (k = 100, the lists' growth included) and at 5.2 TB/s from 80 rows of 2M.
 template <typename T, int VPT>
 __global__ __launch_bounds__(kSelThreads, 6) void select_kernel(SelArgs a) {
   __shared__ SelShared sh;
@@ -531,6 +538,7 @@ __device__ __forceinline__ void copy_piece(const uint8_t *src, uint8_t *dst, int
   for (int64_t i = threadIdx.x; i < m; i += 256) d[i] = src ? s[i] : W{};
 }
 
+// A piece of a row a workgroup: 256 rows of 64 KB move at 4.9 TB/s (7 us).
 __global__ __launch_bounds__(256) void reorder_kernel(StateArgs a) {
   const int64_t b = blockIdx.x;
   int i = 0;
@@ -554,7 +562,9 @@ namespace {
 constexpr int64_t kMax31 = 2147483647ll;
 constexpr int64_t kMaxPieces = 4294967295ll / 256;  // pieces of states in a launch
 
-// Workgroups that fill the card, and the fewest columns worth one of them.
+// Workgroups that fill the card, and the fewest columns worth one of them (2 x
+// 100,000 scores: 10.4 us, with 4096 columns 10.9, with 16384 12.7; 128 x
+// 32768: 10.4, 11.7, 13.2).
 constexpr int64_t kFill = 1024, kMinSeg = 8192;
 
 struct Split {
@@ -584,7 +594,9 @@ Split split_of(int64_t n_rows, int64_t n_cols) {
   return {(int32_t)(s > 1 ? s : 1), seg};
 }
 
-// Groups of up to this many scores go to one workgroup each, in one launch.
+// Groups of up to this many scores go to one workgroup each, in one launch (4
+// beams of 512 columns: 4.6 us, in two launches 8.7; of 4096: 9.8 both ways,
+// 512 such groups 11.7 against 16.8; of 8192: 16.8 against 9.1).
 constexpr int64_t kOneGroup = 16384;
 bool one_launch(int64_t n_cols, int32_t beams) { return n_cols <= kOneGroup / beams; }
 
@@ -597,6 +609,8 @@ void launch_group(const sps::GroupArgs &a, int64_t groups, hipStream_t s) {
     hipLaunchKernelGGL((sps::beam_group_kernel<T, 32>), grid, block, 0, s, a);
 }
 
+// Short segments take tiles of 8 scores a thread (4096 x 2048 scores: 11.8 us,
+// with 32 a thread 17.9).
 template <typename T>
 void launch_select(const sps::SelArgs &a, int64_t rows, hipStream_t s) {
   const uint32_t grid = (uint32_t)(rows * a.splits);
