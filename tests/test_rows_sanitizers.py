@@ -5,7 +5,10 @@ tests/sanitize/rows_abi_main.c through the C ABI, every call of which returns
 before any device work."""
 import os
 
-import test_sanitizers as ts  # the toolchain's flags and helpers
+import pytest
+
+# the toolchain's flags and helpers; a copy of the tree for GPU runs may lack that file
+ts = pytest.importorskip("test_sanitizers")
 
 SOURCES = ("sps_prepare.hip", "sps_score.hip", "sps_bsc.hip", "sps_select.hip", "sps_distill.hip",
            "sps_grad.hip", "sps_api.hip")
