@@ -156,17 +156,19 @@ __device__ __forceinline__ RowTeach teach_row(const int32_t *__restrict__ ids,
   if (!lse) mx = block_max<NT>(mx, sh.wf);
   const double shift = lse ? given : (double)finite_max(mx) * inv_tau;
   double v[3] = {0, 0, (double)has};  // sum e, sum e log e, entries
+  double mine = 0;                    // of this thread's first entry
   for (int i = t; i < k; i += NT)
     if (sh.sid[i] >= 0) {
       const double x = (double)sh.p[i] * inv_tau - shift, e = exp(x);
       v[0] += e;
       v[1] += e == 0 ? 0.0 : e * x;
+      if (i == t) mine = e;
     }
   block_sums<NT>(v, sh.wd);
   const double sum = v[0], scale = lse ? 1.0 : 1.0 / sum;
   for (int i = t; i < k; i += NT) {
-    const bool ok = sh.sid[i] >= 0;
-    sh.p[i] = ok ? (float)(exp((double)sh.p[i] * inv_tau - shift) * scale) : 0.0f;
+    if (i > t) mine = exp((double)sh.p[i] * inv_tau - shift);
+    sh.p[i] = sh.sid[i] >= 0 ? (float)(mine * scale) : 0.0f;
   }
   RowTeach r;
   r.has = v[2] != 0;
@@ -447,12 +449,21 @@ __device__ __forceinline__ Whole whole(double z_rest, double z_list, float m, fl
   return r;
 }
 
-// One wave a row.
+// the sum of L neighbouring lanes, in all of them
+template <int L>
+__device__ __forceinline__ double lanes_total(double v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, L);
+  return v;
+}
+// L lanes a row. Bound by vector issue: three exponentials and two logarithms
+// in 64 bits a row, whatever the lanes, and one a turn of the list.
+template <int L>
 __global__ __launch_bounds__(256) void distill_loss_kernel(DistillDev d, float *__restrict__ loss,
                                                            float *__restrict__ lse) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= d.n_rows) return;  // uniform per wave
+  const int lane = threadIdx.x & (L - 1);
+  const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (row >= d.n_rows) return;  // all lanes of a row
   const int32_t *sid = d.sid + row * d.k;
   const float *x = d.x + row * d.k, *p = d.p + row * d.k;
   const Stat *st = d.stat + row * d.slots;
@@ -460,31 +471,31 @@ __global__ __launch_bounds__(256) void distill_loss_kernel(DistillDev d, float *
   // the columns outside the list by their own largest score: their mass, which the remaining
   // class divides by, must not vanish next to the list's
   float m = -__builtin_inff(), ml = -__builtin_inff();
-  for (int i = lane; i < d.slots; i += 64) m = fmaxf(m, st[i].m);
-  for (int i = lane; i < d.k; i += 64)
+  for (int i = lane; i < d.slots; i += L) m = fmaxf(m, st[i].m);
+  for (int i = lane; i < d.k; i += L)
     if (sid[i] >= 0) ml = fmaxf(ml, x[i]);
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    m = fmaxf(m, __shfl_xor(m, o, 64));
-    ml = fmaxf(ml, __shfl_xor(ml, o, 64));
+  for (int o = L / 2; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor(m, o, L));
+    ml = fmaxf(ml, __shfl_xor(ml, o, L));
   }
   const float mf = finite_max(m), ma = finite_max(fmaxf(m, ml));
   const double c = (double)d.c, ln2 = 0.693147180559945309417;
   double z_rest = 0, z_list = 0;
-  for (int i = lane; i < d.slots; i += 64) {
+  for (int i = lane; i < d.slots; i += L) {
     const Stat s = st[i];
     if (s.s != 0) z_rest += s.s * exp2(((double)s.m - (double)mf) * c);
   }
-  for (int i = lane; i < d.k; i += 64)
+  for (int i = lane; i < d.k; i += L)
     if (sid[i] >= 0) z_list += exp2(((double)x[i] - (double)ma) * c);
-  z_rest = __shfl(wave_total_f64(z_rest), 63, 64);
-  z_list = __shfl(wave_total_f64(z_list), 63, 64);
+  z_rest = lanes_total<L>(z_rest);
+  z_list = lanes_total<L>(z_list);
   const Whole z = whole(z_rest, z_list, mf, ma, c, te.mass, te.rest);
   double l = 0;
-  for (int i = lane; i < d.k; i += 64)
+  for (int i = lane; i < d.k; i += L)
     if (sid[i] >= 0 && p[i] != 0)
       l += (double)p[i] * (z.log_z - ((double)x[i] - (double)ma) * c * ln2);
-  l = __shfl(wave_total_f64(l), 63, 64) + te.entropy;
+  l = lanes_total<L>(l) + te.entropy;
   if (te.rest != 0) l += te.rest * z.rest_term;
   const int32_t live = te.has && z.z != 0;  // a NaN is no 0
   if (lane == 0) {
@@ -939,9 +950,19 @@ void launch_chunk(const DistillDev &d, const sps_scores *x, int32_t first, hipSt
     hipLaunchKernelGGL((sps::distill_chunk_kernel<sps::bf16_t>), grid, block, 0, s, a);
 }
 
+// 16 lanes a row where the rows fill the card, else a wave: (10,000, 32) 6.5
+// against 12.7 us, (10,000, 100) 11.4 : 14.0, (4000, 32) 5.1 : 7.0, (2000, 32)
+// 5.0 : 5.5, (512, 8) 4.5 : 4.8, (50,000, 512) 183 : 195; but (4000, 100) 8.5 :
+// 7.9, (512, 32) 5.0 : 4.7, (10,000, 512) 72 : 38. (Rows, list.)
+constexpr int64_t kLossRows = 64;  // for each entry of the list
 void launch_loss(const DistillDev &d, float *loss, float *lse, hipStream_t s) {
-  hipLaunchKernelGGL(sps::distill_loss_kernel, dim3((uint32_t)((d.n_rows + 3) / 4)), dim3(256), 0,
-                     s, d, loss, lse);
+  const int64_t longest = d.k > d.slots ? d.k : d.slots;
+  if (d.n_rows >= kLossRows * longest)
+    hipLaunchKernelGGL((sps::distill_loss_kernel<16>), dim3((uint32_t)((d.n_rows + 15) / 16)),
+                       dim3(256), 0, s, d, loss, lse);
+  else
+    hipLaunchKernelGGL((sps::distill_loss_kernel<64>), dim3((uint32_t)((d.n_rows + 3) / 4)),
+                       dim3(256), 0, s, d, loss, lse);
 }
 
 sps_status check_grad(const sps_scores *x, const void *grad, int32_t dtype, int64_t ld,

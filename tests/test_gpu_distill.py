@@ -124,6 +124,30 @@ def test_chunks(env, dtype, rest, rows):
         assert float((slse.double() - ref).abs().max()) <= do.U * (160 + float(ref.abs().max()))
 
 
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("rows", [2559, 2560, 2573])
+def test_chunks_of_many_rows(env, rest, rows):
+    """About 64 rows an entry of the list; lists with no entry and rows with no score among them,
+    the last rows too."""
+    torch, sps, dev = env
+    cols, k, tau = 150, 40, 1.5
+    x, ids, t, w = make(env, rows, cols, k, "float32", 17)
+    ids[5::7] = -1
+    x[3::11, 2:] = -np.inf
+    x[4::11] = -np.inf
+    ids[rows - 2] = -1
+    lse = teacher_lse(ids, t, tau, cols, 0.6, 1) if rest else None
+    d = sps.distill_prepare(dev_of(env, ids), dev_of(env, t), cols, tau, dev_of(env, lse))
+    cuts = ((0, 80), (80, cols))
+    for c0, c1 in cuts:
+        sps.distill_chunk(d, x[:, c0:c1], c0, first=c0 == 0)
+    loss = sps.distill_loss(d)
+    g = torch.empty_like(x)
+    for c0, c1 in cuts:
+        sps.distill_chunk_grad(d, x[:, c0:c1], c0, dev_of(env, w), out=g[:, c0:c1])
+    compare(env, loss, g, x, ids, t, tau, lse, w, [*range(96), *range(rows - 40, rows)])
+
+
 def test_long_rows_of_many(env):
     """Rows longer than the columns whose list bits fit LDS at a time."""
     torch, sps, dev = env
