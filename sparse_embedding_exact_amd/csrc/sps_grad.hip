@@ -216,14 +216,17 @@ __global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_
 // LDS then make four products. The norm's part is taken off at the end of the
 // same launch.
 //
-// Measured: 2000 x 8192, 43 entries a row, Zipf(1.1): 203 us, of which unit
-// values and sort 55, table 9, walk 150 (about 46 for G, which the items' side
-// reads 16 bytes of a row at a time, 61 for the long lists, 28 for the short
-// ones, 16 for the rest). Long lists are bound by the loads of their entries
-// and the gathers from LDS: neither more of them in flight (1024, or a next
-// 512 loaded ahead) nor half the bank conflicts (8-byte loads of neighbouring
-// entries, 10 % slower) made them faster. Rows one at a time, without the
-// sharing, took 335 us, prepared corpora instead of the sort 1488.
+// Measured: 2000 x 8192, 43 entries a row, Zipf(1.1): 193 us, of which unit
+// values and sort 45, table 9, walk 142 (without the long lists 80, without
+// the group lists 128, without loading G, which the items' side reads 16 bytes
+// of a row at a time, 117, with none of these 18). Long lists are bound by the
+// loads of their entries and the gathers from LDS: vector issue is busy for
+// half of the walk and LDS for 37 %, half of it bank conflicts, and 93 % of
+// the loads hit in L2 (1001 x 8192). More of them in flight (1024, or a next
+// 512 loaded ahead), four lists a wave at a time and lists handed to whichever
+// wave is free were no faster, half the bank conflicts (8-byte loads of
+// neighbouring entries) 10 % slower. Rows one at a time, without the sharing,
+// took 335 us, prepared corpora instead of the sort 1488.
 // ---------------------------------------------------------------------------
 
 constexpr int kSortThreads = 512;
@@ -390,7 +393,9 @@ __global__ __launch_bounds__(kPrefixWaves * 64) void both_prefix_kernel(BothArgs
 }
 
 // Stable: a block's entries are cut among its waves in order, a wave takes 64
-// at a time, and equal digits among them are ranked by lane.
+// at a time, and equal digits among them are ranked by lane. Entries counted
+// last are placed first, from registers: 10.6 us a pass at 2000 x 8192, loaded
+// again 11.8. What bounds it then is the two stores of an entry, to a line each.
 __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) {
   __shared__ int32_t cnt[kSortWaves][kMaxBins];
   __shared__ int32_t ws[kSortWaves];
@@ -402,16 +407,26 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
   const int64_t part = ((a.per_block / kSortWaves) + 63) / 64 * 64;
   const int64_t e0 = lo + w * part < hi ? lo + w * part : hi;
   const int64_t e1 = w + 1 < kSortWaves && e0 + part < hi ? e0 + part : hi;
-  for (int i = lane; i < bins; i += 64) cnt[w][i] = 0;
-  for (int64_t w0 = e0 + lane; w0 < e1; w0 += 64 * kSortAhead) {
-    int32_t k[kSortAhead];
+  const uint2 *from = a.load[(a.pass + 1) & 1];
+  int32_t k[kSortAhead];
+  uint2 v[kSortAhead];
+  const auto keys = [&](int64_t w0) {
 #pragma unroll
-    for (int i = 0; i < kSortAhead; ++i) k[i] = key_at(a, side, w0 + 64 * i < e1 ? w0 + 64 * i : w0);
+    for (int i = 0; i < kSortAhead; ++i) {
+      const int64_t x = w0 + 64 * i + lane;
+      k[i] = key_at(a, side, x < e1 ? x : w0);
+    }
+  };
+  const auto loads = [&](int64_t w0) {
 #pragma unroll
-    for (int i = 0; i < kSortAhead; ++i)
-      if (w0 + 64 * i < e1) atomicAdd(&cnt[w][digit_of(k[i], a)], 1);
-  }
-  __syncthreads();
+    for (int i = 0; i < kSortAhead; ++i) {
+      const int64_t x = w0 + 64 * i + lane, e = x < e1 ? x : w0;
+      v[i] = a.pass == 0 ? make_uint2((uint32_t)a.row[e], __builtin_bit_cast(uint32_t, a.unit[e]))
+                         : from[e];
+    }
+  };
+  // counted from the last 1024 entries of the wave to the first, which stay in registers
+  const int64_t turns = e1 > e0 ? (e1 - e0 - 1) / (64 * kSortAhead) : 0;
   // thread t places digits 4 t .. 4 t + 3
   int32_t total[4] = {}, before[4] = {};
   if (4 * t < bins) {
@@ -420,6 +435,16 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
     total[0] = v.x, total[1] = v.y, total[2] = v.z, total[3] = v.w;
     before[0] = h.x, before[1] = h.y, before[2] = h.z, before[3] = h.w;
   }
+  for (int i = lane; i < bins; i += 64) cnt[w][i] = 0;
+  for (int64_t n = turns; n >= 0 && e0 < e1; --n) {
+    const int64_t w0 = e0 + n * 64 * kSortAhead;
+    keys(w0);
+    if (n == 0) loads(w0);
+#pragma unroll
+    for (int i = 0; i < kSortAhead; ++i)
+      if (w0 + 64 * i + lane < e1) atomicAdd(&cnt[w][digit_of(k[i], a)], 1);
+  }
+  __syncthreads();
   int32_t all;
   const int32_t sum = total[0] + total[1] + total[2] + total[3];
   int32_t at = block_incl_scan<kSortThreads, int32_t>(sum, ws, &all) - sum + (int32_t)s.base;
@@ -438,16 +463,10 @@ __global__ __launch_bounds__(kSortThreads) void both_scatter_kernel(BothArgs a) 
   __syncthreads();
   int32_t *key = a.key[a.pass & 1];
   uint2 *load = a.load[a.pass & 1];
-  const uint2 *from = a.load[(a.pass + 1) & 1];
   for (int64_t w0 = e0; w0 < e1; w0 += 64 * kSortAhead) {
-    int32_t k[kSortAhead];
-    uint2 v[kSortAhead];
-#pragma unroll
-    for (int i = 0; i < kSortAhead; ++i) {
-      const int64_t x = w0 + 64 * i + lane, e = x < e1 ? x : e0;
-      k[i] = key_at(a, side, e);
-      v[i] = a.pass == 0 ? make_uint2((uint32_t)a.row[e], __builtin_bit_cast(uint32_t, a.unit[e]))
-                         : from[e];
+    if (w0 > e0) {
+      keys(w0);
+      loads(w0);
     }
 #pragma unroll
     for (int i = 0; i < kSortAhead; ++i) {
