@@ -677,8 +677,10 @@ __device__ __forceinline__ void walk(const BothArgs &a, int side, int64_t group,
         sh.tile[c] = make_float4(v[0], v[1], v[2], v[3]);
       }
       __syncthreads();
-      // the list's part in this tile starts where the last tile's ended
-      const bool cut = nc < o.n_rows && h - l > kLaneList;
+      // the list's part in this tile starts where the last tile's ended. A lane's own few entries
+      // are looked at in every tile instead, each for its column; a leading list is cut to the
+      // last entry, since the wave that walks it asks for no column
+      const bool cut = nc < o.n_rows && (leads ? h > l : h - l > kLaneList);
       int32_t next = h;
       if (cut) {
         int32_t m0 = l, m1 = h;

@@ -151,6 +151,54 @@ def test_lists_over_several_tiles(env, nq, ni):
     close(gi, *oracle(it, q, g64.T, nq // 256 + 4))
 
 
+def rests(n, this):
+    """(this side, other side of n rows): dims whose lists of more than 128 entries leave 0, 1, 4
+    or 5 behind the first tile of 4096 columns, in the next tile, in the last one or over both, or
+    lie across the tiles' ends; each held by one row of this side and by five."""
+    r = np.random.RandomState(n)
+    lists = []
+    for many in (129, 400):
+        for k in (0, 1, 4, 5):
+            for late in (np.arange(k) + 4097, n - 1 - np.arange(k),
+                         np.where(np.arange(k) % 2, 5000 + np.arange(k), n - 1 - np.arange(k))):
+                lists.append(np.unique(np.concatenate([r.choice(4096, many, replace=False), late])))
+    lists += [np.arange(4090, 4290), np.arange(4096 - 130, 4097), np.r_[0:127, 4095, 4096, 8191],
+              np.arange(8192 - 131, n), np.r_[4096:4224, n - 1], np.arange(0, n, 61)]
+    dim = 2 * len(lists)
+    rows = [[] for _ in range(n)]
+    for d, x in enumerate(lists):
+        for i in x:
+            rows[i] += [2 * d, 2 * d + 1]
+    other = from_rows(r, rows, dim)
+    mine = from_rows(r, [[d for d in range(dim) if d % 2 or i == d // 2 % 6] if i < 6 else
+                         [7 * i % dim] for i in range(this)], dim)
+    return mine, other
+
+
+def from_rows(r, rows, dim):
+    ptr = np.concatenate([[0], np.cumsum([len(x) for x in rows])]).astype(np.int32)
+    ix = np.concatenate([np.sort(np.array(x, np.int32)) for x in rows]).astype(np.int32)
+    return synth.HostCSR(ptr, ix, r.randn(len(ix)).astype(np.float32), len(rows), dim)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("n,this", [(8193, 6), (9000, 9), (12289, 6), (16400, 7)])
+def test_rests_of_lists_behind_a_tile(env, dtype, n, this):
+    """A long list's last few entries lie tiles behind the others: each counts once, with its own
+    column."""
+    torch, sps, dev = env
+    mine, other = rests(n, this)
+    g = torch.from_numpy(np.random.RandomState(n).randn(this, n).astype(np.float32))
+    g = g.to(getattr(torch, dtype)).to(dev)
+    g64 = g.double().cpu().numpy()
+    mc, oc = sps.CSR.from_host(mine, dev), sps.CSR.from_host(other, dev)
+    want_m, want_o = oracle(mine, other, g64, n // 256 + 4), oracle(other, mine, g64.T, 4)
+    for got_m, got_o in (sps.cosine_grad(mc, oc, g),                       # the queries' side
+                         sps.cosine_grad(oc, mc, g.t().contiguous())[::-1]):  # the items'
+        close(got_m, *want_m)
+        close(got_o, *want_o)
+
+
 def test_rows_of_many_entries(env):
     """Rows of more entries than are walked at a time, over more columns than a tile, dims up
     to the largest key."""
