@@ -107,8 +107,9 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t *best, int k) {
 
 // Puts the m candidates of `buf` into the sorted list (n of at most k): a
 // key's place is the number of larger keys. Every key is compared with the m
-// new ones, a new one with the list by bisection. Returns the list's length;
-// the list is then list[1 - cur].
+// new ones, a new one with the list by bisection; a column offered again with
+// the same score has its listed key once more and stands behind it. Returns
+// the list's length; the list is then list[1 - cur].
 __device__ __forceinline__ int merge_buf(SelShared &sh, int cur, int n, int m, int k) {
   const uint64_t *list = sh.list[cur];
   uint64_t *to = sh.list[1 - cur];
@@ -124,7 +125,7 @@ __device__ __forceinline__ int merge_buf(SelShared &sh, int cur, int n, int m, i
     int lo = 0, hi = n;
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (list[mid] > v) lo = mid + 1;
+      if (list[mid] >= v) lo = mid + 1;
       else hi = mid;
     }
     int r = lo;

@@ -119,6 +119,37 @@ def test_chunks_in_any_order(env, dtype, kind, k):
         check(top, want)
 
 
+def twice(x64, offsets, k, cols):
+    """Best k of each row's columns, `cols` of them given a second time."""
+    both = np.concatenate([x64, x64[:, cols]], 1)
+    at = np.concatenate([np.arange(x64.shape[1]), cols])
+    order = np.argsort(at, kind="stable")  # equal keys go by column
+    want = oracle(both[:, order], offsets, 1, k)
+    return want[0], want[1], np.where(want[2] < 0, -1, at[order][want[2]])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cols,k", [(1, 3), (40, 7), (40, 100), (3000, 5), (3000, 256), (70001, 90)])
+def test_columns_offered_twice(env, dtype, kind, cols, k):
+    """A column offered twice takes two places, next to each other where its key is the same;
+    other columns keep theirs."""
+    torch, sps, dev = env
+    x, x64 = make(env, 3, cols, dtype, cols + k, kind)
+    off = torch.linspace(-1, 1, 3, device=dev)
+    cut = cols // 3
+    for parts in ([(0, cols), (0, cols)], [(0, cols), (cut, cols)], [(cut, cols), (0, cols)],
+                  [(0, cols), (0, cut), (cut, cols)]):
+        top = sps.top_rows(3, k, dev)
+        for j, (a, b) in enumerate(parts):
+            sps.select_chunk(x[:, a:b], top, 5 + a, offsets=off, first=j == 0)
+        seen = np.zeros(cols, int)
+        for a, b in parts:
+            seen[a:b] += 1
+        want = twice(x64, off.cpu().numpy(), k, np.nonzero(seen == 2)[0])
+        check(top, (want[0], None, np.where(want[2] < 0, -1, want[2] + 5)))
+
+
 def test_strides_and_alignment(env):
     torch, sps, dev = env
     for dtype in TYPES:
