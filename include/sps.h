@@ -443,8 +443,8 @@ typedef struct {
  * [0, n_rows) (a place of sps_beam_select that stayed empty). One parent may
  * have many rows. parents: DEVICE int32[n_out]; states: a HOST array, read
  * before the call returns. Bytes between rows are not touched. Errors:
- * SPS_ERR_INVALID_ARGUMENT (NULL, a stride below row_bytes, a dst that
- * overlaps a src), SPS_ERR_OVERFLOW. */
+ * SPS_ERR_INVALID_ARGUMENT (NULL, a stride below row_bytes, a dst that shares
+ * a byte with a src; rows may lie between each other's), SPS_ERR_OVERFLOW. */
 sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const int32_t *parents,
                               int64_t n_out, int64_t n_rows, void *stream);
 
@@ -510,7 +510,9 @@ sps_status sps_distill_loss(sps_distill *h, float *loss, float *lse, void *strea
  * of the same columns): grad[r * ld_grad + j] = row_weights[r] * d loss_r / d
  * s[r, j], of type grad_dtype: the scores' or SPS_F32. row_weights (nullable:
  * 1): DEVICE float[n_rows], the gradient of what is minimised about each row's
- * loss. grad may be the scores themselves (same address, type and ld). */
+ * loss. grad may be the scores themselves (same address, type and ld), or
+ * share no byte with them (other columns of the matrix that holds them, say);
+ * SPS_ERR_INVALID_ARGUMENT otherwise. */
 sps_status sps_distill_chunk_grad(sps_distill *h, const sps_scores *scores,
                                   const float *row_weights, void *grad, int32_t grad_dtype,
                                   int64_t ld_grad, void *stream);

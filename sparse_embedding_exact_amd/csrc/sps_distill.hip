@@ -980,13 +980,10 @@ sps_status check_grad(const sps_scores *x, const void *grad, int32_t dtype, int6
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: gradient not aligned to its elements", what);
   if (x->n_rows > 0 && x->n_cols > 0) {
     // in place, or apart: a gradient that overlaps other scores would overwrite them unread
-    const uintptr_t s0 = reinterpret_cast<uintptr_t>(x->data), g0 = reinterpret_cast<uintptr_t>(grad);
-    const uintptr_t s1 = s0 + ((uintptr_t)(x->n_rows - 1) * x->ld + x->n_cols) *
-                                  (uintptr_t)sps::dtype_size(x->dtype);
-    const uintptr_t g1 =
-        g0 + ((uintptr_t)(x->n_rows - 1) * ld + x->n_cols) * (uintptr_t)sps::dtype_size(dtype);
-    const bool same = s0 == g0 && dtype == x->dtype && (ld == x->ld || x->n_rows == 1);
-    if (!same && g0 < s1 && s0 < g1)
+    const int64_t sx = sps::dtype_size(x->dtype), sg = sps::dtype_size(dtype);
+    const bool same = x->data == grad && dtype == x->dtype && (ld == x->ld || x->n_rows == 1);
+    if (!same && sps::rows_overlap({x->data, x->n_rows, x->n_cols * sx, x->ld * sx},
+                                   {grad, x->n_rows, x->n_cols * sg, ld * sg}))
       return set_error(SPS_ERR_INVALID_ARGUMENT,
                        "%s: the gradient overlaps the scores without being them", what);
   }

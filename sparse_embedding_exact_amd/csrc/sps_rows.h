@@ -80,6 +80,39 @@ inline sps_status check_scores(const sps_scores *s, const char *what) {
   return SPS_OK;
 }
 
+// Whether two sets of rows (n rows of `bytes` bytes, `stride` bytes apart) share a byte: rows may
+// lie between each other's, as the halves of one wide buffer do.
+struct RowBytes {
+  const void *at;
+  int64_t n, bytes, stride;
+};
+inline bool rows_overlap(RowBytes a, RowBytes b) {
+  if (a.n == 0 || b.n == 0 || a.bytes == 0 || b.bytes == 0) return false;
+  if (a.n > b.n) {
+    const RowBytes x = a;
+    a = b;
+    b = x;
+  }
+  const __int128 a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
+  const __int128 a1 = a0 + (__int128)(a.n - 1) * a.stride + a.bytes;
+  const __int128 b1 = b0 + (__int128)(b.n - 1) * b.stride + b.bytes;
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (b.n == 1) return true;
+  // row j of b starts d + j b.stride bytes behind a row of a; they share a byte where that is
+  // above -b.bytes and below a.bytes. With equal strides rows i and j stand as 0 and j - i do
+  const auto floor_div = [](__int128 x, __int128 y) { return x / y - (x % y < 0); };
+  const auto meets = [&](__int128 d, __int128 first) {
+    const __int128 least = floor_div(-b.bytes - d, b.stride) + 1;
+    const __int128 most = floor_div(a.bytes - 1 - d, b.stride);
+    return (least > first ? least : first) <= (most < b.n - 1 ? most : b.n - 1);
+  };
+  if (a.stride == b.stride) return meets(b0 - a0, 1 - a.n);
+  // ranges that meet at different strides: rare, and a launch's rows are at most 2^24
+  for (int64_t i = 0; i < a.n; ++i)
+    if (meets(b0 - a0 - (__int128)i * a.stride, 0)) return true;
+  return false;
+}
+
 // A launch's threads are counted in 32 bits.
 inline sps_status check_grid(int64_t blocks, int64_t threads, const char *what) {
   if (blocks > 4294967295ll / threads)

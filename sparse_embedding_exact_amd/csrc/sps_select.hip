@@ -845,15 +845,10 @@ sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const i
   // sources are read while the destinations are written
   for (int32_t i = 0; i < n_states; ++i) {
     const sps_state &x = states[i];
-    if (x.row_bytes == 0) continue;
-    const uintptr_t d0 = reinterpret_cast<uintptr_t>(x.dst);
-    const uintptr_t d1 = d0 + (uintptr_t)((n_out - 1) * x.dst_stride + x.row_bytes);
-    for (int32_t j = 0; j < n_states && n_rows > 0; ++j) {
+    const sps::RowBytes dst{x.dst, n_out, x.row_bytes, x.dst_stride};
+    for (int32_t j = 0; j < n_states; ++j) {
       const sps_state &y = states[j];
-      if (y.row_bytes == 0) continue;
-      const uintptr_t s0 = reinterpret_cast<uintptr_t>(y.src);
-      const uintptr_t s1 = s0 + (uintptr_t)((n_rows - 1) * y.src_stride + y.row_bytes);
-      if (d0 < s1 && s0 < d1)
+      if (sps::rows_overlap(dst, {y.src, n_rows, y.row_bytes, y.src_stride}))
         return sps::set_error(SPS_ERR_INVALID_ARGUMENT,
                               "sps_reorder_states: output %d overlaps state %d", i, j);
     }

@@ -243,6 +243,25 @@ def test_strides(env):
             assert (out[:, :5] == 7).all() and (out[:, 5 + b - a:] == 7).all()
 
 
+def test_gradient_beside_the_scores(env):
+    """Scores and their gradient in one wide matrix, chunk by chunk and whole."""
+    torch, sps, dev = env
+    for dtype in TYPES:
+        x, ids, t, w = make(env, 5, 700, 9, dtype, 21, 1.0)
+        a = (dev_of(env, ids), dev_of(env, t))
+        wide = torch.full((5, 1501), 3.0, device=dev, dtype=x.dtype)
+        wide[:, 1:701] = x
+        loss, g = sps.distill(wide[:, 1:701], *a, 0.8, out=wide[:, 701:1401])
+        compare(env, loss, g, x, ids, t, 0.8, None, None)
+        assert torch.equal(wide[:, 1:701], x) and (wide[:, 1401:] == 3).all() and (wide[:, 0] == 3).all()
+        d = sps.distill_prepare(*a, 700, 0.8)
+        sps.distill_chunk(d, wide[:, 1:701], 0, first=True)
+        loss = sps.distill_loss(d)
+        sps.distill_chunk_grad(d, wide[:, 1:701], 0, out=wide[:, 701:1401])
+        compare(env, loss, g, x, ids, t, 0.8, None, None)
+        assert torch.equal(wide[:, 1:701], x) and (wide[:, 1401:] == 3).all()
+
+
 def test_against_differences(env):
     """The kernels' gradient against differences of the kernels' own losses: a step of 2^-4
     changes float32 losses near 5 by parts that float32 still resolves."""

@@ -286,6 +286,19 @@ def test_reorder_many_strided(env):
         assert (edges[:, 0] == -7).all() and (edges[:, -2:] == -7).all()
 
 
+def test_reorder_inside_one_buffer(env):
+    """From one half of a buffer to the other, the halves' rows side by side."""
+    torch, sps, dev = env
+    par = torch.tensor([3, 3, -1, 0, 1], dtype=torch.int32, device=dev)
+    for width in (1, 7, 64, 5000):
+        t = torch.arange(5 * 2 * width, device=dev, dtype=torch.int32).view(5, 2, width)
+        was = t.clone()
+        out = sps.reorder_states([t[:, 0]], par, [t[:, 1]])[0]
+        want = was[:, 0][par.clamp(min=0).long()] * (par >= 0).view(-1, 1)
+        assert torch.equal(out, want) and torch.equal(t[:, 1], want)
+        assert torch.equal(t[:, 0], was[:, 0])
+
+
 def test_reorder_refuses_overlap(env):
     torch, sps, dev = env
     t = torch.zeros(8, 16, device=dev)

@@ -1,8 +1,10 @@
 """The refusals of the entry points on rows of scores, without a GPU: every
 call here returns its documented status before any device work."""
 import ctypes
+import random
 
 import pytest
+import torch
 
 import sparse_embedding_exact_amd as sps
 
@@ -109,6 +111,50 @@ def test_reorder_counts(lib):
     # an output that overlaps another state's source
     two = (ctypes.c_int64 * 10)(*state(), *state(src=8 * P, dst=P + 64))
     assert lib.sps_reorder_states(two, 2, P, 8, 8, None) == INV
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls that are accepted would launch")
+def test_rows_that_share_bytes(lib):
+    """Refused if and only if two rows share a byte; calls that are not refused end at the launch,
+    for want of a GPU."""
+    r = random.Random(0)
+    counts = {}
+    for i in range(30000):
+        n_src, n_out, row = r.randint(0, 5), r.randint(1, 5), r.randint(0, 9)
+        ss = r.randint(row, 15)
+        ds = ss if r.random() < 0.5 else r.randint(row, 15)
+        src, dst = P + r.randint(0, 120), P + 60
+        shared = meet(src, n_src, row, ss, dst, n_out, row, ds)
+        st = state(src=src, dst=dst, row=row, ss=ss, ds=ds)
+        got = lib.sps_reorder_states(ctypes.byref(st), 1, P, n_out, n_src, None)
+        assert (got == INV) == shared, (src - P, row, ss, ds, n_src, n_out)
+        counts[ss == ds, shared] = counts.get((ss == ds, shared), 0) + 1
+    assert min(counts.values()) > 2000 and len(counts) == 4
+
+
+def meet(a, na, la, sa, b, nb, lb, sb):
+    one = {a + i * sa + x for i in range(na) for x in range(la)}
+    return any(b + j * sb + x in one for j in range(nb) for x in range(lb))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls that are accepted would launch")
+def test_gradient_beside_the_scores(lib):
+    """A gradient may stand in other columns of the wide matrix that holds the scores."""
+    both = set()
+    for dtype, gtype in ((0, 0), (1, 1), (1, 0), (2, 2)):
+        size, gsize = 2 if dtype else 4, 2 if gtype else 4
+        for rows in (1, 2, 8):
+            for ld in (100, 200, 201, 300, 400):
+                for gld in (100, 150, ld, ld // 2, ld + 1):
+                    for at in (-gld, -101, -100, -99, -50, 0, 50, 99, 100, 101, 200, 300, 301, 9 * ld):
+                        g = P + at * gsize
+                        same = at == 0 and dtype == gtype and (ld == gld or rows == 1)
+                        want = gld < 100 or not same and meet(P, rows, 100 * size, ld * size, g, rows,
+                                                              100 * gsize, gld * gsize)
+                        got = rows_call(lib, view(rows=rows, ld=ld, dtype=dtype), grad=g, gtype=gtype, ld=gld)
+                        assert (got == INV) == want, (dtype, gtype, rows, ld, gld, at)
+                        both.add((want, ld * size == gld * gsize))
+    assert len(both) == 4
 
 
 def test_nothing_to_do(lib):
