@@ -444,7 +444,8 @@ typedef struct {
  * have many rows. parents: DEVICE int32[n_out]; states: a HOST array, read
  * before the call returns. Bytes between rows are not touched. Errors:
  * SPS_ERR_INVALID_ARGUMENT (NULL, a stride below row_bytes, a dst that shares
- * a byte with a src; rows may lie between each other's), SPS_ERR_OVERFLOW. */
+ * a byte with a src, another dst or the parents; rows may lie between each
+ * other's), SPS_ERR_OVERFLOW. */
 sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const int32_t *parents,
                               int64_t n_out, int64_t n_rows, void *stream);
 

@@ -739,8 +739,8 @@ def reorder_states(states, parents: torch.Tensor, outs=None, stream=None) -> lis
     """States follow their parents: out[j] = state[parents[j]] for every tensor of `states`
     (first dimension the beams' rows, each row contiguous, any types), zeros where parents[j]
     is no row. parents: int32, any shape (BeamStep.parents). Returns the outs (allocated if
-    not given; they may share no byte with a state, but lie beside them in one
-    buffer: t[:, 1] for t[:, 0])."""
+    not given; they may share no byte with a state, the parents or each other, but lie
+    beside them in one buffer: t[:, 1] for t[:, 0])."""
     load_library()
     states = list(states)
     dev = _here(parents, *states)

@@ -842,15 +842,21 @@ sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const i
     if ((x.row_bytes + sps::kPieceBytes - 1) / sps::kPieceBytes > kMaxPieces / n_out)
       return sps::set_error(SPS_ERR_OVERFLOW, "sps_reorder_states: state %d exceeds a launch", i);
   }
-  // sources are read while the destinations are written
+  // sources are read while the destinations are written, and those in no order
   for (int32_t i = 0; i < n_states; ++i) {
     const sps_state &x = states[i];
     const sps::RowBytes dst{x.dst, n_out, x.row_bytes, x.dst_stride};
+    if (sps::rows_overlap(dst, {parents, 1, n_out * 4, n_out * 4}))
+      return sps::set_error(SPS_ERR_INVALID_ARGUMENT,
+                            "sps_reorder_states: output %d overlaps the parents", i);
     for (int32_t j = 0; j < n_states; ++j) {
       const sps_state &y = states[j];
       if (sps::rows_overlap(dst, {y.src, n_rows, y.row_bytes, y.src_stride}))
         return sps::set_error(SPS_ERR_INVALID_ARGUMENT,
                               "sps_reorder_states: output %d overlaps state %d", i, j);
+      if (j < i && sps::rows_overlap(dst, {y.dst, n_out, y.row_bytes, y.dst_stride}))
+        return sps::set_error(SPS_ERR_INVALID_ARGUMENT,
+                              "sps_reorder_states: output %d overlaps output %d", i, j);
     }
   }
   int32_t i = 0;

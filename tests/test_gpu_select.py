@@ -297,6 +297,9 @@ def test_reorder_inside_one_buffer(env):
         want = was[:, 0][par.clamp(min=0).long()] * (par >= 0).view(-1, 1)
         assert torch.equal(out, want) and torch.equal(t[:, 1], want)
         assert torch.equal(t[:, 0], was[:, 0])
+    with pytest.raises(sps.SpsError):  # two outputs in one place
+        a, o = torch.zeros(2, 5, 8, device=dev), torch.zeros(5, 12, device=dev)
+        sps.reorder_states([a[0], a[1]], par, [o[:, :8], o[:, 4:]])
 
 
 def test_reorder_refuses_overlap(env):

@@ -113,6 +113,18 @@ def test_reorder_counts(lib):
     assert lib.sps_reorder_states(two, 2, P, 8, 8, None) == INV
 
 
+def test_reorder_outputs_that_overlap(lib):
+    """Two outputs that share bytes would be written in no order."""
+    for off, ds in ((0, 64), (8, 64), (-63, 64), (7 * 64 + 63, 64), (100, 128), (1, 65)):
+        two = (ctypes.c_int64 * 10)(*state(src=0x100000, dst=0x900000, ds=ds),
+                                    *state(src=0x200000, dst=0x900000 + off, ds=ds))
+        assert lib.sps_reorder_states(two, 2, P, 8, 8, None) == INV, (off, ds)
+    # nor may the parents be written over while they are read
+    for at in (0x900000, 0x900000 - 28, 0x900000 + 7 * 64 + 60):
+        one = state(src=0x100000, dst=0x900000)
+        assert lib.sps_reorder_states(ctypes.byref(one), 1, at, 8, 8, None) == INV
+
+
 @pytest.mark.skipif(torch.cuda.is_available(), reason="calls that are accepted would launch")
 def test_rows_that_share_bytes(lib):
     """Refused if and only if two rows share a byte; calls that are not refused end at the launch,
