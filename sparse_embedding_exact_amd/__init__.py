@@ -585,6 +585,11 @@ def _here(*tensors) -> int:
     return cur
 
 
+def _parts(m) -> list:
+    """The tensors of a CSR (or BSC)."""
+    return [t for t in vars(m).values() if isinstance(t, torch.Tensor)]
+
+
 # torch's own way to the current stream's handle, without a Stream object a call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -773,6 +778,7 @@ def reorder_states(states, parents: torch.Tensor, outs=None, stream=None) -> lis
 def bulk_select(queries: CSR, items: CSR, k: int, chunk_size: int = 8192) -> TopRows:
     """The best k items of every query, of all of them (exact): every chunk scored and
     joined to the running lists. The score matrix is never kept; bulk_similarity's loop."""
+    _here(*_parts(queries), *_parts(items))
     it = prepare(items, chunk_size)
     q = prepare_queries(queries, it)
     dev = queries.indptr.device
@@ -839,7 +845,7 @@ def distill_chunk(d: Distill, scores: torch.Tensor, col_begin: int = 0, first: b
                   stream=None) -> None:
     """Take in the student's scores of columns [col_begin, col_begin + scores.shape[1]); every
     column once, in any order of the chunks. first=True forgets what came before."""
-    dev = _here(scores)
+    dev = _here(scores, d._ws)
     v = _view(scores, col_begin)
     _check(_lib.sps_distill_chunk(d._h, ctypes.byref(v), int(first), _stream_of(dev, stream)))
 
@@ -868,7 +874,7 @@ def distill_chunk_grad(d: Distill, scores: torch.Tensor, col_begin: int = 0,
                        stream=None) -> torch.Tensor:
     """row_weights[r] * d loss_r / d scores[r, j] of a chunk, after distill_loss of the same
     scores. out: of the scores' type or float32, may be `scores` itself."""
-    dev = _here(scores, row_weights, out)
+    dev = _here(scores, row_weights, out, d._ws)
     v = _view(scores, col_begin)
     w = _rows_f32(row_weights, v.n_rows, "row_weights")
     with _on(stream):
@@ -916,7 +922,7 @@ def cosine_chunk_grad(rows: CSR, other: Items, chunk: int, grad: torch.Tensor, d
     the queries prepared as a corpus. first=True starts the sums; cosine_grad_values ends
     them."""
     load_library()
-    dev = _here(rows.values, grad, du)
+    dev = _here(*_parts(rows), other._persistent, grad, du)
     assert du.dtype == torch.float32 and du.is_contiguous() and du.numel() == rows.nnz
     v = _view(grad)
     c = rows._c()
@@ -935,7 +941,7 @@ def cosine_grad_values(rows: CSR, du: torch.Tensor, out: torch.Tensor | None = N
     """The gradient about the stored values from that about the unit values (the norm's
     part taken off); out may be du itself."""
     load_library()
-    dev = _here(rows.values, du, out)
+    dev = _here(*_parts(rows), du, out)
     assert du.dtype == torch.float32 and du.is_contiguous() and du.numel() == rows.nnz
     with _on(stream):
         if out is None:
@@ -953,7 +959,7 @@ def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, stream=None):
     bfloat16. The stored structure of both is fixed. Nothing is prepared: a training step's
     batch has new values each time."""
     load_library()
-    dev = _here(queries.values, items.values, grad)
+    dev = _here(*_parts(queries), *_parts(items), grad)
     v = _view(grad)
     q, i = queries._c(), items._c()
     nb = _sized("sps_cosine_grad_both_workspace_size", q.nnz, i.nnz)
@@ -976,6 +982,7 @@ def bulk_distill(queries: CSR, items: CSR, teacher_ids: torch.Tensor,
     cosines / temperature against the teacher's best k of every query (bulk_select's lists of
     another scorer, say). bulk_similarity's loop, twice: once for the sums, once for the
     gradients, with one chunk of scores kept."""
+    _here(*_parts(queries), *_parts(items), teacher_ids, teacher_logits, teacher_lse, row_weights)
     it = prepare(items, chunk_size)
     q = prepare_queries(queries, it)
     qt = prepare(queries, max(min(chunk_size, queries.n_rows), 1))
