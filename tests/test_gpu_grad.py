@@ -393,3 +393,26 @@ def test_distillation_of_a_corpus(env):
         scale = float(np.abs(got.double().cpu().numpy() * v).sum())
         # h^2 of the third derivative along a unit-size direction; float32 work of many entries
         assert abs(diff - d) <= 1e-4 * scale + 1e-9
+
+
+@pytest.mark.parametrize("nq,ni,per_row", [(0, 5, 3), (5, 0, 3), (0, 0, 3), (5, 7, 0), (1, 1, 1)])
+def test_corpus_calls_of_nothing(env, nq, ni, per_row):
+    """No queries, no items, no entries: best lists, losses and gradients of the same sizes."""
+    torch, sps, dev = env
+    r = np.random.RandomState(nq + ni)
+    q, it = corpus(r, nq, 9, lambda i: per_row, False), corpus(r, ni, 9, lambda i: per_row, False)
+    qc, ic = sps.CSR.from_host(q, dev), sps.CSR.from_host(it, dev)
+    top = sps.bulk_select(qc, ic, 3)
+    n = min(ni, 3)
+    assert top.cols.shape == (nq, 3) and (top.cols[:, n:] == -1).all()
+    assert (top.cols[:, :n] >= 0).all() and (top.scores[:, n:] == -np.inf).all()
+    ids = torch.zeros(nq, 2, dtype=torch.int32, device=dev)
+    loss, gq, gi = sps.bulk_distill(qc, ic, ids, torch.zeros(nq, 2, device=dev), 0.1)
+    assert loss.shape == (nq,) and gq.shape == (qc.nnz,) and gi.shape == (ic.nnz,)
+    scores = sps.bulk_similarity(qc, ic) if nq and ni else torch.zeros(nq, ni, device=dev)
+    want, g, l_bound, _ = do.batch(scores.double().cpu().numpy(), ids.cpu().numpy(), np.zeros((nq, 2)), 0.1)
+    assert (np.abs(loss.double().cpu().numpy() - want) <= l_bound + 4 * U).all()
+    gq2, gi2 = sps.cosine_grad(qc, ic, torch.from_numpy(g.astype(np.float32)).view(nq, ni).to(dev))
+    assert gq2.shape == gq.shape and gi2.shape == gi.shape
+    for a in (gq, gi, gq2, gi2):
+        assert torch.isfinite(a).all()
