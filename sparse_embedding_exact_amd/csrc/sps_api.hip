@@ -21,17 +21,19 @@
 constexpr int64_t kStaticScratchDoubles = 1 << 19;  // 4 MiB
 static __device__ __align__(256) double scratch[kStaticScratchDoubles];
 
-namespace {
+static thread_local char g_err[512] = "";
 
-thread_local char g_err[512] = "";
-
-sps_status fail(sps_status s, const char *fmt, ...) {
+int32_t sps::set_error(int32_t status, const char *fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof g_err, fmt, ap);
   va_end(ap);
-  return s;
+  return status;
 }
+
+namespace {
+
+constexpr auto &fail = sps::set_error;
 
 sps_status hip_fail(hipError_t e, const char *where) {
   return fail(SPS_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
@@ -205,14 +207,6 @@ struct sps_queries {
   int32_t qh_gstride;  // halves per row group in qh
   double *rs_part;
 };
-
-int32_t sps::set_error(int32_t status, const char *fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof g_err, fmt, ap);
-  va_end(ap);
-  return status;
-}
 
 namespace {
 // halves per 16-row group of a query batch's heavy-dim tiles: one tile per

@@ -56,7 +56,6 @@ struct DistillDev {
   int32_t k, slots;
   float c;        // log2(e) / temperature
   double inv_tau;
-  bool rest;      // the teacher's mass outside its list is known
   int32_t *sid;   // [rows][k]: column, -1 where the entry takes no part
   float *p;       // [rows][k]
   float *x;       // [rows][k]: the student's score of the entry
@@ -883,8 +882,8 @@ sps_status check_sizes(int64_t n_rows, int32_t k, const char *what) {
 }
 
 // the checks of a list and its workspace; fills d
-sps_status make_dev(const int32_t *ids, const float *logits, const float *lse, int64_t n_rows,
-                    int32_t k, int64_t n_cols, float tau, void *ws, size_t bytes, const char *what,
+sps_status make_dev(const int32_t *ids, const float *logits, int64_t n_rows, int32_t k,
+                    int64_t n_cols, float tau, void *ws, size_t bytes, const char *what,
                     DistillDev *d) {
   sps_status st = check_sizes(n_rows, k, what);
   if (st != SPS_OK) return st;
@@ -908,7 +907,6 @@ sps_status make_dev(const int32_t *ids, const float *logits, const float *lse, i
   d->slots = slots_of(n_rows);
   d->c = (float)(1.44269504088896340736 / (double)tau);
   d->inv_tau = 1.0 / (double)tau;
-  d->rest = lse != nullptr;
   d->sid = reinterpret_cast<int32_t *>(b + L.sid);
   d->p = reinterpret_cast<float *>(b + L.p);
   d->x = reinterpret_cast<float *>(b + L.x);
@@ -1066,7 +1064,7 @@ sps_status sps_distill_prepare(const int32_t *ids, const float *logits, const fl
   if (!out) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output handle pointer");
   *out = nullptr;
   DistillDev d{};
-  sps_status st = make_dev(ids, logits, teacher_lse, n_rows, k, n_cols, temperature, workspace,
+  sps_status st = make_dev(ids, logits, n_rows, k, n_cols, temperature, workspace,
                            workspace_bytes, "sps_distill_prepare", &d);
   if (st != SPS_OK) return st;
   sps_distill *h = new (std::nothrow) sps_distill;
@@ -1126,8 +1124,8 @@ sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const 
   if (scores->col_begin != 0)
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: rows must be whole (col_begin 0)", what);
   DistillDev d{};
-  st = make_dev(ids, logits, teacher_lse, scores->n_rows, k, scores->n_cols, temperature,
-                workspace, workspace_bytes, what, &d);
+  st = make_dev(ids, logits, scores->n_rows, k, scores->n_cols, temperature, workspace,
+                workspace_bytes, what, &d);
   if (st != SPS_OK) return st;
   if (grad) st = check_grad(scores, grad, grad_dtype, ld_grad, what);
   if (st != SPS_OK) return st;
