@@ -521,9 +521,15 @@ sps_status sps_distill_chunk_grad(sps_distill *h, const sps_scores *scores,
 /* Free the host handle (never the caller's workspace). NULL is ignored. */
 void sps_distill_destroy(sps_distill *h);
 
+/* Bytes of the workspace of sps_distill_rows (256 where one launch takes the
+ * rows and keeps nothing there; never above sps_distill_workspace_size's). Pure
+ * host. */
+sps_status sps_distill_rows_workspace_size(int64_t n_rows, int64_t n_cols, int32_t k,
+                                           size_t *bytes);
+
 /* All of the above for rows that are whole (asynchronous): scores->col_begin
  * is 0 and its n_cols the whole. loss and grad as above (grad nullable: the
- * losses alone). workspace: as for sps_distill_prepare, free again once the
+ * losses alone). workspace: DEVICE, 256-byte aligned, free again once the
  * stream work has completed. */
 sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const float *logits,
                             const float *teacher_lse, int32_t k, float temperature,

@@ -107,6 +107,7 @@ SIGNATURES = {
     "sps_beam_join": (_I32, [_P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),
     "sps_reorder_states": (_I32, [_P, _I32, _P, _I64, _I64, _P]),
     "sps_distill_workspace_size": (_I32, [_I64, _I32, ctypes.POINTER(_SZ)]),
+    "sps_distill_rows_workspace_size": (_I32, [_I64, _I64, _I32, ctypes.POINTER(_SZ)]),
     "sps_distill_prepare": (_I32, [_P, _P, _P, _I64, _I32, _I64, ctypes.c_float, _P, _SZ, _P,
                                    ctypes.POINTER(_P)]),
     "sps_distill_chunk": (_I32, [_P, ctypes.POINTER(_Scores), _I32, _P]),
@@ -896,7 +897,7 @@ def distill(scores: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: tor
     n, k, lse = _teacher(teacher_ids, teacher_logits, teacher_lse)
     assert n == v.n_rows, "one list a row"
     w = _rows_f32(row_weights, n, "row_weights")
-    nb = _sized("sps_distill_workspace_size", n, k)
+    nb = _sized("sps_distill_rows_workspace_size", n, v.n_cols, k)
     with _on(stream):
         loss = torch.empty(n, dtype=torch.float32, device=scores.device)
         ld = 0

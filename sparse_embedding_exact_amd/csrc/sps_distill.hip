@@ -881,25 +881,38 @@ sps_status check_sizes(int64_t n_rows, int32_t k, const char *what) {
   return sps::check_grid(n_rows, 1024, what);
 }
 
-// the checks of a list and its workspace; fills d
-sps_status make_dev(const int32_t *ids, const float *logits, int64_t n_rows, int32_t k,
-                    int64_t n_cols, float tau, void *ws, size_t bytes, const char *what,
-                    DistillDev *d) {
-  sps_status st = check_sizes(n_rows, k, what);
-  if (st != SPS_OK) return st;
+sps_status check_cols(int64_t n_cols, const char *what) {
   if (n_cols < 0) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: negative size", what);
   if (n_cols >= kMax31) return set_error(SPS_ERR_OVERFLOW, "%s: columns must be below 2^31", what);
+  return SPS_OK;
+}
+
+bool one_launch(int64_t n_rows, int64_t n_cols) {
+  return n_cols <= kOneTile || n_rows >= kManyRows;
+}
+// Whole rows in one launch keep nothing between kernels; the call still asks for an aligned
+// workspace, the least there is.
+size_t rows_bytes(int64_t n_rows, int64_t n_cols, int32_t k) {
+  if (n_rows == 0) return 0;
+  return one_launch(n_rows, n_cols) ? 256 : layout_of(n_rows, k).total;
+}
+
+// the checks of a list and its workspace of `need` bytes; fills d
+sps_status make_dev(const int32_t *ids, const float *logits, int64_t n_rows, int32_t k,
+                    int64_t n_cols, float tau, void *ws, size_t bytes, size_t need,
+                    const char *what, DistillDev *d) {
+  const sps_status st = check_cols(n_cols, what);
+  if (st != SPS_OK) return st;
   if (!(tau >= 1e-6f && tau <= 1e6f))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: temperature must be in [1e-6, 1e6]", what);
   if (n_rows > 0 && (!ids || !logits))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL list", what);
-  const Layout L = layout_of(n_rows, k);
   if (n_rows > 0 && !ws) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL workspace", what);
-  if (bytes < L.total)
-    return set_error(SPS_ERR_WORKSPACE_TOO_SMALL, "%s: need %zu bytes, got %zu", what, L.total,
-                     bytes);
+  if (bytes < need)
+    return set_error(SPS_ERR_WORKSPACE_TOO_SMALL, "%s: need %zu bytes, got %zu", what, need, bytes);
   if (reinterpret_cast<uintptr_t>(ws) & 255)
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", what);
+  const Layout L = layout_of(n_rows, k);
   char *b = static_cast<char *>(ws);
   d->n_rows = n_rows;
   d->n_cols = n_cols;
@@ -1057,22 +1070,36 @@ sps_status sps_distill_workspace_size(int64_t n_rows, int32_t k, size_t *bytes) 
   return SPS_OK;
 }
 
+sps_status sps_distill_rows_workspace_size(int64_t n_rows, int64_t n_cols, int32_t k,
+                                           size_t *bytes) {
+  const char *what = "sps_distill_rows_workspace_size";
+  if (!bytes) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output pointer");
+  sps_status st = check_sizes(n_rows, k, what);
+  if (st == SPS_OK) st = check_cols(n_cols, what);
+  if (st != SPS_OK) return st;
+  *bytes = rows_bytes(n_rows, n_cols, k);
+  return SPS_OK;
+}
+
 sps_status sps_distill_prepare(const int32_t *ids, const float *logits, const float *teacher_lse,
                                int64_t n_rows, int32_t k, int64_t n_cols, float temperature,
                                void *workspace, size_t workspace_bytes, void *stream,
                                sps_distill **out) {
   if (!out) return set_error(SPS_ERR_INVALID_ARGUMENT, "NULL output handle pointer");
   *out = nullptr;
+  const char *what = "sps_distill_prepare";
   DistillDev d{};
-  sps_status st = make_dev(ids, logits, n_rows, k, n_cols, temperature, workspace,
-                           workspace_bytes, "sps_distill_prepare", &d);
+  sps_status st = check_sizes(n_rows, k, what);
+  if (st != SPS_OK) return st;
+  st = make_dev(ids, logits, n_rows, k, n_cols, temperature, workspace, workspace_bytes,
+                layout_of(n_rows, k).total, what, &d);
   if (st != SPS_OK) return st;
   sps_distill *h = new (std::nothrow) sps_distill;
   if (!h) return set_error(SPS_ERR_INVALID_ARGUMENT, "out of host memory");
   h->d = d;
   if (n_rows > 0) {
     launch_prepare(d, ids, logits, teacher_lse, reinterpret_cast<hipStream_t>(stream));
-    st = sps::launch_status("sps_distill_prepare");
+    st = sps::launch_status(what);
     if (st != SPS_OK) {
       delete h;
       return st;
@@ -1124,15 +1151,17 @@ sps_status sps_distill_rows(const sps_scores *scores, const int32_t *ids, const 
   if (scores->col_begin != 0)
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: rows must be whole (col_begin 0)", what);
   DistillDev d{};
+  st = check_sizes(scores->n_rows, k, what);
+  if (st != SPS_OK) return st;
   st = make_dev(ids, logits, scores->n_rows, k, scores->n_cols, temperature, workspace,
-                workspace_bytes, what, &d);
+                workspace_bytes, rows_bytes(scores->n_rows, scores->n_cols, k), what, &d);
   if (st != SPS_OK) return st;
   if (grad) st = check_grad(scores, grad, grad_dtype, ld_grad, what);
   if (st != SPS_OK) return st;
   if (d.n_rows == 0) return SPS_OK;
   if (!loss) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL loss", what);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (scores->n_cols <= kOneTile || scores->n_rows >= kManyRows) {
+  if (one_launch(scores->n_rows, scores->n_cols)) {
     sps::RowsArgs a{};
     a.x = scores->data;
     a.g = scores->n_cols > 0 ? grad : nullptr;

@@ -262,6 +262,20 @@ def test_gradient_beside_the_scores(env):
         assert torch.equal(wide[:, 1:701], x) and (wide[:, 1401:] == 3).all()
 
 
+def test_memory_of_whole_rows(env):
+    """Rows in one launch need their outputs' memory, not the lists' again."""
+    torch, sps, dev = env
+    x, ids, t, _ = make(env, 600, 2000, 1024, "float32", 6, 1.0)
+    a = (dev_of(env, ids), dev_of(env, t))
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    loss, grad = sps.distill(x, *a, 0.8)
+    more = torch.cuda.max_memory_allocated() - before
+    assert more <= grad.numel() * 4 + loss.numel() * 4 + 8192  # the lists' workspace: 7.4 MB
+    compare(env, loss, grad, x, ids, t, 0.8, None, None, range(4))
+
+
 def test_against_differences(env):
     """The kernels' gradient against differences of the kernels' own losses: a step of 2^-4
     changes float32 losses near 5 by parts that float32 still resolves."""

@@ -225,6 +225,34 @@ def test_distill_rows_refusals(lib, kw, want):
                                 None, P, None, 0, 0, a["ws"], a["bytes_"], None) == want
 
 
+def rows_size(lib, n, cols, k):
+    b = ctypes.c_size_t()
+    assert lib.sps_distill_rows_workspace_size(n, cols, k, ctypes.byref(b)) == 0
+    return b.value
+
+
+def test_distill_rows_sizes(lib):
+    """Rows that one launch takes keep nothing in the workspace."""
+    b = ctypes.c_size_t()
+    for n, cols, k in ((8, 100, 16), (10000, 8192, 1024), (4, 32768, 1024), (128, 10**6, 64)):
+        assert rows_size(lib, n, cols, k) == 256
+        if not torch.cuda.is_available():  # accepted: ends at the launch, for want of a GPU
+            st = lib.sps_distill_rows(view(rows=n, cols=cols, ld=cols), P, P, None, k, 1.0, None, P, None,
+                                      0, 0, P, 256, None)
+            assert st not in (0, INV, WS, OVF)
+    for n, cols, k in ((4, 32769, 16), (127, 10**6, 1024)):
+        assert rows_size(lib, n, cols, k) == size(lib, n, k)
+        assert lib.sps_distill_rows(view(rows=n, cols=cols, ld=cols), P, P, None, k, 1.0, None, P, None, 0,
+                                    0, P, size(lib, n, k) - 1, None) == WS
+    assert rows_size(lib, 0, 100, 16) == 0
+    assert lib.sps_distill_rows(view(rows=0, data=None), None, None, None, 16, 1.0, None, None, None, 0, 0,
+                                None, 0, None) == 0
+    for n, cols, k, want in ((-1, 9, 4, INV), (9, -1, 4, INV), (9, 9, 0, INV), (9, 9, 1025, INV),
+                             (2**31, 9, 4, OVF), (9, 2**31, 4, OVF), (2**23, 9, 4, OVF)):
+        assert lib.sps_distill_rows_workspace_size(n, cols, k, ctypes.byref(b)) == want
+    assert lib.sps_distill_rows_workspace_size(9, 9, 4, None) == INV
+
+
 def rows_call(lib, v, loss=P, grad=None, gtype=0, ld=100):
     return lib.sps_distill_rows(v, P, P, None, 16, 1.0, None, loss, grad, gtype, ld, P, 1 << 30, None)
 
