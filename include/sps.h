@@ -473,10 +473,13 @@ sps_status sps_reorder_states(const sps_state *states, int32_t n_states, const i
  * has.
  * A row without any entry left, or whose scores are all -inf, has loss 0 and
  * gradient 0. A score of -inf has q = 0 and gradient 0 outside the list; a
- * listed one with p > 0 makes the loss +inf. NaN (and +inf scores) make their
- * own row's loss and gradient NaN. Sums and the statistics of the softmax are
- * kept in float32 per thread and float64 beyond; gradients are rounded once to
- * their type. Results are bitwise reproducible. */
+ * listed one with p > 0 (in float64) makes the loss +inf. So does p_rest > 0
+ * where no column outside the list has a score, be it only what a rounded
+ * teacher_lse leaves of 1: a list of every column goes without teacher_lse.
+ * NaN (and +inf scores) make their own row's loss and gradient NaN. Sums and
+ * the statistics of the softmax are kept in float32 per thread and float64
+ * beyond; gradients are rounded once to their type. Results are bitwise
+ * reproducible. */
 
 /* Opaque host handle of a batch's lists and running statistics. */
 typedef struct sps_distill sps_distill;

@@ -826,7 +826,9 @@ def distill_prepare(teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, n_c
     distill_chunk for every chunk, distill_loss, distill_chunk_grad for every chunk. ids
     outside [0, n_cols) (pad with -1), an id's repetitions in its row and logits of -inf take
     no part. With teacher_lse (the teacher's log-sum-exp of logits / temperature over all
-    columns) its mass outside the list is one more class; without, the list's is all."""
+    columns) its mass outside the list is one more class; without, the list's is all (a list
+    of every column that has a score goes without: what rounding leaves of 1 would have no
+    column to go to, an infinite loss). The temperature is used as the nearest float32."""
     load_library()
     cur = _here(teacher_ids, teacher_logits, teacher_lse)
     n, k, lse = _teacher(teacher_ids, teacher_logits, teacher_lse)

@@ -165,9 +165,13 @@ __device__ __forceinline__ RowTeach teach_row(const int32_t *__restrict__ ids,
     }
   block_sums<NT>(v, sh.wd);
   const double sum = v[0], scale = lse ? 1.0 : 1.0 / sum;
+  // a mass below float32's range stays above 0: a listed column whose score is -inf makes the
+  // loss +inf whatever its mass
+  constexpr double kLeast = 1.401298464324817e-45;
   for (int i = t; i < k; i += NT) {
     if (i > t) mine = exp((double)sh.p[i] * inv_tau - shift);
-    sh.p[i] = sh.sid[i] >= 0 ? (float)(mine * scale) : 0.0f;
+    const double p = mine * scale;
+    sh.p[i] = sh.sid[i] >= 0 ? (float)(p > 0 && p < kLeast ? kLeast : p) : 0.0f;
   }
   RowTeach r;
   r.has = v[2] != 0;

@@ -262,6 +262,38 @@ def test_gradient_beside_the_scores(env):
         assert torch.equal(wide[:, 1:701], x) and (wide[:, 1401:] == 3).all()
 
 
+@pytest.mark.parametrize("chunked", [False, True])
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("cols", [700, 40000])
+def test_masses_below_float32(env, chunked, rest, cols):
+    """A sharp teacher's last entries have masses of e^-50 to e^-700: next to nothing where the
+    student has the column, an infinite loss where it is struck out."""
+    torch, sps, dev = env
+    x, ids, t, w = make(env, 7, cols, 4, "float32", 13, 0.05)
+    ids[:] = np.arange(4) * 31
+    tau = 0.01
+    t[:] = [0.0, -0.02, -0.01, 0.0]
+    for i, gap in enumerate((0.5, 0.85, 0.95, 1.05, 1.5, 7.0, 1.5)):
+        t[i, 3] = -gap
+        if i < 6:
+            x[i, ids[i, 3]] = -np.inf
+    lse = teacher_lse(ids, t, tau, cols, 0.6, 1) if rest else None
+    a = (dev_of(env, ids), dev_of(env, t))
+    if chunked:
+        d = sps.distill_prepare(*a, cols, tau, dev_of(env, lse))
+        sps.distill_chunk(d, x[:, :300], 0, first=True)
+        sps.distill_chunk(d, x[:, 300:], 300)
+        loss = sps.distill_loss(d)
+        grad = torch.cat([sps.distill_chunk_grad(d, x[:, :300], 0, dev_of(env, w)),
+                          sps.distill_chunk_grad(d, x[:, 300:], 300, dev_of(env, w))], 1)
+    else:
+        loss, grad = sps.distill(x, *a, tau, dev_of(env, lse), row_weights=dev_of(env, w))
+    assert (loss[:6] == np.inf).all() and torch.isfinite(loss[6]) and torch.isfinite(grad).all()
+    # the temperature is a float32 (a mass of e^-50 moves by 50 parts in 2^25 with its rounding,
+    # which is the definition's, not an error)
+    compare(env, loss, grad, x, ids, t, float(np.float32(tau)), lse, w)
+
+
 def test_memory_of_whole_rows(env):
     """Rows in one launch need their outputs' memory, not the lists' again."""
     torch, sps, dev = env
