@@ -304,7 +304,9 @@ def test_memory_of_whole_rows(env):
     before = torch.cuda.memory_allocated()
     loss, grad = sps.distill(x, *a, 0.8)
     more = torch.cuda.max_memory_allocated() - before
-    assert more <= grad.numel() * 4 + loss.numel() * 4 + 8192  # the lists' workspace: 7.4 MB
+    # torch counts whole blocks: of 512 bytes up to 1 MiB, above it (the gradient) a kept block
+    # whose rest below 1 MiB is not cut off. The lists' workspace would be 7.4 MB
+    assert more <= grad.numel() * 4 + loss.numel() * 4 + 2**20 + 8192
     compare(env, loss, grad, x, ids, t, 0.8, None, None, range(4))
 
 
