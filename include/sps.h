@@ -586,8 +586,10 @@ sps_status sps_cosine_grad_both_workspace_size(int64_t nnz_queries, int64_t nnz_
  * fewer than 2^31 - 2^16 entries. workspace:
  * DEVICE, 256-byte aligned, used until the call's stream work is done. Sums
  * are float32 in a fixed order, those of the norms float64: bitwise
- * reproducible. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,
- * SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW. */
+ * reproducible. The CSRs are taken as canonical (sps_validate_csr): no check is
+ * made here, and the gradients of one that is not are undefined. A row with a du
+ * that is not finite has no finite gradient (infinite or NaN). Errors: SPS_ERR_INVALID_ARGUMENT,
+ * SPS_ERR_DIM_MISMATCH, SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW. */
 sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
                                 const sps_scores *grad, float *grad_queries, float *grad_items,
                                 void *workspace, size_t workspace_bytes, void *stream);

@@ -960,7 +960,8 @@ def cosine_grad(queries: CSR, items: CSR, grad: torch.Tensor, stream=None):
     """(gradient of the queries' values, gradient of the items' values), float32 (nnz,) each,
     from the gradient of their whole score matrix (n_query, n_item): float32, float16 or
     bfloat16. The stored structure of both is fixed. Nothing is prepared: a training step's
-    batch has new values each time."""
+    batch has new values each time. Nothing is checked on the device either: the gradients of
+    a CSR that is not canonical are undefined."""
     load_library()
     dev = _here(*_parts(queries), *_parts(items), grad)
     v = _view(grad)

@@ -612,9 +612,11 @@ struct RowsShared {
 
 // The waves a SIMD holds: the other rows of a CU are what hides a row's chain
 // of loads, barriers and reductions. Two workgroups of 1024 need 64 registers
-// a thread (a few values spill; one workgroup without spills is slower, 220
-// against 149 us at 4095 x 30522); smaller workgroups fit the registers of a
-// thread's scores (`regs`) and about 60 more.
+// a thread: 20 values of 16-bit scores spill, 80 to 84 bytes of scratch a lane,
+// and one workgroup without spills is slower all the same (220 against 149 us
+// at 4095 x 30522). Smaller workgroups get the registers of a thread's scores
+// (`regs`) and about 60 more, 2 to 4 values short of what 32 scores a thread
+// take (12 to 20 bytes of scratch); 8 scores a thread spill nothing.
 constexpr int rows_waves(int nt, int regs) {
   return nt == 1024 ? (regs <= 16 ? 8 : 4) : (regs <= 16 ? 6 : 5);
 }
@@ -965,8 +967,9 @@ void launch_chunk(const DistillDev &d, const sps_scores *x, int32_t first, hipSt
     hipLaunchKernelGGL((sps::distill_chunk_kernel<sps::bf16_t>), grid, block, 0, s, a);
 }
 
-// 16 lanes a row where the rows fill the card, else a wave: (10,000, 32) 6.5
-// against 12.7 us, (10,000, 100) 11.4 : 14.0, (4000, 32) 5.1 : 7.0, (2000, 32)
+// 16 lanes a row where the rows fill the card, else a wave (full lists, no
+// remaining class, whose two more logarithms and its term take 8.2 us at
+// (10,000, 32)): (10,000, 32) 6.5 against 12.7 us, (10,000, 100) 11.4 : 14.0, (4000, 32) 5.1 : 7.0, (2000, 32)
 // 5.0 : 5.5, (512, 8) 4.5 : 4.8, (50,000, 512) 183 : 195; but (4000, 100) 8.5 :
 // 7.9, (512, 32) 5.0 : 4.7, (10,000, 512) 72 : 38. (Rows, list.)
 constexpr int64_t kLossRows = 64;  // for each entry of the list

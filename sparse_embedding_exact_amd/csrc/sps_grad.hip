@@ -14,9 +14,11 @@
 // entry of a row gets one float32 sum a slice, in a fixed order, and a second
 // pass adds the slices. G is read once; the lists come from the L2 of the XCD
 // that works on the slice, since consecutive workgroups of an XCD take
-// consecutive row groups of the same slice. 2000 queries x one chunk of 8192: 131
-// us for the queries' side, 139 for the items', bound by the latency of short
-// lists and by the loads of long ones.
+// consecutive row groups of the same slice. 2000 queries x chunks of 8192 of
+// the same corpus in turn: 134 us for the queries' side, 147 for the items',
+// bound by the latency of short lists and by the loads of long ones, which
+// every row walks for itself (rows of a workgroup do not share a list here, as
+// they do in the walk of a whole matrix below).
 #include "sps_rows.h"
 
 namespace sps {
@@ -203,9 +205,14 @@ __global__ __launch_bounds__(256) void grad_values_kernel(int64_t n_rows, int64_
 // and unit value as the load), not taken from a prepared corpus: a training
 // step has new values every time, its batches are small, and a corpus'
 // per-slice sorts and dim index would keep 8 to 16 workgroups busy for longer
-// than all that follows. Unit values; a histogram, its prefix and a scatter a
-// pass of up to 11 bits (two for dims up to 2^22); the table of the lists; the
-// walk: eight launches.
+// than all that follows. Unit values with the first histogram; a prefix and a
+// scatter a pass of up to 11 bits, a histogram for each pass but the first; the
+// table of the lists; the walk: 2 + 3 launches a pass, 5 for dims up to 2^11, 8
+// up to 2^22, 11 beyond.
+//
+// Rows are canonical: dims ascend and differ. A row whose dims do not gives
+// undefined gradients (the bisection for a dim's mates misses some), but places
+// and columns are clamped or masked, so that nothing out of range is accessed.
 //
 // The walk keeps four rows of G over 4096 columns in LDS, the four values of a
 // column side by side, and gives each entry of its rows a lane, which looks the
@@ -553,6 +560,9 @@ struct __attribute__((packed, aligned(8))) Pair {
 
 // Up to 128 N entries of a list from q on (this lane: q, q + 1, and every 128
 // further), times the four rows' values of their columns; none at or past h.
+// Lanes past h take the last entry times zero: where G is infinite there, NaN
+// stands in place of an infinity, in rows that the norm's part leaves without a
+// finite gradient either way.
 template <int N, bool WHOLE>
 __device__ __forceinline__ void four_rows(const uint2 *load, int32_t q, int32_t h, uint32_t c0,
                                           const float4 *tile, float4 &s) {
