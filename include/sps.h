@@ -595,6 +595,101 @@ sps_status sps_cosine_grad_both(const sps_csr *queries, const sps_csr *items,
                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Dense rows in 8 bits                                                */
+/* ------------------------------------------------------------------ */
+
+/* Dense rows held as integers in [-127, 127] with a scale each: row r stands
+ * for values[r * ld + d] * scales[r], d < dim. values: DEVICE, 16-byte
+ * aligned, ld a multiple of 16; the bytes of a row from dim to the next
+ * multiple of 16 are zeros (sps_quantize_rows writes them so). dim: 1..131072
+ * (a sum of products stays below 2^31). ld is below 2^23. */
+typedef struct {
+  int8_t *values;
+  float *scales; /* DEVICE float[n_rows] */
+  int64_t n_rows;
+  int64_t dim;
+  int64_t ld;
+} sps_int8_rows;
+
+/* Rows to 8 bits (asynchronous): with a the largest magnitude of a row, its
+ * scale is fl32(a / 127) and its integers are the nearest of 127 x / a, ties
+ * to the even one, exactly. A row of zeros has scale 0 and integers 0. A row
+ * that holds NaN or an infinity has scale NaN and integers 0. x: n_rows x dim
+ * values of any view's type (col_begin is not used); values, ld, scales: as in
+ * sps_int8_rows; nothing past the next multiple of 16 of a row is written.
+ * Errors: SPS_ERR_INVALID_ARGUMENT (an output that shares a byte with the rows
+ * among them), SPS_ERR_OVERFLOW, SPS_ERR_UNSUPPORTED (dim). */
+sps_status sps_quantize_rows(const sps_scores *x, int8_t *values, int64_t ld, float *scales,
+                             void *stream);
+
+/* The values that 8-bit rows stand for (asynchronous): out[r * ld_out + d] =
+ * values[r][d] * scales[r], to half a step of dtype (16-bit types: and half a
+ * step of float32, which the product may be rounded to before). */
+sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype, int64_t ld_out,
+                               void *stream);
+
+/* Scores of 8-bit rows (asynchronous): out[q * ld_out + i] = (sum over d of
+ * queries[q][d] * items[i][d]) * scale_q * scale_i, n_query x n_item, of type
+ * dtype: rows of scores as sps_cosine_chunk's (cosines, where the rows that
+ * were put into 8 bits have norm 1). A chunk of the items is a part of their
+ * rows. The sum is exact; its float32, the two products with the scales and
+ * the type are rounded. Bitwise reproducible, whatever the number of queries.
+ * Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH, SPS_ERR_OVERFLOW,
+ * SPS_ERR_UNSUPPORTED. */
+sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *items, void *out,
+                           int32_t dtype, int64_t ld_out, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Dense rows: cross entropy                                           */
+/* ------------------------------------------------------------------ */
+
+/* Softmax cross entropy of every query against all items (a corpus, or a
+ * vocabulary's rows), and its gradients, without the matrix of logits. With
+ *   z[r, j] = queries[r] . items[j] / temperature + bias[j],
+ *   loss[r] = log sum over j of exp(z[r, j]) - z[r, targets[r]],
+ *   G[r, j] = row_weights[r] / temperature * (softmax(z[r])_j - [j = targets[r]]),
+ *   grad_queries = G items,   grad_items = G^T queries.
+ * A row whose target is outside [0, n_item) (pad with -1) takes no part: loss
+ * and gradient 0, and nothing of it reaches the items' gradient, whatever it
+ * holds. Neither does a row of weight 0 (its loss is still given). An item
+ * whose bias is -inf is struck out: no part in any softmax, gradient 0,
+ * whatever its row holds; a row whose target is struck out has loss +inf and
+ * G[r] without the target's term; a row without any item left has loss 0 and gradient 0.
+ * bias is a constant (masks, sampling corrections) and gets no gradient.
+ * Otherwise NaN and infinities of a row that takes part make its own loss and
+ * gradient NaN, and those of the other side's rows that it reaches.
+ * Products of 16-bit rows are exact and summed in float32, float32 rows are
+ * multiplied to 2^-24 of each product; statistics of the softmax are float32
+ * within a block of columns and float64 beyond; G is rounded to the rows' type
+ * (float32: kept to 24 bits) before its two products, whose float32 sums are
+ * rounded once to grad_dtype. fp16: G is scaled by a power of two so that the
+ * largest weight uses the type's range; weights more than about 2^24 below it
+ * lose precision. Bitwise reproducible. */
+
+/* Bytes of the workspace of sps_dense_ce for these rows (their addresses and
+ * ld matter, nothing is read), with either gradient or both. Pure host. It
+ * grows with the rows and with a piece of the logits of at most about 1 GiB
+ * (or 256 queries). At most 2^22 items and 65536 dims (SPS_ERR_UNSUPPORTED). */
+sps_status sps_dense_ce_workspace_size(const sps_scores *queries, const sps_scores *items,
+                                       int32_t grad_queries, int32_t grad_items, size_t *bytes);
+
+/* The loss of every query and the gradients (asynchronous). queries, items:
+ * rows of one type, n_query x dim and n_item x dim (col_begin is not used; the
+ * fastest form has rows on 16-byte boundaries, dim a multiple of 8 and 16-bit
+ * values). targets: DEVICE int32[n_query]. bias (nullable): DEVICE
+ * float[n_item]. temperature: 1e-6 to 1e6. row_weights (nullable: 1): DEVICE
+ * float[n_query], the gradient of what is minimised about each loss. loss:
+ * DEVICE float[n_query]. grad_queries, grad_items (each nullable: not
+ * computed): of the rows' type or SPS_F32, sharing no byte with the rows or
+ * each other. workspace: DEVICE, 256-byte aligned, free again once the stream
+ * work has completed. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,
+ * SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW, SPS_ERR_UNSUPPORTED. */
+sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, const int32_t *targets,
+                        const float *bias, float temperature, const float *row_weights, float *loss,
+                        void *grad_queries, int64_t ld_queries, void *grad_items, int64_t ld_items,
+                        int32_t grad_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Block-Sparse CSR codec                                              */
 /* ------------------------------------------------------------------ */
 

@@ -69,6 +69,11 @@ class _Scores(ctypes.Structure):
                 ("n_cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("col_begin", ctypes.c_int64)]
 
 
+class _Int8Rows(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("n_rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("ld", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -123,6 +128,14 @@ SIGNATURES = {
     "sps_cosine_grad_both": (_I32, [ctypes.POINTER(_Csr), ctypes.POINTER(_Csr),
                                     ctypes.POINTER(_Scores), _P, _P, _P, _SZ, _P]),
     "sps_cosine_grad_values": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P]),
+    "sps_quantize_rows": (_I32, [ctypes.POINTER(_Scores), _P, _I64, _P, _P]),
+    "sps_dequantize_rows": (_I32, [ctypes.POINTER(_Int8Rows), _P, _I32, _I64, _P]),
+    "sps_int8_scores": (_I32, [ctypes.POINTER(_Int8Rows), ctypes.POINTER(_Int8Rows), _P, _I32, _I64,
+                               _P]),
+    "sps_dense_ce_workspace_size": (_I32, [ctypes.POINTER(_Scores), ctypes.POINTER(_Scores), _I32,
+                                           _I32, ctypes.POINTER(_SZ)]),
+    "sps_dense_ce": (_I32, [ctypes.POINTER(_Scores), ctypes.POINTER(_Scores), _P, _P, ctypes.c_float,
+                            _P, _P, _P, _I64, _P, _I64, _I32, _P, _SZ, _P]),
     "sps_row_inv_norms": (_I32, [ctypes.POINTER(_Csr), _P, _P]),
     "sps_bsc_offsets_bytes": (_I32, [_I64, ctypes.POINTER(_SZ)]),
     "sps_bsc_encode_sizes": (_I32, [ctypes.POINTER(_Csr), _P, _P, _P, ctypes.POINTER(_I64)]),
@@ -1017,6 +1030,149 @@ def bulk_distill(queries: CSR, items: CSR, teacher_ids: torch.Tensor,
             cosine_chunk_grad(part, qt, j, g[b:b + qt.chunk_len(j)], gi[lo:hi], transposed=True,
                               first=j == 0)
     return loss, cosine_grad_values(queries, gq, gq), cosine_grad_values(items, gi, gi)
+
+
+# ---------------------------------------------------------------------------
+# dense rows
+
+@dataclass
+class Int8Rows:
+    """Dense rows in 8 bits: row r stands for values[r, :dim] * scales[r]. values: int8
+    (n_rows, ld), rows on 16-byte boundaries with zeros from dim to the next multiple of 16;
+    scales: float32 (n_rows,). quantize_rows makes them so; rows[a:b] is a part of the rows."""
+    values: torch.Tensor
+    scales: torch.Tensor
+    dim: int
+
+    @property
+    def n_rows(self) -> int:
+        return int(self.values.shape[0])
+
+    def __getitem__(self, part: slice) -> "Int8Rows":
+        return Int8Rows(self.values[part], self.scales[part], self.dim)
+
+    def _c(self) -> _Int8Rows:
+        v, s = self.values, self.scales
+        assert v.dim() == 2 and v.dtype == torch.int8, "values must be int8 (rows, ld)"
+        n, m = v.shape
+        assert m <= 1 or v.stride(1) == 1, "rows must be contiguous"
+        # a row's chunks of 16 bytes belong to it, the last one whole
+        assert m >= (self.dim + 15) // 16 * 16, "values must hold whole 16-byte chunks of a row"
+        return _Int8Rows(v.data_ptr() if n else None, _rows_f32(s, n, "scales") if n else None, n,
+                         self.dim, v.stride(0) if n > 1 else (m + 15) // 16 * 16)
+
+
+def quantize_rows(x: torch.Tensor, stream=None) -> Int8Rows:
+    """Dense rows (n, dim) of float32, float16 or bfloat16 in 8 bits, a scale a row: the scale
+    is the largest magnitude / 127, the integers the nearest of x / scale, ties to even. A row
+    that holds NaN or an infinity has scale NaN."""
+    load_library()
+    dev = _here(x)
+    v = _view(x)
+    n, dim = v.n_rows, v.n_cols
+    ld = (dim + 15) // 16 * 16
+    with _on(stream):
+        values = torch.empty((n, ld), dtype=torch.int8, device=x.device)
+        scales = torch.empty(n, dtype=torch.float32, device=x.device)
+        _check(_lib.sps_quantize_rows(ctypes.byref(v), values.data_ptr() if n else None, ld,
+                                      scales.data_ptr() if n else None, _stream_of(dev, stream)))
+    return Int8Rows(values, scales, dim)
+
+
+def dequantize_rows(rows: Int8Rows, dtype: torch.dtype = torch.float32,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values (n, dim) that 8-bit rows stand for, in dtype (or out's type)."""
+    load_library()
+    dev = _here(rows.values, rows.scales, out)
+    c = rows._c()
+    with _on(stream):
+        if out is None:
+            out = torch.empty((rows.n_rows, rows.dim), dtype=dtype, device=rows.values.device)
+        assert out.shape == (rows.n_rows, rows.dim)
+        o = _view(out)
+        _check(_lib.sps_dequantize_rows(ctypes.byref(c), o.data, o.dtype, o.ld,
+                                        _stream_of(dev, stream)))
+    return out
+
+
+def int8_scores(queries: Int8Rows, items: Int8Rows, out: torch.Tensor | None = None,
+                dtype: torch.dtype = torch.float32, stream=None) -> torch.Tensor:
+    """The products of 8-bit rows, scaled: (n_query, n_item) scores of dtype (or of out's type).
+    items[a:b] scores a chunk of the items."""
+    load_library()
+    dev = _here(queries.values, queries.scales, items.values, items.scales, out)
+    q, i = queries._c(), items._c()
+    with _on(stream):
+        if out is None:
+            out = torch.empty((q.n_rows, i.n_rows), dtype=dtype, device=queries.values.device)
+        assert out.shape == (q.n_rows, i.n_rows)
+        o = _view(out)
+        _check(_lib.sps_int8_scores(ctypes.byref(q), ctypes.byref(i), o.data, o.dtype, o.ld,
+                                    _stream_of(dev, stream)))
+    return out
+
+
+def int8_select(queries: Int8Rows, items: Int8Rows, k: int, chunk_size: int = 65536) -> TopRows:
+    """The best k items of every query by their 8-bit rows' scores, exact, ties to the lower
+    item: every chunk scored and joined to the running lists (bulk_select's loop). Queries go
+    in batches, so that a chunk's scores stay within 2 GiB."""
+    _here(queries.values, queries.scales, items.values, items.scales)
+    n, m = queries.n_rows, items.n_rows
+    dev = queries.values.device
+    top = top_rows(n, k, dev)
+    width = min(chunk_size, m)
+    batch = max(1, min(n, (1 << 29) // max(width, 1)))
+    buf = torch.empty(batch, width, dtype=torch.float32, device=dev)
+    for a in range(0, n, batch):
+        part = TopRows(top.scores[a:a + batch], top.cols[a:a + batch])
+        q = queries[a:a + batch]
+        if m == 0:
+            select_chunk(buf[:q.n_rows], part, 0, first=True)
+        for b in range(0, m, chunk_size):
+            chunk = items[b:b + chunk_size]
+            scores = int8_scores(q, chunk, buf[:q.n_rows, :chunk.n_rows])
+            select_chunk(scores, part, b, first=b == 0)
+    return top
+
+
+def dense_cross_entropy(queries: torch.Tensor, items: torch.Tensor, targets: torch.Tensor,
+                        temperature: float = 1.0, bias: torch.Tensor | None = None,
+                        row_weights: torch.Tensor | None = None, need_grad=True,
+                        grad_dtype: torch.dtype | None = None, stream=None):
+    """(loss of every query, gradient of the queries, gradient of the items): softmax cross
+    entropy of z = queries . items / temperature + bias over all items, without the logits.
+    queries (n, dim) and items (m, dim): rows of one type, float32, float16 or bfloat16;
+    targets: int32 (n,), outside [0, m) a row takes no part; bias: float32 (m,), a constant,
+    -inf strikes an item out; row_weights: float32 (n,), the gradient about each loss.
+    need_grad: True, False, "queries" or "items" (the other is None); gradients have the rows'
+    type or grad_dtype=torch.float32."""
+    load_library()
+    dev = _here(queries, items, targets, bias, row_weights)
+    q, i = _view(queries), _view(items)
+    n, m, dim = q.n_rows, i.n_rows, q.n_cols
+    assert items.dtype == queries.dtype, "queries and items must have one type"
+    assert targets.dtype == torch.int32 and targets.is_contiguous() and targets.numel() == n, \
+        "targets must be %d contiguous int32" % n
+    assert need_grad in (True, False, "queries", "items"), "need_grad: True, False, queries or items"
+    bp = _rows_f32(bias, m, "bias")
+    w = _rows_f32(row_weights, n, "row_weights")
+    gt = queries.dtype if grad_dtype is None else grad_dtype
+    assert gt in (queries.dtype, torch.float32), "gradients have the rows' type or float32"
+    want_q, want_i = need_grad in (True, "queries"), need_grad in (True, "items")
+    nb = _SZ()
+    _check(_lib.sps_dense_ce_workspace_size(ctypes.byref(q), ctypes.byref(i), int(want_q),
+                                            int(want_i), ctypes.byref(nb)))
+    with _on(stream):
+        loss = torch.empty(n, dtype=torch.float32, device=queries.device)
+        gq = torch.empty((n, dim), dtype=gt, device=queries.device) if want_q else None
+        gi = torch.empty((m, dim), dtype=gt, device=queries.device) if want_i else None
+        buf, ptr = _workspace(nb.value, queries.device)
+        _check(_lib.sps_dense_ce(ctypes.byref(q), ctypes.byref(i), targets.data_ptr(), bp,
+                                 float(temperature), w, loss.data_ptr(),
+                                 gq.data_ptr() if want_q and n else None, dim,
+                                 gi.data_ptr() if want_i and m else None, dim, _SCORE_TYPES[gt],
+                                 ptr, nb.value, _stream_of(dev, stream)))
+    return loss, gq, gi
 
 
 def row_inv_norms(m: CSR, stream=None) -> torch.Tensor:

@@ -10,9 +10,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("sps_prepare.hip", "sps_score.hip", "sps_bsc.hip",
                                               "sps_select.hip", "sps_distill.hip",
-                                              "sps_grad.hip", "sps_api.hip")]
+                                              "sps_grad.hip", "sps_int8.hip", "sps_dense.hip",
+                                              "sps_api.hip")]
 HEADERS = [os.path.join(ROOT, "include", "sps.h"), os.path.join(CSRC, "sps_internal.h"),
-           os.path.join(CSRC, "sps_device.h"), os.path.join(CSRC, "sps_rows.h")]
+           os.path.join(CSRC, "sps_device.h"), os.path.join(CSRC, "sps_rows.h"),
+           os.path.join(CSRC, "sps_gemm.h")]
 LIB = os.path.join(PKG, "libsps.so")
 
 HIPCC_FLAGS = [

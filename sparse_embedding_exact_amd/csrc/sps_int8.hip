@@ -1,0 +1,400 @@
+// sps_int8.hip -- dense rows in 8 bits: to integers and back, and the products
+// of two sets of such rows.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sps_gemm.h"
+
+namespace sps {
+
+// ---------------------------------------------------------------------------
+// rows to 8 bits
+
+struct QuantArgs {
+  const void *x;
+  int64_t ld;  // elements
+  int64_t n_rows, dim;
+  int8_t *q;
+  int64_t ld_q;
+  float *scales;
+};
+
+// The nearest integer of 127 x / amax, ties to even. y is within 3e-5 of the
+// quotient; only where that leaves the side of a half open are the exact
+// 254 |x| and (2 h + 1) amax compared, which float64 holds without rounding.
+__device__ __forceinline__ int32_t nearest_int8(float x, float y, float amax) {
+  const float k = rintf(y);
+  if (__builtin_expect(fabsf(y - k) > 0.4999f, 0)) {
+    const float h = floorf(fabsf(y));
+    const double d = 254.0 * (double)fabsf(x) - (2.0 * (double)h + 1.0) * (double)amax;
+    const int32_t m = (int32_t)h + (d > 0.0 || (d == 0.0 && ((int32_t)h & 1)));
+    return x < 0.0f ? -m : m;
+  }
+  return (int32_t)k;
+}
+
+// A wave a row. The row's first vectors stay in registers between the maximum
+// and the integers, the rest is read again (from the caches). Bound by memory.
+constexpr int kQuantKeep = 4;
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
+  constexpr int V = kVec<T>;
+  const int lane = threadIdx.x & 63;
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= a.n_rows) return;
+  const T *const x = static_cast<const T *>(a.x) + r * a.ld;
+  const int64_t whole = a.dim / V;  // whole vectors; the rest of the row is one short one
+  const int tail = (int)(a.dim - whole * V);
+  const auto fetch = [&](int64_t v) {
+    Vec<T> t{};
+    if (v < whole) t = *reinterpret_cast<const Vec<T> *>(x + v * V);
+    else if (v == whole) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (e < tail) t.e[e] = x[v * V + e];
+    }
+    return t;
+  };
+  Vec<T> keep[kQuantKeep];
+  uint32_t top = 0;  // bits of magnitudes: their order, NaN above infinity
+  const auto see = [&](const Vec<T> &t) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const uint32_t b = __builtin_bit_cast(uint32_t, to_f32(t.e[e])) & 0x7fffffffu;
+      top = b > top ? b : top;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kQuantKeep; ++i) keep[i] = fetch(lane + 64 * i);
+#pragma unroll
+  for (int i = 0; i < kQuantKeep; ++i) see(keep[i]);
+  for (int64_t v = lane + 64 * kQuantKeep; v <= whole; v += 64) see(fetch(v));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint32_t b = (uint32_t)__shfl_xor((int)top, o, 64);
+    top = b > top ? b : top;
+  }
+  const float amax = __builtin_bit_cast(float, top);
+  const bool finite = top < 0x7f800000u;
+  // rows of very small values are taken 2^64 times as large: 127 / amax must not overflow
+  const float up = amax < 0x1p-60f ? 0x1p64f : 1.0f;
+  const float inv = finite && top ? 127.0f / (amax * up) : 0.0f;
+  int8_t *const q = a.q + r * a.ld_q;
+  const int64_t room = (a.dim + 15) & ~15ll;
+  const auto put = [&](int64_t v, const Vec<T> &t) {
+    if (v * V >= room) return;
+    uint32_t w[V / 4];
+#pragma unroll
+    for (int j = 0; j < V / 4; ++j) {
+      w[j] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f = to_f32(t.e[4 * j + e]);
+        const int32_t k = inv > 0.0f ? nearest_int8(f, f * up * inv, amax) : 0;
+        w[j] |= (uint32_t)(k & 255) << (8 * e);
+      }
+    }
+    __builtin_memcpy(__builtin_assume_aligned(q + v * V, V), w, V);
+  };
+#pragma unroll
+  for (int i = 0; i < kQuantKeep; ++i) put(lane + 64 * i, keep[i]);
+  // up to the next multiple of 16 the row is filled with zeros
+  for (int64_t v = lane + 64 * kQuantKeep; v * V < room; v += 64) put(v, fetch(v));
+  if (lane == 0) a.scales[r] = finite ? amax / 127.0f : __builtin_nanf("");
+}
+
+struct DequantArgs {
+  const int8_t *q;
+  int64_t ld_q;
+  const float *scales;
+  int64_t n_rows, dim;
+  void *out;
+  int64_t ld;  // elements
+};
+
+// 16 integers a thread.
+template <typename T>
+__global__ __launch_bounds__(256) void dequantize_rows_kernel(DequantArgs a) {
+  const int64_t per = (a.dim + 15) / 16, all = a.n_rows * per;
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
+    const int64_t r = i / per, c = (i - r * per) * 16;
+    const i32x4 w = *reinterpret_cast<const i32x4 *>(a.q + r * a.ld_q + c);
+    const float s = a.scales[r];
+    T *const out = static_cast<T *>(a.out) + r * a.ld + c;
+    constexpr int V = kVec<T>;
+#pragma unroll
+    for (int j = 0; j < 16 / V; ++j) {
+      Vec<T> t;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int k = j * V + e;
+        t.e[e] = from_f32<T>((float)(int8_t)((uint32_t)w[k / 4] >> (8 * (k % 4))) * s);
+      }
+      if (c + (j + 1) * V <= a.dim) *reinterpret_cast<Vec<T> *>(out + j * V) = t;
+      else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c + j * V + e < a.dim) out[j * V + e] = t.e[e];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// scores
+
+struct Int8Args {
+  GemmArgs g;  // q: queries, p: items
+  const float *scale_q, *scale_p;
+  void *out;
+  int64_t ld;  // elements
+};
+
+// The integers' sums are exact; a score is rounded as an integer above 2^24,
+// by either scale and to its type.
+template <typename T, int TC, int TR, int WC, int WR>
+__global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
+  using Tile = GemmTile<OpI8, TC, TR, WC, WR>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Tile::kBuf];
+  const GemmPlace at = gemm_place<TC, TR>(a.g);
+  Tile t;
+  t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
+  float sp[Tile::kFragC][4];
+#pragma unroll
+  for (int i = 0; i < Tile::kFragC; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int64_t c = at.col0 + t.col_of(i) + e;
+      sp[i][e] = c < a.g.p.rows ? a.scale_p[c] : 0.0f;
+    }
+#pragma unroll
+  for (int j = 0; j < Tile::kFragR; ++j) {
+    const int64_t r = at.row0 + t.row_of(j);
+    if (r >= a.g.q.rows) continue;
+    const float sq = a.scale_q[r];
+    T *const out = static_cast<T *>(a.out) + r * a.ld;
+#pragma unroll
+    for (int i = 0; i < Tile::kFragC; ++i) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = (float)t.acc[i][j][e] * sq * sp[i][e];
+      put_four<T>(out, at.col0 + t.col_of(i), a.g.p.rows, v);
+    }
+  }
+}
+
+// Few queries (up to 16 NQ): bound by reading the items once. A wave takes 16
+// items at a time straight from memory into a matrix instruction's operand,
+// the queries lie in LDS in the order the instructions read them.
+template <typename T, int NQ>
+__global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int steps = (int)((a.g.k_bytes + 63) / 64);
+  i32x4 *const qs = reinterpret_cast<i32x4 *>(few_lds);
+  for (int i = threadIdx.x; i < steps * NQ * 64; i += 256) {
+    const int l = i & 63, f = (i >> 6) % NQ, s = (i >> 6) / NQ;
+    const int64_t r = f * 16 + (l & 15), k = (int64_t)s * 64 + (l >> 4) * 16;
+    qs[i] = r < a.g.q.rows && k < a.g.k_bytes
+                ? *reinterpret_cast<const i32x4 *>(a.g.q.base + r * a.g.q.ld + k)
+                : i32x4{};
+  }
+  __syncthreads();
+  const int64_t groups = (a.g.p.rows + 15) / 16, stride = (int64_t)gridDim.x * 4;
+  for (int64_t g = (int64_t)blockIdx.x * 4 + wave; g < groups; g += stride) {
+    const int64_t item = g * 16 + (lane & 15);
+    const bool there = item < a.g.p.rows;
+    const uint8_t *const row = a.g.p.base + (there ? item : a.g.p.rows - 1) * a.g.p.ld;
+    const int64_t c0 = g * 16 + (lane >> 4) * 4;
+    i32x4 acc[NQ] = {};
+    constexpr int U = 4;  // loads of items in flight
+    for (int s = 0; s < steps; s += U) {
+      i32x4 p[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t k = (int64_t)(s + u) * 64 + (lane >> 4) * 16;
+        // past the row's end the queries are zeros: any finite bytes do
+        p[u] = *reinterpret_cast<const i32x4 *>(row + (k < a.g.k_bytes ? k : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s + u < steps)
+#pragma unroll
+          for (int f = 0; f < NQ; ++f)
+            acc[f] = OpI8::mma(p[u], qs[((s + u) * NQ + f) * 64 + lane], acc[f]);
+    }
+    float sp[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sp[e] = c0 + e < a.g.p.rows ? a.scale_p[c0 + e] : 0.0f;
+#pragma unroll
+    for (int f = 0; f < NQ; ++f) {
+      const int64_t r = f * 16 + (lane & 15);
+      if (r >= a.g.q.rows) continue;
+      const float sq = a.scale_q[r];
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = (float)acc[f][e] * sq * sp[e];
+      put_four<T>(static_cast<T *>(a.out) + r * a.ld, c0, a.g.p.rows, v);
+    }
+  }
+}
+
+}  // namespace sps
+
+using sps::set_error;
+
+namespace {
+
+constexpr int64_t kMax31 = 2147483647ll;
+constexpr int64_t kInt8MaxDim = 131072;  // 127^2 dim stays below 2^31
+
+sps_status check_rows8(const sps_int8_rows *x, const char *what) {
+  if (!x) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL rows", what);
+  if (x->n_rows < 0 || x->dim < 1)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: negative rows or no dims", what);
+  if (x->n_rows >= kMax31) return set_error(SPS_ERR_OVERFLOW, "%s: rows must be below 2^31", what);
+  if (x->dim > kInt8MaxDim)
+    return set_error(SPS_ERR_UNSUPPORTED, "%s: at most %lld dims", what, (long long)kInt8MaxDim);
+  if (x->ld < x->dim || x->ld % 16)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: ld %lld, a multiple of 16 from %lld on", what,
+                     (long long)x->ld, (long long)x->dim);
+  if (x->ld > sps::kMostBytes / 256)
+    return set_error(SPS_ERR_OVERFLOW, "%s: ld must be below 2^23", what);
+  if (x->n_rows > 0 && (!x->values || !x->scales))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: NULL values or scales", what);
+  if (reinterpret_cast<uintptr_t>(x->values) % 16)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: values must be 16-byte aligned", what);
+  if (reinterpret_cast<uintptr_t>(x->scales) % 4)
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: scales not aligned to their elements", what);
+  return SPS_OK;
+}
+
+template <typename T, int NQ>
+void launch_few(const sps::Int8Args &a, hipStream_t s) {
+  const size_t lds = (size_t)((a.g.k_bytes + 63) / 64) * NQ * 1024;
+  int64_t blocks = sps::ceil_div(sps::ceil_div(a.g.p.rows, 16), 4);
+  if (blocks > 2048) blocks = 2048;
+  hipLaunchKernelGGL((sps::int8_few_kernel<T, NQ>), dim3((uint32_t)blocks), dim3(256), lds, s, a);
+}
+
+template <typename T, int TC, int TR, int WC, int WR>
+void launch_tiles(sps::Int8Args &a, hipStream_t s) {
+  a.g.tiles_c = (int32_t)sps::ceil_div(a.g.p.rows, TC);
+  a.g.tiles_r = (int32_t)sps::ceil_div(a.g.q.rows, TR);
+  const int64_t tiles = (int64_t)a.g.tiles_c * a.g.tiles_r;
+  hipLaunchKernelGGL((sps::int8_scores_kernel<T, TC, TR, WC, WR>), dim3((uint32_t)tiles),
+                     dim3(64 * WC * WR), 0, s, a);
+}
+
+constexpr int64_t kFewLds = 64 * 1024;
+
+template <typename T>
+void launch_scores(sps::Int8Args &a, hipStream_t s) {
+  const int64_t n = a.g.q.rows, steps = (a.g.k_bytes + 63) / 64;
+  if (n <= 16 && steps * 1024 <= kFewLds) return launch_few<T, 1>(a, s);
+  if (n <= 32 && steps * 2048 <= kFewLds) return launch_few<T, 2>(a, s);
+  if (n <= 64 && steps * 4096 <= kFewLds) return launch_few<T, 4>(a, s);
+  const int64_t big = sps::ceil_div(a.g.p.rows, 256) * sps::ceil_div(n, 256);
+  if (big >= 256) launch_tiles<T, 256, 256, 2, 4>(a, s);
+  else launch_tiles<T, 128, 128, 2, 2>(a, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+sps_status sps_quantize_rows(const sps_scores *x, int8_t *values, int64_t ld, float *scales,
+                             void *stream) {
+  const char *what = "sps_quantize_rows";
+  sps_status st = sps::check_scores(x, what);
+  if (st != SPS_OK) return st;
+  const sps_int8_rows out{values, scales, x->n_rows, x->n_cols, ld};
+  st = check_rows8(&out, what);
+  if (st == SPS_OK) st = sps::check_grid(sps::ceil_div(x->n_rows, 4), 256, what);
+  if (st != SPS_OK) return st;
+  if (x->n_rows == 0) return SPS_OK;
+  const int64_t size = sps::dtype_size(x->dtype);
+  if (sps::rows_overlap({x->data, x->n_rows, x->n_cols * size, x->ld * size},
+                        {values, x->n_rows, (x->n_cols + 15) & ~15ll, ld}))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the integers overlap the rows", what);
+  sps::QuantArgs a{x->data, x->ld, x->n_rows, x->n_cols, values, ld, scales};
+  const dim3 grid((uint32_t)sps::ceil_div(x->n_rows, 4)), block(256);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (x->dtype == SPS_F32)
+    hipLaunchKernelGGL((sps::quantize_rows_kernel<float>), grid, block, 0, s, a);
+  else if (x->dtype == SPS_F16)
+    hipLaunchKernelGGL((sps::quantize_rows_kernel<sps::f16_t>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::quantize_rows_kernel<sps::bf16_t>), grid, block, 0, s, a);
+  return sps::launch_status(what);
+}
+
+sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype, int64_t ld_out,
+                               void *stream) {
+  const char *what = "sps_dequantize_rows";
+  sps_status st = check_rows8(x, what);
+  if (st != SPS_OK) return st;
+  const sps_scores view{out, dtype, x->n_rows, x->dim, ld_out, 0};
+  st = sps::check_scores(&view, what);
+  if (st != SPS_OK) return st;
+  if (x->n_rows == 0) return SPS_OK;
+  const int64_t size = sps::dtype_size(dtype);
+  if (sps::rows_overlap({out, x->n_rows, x->dim * size, ld_out * size},
+                        {x->values, x->n_rows, (x->dim + 15) & ~15ll, x->ld}))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the output overlaps the integers", what);
+  sps::DequantArgs a{x->values, x->ld, x->scales, x->n_rows, x->dim, out, ld_out};
+  int64_t blocks = sps::ceil_div(x->n_rows * sps::ceil_div(x->dim, 16), 256);
+  if (blocks > 65536) blocks = 65536;
+  const dim3 grid((uint32_t)blocks), block(256);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == SPS_F32)
+    hipLaunchKernelGGL((sps::dequantize_rows_kernel<float>), grid, block, 0, s, a);
+  else if (dtype == SPS_F16)
+    hipLaunchKernelGGL((sps::dequantize_rows_kernel<sps::f16_t>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::dequantize_rows_kernel<sps::bf16_t>), grid, block, 0, s, a);
+  return sps::launch_status(what);
+}
+
+sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *items, void *out,
+                           int32_t dtype, int64_t ld_out, void *stream) {
+  const char *what = "sps_int8_scores";
+  sps_status st = check_rows8(queries, what);
+  if (st == SPS_OK) st = check_rows8(items, what);
+  if (st != SPS_OK) return st;
+  if (queries->dim != items->dim)
+    return set_error(SPS_ERR_DIM_MISMATCH, "%s: queries have %lld dims, items %lld", what,
+                     (long long)queries->dim, (long long)items->dim);
+  const sps_scores view{out, dtype, queries->n_rows, items->n_rows, ld_out, 0};
+  st = sps::check_scores(&view, what);
+  // a workgroup of 256 threads for 128 x 128 scores at the least
+  if (st == SPS_OK)
+    st = sps::check_grid(sps::ceil_div(queries->n_rows, 128) * sps::ceil_div(items->n_rows, 128),
+                         512, what);
+  if (st != SPS_OK) return st;
+  if (queries->n_rows == 0 || items->n_rows == 0) return SPS_OK;
+  const int64_t size = sps::dtype_size(dtype), k = (queries->dim + 15) & ~15ll;
+  const sps::RowBytes o{out, queries->n_rows, items->n_rows * size, ld_out * size};
+  if (sps::rows_overlap(o, {queries->values, queries->n_rows, k, queries->ld}) ||
+      sps::rows_overlap(o, {items->values, items->n_rows, k, items->ld}) ||
+      sps::rows_overlap(o, {queries->scales, 1, queries->n_rows * 4, queries->n_rows * 4}) ||
+      sps::rows_overlap(o, {items->scales, 1, items->n_rows * 4, items->n_rows * 4}))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the scores overlap the rows", what);
+  sps::Int8Args a{};
+  a.g.q = {reinterpret_cast<const uint8_t *>(queries->values), queries->n_rows, queries->ld, 0};
+  a.g.p = {reinterpret_cast<const uint8_t *>(items->values), items->n_rows, items->ld, 0};
+  a.g.k_bytes = k;
+  a.g.splits = 1;
+  a.scale_q = queries->scales;
+  a.scale_p = items->scales;
+  a.out = out;
+  a.ld = ld_out;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == SPS_F32) launch_scores<float>(a, s);
+  else if (dtype == SPS_F16) launch_scores<sps::f16_t>(a, s);
+  else launch_scores<sps::bf16_t>(a, s);
+  return sps::launch_status(what);
+}
+
+}  // extern "C"
