@@ -9,9 +9,9 @@
 //   2. sums: a row's log-sum-exp and loss from its blocks' statistics;
 //   3. gradient of the logits: code to G in place, and G transposed;
 //   4. two products with G, whose k (items, or rows) lies in one run.
-// Code: 4 bits of exponent and 12 of mantissa below the block's maximum (an
-// error of 2^-13, next to the 2^-9 or 2^-12 that G is rounded by to enter
-// the matrix instructions), so z is not computed twice. G's own column at the
+// Code: a 16-bit float below the block's maximum, with 3 or 2 bits more than
+// G keeps when it is rounded to enter the matrix instructions, so z is not
+// computed twice. G's own column at the
 // target is 1 - p from the loss, never p - 1 of a rounded p.
 // fp16: G is held 2^k times as large, 2^k the power of two that takes the
 // largest weight to [2^14, 2^15), so that p down to 2^-29 keeps all its bits.
@@ -108,14 +108,38 @@ __global__ __launch_bounds__(256) void lay_kernel(LayArgs a) {
 // ---------------------------------------------------------------------------
 // 1. logits
 
-// e^(z - max) in 16 bits: float32's own bits of p 2^-112 but the last 11, which
-// has 4 bits of exponent left and runs out gradually below 2^-14.
-__device__ __forceinline__ uint32_t code_of(float p) {
-  return (__builtin_bit_cast(uint32_t, p * 0x1p-112f) + 0x400u) >> 11;
-}
-__device__ __forceinline__ float code_value(uint32_t c) {
-  return __builtin_bit_cast(float, c << 11) * 0x1p112f;
-}
+// How e^(z - max) is kept, in units of 2^-kShift, so that small ones stay
+// normal numbers.
+// bf16: as fp16 (an error of 2^-12 where G is rounded by 2^-9).
+struct CodeBf16 {
+  using Word = uint16_t;
+  static constexpr int kShift = 15;
+  static __device__ __forceinline__ uint32_t two(float a, float b) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+  }
+  static __device__ __forceinline__ float value(uint32_t w) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+  }
+};
+// fp16: float32's own bits of p 2^-112 but the last 11: 4 bits of exponent, 12
+// of mantissa (an error of 2^-13 where G is rounded by 2^-12), running out
+// gradually below 2^-14.
+struct CodeF16 {
+  using Word = uint16_t;
+  static constexpr int kShift = 0;
+  static __device__ __forceinline__ uint32_t one(float p) {
+    return (__builtin_bit_cast(uint32_t, p * 0x1p-112f) + 0x400u) >> 11;
+  }
+  static __device__ __forceinline__ uint32_t two(float a, float b) { return one(a) | one(b) << 16; }
+  static __device__ __forceinline__ float value(uint32_t w) {
+    return __builtin_bit_cast(float, w << 11) * 0x1p112f;
+  }
+};
+struct CodeF32 {
+  using Word = float;
+  static constexpr int kShift = 0;
+};
 
 struct LogitArgs {
   GemmArgs g;         // q: the piece's queries, p: items
@@ -131,75 +155,83 @@ struct LogitArgs {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-template <class Op, typename P, int TC, int TR, int WC, int WR>
+template <class Op, class Code, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   using Tile = GemmTile<Op, TC, TR, WC, WR>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Tile::kBuf];
-  const GemmPlace at = gemm_place<TC, TR>(a.g);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
+  const GemmPlace at = gemm_place<Op, TC, TR>(a.g);
   Tile t;
   t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
   constexpr float kInf = __builtin_inff();
-  constexpr int FC = Tile::kFragC;
+  constexpr int FC = Tile::kFragC, FR = Tile::kFragR;
   const int64_t cols = a.g.p.rows;
-  float b[FC][4];
-#pragma unroll
-  for (int i = 0; i < FC; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = at.col0 + t.col_of(i) + e;
-      b[i][e] = c < cols ? (a.bias ? a.bias[c] * kLog2e : 0.0f) : -kInf;
-    }
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t block = at.col0 / (TC / WC) + wave % WC;
+  const int64_t first_col = at.col0 + (wave % WC) * (TC / WC);  // of this wave
+  // The logits are c times the sums, and where there is a bias or an edge, what is put in their
+  // place here.
+  float c = a.c;
+  if (a.bias || at.col0 + TC > cols) {
 #pragma unroll
-  for (int j = 0; j < Tile::kFragR; ++j) {
+    for (int i = 0; i < FC; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t col = at.col0 + t.col_of(i) + e;
+        const float b = col < cols ? (a.bias ? a.bias[col] * kLog2e : 0.0f) : -kInf;
+#pragma unroll
+        for (int j = 0; j < FR; ++j)  // a column that is struck out has no logit, whatever its item holds
+          t.acc[i][j][e] = b == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], c, b);
+      }
+    c = 1.0f;
+  }
+  const int64_t block = first_col / (TC / WC);
+  using Word = typename Code::Word;
+  uint8_t *const mine = t.wave_lds(lds);
+#pragma unroll
+  for (int j = 0; j < FR; ++j) {
     const int64_t r = at.row0 + t.row_of(j);
     const bool there = r < a.g.q.rows;
     float top = -kInf;
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // a column that is struck out has no logit, whatever its item holds
-        const float z = b[i][e] == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], a.c, b[i][e]);
-        t.acc[i][j][e] = z;
-        top = fmaxf(top, z);
-      }
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, t.acc[i][j][e]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    const float base = top == -kInf ? 0.0f : top;
-    const int first = there ? (int)(a.targets[r] - at.col0) : -1;  // the target's place in the tile
-    float zt = 0.0f, sum = 0.0f;
-    bool mine = false;
+    top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
+    // the target's logit, where it is one of this wave's columns
+    const int first = there ? (int)(a.targets[r] - at.col0) : -1;
+    if ((uint32_t)(first - (wave % WC) * (TC / WC)) < (uint32_t)(TC / WC)) {
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (first == t.col_of(i) + e) a.z_target[r] = t.acc[i][j][e] * c;
+    }
+    const float base = (float)Code::kShift - (top == -kInf ? 0.0f : top);
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < FC; ++i) {
       float p[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float z = t.acc[i][j][e];
-        if (first == t.col_of(i) + e) {
-          zt = z;
-          mine = true;
-        }
-        p[e] = __builtin_amdgcn_exp2f(z - base);
+        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e], c, base));
         sum += p[e];
       }
-      const int64_t col = at.col0 + t.col_of(i);
-      if (a.code && there && col < cols) {  // rows are padded to a multiple of 4 values
-        if constexpr (sizeof(P) == 2) {
-          const uint2 v = {code_of(p[0]) | code_of(p[1]) << 16, code_of(p[2]) | code_of(p[3]) << 16};
-          *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.code) + r * a.ld + col) = v;
-        } else {
-          *reinterpret_cast<f32x4 *>(static_cast<float *>(a.code) + r * a.ld + col) =
-              f32x4{p[0], p[1], p[2], p[3]};
-        }
+      if (a.code) {
+        if constexpr (sizeof(Word) == 2)
+          t.template stage<Word>(mine, i, u32x2{Code::two(p[0], p[1]), Code::two(p[2], p[3])});
+        else
+          t.template stage<Word>(mine, i, f32x4{p[0], p[1], p[2], p[3]});
       }
+    }
+    if (a.code) {  // rows of codes are padded to a multiple of 64
+      const int64_t r0 = at.row0 + t.rows_at(j);
+      t.template store<Word>(mine, static_cast<Word *>(a.code) + r0 * a.ld + first_col, a.ld,
+                             a.g.q.rows - r0, ((cols + 63) & ~63ll) - first_col);
     }
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
-    if (there && lane < 16 && at.col0 + (wave % WC) * (TC / WC) < cols)
-      a.stats[block * a.rows_pad + r] = {top, sum};
-    if (mine) a.z_target[r] = zt;
+    if (there && lane < 16 && first_col < cols)
+      a.stats[block * a.rows_pad + r] = {top, sum * (1.0f / (float)(1 << Code::kShift))};
   }
 }
 
@@ -304,7 +336,7 @@ struct TurnArgs {
 };
 
 // Tiles of 64 x 64, 16 bytes of G a thread and step both ways; bound by memory.
-template <typename T, typename P>
+template <typename T, class Code>
 __global__ __launch_bounds__(256) void ce_turn_kernel(TurnArgs a) {
   constexpr int NP = kPlanes<T>;
   __shared__ __attribute__((aligned(16))) uint16_t tile[NP][64][72];
@@ -319,14 +351,16 @@ __global__ __launch_bounds__(256) void ce_turn_kernel(TurnArgs a) {
       const RowSum s = a.sums[r];
       if (s.factor != 0.0f) {
         const float f =
-            __builtin_amdgcn_exp2f(a.stats[(c / a.block) * a.rows_pad + r].x - s.lse2) * s.factor;
+            __builtin_amdgcn_exp2f(a.stats[(c / a.block) * a.rows_pad + r].x - s.lse2 -
+                                  (float)Code::kShift) *
+            s.factor;
         float p[8];
-        if constexpr (sizeof(P) == 2) {
+        if constexpr (sizeof(typename Code::Word) == 2) {
           const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.code) +
                                                            r * a.ld + c);
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = code_value((u[e / 2] >> (16 * (e & 1))) & 0xffffu);
+          for (int e = 0; e < 8; ++e) p[e] = Code::value((u[e / 2] >> (16 * (e & 1))) & 0xffffu);
         } else {
           const f32x4 *const w =
               reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.code) + r * a.ld + c);
@@ -405,39 +439,48 @@ __device__ __forceinline__ void put_typed(void *out, int32_t dtype, int64_t at, 
   else put_four<bf16_t>(static_cast<bf16_t *>(out) + at, col, cols, v);
 }
 
-template <class Op, int TC, int TR, int WC, int WR>
-__global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a) {
-  using Tile = GemmTile<Op, TC, TR, WC, WR>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Tile::kBuf];
-  const GemmPlace at = gemm_place<TC, TR>(a.g);
-  Tile t;
-  t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
+// The tile's sums, after those of earlier pieces, times alpha, to rows of T.
+template <typename T, class Tile>
+__device__ __forceinline__ void product_out(const ProductArgs &a, Tile &t, const GemmPlace &at,
+                                            uint8_t *mine, T *out, int64_t ld, float alpha,
+                                            const OutMask &mask) {
   const int64_t rows = a.g.q.rows, cols = a.g.p.rows;
-  const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
 #pragma unroll
   for (int j = 0; j < Tile::kFragR; ++j) {
     const int64_t r = at.row0 + t.row_of(j);
-    if (r >= rows) continue;
-    const bool zero = !a.part && a.mask.out(r);
+    const bool zero = r < rows && mask.out(r);
 #pragma unroll
     for (int i = 0; i < Tile::kFragC; ++i) {
       const int64_t c = at.col0 + t.col_of(i);
-      if (c >= cols) continue;
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e] = t.acc[i][j][e];
-        if (a.before && c + e < cols) v[e] += a.before[r * cols + c + e];
+        if (a.before && r < rows && c + e < cols) v[e] += a.before[r * cols + c + e];
+        v[e] = zero ? 0.0f : v[e] * alpha;
       }
-      if (a.part) {
-        put_four<float>(a.part + at.z * a.stride + r * cols, c, cols, v);
-        continue;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : v[e] * alpha;
-      put_typed(a.out, a.dtype, r * a.ld, c, cols, v);
+      t.template stage<T>(mine, i, quad_of<T>(v));
     }
+    const int64_t r0 = at.row0 + t.rows_at(j), c0 = at.col0 + t.cols_at();
+    t.template store<T>(mine, out + r0 * ld + c0, ld, rows - r0, cols - c0);
   }
+}
+
+template <class Op, int TC, int TR, int WC, int WR>
+__global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a) {
+  using Tile = GemmTile<Op, TC, TR, WC, WR>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
+  const GemmPlace at = gemm_place<Op, TC, TR>(a.g);
+  Tile t;
+  t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
+  const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
+  uint8_t *const mine = t.wave_lds(lds);
+  if (a.part) product_out<float>(a, t, at, mine, a.part + at.z * a.stride, a.g.p.rows, 1.0f, {});
+  else if (a.dtype == SPS_F32)
+    product_out<float>(a, t, at, mine, static_cast<float *>(a.out), a.ld, alpha, a.mask);
+  else  // the rows' own type: that of the products
+    product_out<typename Op::Type>(a, t, at, mine, static_cast<typename Op::Type *>(a.out), a.ld, alpha,
+                                   a.mask);
 }
 
 struct JoinArgs {
@@ -513,7 +556,7 @@ struct Shape {
   int64_t ld_g;      // items, padded
   int32_t block;     // columns of a block of statistics
   int64_t blocks;
-  int splits_q;      // of the product for the queries
+  sps::TilePlan plan_q, plan_i;  // of the products for the queries and the items
 };
 
 struct Layout {
@@ -522,8 +565,15 @@ struct Layout {
 };
 
 int planes(const Shape &s) { return s.dtype == SPS_F32 ? 3 : 1; }
-int64_t packed_ld(const Shape &s) { return up(s.d, 8); }
-int64_t turned_ld(int64_t rows) { return up(rows, 64); }
+
+// Rows of 16-bit values that hold `k`, an odd number of 128 bytes: equal places
+// of neighbouring rows fall into different channels of L2.
+int64_t odd_ld(int64_t k) { return (ceil_div(k, 64) | 1) * 64; }
+int64_t turned_ld(int64_t rows) { return odd_ld(rows); }
+int64_t packed_ld(const Shape &s) {
+  const int64_t ld = up(s.d, 8);
+  return ld % 256 ? ld : ld + 64;
+}
 
 // 16-byte rows and whole 16-byte chunks of k are read where they lie
 bool must_pack(const sps_scores *x) {
@@ -541,7 +591,7 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   s.gi = gi;
   s.pack_q = must_pack(q);
   s.pack_i = must_pack(i);
-  s.ld_g = up(s.m, 64);
+  s.ld_g = odd_ld(s.m);
   const bool grad = gq || gi;
   const int64_t each = s.dtype == SPS_F32 ? 4 + 6 * gq + 6 * gi : 2 + 2 * gi;
   s.block = 64;
@@ -550,16 +600,15 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   if (rows < 256) rows = 256;
   if (rows > kMaxPiece) rows = kMaxPiece;
   s.piece = rows < s.n ? rows : up(s.n, 64);
-  s.big = ceil_div(s.m, 256) * ceil_div(s.piece, 256) >= 256;
+  const int seg = s.dtype == SPS_F32 ? sps::kSegments : 1;
+  const int64_t at_once = s.piece < s.n ? s.piece : s.n;
+  const auto steps = [&](int64_t k) { return ceil_div(k * 2, sps::kStep) * seg; };
+  s.big = sps::plan_tiles(at_once, s.m, steps(s.d), 1).big;
   s.block = s.big ? 128 : 64;
   s.blocks = ceil_div(s.m, s.block);
   // the queries' product: few tiles and a long k, split to fill the card
-  const int64_t tiles = ceil_div(s.d, 128) * ceil_div(s.piece < s.n ? s.piece : s.n, 128);
-  const int64_t steps = ceil_div(s.m * 2, sps::kStep) * (s.dtype == SPS_F32 ? sps::kSegments : 1);
-  int64_t z = 512 / (tiles > 0 ? tiles : 1);
-  if (z > steps / 8) z = steps / 8;
-  if (z > 64) z = 64;
-  s.splits_q = z < 1 ? 1 : (int)z;
+  s.plan_q = sps::plan_tiles(at_once, s.d, steps(s.m), 64);
+  s.plan_i = sps::plan_tiles(s.m, s.d, steps(at_once), 1);
   return s;
 }
 
@@ -583,11 +632,11 @@ Layout layout_of(const Shape &s) {
     if (s.gq) {
       L.turned_i = take(s.d * turned_ld(s.m) * 2 * p);
       L.g = p == 3 ? take(s.piece * s.ld_g * 6) : L.code;
-      if (s.splits_q > 1) L.part = take((int64_t)s.splits_q * s.piece * s.d * 4);
+      if (s.plan_q.splits > 1) L.part = take((int64_t)s.plan_q.splits * s.piece * s.d * 4);
     }
     if (s.gi) {
       L.turned_q = take(s.d * turned_ld(s.n) * 2 * p);
-      L.gt = take(s.m * s.piece * 2 * p);
+      L.gt = take(s.m * odd_ld(s.piece) * 2 * p);
       if (s.piece < s.n) L.sum_i = take(s.m * s.d * 4);
     }
   }
@@ -643,35 +692,35 @@ void launch_lay(int32_t dtype, const sps::LayArgs &a, hipStream_t s) {
   else launch_lay_t<sps::bf16_t>(a, s);
 }
 
-template <class Op, typename P>
+template <class Op, class Code>
 void launch_logits(bool big, sps::LogitArgs a, hipStream_t s) {
   const int64_t t = big ? 256 : 128;
   a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
   a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
   const dim3 grid((uint32_t)a.g.tiles_c * (uint32_t)a.g.tiles_r);
-  if (big) hipLaunchKernelGGL((sps::ce_logits_kernel<Op, P, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((sps::ce_logits_kernel<Op, P, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
+  if (big) hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <class Op>
-void launch_product(sps::ProductArgs a, hipStream_t s) {
-  const int64_t big = ceil_div(a.g.p.rows, 256) * ceil_div(a.g.q.rows, 256);
-  const int64_t t = big >= 256 ? 256 : 128;
+void launch_product(sps::TilePlan plan, sps::ProductArgs a, hipStream_t s) {
+  const int64_t t = plan.big ? 256 : 128;
+  a.g.splits = plan.splits;
   a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
   a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
   const dim3 grid((uint32_t)a.g.tiles_c * (uint32_t)a.g.tiles_r * (uint32_t)a.g.splits);
-  if (t == 256) hipLaunchKernelGGL((sps::ce_product_kernel<Op, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
+  if (plan.big) hipLaunchKernelGGL((sps::ce_product_kernel<Op, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((sps::ce_product_kernel<Op, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 void launch_turn(int32_t dtype, const sps::TurnArgs &a, hipStream_t s) {
   const dim3 grid((uint32_t)ceil_div(a.cols, 64), (uint32_t)ceil_div(a.rows, 64));
   if (dtype == SPS_F32)
-    hipLaunchKernelGGL((sps::ce_turn_kernel<float, float>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((sps::ce_turn_kernel<float, sps::CodeF32>), grid, dim3(256), 0, s, a);
   else if (dtype == SPS_F16)
-    hipLaunchKernelGGL((sps::ce_turn_kernel<sps::f16_t, uint16_t>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((sps::ce_turn_kernel<sps::f16_t, sps::CodeF16>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((sps::ce_turn_kernel<sps::bf16_t, uint16_t>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((sps::ce_turn_kernel<sps::bf16_t, sps::CodeBf16>), grid, dim3(256), 0, s, a);
 }
 
 void launch_zero(void *out, int64_t rows, int64_t bytes, int64_t stride, hipStream_t s) {
@@ -775,7 +824,6 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.g.q = {oq.base + r0 * oq.ld, rows, oq.ld, oq.plane};
     a.g.p = oi;
     a.g.k_bytes = k_logits;
-    a.g.planes = wide;
     a.g.splits = 1;
     a.c = (float)(1.44269504088896340736 / (double)temperature);
     a.bias = bias;
@@ -785,9 +833,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
     a.rows_pad = h.piece;
     a.z_target = reinterpret_cast<float *>(ws + L.z_target);
-    if (wide) launch_logits<sps::OpBf16, float>(h.big, a, s);
-    else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, uint16_t>(h.big, a, s);
-    else launch_logits<sps::OpBf16, uint16_t>(h.big, a, s);
+    if (wide) launch_logits<sps::OpF32, sps::CodeF32>(h.big, a, s);
+    else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, sps::CodeF16>(h.big, a, s);
+    else launch_logits<sps::OpBf16, sps::CodeBf16>(h.big, a, s);
 
     sps::RowSum *const sums = grad ? reinterpret_cast<sps::RowSum *>(ws + L.sums) : nullptr;
     const sps::SumArgs b{a.stats, h.piece, rows, m, (int32_t)h.blocks, a.z_target,
@@ -810,8 +858,8 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     }
     if (h.gi) {
       c.turned = reinterpret_cast<uint16_t *>(ws + L.gt);
-      c.ld_t = h.piece;
-      c.plane_t = h.piece * m;
+      c.ld_t = odd_ld(h.piece);
+      c.plane_t = c.ld_t * m;
     }
     launch_turn(h.dtype, c, s);
 
@@ -819,23 +867,22 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     p.dtype = grad_dtype;
     p.alpha = (float)(1.0 / (double)temperature);
     p.scale = scale;
-    p.g.planes = wide;
     if (h.gq) {
       p.g.q = {reinterpret_cast<const uint8_t *>(c.g), rows, h.ld_g * 2, c.plane_g * 2};
       p.g.p = {ws + L.turned_i, d, turned_ld(m) * 2, turned_ld(m) * d * 2};
-      p.g.k_bytes = h.ld_g * 2;
-      p.g.splits = h.splits_q;
+      p.g.k_bytes = up(m, 64) * 2;
       p.out = static_cast<uint8_t *>(grad_queries) + r0 * ld_queries * sg;
       p.ld = ld_queries;
       p.mask = {sums, nullptr};
-      if (h.splits_q > 1) {
+      if (h.plan_q.splits > 1) {
         p.part = reinterpret_cast<float *>(ws + L.part);
         p.stride = rows * d;
       }
-      if (h.dtype == SPS_F16) launch_product<sps::OpF16>(p, s);
-      else launch_product<sps::OpBf16>(p, s);
-      if (h.splits_q > 1) {
-        const sps::JoinArgs j{p.part, p.stride, rows, d, h.splits_q, p.out, p.ld, grad_dtype, p.alpha,
+      if (wide) launch_product<sps::OpF32>(h.plan_q, p, s);
+      else if (h.dtype == SPS_F16) launch_product<sps::OpF16>(h.plan_q, p, s);
+      else launch_product<sps::OpBf16>(h.plan_q, p, s);
+      if (h.plan_q.splits > 1) {
+        const sps::JoinArgs j{p.part, p.stride, rows, d, h.plan_q.splits, p.out, p.ld, grad_dtype, p.alpha,
                               scale, p.mask};
         int64_t blocks = ceil_div(rows * ceil_div(d, 4), 256);
         if (blocks > 4096) blocks = 4096;
@@ -844,10 +891,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     }
     if (h.gi) {
       const bool last = r0 + rows == n;
-      p.g.q = {ws + L.gt, m, h.piece * 2, h.piece * m * 2};
+      p.g.q = {ws + L.gt, m, c.ld_t * 2, c.plane_t * 2};
       p.g.p = {ws + L.turned_q + r0 * 2, d, turned_ld(n) * 2, turned_ld(n) * d * 2};
       p.g.k_bytes = up(rows, 8) * 2;
-      p.g.splits = 1;
       float *const sum = reinterpret_cast<float *>(ws + L.sum_i);
       p.before = r0 > 0 ? sum : nullptr;
       p.part = last ? nullptr : sum;
@@ -855,8 +901,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       p.out = grad_items;
       p.ld = ld_items;
       p.mask = {nullptr, bias};
-      if (h.dtype == SPS_F16) launch_product<sps::OpF16>(p, s);
-      else launch_product<sps::OpBf16>(p, s);
+      if (wide) launch_product<sps::OpF32>(h.plan_i, p, s);
+      else if (h.dtype == SPS_F16) launch_product<sps::OpF16>(h.plan_i, p, s);
+      else launch_product<sps::OpBf16>(h.plan_i, p, s);
     }
   }
   return sps::launch_status(what);

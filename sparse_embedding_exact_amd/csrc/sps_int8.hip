@@ -156,8 +156,8 @@ struct Int8Args {
 template <typename T, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
   using Tile = GemmTile<OpI8, TC, TR, WC, WR>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * Tile::kBuf];
-  const GemmPlace at = gemm_place<TC, TR>(a.g);
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
+  const GemmPlace at = gemm_place<OpI8, TC, TR>(a.g);
   Tile t;
   t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
   float sp[Tile::kFragC][4];
@@ -168,19 +168,21 @@ __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
       const int64_t c = at.col0 + t.col_of(i) + e;
       sp[i][e] = c < a.g.p.rows ? a.scale_p[c] : 0.0f;
     }
+  uint8_t *const mine = t.wave_lds(lds);
 #pragma unroll
   for (int j = 0; j < Tile::kFragR; ++j) {
     const int64_t r = at.row0 + t.row_of(j);
-    if (r >= a.g.q.rows) continue;
-    const float sq = a.scale_q[r];
-    T *const out = static_cast<T *>(a.out) + r * a.ld;
+    const float sq = r < a.g.q.rows ? a.scale_q[r] : 0.0f;
 #pragma unroll
     for (int i = 0; i < Tile::kFragC; ++i) {
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = (float)t.acc[i][j][e] * sq * sp[i][e];
-      put_four<T>(out, at.col0 + t.col_of(i), a.g.p.rows, v);
+      t.template stage<T>(mine, i, quad_of<T>(v));
     }
+    const int64_t r0 = at.row0 + t.rows_at(j), c0 = at.col0 + t.cols_at();
+    t.template store<T>(mine, static_cast<T *>(a.out) + r0 * a.ld + c0, a.ld, a.g.q.rows - r0,
+                        a.g.p.rows - c0);
   }
 }
 
@@ -295,8 +297,8 @@ void launch_scores(sps::Int8Args &a, hipStream_t s) {
   if (n <= 16 && steps * 1024 <= kFewLds) return launch_few<T, 1>(a, s);
   if (n <= 32 && steps * 2048 <= kFewLds) return launch_few<T, 2>(a, s);
   if (n <= 64 && steps * 4096 <= kFewLds) return launch_few<T, 4>(a, s);
-  const int64_t big = sps::ceil_div(a.g.p.rows, 256) * sps::ceil_div(n, 256);
-  if (big >= 256) launch_tiles<T, 256, 256, 2, 4>(a, s);
+  if (sps::plan_tiles(n, a.g.p.rows, sps::ceil_div(a.g.k_bytes, sps::kStep), 1).big)
+    launch_tiles<T, 256, 256, 2, 4>(a, s);
   else launch_tiles<T, 128, 128, 2, 2>(a, s);
 }
 
