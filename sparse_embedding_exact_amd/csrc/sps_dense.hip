@@ -6,9 +6,10 @@
 // Three matrix products, the least there is, for a piece of the rows at a time:
 //   1. logits: a tile's z in registers; its rows' maxima and sums of
 //      exponentials go to `stats`, and e^(z - max) in 16 bits to `code`;
-//   2. sums: a row's log-sum-exp and loss from its blocks' statistics;
-//   3. gradient of the logits: code to G in place, and G transposed;
-//   4. two products with G, whose k (items, or rows) lies in one run.
+//   2. a row's log-sum-exp and loss from its blocks' statistics, and its codes to
+//      G in place;
+//   3. two products with G: for the queries its k (items) lies in one run, for
+//      the items it is read turned.
 // Code: a 16-bit float below the block's maximum, with 3 or 2 bits more than
 // G keeps when it is rounded to enter the matrix instructions, so z is not
 // computed twice. G's own column at the
@@ -148,8 +149,8 @@ struct LogitArgs {
   const int32_t *targets;
   void *code;  // nullable: uint16 (float32: float) [rows][ld]
   int64_t ld;
-  float2 *stats;  // [block of columns][rows_pad]: (max, sum of 2^(z - max))
-  int64_t rows_pad;
+  float2 *stats;  // [rows][blocks]: of a block of columns (max, sum of 2^(z - max))
+  int64_t blocks;
   float *z_target;
 };
 
@@ -161,6 +162,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
   const GemmPlace at = gemm_place<Op, TC, TR>(a.g);
   Tile t;
+  t.clear();
   t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
   constexpr float kInf = __builtin_inff();
   constexpr int FC = Tile::kFragC, FR = Tile::kFragR;
@@ -231,72 +233,151 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
     sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
     if (there && lane < 16 && first_col < cols)
-      a.stats[block * a.rows_pad + r] = {top, sum * (1.0f / (float)(1 << Code::kShift))};
+      a.stats[r * a.blocks + block] = {top, sum * (1.0f / (float)(1 << Code::kShift))};
   }
 }
 
 // ---------------------------------------------------------------------------
-// 2. sums
+// 2. sums, and the gradient of the logits
 
-// What the gradient of a row's logits needs: 2^(z - lse2) and the row's factor
-// (0: no gradient), and 1 - p of the target.
-struct RowSum {
-  float lse2, factor, rest;
-  int32_t target;
-};
-
-struct SumArgs {
+struct GradArgs {
   const float2 *stats;
-  int64_t rows_pad, rows, cols;
-  int32_t blocks;
+  int64_t rows, cols;
+  int32_t blocks, block;  // their number and columns
   const float *z_target, *weights;  // weights nullable
   const int32_t *targets;
   const float *scale;  // nullable: 1
   float *loss;
-  RowSum *out;
+  const void *code;  // [rows][ld]
+  int64_t ld;
+  uint16_t *g;  // planes of [rows][ld]; a 16-bit code's own place
+  int64_t plane_g;
+  float *factor;  // [rows]: 0 where a row has no gradient
 };
 
-// 16 rows a workgroup, 16 threads a row; sums beyond a block in float64.
-__global__ __launch_bounds__(256) void ce_sum_kernel(SumArgs a) {
-  __shared__ float tops[16][17];
-  __shared__ double sums[16][17];
-  const int i = threadIdx.x & 15, g = threadIdx.x >> 4;
-  const int64_t r = (int64_t)blockIdx.x * 16 + i;
-  float top = -__builtin_inff();
-  double sum = 0.0;
-  if (r < a.rows)
-    for (int32_t b = g; b < a.blocks; b += 16) {
-      const float2 s = a.stats[b * a.rows_pad + r];
-      const float m = fmaxf(top, s.x);
-      if (m == -__builtin_inff()) sum += (double)s.y;
-      else
-        sum = sum * (double)__builtin_amdgcn_exp2f(top - m) +
-              (double)s.y * (double)__builtin_amdgcn_exp2f(s.x - m);
-      top = m;
-    }
-  tops[i][g] = top;
-  sums[i][g] = sum;
-  __syncthreads();
-  if (threadIdx.x >= 16 || r >= a.rows) return;
-  float m = -__builtin_inff();
-  for (int k = 0; k < 16; ++k) m = fmaxf(m, tops[i][k]);
-  double l = 0.0;
-  for (int k = 0; k < 16; ++k)
-    l += m == -__builtin_inff() ? sums[i][k]
-                                : sums[i][k] * (double)__builtin_amdgcn_exp2f(tops[i][k] - m);
+// Sums beyond a block in float64.
+struct Running {
+  float top;
+  double sum;
+  __device__ __forceinline__ void join(float t, double s) {
+    const float m = fmaxf(top, t);
+    if (m == -__builtin_inff()) sum += s;  // 0, or NaN
+    else
+      sum = sum * (double)__builtin_amdgcn_exp2f(top - m) + s * (double)__builtin_amdgcn_exp2f(t - m);
+    top = m;
+  }
+};
+template <int LANES>
+__device__ __forceinline__ Running run_row(const float2 *stats, int32_t blocks, int lane, int step) {
+  Running x{-__builtin_inff(), 0.0};
+  for (int32_t b = lane; b < blocks; b += step) {
+    const float2 s = stats[b];
+    x.join(s.x, (double)s.y);
+  }
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) {
+    const float t = __shfl_xor(x.top, o, 64);
+    const double s = __shfl_xor(x.sum, o, 64);
+    x.join(t, s);
+  }
+  return x;
+}
+// The loss of a row, and whether it has one: its target is a column and some
+// column is left.
+__device__ __forceinline__ bool loss_of(const GradArgs &a, int64_t r, const Running &x, double *loss) {
   const int32_t t = a.targets[r];
-  const bool takes = t >= 0 && t < a.cols && !(l == 0.0);  // 0: every column is struck out
-  // log2 of the sum relative to the target's term
-  const double d = takes ? ((double)m - (double)a.z_target[r]) + log2(l) : 0.0;
-  const double loss = takes ? d * 0.69314718055994530942 : 0.0;
+  if (t < 0 || t >= a.cols || x.sum == 0.0) {
+    *loss = 0.0;
+    return false;
+  }
+  *loss = (((double)x.top - (double)a.z_target[r]) + log2(x.sum)) * 0.69314718055994530942;
+  return true;
+}
+
+// Losses alone: 16 lanes a row.
+__global__ __launch_bounds__(256) void ce_loss_kernel(GradArgs a) {
+  const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  const Running x = run_row<16>(a.stats + (r < a.rows ? r : 0) * a.blocks, a.blocks, lane, 16);
+  if (r >= a.rows || lane != 0) return;
+  double loss;
+  loss_of(a, r, x, &loss);
   a.loss[r] = (float)loss;
-  if (!a.out) return;
-  RowSum o;
-  o.lse2 = (float)((double)m + log2(l));
-  o.factor = takes ? (a.weights ? a.weights[r] : 1.0f) * (a.scale ? *a.scale : 1.0f) : 0.0f;
-  o.rest = takes ? (float)-expm1(-loss) : 0.0f;
-  o.target = t;
-  a.out[r] = o;
+}
+
+// A workgroup a row, 8 values a thread and step; the first ones are on their
+// way while the row's sums are joined. Bound by memory.
+constexpr int kGradAhead = 4;
+template <typename T, class Code>
+__global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
+  constexpr int NP = kPlanes<T>;
+  __shared__ Running parts[4];
+  const int64_t r = blockIdx.x;
+  const int64_t vecs = (a.cols + 63) / 64 * 8;  // G is filled with zeros to whole steps of a product
+  using Word = typename Code::Word;
+  struct Codes {
+    u32x4 w[sizeof(Word) / 2];
+  };
+  const Word *const code = static_cast<const Word *>(a.code) + r * a.ld;
+  const auto fetch = [&](int64_t v) { return *reinterpret_cast<const Codes *>(code + v * 8); };
+  Codes ahead[kGradAhead] = {};
+#pragma unroll
+  for (int i = 0; i < kGradAhead; ++i)
+    if (threadIdx.x + 256 * i < vecs) ahead[i] = fetch(threadIdx.x + 256 * i);
+
+  const float2 *const stats = a.stats + r * a.blocks;
+  const Running mine = run_row<64>(stats, a.blocks, threadIdx.x, 256);
+  if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = mine;
+  __syncthreads();
+  Running x = parts[0];
+  for (int i = 1; i < 4; ++i) x.join(parts[i].top, parts[i].sum);
+  double loss;
+  const bool takes = loss_of(a, r, x, &loss);
+  const float factor =
+      takes ? (a.weights ? a.weights[r] : 1.0f) * (a.scale ? *a.scale : 1.0f) : 0.0f;
+  if (threadIdx.x == 0) {
+    a.loss[r] = (float)loss;
+    a.factor[r] = factor;
+  }
+  const float lse2 = (float)((double)x.top + log2(x.sum)) + (float)Code::kShift;
+  const float at_target = takes ? (float)expm1(-loss) * factor : 0.0f;
+  const int32_t target = a.targets[r];
+
+  const auto put = [&](int64_t v, const Codes &c) {
+    const int64_t col = v * 8;
+    uint16_t o[NP][8] = {};
+    if (factor != 0.0f) {
+      const float f = col < a.cols
+                          ? __builtin_amdgcn_exp2f(stats[col / a.block].x - lse2) * factor : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float p;
+        if constexpr (sizeof(Word) == 2) {
+          p = Code::value((c.w[0][e / 2] >> (16 * (e & 1))) & 0xffffu);
+        } else {
+          const uint32_t u = c.w[e / 4][e & 3];
+          p = __builtin_bit_cast(float, u);
+        }
+        const float g = col + e < a.cols ? (col + e == target ? at_target : p * f) : 0.0f;
+        uint16_t w[NP];
+        if constexpr (NP == 1) w[0] = from_f32<T>(g).u;
+        else split(g, w);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) o[k][e] = w[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)o[k][2 * e] | (uint32_t)o[k][2 * e + 1] << 16;
+      *reinterpret_cast<u32x4 *>(a.g + k * a.plane_g + r * a.ld + col) = w;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kGradAhead; ++i)
+    if (threadIdx.x + 256 * i < vecs) put(threadIdx.x + 256 * i, ahead[i]);
+  for (int64_t v = threadIdx.x + 256 * kGradAhead; v < vecs; v += 256) put(v, fetch(v));
 }
 
 // The power of two that takes the largest weight to [2^14, 2^15).
@@ -321,101 +402,14 @@ __global__ __launch_bounds__(1024) void ce_scale_kernel(const float *weights, co
 }
 
 // ---------------------------------------------------------------------------
-// 3. gradient of the logits
-
-struct TurnArgs {
-  const void *code;  // [rows][ld]
-  int64_t ld, rows, cols, rows_pad;
-  const float2 *stats;
-  int32_t block;  // columns of a block of statistics
-  const RowSum *sums;
-  uint16_t *g;  // nullable: planes of [rows][ld]; a 16-bit code's own place
-  int64_t plane_g;
-  uint16_t *turned;  // nullable: planes of [cols][ld_t]
-  int64_t ld_t, plane_t;
-};
-
-// Tiles of 64 x 64, 16 bytes of G a thread and step both ways; bound by memory.
-template <typename T, class Code>
-__global__ __launch_bounds__(256) void ce_turn_kernel(TurnArgs a) {
-  constexpr int NP = kPlanes<T>;
-  __shared__ __attribute__((aligned(16))) uint16_t tile[NP][64][72];
-  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-  const int i8 = (threadIdx.x & 7) * 8;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = (threadIdx.x >> 3) + 32 * h;
-    const int64_t r = r0 + i, c = c0 + i8;
-    uint16_t v[NP][8] = {};
-    if (r < a.rows) {
-      const RowSum s = a.sums[r];
-      if (s.factor != 0.0f) {
-        const float f =
-            __builtin_amdgcn_exp2f(a.stats[(c / a.block) * a.rows_pad + r].x - s.lse2 -
-                                  (float)Code::kShift) *
-            s.factor;
-        float p[8];
-        if constexpr (sizeof(typename Code::Word) == 2) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.code) +
-                                                           r * a.ld + c);
-          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = Code::value((u[e / 2] >> (16 * (e & 1))) & 0xffffu);
-        } else {
-          const f32x4 *const w =
-              reinterpret_cast<const f32x4 *>(static_cast<const float *>(a.code) + r * a.ld + c);
-          const f32x4 w0 = w[0], w1 = w[1];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = e < 4 ? w0[e & 3] : w1[e & 3];
-        }
-        const int64_t t = s.target - c;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = c + e < a.cols ? (t == e ? -s.rest * s.factor : p[e] * f) : 0.0f;
-          uint16_t o[NP];
-          if constexpr (NP == 1) o[0] = from_f32<T>(x).u;
-          else split(x, o);
-#pragma unroll
-          for (int k = 0; k < NP; ++k) v[k][e] = o[k];
-        }
-      }
-      if (a.g)
-#pragma unroll
-        for (int k = 0; k < NP; ++k)
-          *reinterpret_cast<uint4 *>(a.g + k * a.plane_g + r * a.ld + c) =
-              *reinterpret_cast<const uint4 *>(v[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < NP; ++k)
-      *reinterpret_cast<uint4 *>(&tile[k][i][i8]) = *reinterpret_cast<const uint4 *>(v[k]);
-  }
-  if (!a.turned) return;
-  __syncthreads();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = (threadIdx.x >> 3) + 32 * h;
-    const int64_t c = c0 + i, r = r0 + i8;
-    if (c >= a.cols || r >= a.ld_t) continue;
-#pragma unroll
-    for (int k = 0; k < NP; ++k) {
-      uint16_t v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = tile[k][i8 + e][i];
-      *reinterpret_cast<uint4 *>(a.turned + k * a.plane_t + c * a.ld_t + r) =
-          *reinterpret_cast<const uint4 *>(v);
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// 4. products with the gradient
+// 3. products with the gradient
 
 // Which rows of the gradient are zeros whatever the sums say.
 struct OutMask {
-  const RowSum *sums;  // nullable: rows without a factor
+  const float *factor;  // nullable: rows without one
   const float *bias;   // nullable: items struck out
   __device__ __forceinline__ bool out(int64_t r) const {
-    return (sums && sums[r].factor == 0.0f) || (bias && bias[r] == -__builtin_inff());
+    return (factor && factor[r] == 0.0f) || (bias && bias[r] == -__builtin_inff());
   }
 };
 
@@ -439,7 +433,7 @@ __device__ __forceinline__ void put_typed(void *out, int32_t dtype, int64_t at, 
   else put_four<bf16_t>(static_cast<bf16_t *>(out) + at, col, cols, v);
 }
 
-// The tile's sums, after those of earlier pieces, times alpha, to rows of T.
+// The tile's sums times alpha, to rows of T.
 template <typename T, class Tile>
 __device__ __forceinline__ void product_out(const ProductArgs &a, Tile &t, const GemmPlace &at,
                                             uint8_t *mine, T *out, int64_t ld, float alpha,
@@ -451,14 +445,9 @@ __device__ __forceinline__ void product_out(const ProductArgs &a, Tile &t, const
     const bool zero = r < rows && mask.out(r);
 #pragma unroll
     for (int i = 0; i < Tile::kFragC; ++i) {
-      const int64_t c = at.col0 + t.col_of(i);
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = t.acc[i][j][e];
-        if (a.before && r < rows && c + e < cols) v[e] += a.before[r * cols + c + e];
-        v[e] = zero ? 0.0f : v[e] * alpha;
-      }
+      for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : t.acc[i][j][e] * alpha;
       t.template stage<T>(mine, i, quad_of<T>(v));
     }
     const int64_t r0 = at.row0 + t.rows_at(j), c0 = at.col0 + t.cols_at();
@@ -466,12 +455,14 @@ __device__ __forceinline__ void product_out(const ProductArgs &a, Tile &t, const
   }
 }
 
-template <class Op, int TC, int TR, int WC, int WR>
+template <class Op, bool QT, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a) {
-  using Tile = GemmTile<Op, TC, TR, WC, WR>;
+  using Tile = GemmTile<Op, TC, TR, WC, WR, QT>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
   const GemmPlace at = gemm_place<Op, TC, TR>(a.g);
   Tile t;
+  if (a.before) t.start(a.before, a.g.q.rows, a.g.p.rows, at.row0, at.col0);
+  else t.clear();
   t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
   const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
   uint8_t *const mine = t.wave_lds(lds);
@@ -538,8 +529,8 @@ namespace {
 
 constexpr int64_t kMaxItems = 1ll << 22;  // a tile's rows of G stay below 2^31 bytes
 constexpr int64_t kMaxDim = 1ll << 16;
-// Bytes of a piece's codes and gradients (both layouts), and of statistics
-// where there are no codes.
+// Bytes of a piece's codes and gradients, and of statistics where there are no
+// codes.
 constexpr int64_t kPieceBytes = 1ll << 30;
 constexpr int64_t kStatBytes = 1ll << 28;
 constexpr int64_t kMaxPiece = 1ll << 20;
@@ -560,8 +551,8 @@ struct Shape {
 };
 
 struct Layout {
-  size_t scale, sums, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, gt, part,
-      sum_i, total;
+  size_t scale, factor, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, part, sum_i,
+      total;
 };
 
 int planes(const Shape &s) { return s.dtype == SPS_F32 ? 3 : 1; }
@@ -593,13 +584,13 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   s.pack_i = must_pack(i);
   s.ld_g = odd_ld(s.m);
   const bool grad = gq || gi;
-  const int64_t each = s.dtype == SPS_F32 ? 4 + 6 * gq + 6 * gi : 2 + 2 * gi;
+  const int64_t each = s.dtype == SPS_F32 ? 10 : 2;
   s.block = 64;
   int64_t rows = grad ? kPieceBytes / (s.ld_g * each) : kStatBytes / (8 * ceil_div(s.m, 64));
   rows = rows / 256 * 256;
   if (rows < 256) rows = 256;
   if (rows > kMaxPiece) rows = kMaxPiece;
-  s.piece = rows < s.n ? rows : up(s.n, 64);
+  s.piece = rows < s.n ? up(ceil_div(s.n, ceil_div(s.n, rows)), 256) : up(s.n, 64);
   const int seg = s.dtype == SPS_F32 ? sps::kSegments : 1;
   const int64_t at_once = s.piece < s.n ? s.piece : s.n;
   const auto steps = [&](int64_t k) { return ceil_div(k * 2, sps::kStep) * seg; };
@@ -627,16 +618,15 @@ Layout layout_of(const Shape &s) {
   if (s.pack_q) L.packed_q = take(s.n * packed_ld(s) * 2 * p);
   if (s.pack_i) L.packed_i = take(s.m * packed_ld(s) * 2 * p);
   if (s.gq || s.gi) {
-    L.sums = take(s.piece * (int64_t)sizeof(sps::RowSum));
+    L.factor = take(s.piece * 4);
     L.code = take(s.piece * s.ld_g * (p == 3 ? 4 : 2));
+    L.g = p == 3 ? take(s.piece * s.ld_g * 6) : L.code;
     if (s.gq) {
       L.turned_i = take(s.d * turned_ld(s.m) * 2 * p);
-      L.g = p == 3 ? take(s.piece * s.ld_g * 6) : L.code;
       if (s.plan_q.splits > 1) L.part = take((int64_t)s.plan_q.splits * s.piece * s.d * 4);
     }
     if (s.gi) {
       L.turned_q = take(s.d * turned_ld(s.n) * 2 * p);
-      L.gt = take(s.m * odd_ld(s.piece) * 2 * p);
       if (s.piece < s.n) L.sum_i = take(s.m * s.d * 4);
     }
   }
@@ -702,25 +692,25 @@ void launch_logits(bool big, sps::LogitArgs a, hipStream_t s) {
   else hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
-template <class Op>
+template <class Op, bool QT>
 void launch_product(sps::TilePlan plan, sps::ProductArgs a, hipStream_t s) {
   const int64_t t = plan.big ? 256 : 128;
   a.g.splits = plan.splits;
   a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
   a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
   const dim3 grid((uint32_t)a.g.tiles_c * (uint32_t)a.g.tiles_r * (uint32_t)a.g.splits);
-  if (plan.big) hipLaunchKernelGGL((sps::ce_product_kernel<Op, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((sps::ce_product_kernel<Op, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
+  if (plan.big) hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
-void launch_turn(int32_t dtype, const sps::TurnArgs &a, hipStream_t s) {
-  const dim3 grid((uint32_t)ceil_div(a.cols, 64), (uint32_t)ceil_div(a.rows, 64));
+void launch_grad(int32_t dtype, const sps::GradArgs &a, hipStream_t s) {
+  const dim3 grid((uint32_t)a.rows), block(256);
   if (dtype == SPS_F32)
-    hipLaunchKernelGGL((sps::ce_turn_kernel<float, sps::CodeF32>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((sps::ce_grad_kernel<float, sps::CodeF32>), grid, block, 0, s, a);
   else if (dtype == SPS_F16)
-    hipLaunchKernelGGL((sps::ce_turn_kernel<sps::f16_t, sps::CodeF16>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((sps::ce_grad_kernel<sps::f16_t, sps::CodeF16>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((sps::ce_turn_kernel<sps::bf16_t, sps::CodeBf16>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((sps::ce_grad_kernel<sps::bf16_t, sps::CodeBf16>), grid, block, 0, s, a);
 }
 
 void launch_zero(void *out, int64_t rows, int64_t bytes, int64_t stride, hipStream_t s) {
@@ -831,37 +821,33 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.code = grad ? ws + L.code : nullptr;
     a.ld = h.ld_g;
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
-    a.rows_pad = h.piece;
+    a.blocks = h.blocks;
     a.z_target = reinterpret_cast<float *>(ws + L.z_target);
     if (wide) launch_logits<sps::OpF32, sps::CodeF32>(h.big, a, s);
     else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, sps::CodeF16>(h.big, a, s);
     else launch_logits<sps::OpBf16, sps::CodeBf16>(h.big, a, s);
 
-    sps::RowSum *const sums = grad ? reinterpret_cast<sps::RowSum *>(ws + L.sums) : nullptr;
-    const sps::SumArgs b{a.stats, h.piece, rows, m, (int32_t)h.blocks, a.z_target,
-                         row_weights ? row_weights + r0 : nullptr, a.targets, scale, loss + r0, sums};
-    hipLaunchKernelGGL(sps::ce_sum_kernel, dim3((uint32_t)ceil_div(rows, 16)), dim3(256), 0, s, b);
-    if (!grad) continue;
-
-    sps::TurnArgs c{};
-    c.code = a.code;
-    c.ld = h.ld_g;
+    sps::GradArgs c{};
+    c.stats = a.stats;
     c.rows = rows;
     c.cols = m;
-    c.rows_pad = h.piece;
-    c.stats = a.stats;
+    c.blocks = (int32_t)h.blocks;
     c.block = h.block;
-    c.sums = sums;
-    if (h.gq) {
-      c.g = reinterpret_cast<uint16_t *>(ws + L.g);
-      c.plane_g = h.piece * h.ld_g;
+    c.z_target = a.z_target;
+    c.weights = row_weights ? row_weights + r0 : nullptr;
+    c.targets = a.targets;
+    c.scale = scale;
+    c.loss = loss + r0;
+    if (!grad) {
+      hipLaunchKernelGGL(sps::ce_loss_kernel, dim3((uint32_t)ceil_div(rows, 16)), dim3(256), 0, s, c);
+      continue;
     }
-    if (h.gi) {
-      c.turned = reinterpret_cast<uint16_t *>(ws + L.gt);
-      c.ld_t = odd_ld(h.piece);
-      c.plane_t = c.ld_t * m;
-    }
-    launch_turn(h.dtype, c, s);
+    c.code = a.code;
+    c.ld = h.ld_g;
+    c.g = reinterpret_cast<uint16_t *>(ws + L.g);
+    c.plane_g = h.piece * h.ld_g;
+    c.factor = reinterpret_cast<float *>(ws + L.factor);
+    launch_grad(h.dtype, c, s);
 
     sps::ProductArgs p{};
     p.dtype = grad_dtype;
@@ -873,14 +859,14 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       p.g.k_bytes = up(m, 64) * 2;
       p.out = static_cast<uint8_t *>(grad_queries) + r0 * ld_queries * sg;
       p.ld = ld_queries;
-      p.mask = {sums, nullptr};
+      p.mask = {c.factor, nullptr};
       if (h.plan_q.splits > 1) {
         p.part = reinterpret_cast<float *>(ws + L.part);
         p.stride = rows * d;
       }
-      if (wide) launch_product<sps::OpF32>(h.plan_q, p, s);
-      else if (h.dtype == SPS_F16) launch_product<sps::OpF16>(h.plan_q, p, s);
-      else launch_product<sps::OpBf16>(h.plan_q, p, s);
+      if (wide) launch_product<sps::OpF32, false>(h.plan_q, p, s);
+      else if (h.dtype == SPS_F16) launch_product<sps::OpF16, false>(h.plan_q, p, s);
+      else launch_product<sps::OpBf16, false>(h.plan_q, p, s);
       if (h.plan_q.splits > 1) {
         const sps::JoinArgs j{p.part, p.stride, rows, d, h.plan_q.splits, p.out, p.ld, grad_dtype, p.alpha,
                               scale, p.mask};
@@ -891,7 +877,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     }
     if (h.gi) {
       const bool last = r0 + rows == n;
-      p.g.q = {ws + L.gt, m, c.ld_t * 2, c.plane_t * 2};
+      p.part = nullptr;
+      p.g.q = {reinterpret_cast<const uint8_t *>(c.g), m, h.ld_g * 2, c.plane_g * 2};
+      p.g.k_rows = rows;
       p.g.p = {ws + L.turned_q + r0 * 2, d, turned_ld(n) * 2, turned_ld(n) * d * 2};
       p.g.k_bytes = up(rows, 8) * 2;
       float *const sum = reinterpret_cast<float *>(ws + L.sum_i);
@@ -901,9 +889,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       p.out = grad_items;
       p.ld = ld_items;
       p.mask = {nullptr, bias};
-      if (wide) launch_product<sps::OpF32>(h.plan_i, p, s);
-      else if (h.dtype == SPS_F16) launch_product<sps::OpF16>(h.plan_i, p, s);
-      else launch_product<sps::OpBf16>(h.plan_i, p, s);
+      if (wide) launch_product<sps::OpF32, true>(h.plan_i, p, s);
+      else if (h.dtype == SPS_F16) launch_product<sps::OpF16, true>(h.plan_i, p, s);
+      else launch_product<sps::OpBf16, true>(h.plan_i, p, s);
     }
   }
   return sps::launch_status(what);

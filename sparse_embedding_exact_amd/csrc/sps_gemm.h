@@ -6,6 +6,9 @@
 // bits, 128 of 8), a matrix instruction 64 of them, 16 bytes a lane, whatever
 // the type, so one body serves bf16, fp16 and int8.
 //
+// Or Q stands turned, Q[k][r] with a run of r a row of k (16-bit values): its
+// tile is then 64 rows of k, read through the transposing LDS load.
+//
 // Tile: TC columns by TR rows of D a workgroup, WC x WR waves. P is the matrix
 // instructions' first operand, so a lane holds four neighbouring columns of
 // one row: rows of D are stored, reduced and scaled without a move between
@@ -83,6 +86,7 @@ struct GemmOperand {
 struct GemmArgs {
   GemmOperand q, p;
   int64_t k_bytes;
+  int64_t k_rows;  // of a turned q
   int32_t splits;
   int32_t tiles_c, tiles_r;
 };
@@ -147,7 +151,7 @@ __device__ __forceinline__ Quad<T> quad_of(const float v[4]) {
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-template <class Op, int TC, int TR, int WC, int WR>
+template <class Op, int TC, int TR, int WC, int WR, bool QT = false>
 struct GemmTile {
   static constexpr int kThreads = 64 * WC * WR;
   static constexpr int kC = TC, kR = TR;
@@ -170,7 +174,34 @@ struct GemmTile {
     asm volatile("" ::: "memory");
   }
 
-  // The sum over steps [begin, end) for the tile at (row0, col0). The steps are
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kFragC; ++i)
+#pragma unroll
+      for (int j = 0; j < kFragR; ++j) acc[i][j] = Acc{};
+  }
+  // Sums that go on from those in rows of cols values.
+  __device__ __forceinline__ void start(const float *before, int64_t rows, int64_t cols, int64_t row0,
+                                        int64_t col0) {
+#pragma unroll
+    for (int j = 0; j < kFragR; ++j) {
+      const int64_t r = row0 + row_of(j);
+#pragma unroll
+      for (int i = 0; i < kFragC; ++i) {
+        const int64_t c = col0 + col_of(i);
+        const float *const x = before + r * cols + c;
+        if (r < rows && c + 4 <= cols) {
+          const Four<float> f = *reinterpret_cast<const Four<float> *>(x);
+          acc[i][j] = Acc{f.e[0], f.e[1], f.e[2], f.e[3]};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = r < rows && c + e < cols ? x[e] : 0.0f;
+        }
+      }
+    }
+  }
+
+  // Adds the sum over steps [begin, end) for the tile at (row0, col0). The steps are
   // taken from the turn-th on, round: rows whose length is a large power of two
   // have equal steps in few of L2's channels, and neighbouring tiles would ask
   // for them at once.
@@ -178,26 +209,31 @@ struct GemmTile {
                                       int end, uint8_t *lds) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wc = wave % WC, wr = wave / WC;
-#pragma unroll
-    for (int i = 0; i < kFragC; ++i)
-#pragma unroll
-      for (int j = 0; j < kFragR; ++j) acc[i][j] = Acc{};
     if (begin >= end) return;
 
     const uint32_t ld_p = (uint32_t)a.p.ld, ld_q = (uint32_t)a.q.ld;
-    const auto left = [](int64_t rows, int64_t first, int64_t ld) {
-      const int64_t b = (rows - first) * ld;  // rows past the last read as zeros
+    const auto left = [](int64_t rows, int64_t first, int64_t ld, int64_t in = 0) {
+      const int64_t b = (rows - first) * ld - in;  // rows past the last read as zeros
       return (int)(b < (int64_t)kMostBytes ? b : (int64_t)kMostBytes);
     };
-    const int size_p = left(a.p.rows, col0, a.p.ld), size_q = left(a.q.rows, row0, a.q.ld);
+    const int size_p = left(a.p.rows, col0, a.p.ld);
+    const int size_q = QT ? 0 : left(a.q.rows, row0, a.q.ld);
     uint8_t *const base_p = const_cast<uint8_t *>(a.p.base) + col0 * a.p.ld;
-    uint8_t *const base_q = const_cast<uint8_t *>(a.q.base) + row0 * a.q.ld;
+    uint8_t *const base_q = const_cast<uint8_t *>(a.q.base) + (QT ? row0 * 2 : row0 * a.q.ld);
 
     // this lane's place in a load: row lane / 8 of the wave's eight, and the chunk that belongs there
     const uint32_t row = (uint32_t)(wave * 8 + (lane >> 3));
     const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
-    const uint32_t off_p = row * ld_p + chunk, off_q = row * ld_q + chunk;
-    uint8_t *const to = lds + wave * 1024;
+    const uint32_t off_p = row * ld_p + chunk;
+    // Turned: 1024 bytes are 1024 / (2 TR) rows of k. A transposing read takes 32 bytes of 16 of
+    // them, rows k and k + 8 apart among them: pair p of 16-byte chunks of row k stands at p ^ turn(k),
+    // turn(k) = k % 4 + 4 (k / 8 % 2), so that 8 rows meet every bank once.
+    constexpr int kPlaces = TR * 2 / 16;
+    const uint32_t k_row = (uint32_t)(wave * (64 / kPlaces) + lane / kPlaces), place_q = (uint32_t)(lane % kPlaces);
+    const uint32_t turn = (k_row & 3) | (k_row >> 3 & 1) << 2;
+    const uint32_t off_q = QT ? k_row * ld_q + (place_q ^ (turn << 1)) * 16 : row * ld_q + chunk;
+    constexpr int kNextQ = QT ? (64 / kPlaces) * WC * WR : kRowsLoad;  // rows between a wave's loads
+    static_assert(!QT || kNextQ % 16 == 0, "one turn(k) for all loads of a lane");
 
     const uint32_t k_end = (uint32_t)a.k_bytes;  // of one segment
     const int many = end - begin;
@@ -214,14 +250,18 @@ struct GemmTile {
       }
     };
     place(at_step);
-    auto load = [&](uint8_t *b) {
+    auto load = [&](uint8_t *buf) {
+      uint8_t *const b = buf + wave * 1024;
       const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
           base_p + (Op::kPlanes > 1 ? seg_p(seg) * a.p.plane : 0), 0, size_p, 0x00020000);
       const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
-          base_q + (Op::kPlanes > 1 ? seg_q(seg) * a.q.plane : 0), 0, size_q, 0x00020000);
+          base_q + (Op::kPlanes > 1 ? seg_q(seg) * a.q.plane : 0) +
+              (QT ? (int64_t)(k / 2) * a.q.ld : 0),
+          0, QT ? left(a.k_rows, (int64_t)(k / 2), a.q.ld, row0 * 2) : size_q, 0x00020000);
       // past the end of k: an offset past the buffer's, which reads zeros
       const bool in = k + chunk < k_end;
-      const uint32_t at_p = in ? off_p + k : 0x80000000u, at_q = in ? off_q + k : 0x80000000u;
+      const uint32_t at_p = in ? off_p + k : 0x80000000u;
+      const uint32_t at_q = QT ? off_q : in ? off_q + k : 0x80000000u;
 #pragma unroll
       for (int i = 0; i < kLoadsP; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_u8 *)(b + i * kRowsLoad * kStep), 16,
@@ -229,7 +269,7 @@ struct GemmTile {
 #pragma unroll
       for (int i = 0; i < kLoadsQ; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_u8 *)(b + (TC + i * kRowsLoad) * kStep), 16,
-                                                 (int)(at_q + (uint32_t)i * kRowsLoad * ld_q), 0, 0, 0);
+                                                 (int)(at_q + (uint32_t)i * kNextQ * ld_q), 0, 0, 0);
       if (++at_step == end) {
         at_step = begin;
         place(begin);
@@ -245,48 +285,102 @@ struct GemmTile {
     // a fragment: row lane % 16, bytes 16 (lane / 16) of 64; the other 64 bytes are places ^ 4
     const int at0 = (lane & 15) * kStep + (((lane >> 4) ^ (lane & 7)) * 16), at1 = at0 ^ 64;
     const int from_p = wc * (kFragC * 16) * kStep, from_q = (TC + wr * (kFragR * 16)) * kStep;
-    auto read = [&](const uint8_t *b, Frag (&p)[kFragC], Frag (&q)[kFragR]) {
+    // turned: four lanes' 8 bytes are 16 columns of a row of k, 16 lanes' four rows, and a lane
+    // receives a column of them: rows 8 (lane / 16) to + 3 of 32, and the four behind with a second read
+    int turned[kFragR];
 #pragma unroll
-      for (int j = 0; j < kFragR; ++j)
-        q[j] = *reinterpret_cast<const Frag *>(b + from_q + j * 16 * kStep);
+    for (int j = 0; j < kFragR; ++j) {
+      const int four = (lane & 15) >> 2, k_at = (lane >> 4) * 8 + four;
+      turned[j] = TC * kStep + k_at * TR * 2 +
+                  ((wr * kFragR + j) ^ (four | ((lane >> 4) & 1) << 2)) * 32 + (lane & 3) * 8;
+    }
+    auto read_p = [&](const uint8_t *b, bool half, Frag (&p)[kFragC]) {
 #pragma unroll
       for (int i = 0; i < kFragC; ++i)
-        p[i] = *reinterpret_cast<const Frag *>(b + from_p + i * 16 * kStep);
+        p[i] = *reinterpret_cast<const Frag *>(b + from_p + i * 16 * kStep + (half ? at1 : at0));
     };
-    auto multiply = [&](Frag (&p)[kFragC], Frag (&q)[kFragR]) {
+    auto read_q = [&](const uint8_t *b, bool half, Frag (&q)[kFragR]) {
+      if constexpr (QT) {
+        // In assembly, since the compiler makes the builtin wait for every load to LDS on its way,
+        // also those to the other buffer; the block ends with its own wait.
+        static_assert(kFragR == 4, "four fragments a block");
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        s16x4 x[8];
+        uint32_t at[4];
 #pragma unroll
-      for (int i = 0; i < kFragC; ++i)
+        for (int j = 0; j < 4; ++j)
+          at[j] = (uint32_t)(uintptr_t)(lds_u8 *)const_cast<uint8_t *>(b) + turned[j] +
+                  (half ? 32 * TR * 2 : 0);
+        asm volatile(
+            "ds_read_b64_tr_b16 %0, %8\n\t"
+            "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+            "ds_read_b64_tr_b16 %2, %9\n\t"
+            "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+            "ds_read_b64_tr_b16 %4, %10\n\t"
+            "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+            "ds_read_b64_tr_b16 %6, %11\n\t"
+            "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]),
+              "=&v"(x[6]), "=&v"(x[7])
+            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(4 * TR * 2)
+            : "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const s16x4 lo = x[2 * j], hi = x[2 * j + 1];
+          const s16x8 both = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          q[j] = __builtin_bit_cast(Frag, both);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kFragR; ++j)
+          q[j] = *reinterpret_cast<const Frag *>(b + from_q + j * 16 * kStep + (half ? at1 : at0));
+      }
+    };
+    // Half a step from registers, while the next half is read into others.
+    auto half_step = [&](Frag (&p)[kFragC], Frag (&q)[kFragR], bool more, const uint8_t *b, bool half,
+                         Frag (&pn)[kFragC], Frag (&qn)[kFragR]) {
+      if (more && !QT) read_q(b, half, qn);
+      if (more) read_p(b, half, pn);
+#pragma unroll
+      for (int i = 0; i < kFragC; ++i) {
 #pragma unroll
         for (int j = 0; j < kFragR; ++j) acc[i][j] = Op::mma(p[i], q[j], acc[i][j]);
-      // the reads of the next half among them
-      constexpr int kReads = kFragC + kFragR, kEach = kFragC * kFragR / kReads;
+        if (QT && i == kFragC / 2 - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (more) read_q(b, half, qn);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (!QT) {  // matrix instructions between the reads
+        constexpr int kReads = kFragC + kFragR, kEach = kFragC * kFragR / kReads;
 #pragma unroll
-      for (int i = 0; i < kReads; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        for (int i = 0; i < kReads; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     };
 
-    // Half a step is multiplied from registers while the next half is read into others. Behind the
-    // barrier in a step's middle its buffer has been read to the end and is loaded again, and the
-    // next step, which had a whole step's time, is in the other.
+    // Behind the barrier in a step's middle its buffer has been read to the end and is loaded again,
+    // and the next step, which had a whole step's time, is in the other.
     Frag p0[kFragC], q0[kFragR], p1[kFragC], q1[kFragR];
-    load(to);
+    load(lds);
     arrive();
-    if (many > 1) load(to + kBuf);
-    read(lds + at0, p0, q0);
+    if (many > 1) load(lds + kBuf);
+    read_q(lds, false, q0);
+    read_p(lds, false, p0);
     __builtin_amdgcn_sched_barrier(0);
     int here = 0;
     for (int s = 0; s < many; ++s) {
-      read(lds + here + at1, p1, q1);
-      multiply(p0, q0);
+      half_step(p0, q0, true, lds + here, true, p1, q1);
       arrive();
-      if (s + 2 < many) load(to + here);
+      if (s + 2 < many) load(lds + here);
       __builtin_amdgcn_sched_barrier(0);
       here ^= kBuf;
-      if (s + 1 < many) read(lds + here + at0, p0, q0);
-      multiply(p1, q1);
+      half_step(p1, q1, s + 1 < many, lds + here, false, p0, q0);
     }
     arrive();  // LDS is free for what follows
   }
@@ -386,8 +480,8 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tiles of 256 x 256 (one workgroup a CU) or 128 x 128 (two), and into how
 // many parts k goes, by what each would take on 256 CUs: rounds of workgroups,
 // each its steps and what comes before and after them, and sums of parts
-// written and read. Measured in us: a step of a large tile 1.8, of a small one
-// 1.13 (two at a time); before and after 8 and 5.
+// written and read. Measured in us: a step of a large tile 1.7, of a small one
+// 1.2 (two at a time); before and after 8 and 6.
 struct TilePlan {
   bool big;
   int32_t splits;
@@ -399,7 +493,7 @@ inline TilePlan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int most_s
     const int64_t t = big ? 256 : 128, slots = big ? 256 : 512;
     const int64_t tiles = ceil_div(rows, t) * ceil_div(cols, t);
     for (int z = 1; z <= most_splits && (z == 1 || z * 4 <= steps); ++z) {
-      const double each = (double)ceil_div(steps, z) * (big ? 1.8 : 1.13) + (big ? 8.0 : 5.0);
+      const double each = (double)ceil_div(steps, z) * (big ? 1.7 : 1.2) + (big ? 8.0 : 6.0);
       const double join = z > 1 ? 5.0 + (double)z * (double)rows * (double)cols * 8.0 / 4e6 : 0.0;
       const double us = (double)ceil_div(tiles * z, slots) * each + join;
       if (us < least) {

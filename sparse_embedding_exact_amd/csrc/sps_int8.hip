@@ -159,6 +159,7 @@ __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
   const GemmPlace at = gemm_place<OpI8, TC, TR>(a.g);
   Tile t;
+  t.clear();
   t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
   float sp[Tile::kFragC][4];
 #pragma unroll
