@@ -76,33 +76,69 @@ struct LayArgs {
   RowMask mask;
 };
 
-// Tiles of 64 x 64 through LDS; bound by memory. Planes in elements.
+// Tiles of 64 x 64 through LDS, 8 values a thread and step both ways; bound by
+// memory. Planes in elements.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Eight {
+  T e[8];
+};
 template <typename T>
 __global__ __launch_bounds__(256) void lay_kernel(LayArgs a) {
   constexpr int NP = kPlanes<T>;
-  __shared__ uint16_t tile[NP][64][66];
+  __shared__ __attribute__((aligned(16))) uint16_t tile[NP][64][72];
   const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int in = (threadIdx.x & 7) * 8;
   const T *const x = static_cast<const T *>(a.x);
-  for (int i = wave; i < 64; i += 4) {
-    const int64_t r = r0 + i, c = c0 + lane;
-    uint16_t v[NP] = {};
-    if (r < a.rows && c < a.cols) split(x[r * a.ld + c], v);
-    if (a.packed && r < a.rows && c < a.ld_p)
 #pragma unroll
-      for (int p = 0; p < NP; ++p) a.packed[p * a.plane_p + r * a.ld_p + c] = v[p];
-    if (!a.turned) continue;
-    const bool out = r < a.rows && a.mask.out(r);
+  for (int h = 0; h < 2; ++h) {
+    const int i = (threadIdx.x >> 3) + 32 * h;
+    const int64_t r = r0 + i, c = c0 + in;
+    uint16_t v[NP][8] = {};
+    bool out = true;
+    if (r < a.rows) {
+      Eight<T> t{};
+      if (c + 8 <= a.cols) t = *reinterpret_cast<const Eight<T> *>(x + r * a.ld + c);
+      else {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) tile[p][i][lane] = out ? (uint16_t)0 : v[p];
+        for (int e = 0; e < 8; ++e)
+          if (c + e < a.cols) t.e[e] = x[r * a.ld + c + e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint16_t w[NP];
+        split(t.e[e], w);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) v[p][e] = w[p];
+      }
+      out = a.turned && a.mask.out(r);
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)v[p][2 * e] | (uint32_t)v[p][2 * e + 1] << 16;
+      if (a.packed && r < a.rows && c < a.ld_p)
+        *reinterpret_cast<u32x4 *>(a.packed + p * a.plane_p + r * a.ld_p + c) = w;
+      *reinterpret_cast<u32x4 *>(&tile[p][i][in]) = out ? u32x4{} : w;
+    }
   }
   if (!a.turned) return;
   __syncthreads();
-  for (int i = wave; i < 64; i += 4) {
-    const int64_t c = c0 + i, r = r0 + lane;
-    if (c < a.cols && r < a.ld_t)
+  // a thread takes 8 rows of one column: neighbouring threads neighbouring columns
+  const int c_in = threadIdx.x & 63;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) a.turned[p * a.plane_t + c * a.ld_t + r] = tile[p][lane][i];
+  for (int h = 0; h < 2; ++h) {
+    const int r_in = ((threadIdx.x >> 6) + 4 * h) * 8;
+    const int64_t c = c0 + c_in, r = r0 + r_in;
+    if (c >= a.cols || r >= a.ld_t) continue;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = (uint32_t)tile[p][r_in + 2 * e][c_in] | (uint32_t)tile[p][r_in + 2 * e + 1][c_in] << 16;
+      *reinterpret_cast<u32x4 *>(a.turned + p * a.plane_t + c * a.ld_t + r) = w;
+    }
   }
 }
 

@@ -33,19 +33,20 @@ __device__ __forceinline__ int32_t nearest_int8(float x, float y, float amax) {
   return (int32_t)k;
 }
 
-// A wave a row. The row's first vectors stay in registers between the maximum
-// and the integers, the rest is read again (from the caches). Bound by memory.
+// L lanes a row, so that most rows fit the four vectors that a lane keeps in
+// registers between the maximum and the integers and few lanes are left over;
+// what does not fit is read again (from the caches). Bound by memory.
 constexpr int kQuantKeep = 4;
-template <typename T>
+template <typename T, int L>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   constexpr int V = kVec<T>;
-  const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= a.n_rows) return;
-  const T *const x = static_cast<const T *>(a.x) + r * a.ld;
-  const int64_t whole = a.dim / V;  // whole vectors; the rest of the row is one short one
-  const int tail = (int)(a.dim - whole * V);
-  const auto fetch = [&](int64_t v) {
+  const int lane = threadIdx.x % L;
+  const int64_t r = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const bool there = r < a.n_rows;
+  const T *const x = static_cast<const T *>(a.x) + (there ? r : 0) * a.ld;
+  const int dim = (int)a.dim, whole = dim / V;  // whole vectors; the rest of the row is one short one
+  const int tail = dim - whole * V, vecs = whole + (tail > 0);
+  const auto fetch = [&](int v) {
     Vec<T> t{};
     if (v < whole) t = *reinterpret_cast<const Vec<T> *>(x + v * V);
     else if (v == whole) {
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     }
     return t;
   };
-  Vec<T> keep[kQuantKeep];
+  Vec<T> keep[kQuantKeep] = {};
   uint32_t top = 0;  // bits of magnitudes: their order, NaN above infinity
   const auto see = [&](const Vec<T> &t) {
 #pragma unroll
@@ -65,23 +66,26 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     }
   };
 #pragma unroll
-  for (int i = 0; i < kQuantKeep; ++i) keep[i] = fetch(lane + 64 * i);
+  for (int i = 0; i < kQuantKeep; ++i)
+    if (L * i < vecs) keep[i] = fetch(lane + L * i);
 #pragma unroll
-  for (int i = 0; i < kQuantKeep; ++i) see(keep[i]);
-  for (int64_t v = lane + 64 * kQuantKeep; v <= whole; v += 64) see(fetch(v));
+  for (int i = 0; i < kQuantKeep; ++i)
+    if (L * i < vecs) see(keep[i]);
+  for (int v = lane + L * kQuantKeep; v < vecs; v += L) see(fetch(v));
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
+  for (int o = L / 2; o > 0; o >>= 1) {
     const uint32_t b = (uint32_t)__shfl_xor((int)top, o, 64);
     top = b > top ? b : top;
   }
+  if (!there) return;
   const float amax = __builtin_bit_cast(float, top);
   const bool finite = top < 0x7f800000u;
   // rows of very small values are taken 2^64 times as large: 127 / amax must not overflow
   const float up = amax < 0x1p-60f ? 0x1p64f : 1.0f;
   const float inv = finite && top ? 127.0f / (amax * up) : 0.0f;
   int8_t *const q = a.q + r * a.ld_q;
-  const int64_t room = (a.dim + 15) & ~15ll;
-  const auto put = [&](int64_t v, const Vec<T> &t) {
+  const int room = (dim + 15) & ~15;  // up to there the row is filled with zeros
+  const auto put = [&](int v, const Vec<T> &t) {
     if (v * V >= room) return;
     uint32_t w[V / 4];
 #pragma unroll
@@ -97,9 +101,9 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     __builtin_memcpy(__builtin_assume_aligned(q + v * V, V), w, V);
   };
 #pragma unroll
-  for (int i = 0; i < kQuantKeep; ++i) put(lane + 64 * i, keep[i]);
-  // up to the next multiple of 16 the row is filled with zeros
-  for (int64_t v = lane + 64 * kQuantKeep; v * V < room; v += 64) put(v, fetch(v));
+  for (int i = 0; i < kQuantKeep; ++i)
+    if (L * i * V < room) put(lane + L * i, keep[i]);
+  for (int v = lane + L * kQuantKeep; v * V < room; v += L) put(v, fetch(v));
   if (lane == 0) a.scales[r] = finite ? amax / 127.0f : __builtin_nanf("");
 }
 
@@ -112,31 +116,28 @@ struct DequantArgs {
   int64_t ld;  // elements
 };
 
-// 16 integers a thread.
-template <typename T>
+// L lanes a row, 16 bytes of values a lane and step. Bound by memory.
+template <typename T, int L>
 __global__ __launch_bounds__(256) void dequantize_rows_kernel(DequantArgs a) {
-  const int64_t per = (a.dim + 15) / 16, all = a.n_rows * per;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
-    const int64_t r = i / per, c = (i - r * per) * 16;
-    const i32x4 w = *reinterpret_cast<const i32x4 *>(a.q + r * a.ld_q + c);
-    const float s = a.scales[r];
-    T *const out = static_cast<T *>(a.out) + r * a.ld + c;
-    constexpr int V = kVec<T>;
+  constexpr int V = kVec<T>;
+  const int64_t r = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (r >= a.n_rows) return;
+  const int dim = (int)a.dim;
+  const int8_t *const q = a.q + r * a.ld_q;
+  const float s = a.scales[r];
+  T *const out = static_cast<T *>(a.out) + r * a.ld;
+#pragma unroll 4
+  for (int c = (int)(threadIdx.x % L) * V; c < dim; c += L * V) {
+    int8_t w[V];  // the row's bytes reach to the next multiple of 16
+    __builtin_memcpy(w, __builtin_assume_aligned(q + c, V), V);
+    Vec<T> t;
 #pragma unroll
-    for (int j = 0; j < 16 / V; ++j) {
-      Vec<T> t;
+    for (int e = 0; e < V; ++e) t.e[e] = from_f32<T>((float)w[e] * s);
+    if (c + V <= dim) *reinterpret_cast<Vec<T> *>(out + c) = t;
+    else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const int k = j * V + e;
-        t.e[e] = from_f32<T>((float)(int8_t)((uint32_t)w[k / 4] >> (8 * (k % 4))) * s);
-      }
-      if (c + (j + 1) * V <= a.dim) *reinterpret_cast<Vec<T> *>(out + j * V) = t;
-      else {
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (c + j * V + e < a.dim) out[j * V + e] = t.e[e];
-      }
+      for (int e = 0; e < V; ++e)
+        if (c + e < dim) out[c + e] = t.e[e];
     }
   }
 }
@@ -273,6 +274,31 @@ sps_status check_rows8(const sps_int8_rows *x, const char *what) {
   return SPS_OK;
 }
 
+// Lanes a row: the fewest whose four vectors each hold it.
+template <typename T, template <typename, int> class Launch, class Args>
+void launch_lanes(const Args &a, hipStream_t s) {
+  const int64_t vecs = sps::ceil_div(a.dim, sps::kVec<T>);
+  if (vecs <= 16) Launch<T, 4>::go(a, s);
+  else if (vecs <= 32) Launch<T, 8>::go(a, s);
+  else if (vecs <= 64) Launch<T, 16>::go(a, s);
+  else if (vecs <= 128) Launch<T, 32>::go(a, s);
+  else Launch<T, 64>::go(a, s);
+}
+template <typename T, int L>
+struct Quantize {
+  static void go(const sps::QuantArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((sps::quantize_rows_kernel<T, L>), dim3((uint32_t)sps::ceil_div(a.n_rows, 256 / L)),
+                       dim3(256), 0, s, a);
+  }
+};
+template <typename T, int L>
+struct Dequantize {
+  static void go(const sps::DequantArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((sps::dequantize_rows_kernel<T, L>), dim3((uint32_t)sps::ceil_div(a.n_rows, 256 / L)),
+                       dim3(256), 0, s, a);
+  }
+};
+
 template <typename T, int NQ>
 void launch_few(const sps::Int8Args &a, hipStream_t s) {
   const size_t lds = (size_t)((a.g.k_bytes + 63) / 64) * NQ * 1024;
@@ -322,14 +348,10 @@ sps_status sps_quantize_rows(const sps_scores *x, int8_t *values, int64_t ld, fl
                         {values, x->n_rows, (x->n_cols + 15) & ~15ll, ld}))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the integers overlap the rows", what);
   sps::QuantArgs a{x->data, x->ld, x->n_rows, x->n_cols, values, ld, scales};
-  const dim3 grid((uint32_t)sps::ceil_div(x->n_rows, 4)), block(256);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (x->dtype == SPS_F32)
-    hipLaunchKernelGGL((sps::quantize_rows_kernel<float>), grid, block, 0, s, a);
-  else if (x->dtype == SPS_F16)
-    hipLaunchKernelGGL((sps::quantize_rows_kernel<sps::f16_t>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((sps::quantize_rows_kernel<sps::bf16_t>), grid, block, 0, s, a);
+  if (x->dtype == SPS_F32) launch_lanes<float, Quantize>(a, s);
+  else if (x->dtype == SPS_F16) launch_lanes<sps::f16_t, Quantize>(a, s);
+  else launch_lanes<sps::bf16_t, Quantize>(a, s);
   return sps::launch_status(what);
 }
 
@@ -340,6 +362,7 @@ sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype,
   if (st != SPS_OK) return st;
   const sps_scores view{out, dtype, x->n_rows, x->dim, ld_out, 0};
   st = sps::check_scores(&view, what);
+  if (st == SPS_OK) st = sps::check_grid(sps::ceil_div(x->n_rows, 4), 256, what);
   if (st != SPS_OK) return st;
   if (x->n_rows == 0) return SPS_OK;
   const int64_t size = sps::dtype_size(dtype);
@@ -347,16 +370,10 @@ sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype,
                         {x->values, x->n_rows, (x->dim + 15) & ~15ll, x->ld}))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the output overlaps the integers", what);
   sps::DequantArgs a{x->values, x->ld, x->scales, x->n_rows, x->dim, out, ld_out};
-  int64_t blocks = sps::ceil_div(x->n_rows * sps::ceil_div(x->dim, 16), 256);
-  if (blocks > 65536) blocks = 65536;
-  const dim3 grid((uint32_t)blocks), block(256);
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == SPS_F32)
-    hipLaunchKernelGGL((sps::dequantize_rows_kernel<float>), grid, block, 0, s, a);
-  else if (dtype == SPS_F16)
-    hipLaunchKernelGGL((sps::dequantize_rows_kernel<sps::f16_t>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((sps::dequantize_rows_kernel<sps::bf16_t>), grid, block, 0, s, a);
+  if (dtype == SPS_F32) launch_lanes<float, Dequantize>(a, s);
+  else if (dtype == SPS_F16) launch_lanes<sps::f16_t, Dequantize>(a, s);
+  else launch_lanes<sps::bf16_t, Dequantize>(a, s);
   return sps::launch_status(what);
 }
 
