@@ -21,6 +21,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sps_gemm.h"
 
 namespace sps {
@@ -196,81 +198,97 @@ template <class Op, class Code, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   using Tile = GemmTile<Op, TC, TR, WC, WR>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
-  const GemmPlace at = gemm_place<Op, TC, TR>(a.g);
-  Tile t;
-  t.clear();
-  t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
+  Tile t(a.g, lds);
+  using Word = typename Code::Word;
   constexpr float kInf = __builtin_inff();
   constexpr int FC = Tile::kFragC, FR = Tile::kFragR;
-  const int64_t cols = a.g.p.rows;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t first_col = at.col0 + (wave % WC) * (TC / WC);  // of this wave
-  // The logits are c times the sums, and where there is a bias or an edge, what is put in their
-  // place here.
-  float c = a.c;
-  if (a.bias || at.col0 + TC > cols) {
+  const int64_t rows = a.g.q.rows, cols = a.g.p.rows;
+  const int wave_col = t.wc * (TC / WC);
+  float c;
+  int32_t target[FR];
+  const auto take = [&] {
+    // The logits are c times the sums, and where there is a bias or an edge, what is put in their
+    // place here.
+    c = a.c;
 #pragma unroll
-    for (int i = 0; i < FC; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t col = at.col0 + t.col_of(i) + e;
-        const float b = col < cols ? (a.bias ? a.bias[col] * kLog2e : 0.0f) : -kInf;
-#pragma unroll
-        for (int j = 0; j < FR; ++j)  // a column that is struck out has no logit, whatever its item holds
-          t.acc[i][j][e] = b == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], c, b);
-      }
-    c = 1.0f;
-  }
-  const int64_t block = first_col / (TC / WC);
-  using Word = typename Code::Word;
-  uint8_t *const mine = t.wave_lds(lds);
-#pragma unroll
-  for (int j = 0; j < FR; ++j) {
-    const int64_t r = at.row0 + t.row_of(j);
-    const bool there = r < a.g.q.rows;
-    float top = -kInf;
-#pragma unroll
-    for (int i = 0; i < FC; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, t.acc[i][j][e]);
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
-    // the target's logit, where it is one of this wave's columns
-    const int first = there ? (int)(a.targets[r] - at.col0) : -1;
-    if ((uint32_t)(first - (wave % WC) * (TC / WC)) < (uint32_t)(TC / WC)) {
+    for (int j = 0; j < FR; ++j) {
+      const int64_t r = t.at.row0 + t.row_of(j);
+      target[j] = a.targets[r < rows ? r : rows - 1];
+    }
+    if (!a.bias && t.at.col0 + TC <= cols) return;
+    float b[FC][4];
+    if (a.bias) {
+      t.of_columns(a.bias, -kInf, b);
 #pragma unroll
       for (int i = 0; i < FC; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (first == t.col_of(i) + e) a.z_target[r] = t.acc[i][j][e] * c;
-    }
-    const float base = (float)Code::kShift - (top == -kInf ? 0.0f : top);
-    float sum = 0.0f;
+        for (int e = 0; e < 4; ++e) b[i][e] *= kLog2e;
+    } else {
 #pragma unroll
-    for (int i = 0; i < FC; ++i) {
-      float p[4];
+      for (int i = 0; i < FC; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e], c, base));
-        sum += p[e];
-      }
-      if (a.code) {
-        if constexpr (sizeof(Word) == 2)
-          t.template stage<Word>(mine, i, u32x2{Code::two(p[0], p[1]), Code::two(p[2], p[3])});
-        else
-          t.template stage<Word>(mine, i, f32x4{p[0], p[1], p[2], p[3]});
-      }
+        for (int e = 0; e < 4; ++e) b[i][e] = t.at.col0 + t.col_of(i) + e < cols ? 0.0f : -kInf;
     }
-    if (a.code) {  // rows of codes are padded to a multiple of 64
-      const int64_t r0 = at.row0 + t.rows_at(j);
-      t.template store<Word>(mine, static_cast<Word *>(a.code) + r0 * a.ld + first_col, a.ld,
-                             a.g.q.rows - r0, ((cols + 63) & ~63ll) - first_col);
+#pragma unroll
+    for (int i = 0; i < FC; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < FR; ++j)  // a column that is struck out has no logit, whatever its item holds
+          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], c, b[i][e]);
+    c = 1.0f;
+  };
+  const auto put_all = [&](auto whole) {
+    const int64_t block = (t.at.col0 + wave_col) / (TC / WC);
+#pragma unroll
+    for (int j = 0; j < FR; ++j) {
+      const int64_t r = t.at.row0 + t.row_of(j);
+      float top = -kInf;
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, t.acc[i][j][e]);
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
+      // the target's logit, where it is one of this wave's columns
+      const int first = (int)(target[j] - t.at.col0);
+      if (r < rows && (uint32_t)(first - wave_col) < (uint32_t)(TC / WC)) {
+#pragma unroll
+        for (int i = 0; i < FC; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (first == t.col_of(i) + e) a.z_target[r] = t.acc[i][j][e] * c;
+      }
+      const float base = (float)Code::kShift - (top == -kInf ? 0.0f : top);
+      float sum = 0.0f;
+      typename QuadOf<Word>::Bits w[FC];
+#pragma unroll
+      for (int i = 0; i < FC; ++i) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e], c, base));
+          sum += p[e];
+        }
+        if constexpr (sizeof(Word) == 2) w[i] = {Code::two(p[0], p[1]), Code::two(p[2], p[3])};
+        else w[i] = quad_of<float>(p);
+      }
+      if (a.code)  // rows of codes are padded to a multiple of 64
+        t.template store<Word, whole.value>(j, w, static_cast<Word *>(a.code), a.ld, rows,
+                                            (cols + 63) & ~63ll);
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      if (r < rows && t.lane < 16 && t.at.col0 + wave_col < cols)
+        a.stats[r * a.blocks + block] = {top, sum * (1.0f / (float)(1 << Code::kShift))};
     }
-    sum += __shfl_xor(sum, 16, 64);
-    sum += __shfl_xor(sum, 32, 64);
-    if (there && lane < 16 && first_col < cols)
-      a.stats[r * a.blocks + block] = {top, sum * (1.0f / (float)(1 << Code::kShift))};
-  }
+  };
+  const auto put = [&] {
+    const bool whole = t.full();
+    if (whole) put_all(std::true_type{});
+    else put_all(std::false_type{});
+    return a.code && whole;
+  };
+  gemm_tiles<Tile::template kStores<Word>>(t, a.g, Op{}, [&] { t.clear(); }, take, put);
 }
 
 // ---------------------------------------------------------------------------
@@ -470,24 +488,23 @@ __device__ __forceinline__ void put_typed(void *out, int32_t dtype, int64_t at, 
 }
 
 // The tile's sums times alpha, to rows of T.
-template <typename T, class Tile>
-__device__ __forceinline__ void product_out(const ProductArgs &a, Tile &t, const GemmPlace &at,
-                                            uint8_t *mine, T *out, int64_t ld, float alpha,
+template <typename T, bool FULL, class Tile>
+__device__ __forceinline__ void product_out(Tile &t, T *out, int64_t ld, float alpha,
                                             const OutMask &mask) {
-  const int64_t rows = a.g.q.rows, cols = a.g.p.rows;
+  const int64_t rows = t.a.q.rows, cols = t.a.p.rows;
 #pragma unroll
   for (int j = 0; j < Tile::kFragR; ++j) {
-    const int64_t r = at.row0 + t.row_of(j);
+    const int64_t r = t.at.row0 + t.row_of(j);
     const bool zero = r < rows && mask.out(r);
+    typename QuadOf<T>::Bits w[Tile::kFragC];
 #pragma unroll
     for (int i = 0; i < Tile::kFragC; ++i) {
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : t.acc[i][j][e] * alpha;
-      t.template stage<T>(mine, i, quad_of<T>(v));
+      w[i] = quad_of<T>(v);
     }
-    const int64_t r0 = at.row0 + t.rows_at(j), c0 = at.col0 + t.cols_at();
-    t.template store<T>(mine, out + r0 * ld + c0, ld, rows - r0, cols - c0);
+    t.template store<T, FULL>(j, w, out, ld, rows, cols);
   }
 }
 
@@ -495,19 +512,28 @@ template <class Op, bool QT, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a) {
   using Tile = GemmTile<Op, TC, TR, WC, WR, QT>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
-  const GemmPlace at = gemm_place<Op, TC, TR>(a.g);
-  Tile t;
-  if (a.before) t.start(a.before, a.g.q.rows, a.g.p.rows, at.row0, at.col0);
-  else t.clear();
-  t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
+  Tile t(a.g, lds);
   const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
-  uint8_t *const mine = t.wave_lds(lds);
-  if (a.part) product_out<float>(a, t, at, mine, a.part + at.z * a.stride, a.g.p.rows, 1.0f, {});
-  else if (a.dtype == SPS_F32)
-    product_out<float>(a, t, at, mine, static_cast<float *>(a.out), a.ld, alpha, a.mask);
-  else  // the rows' own type: that of the products
-    product_out<typename Op::Type>(a, t, at, mine, static_cast<typename Op::Type *>(a.out), a.ld, alpha,
-                                   a.mask);
+  using Type = typename Op::Type;  // the rows' own: that of the products
+  const auto start = [&] {
+    if (a.before) t.start(a.before, a.g.q.rows, a.g.p.rows);
+    else t.clear();
+  };
+  const auto put_all = [&](auto whole) {
+    constexpr bool FULL = whole.value;
+    if (a.part) product_out<float, FULL>(t, a.part + t.at.z * a.stride, a.g.p.rows, 1.0f, {});
+    else if (a.dtype == SPS_F32)
+      product_out<float, FULL>(t, static_cast<float *>(a.out), a.ld, alpha, a.mask);
+    else product_out<Type, FULL>(t, static_cast<Type *>(a.out), a.ld, alpha, a.mask);
+  };
+  const auto put = [&] {
+    const bool whole = t.full();
+    if (whole) put_all(std::true_type{});
+    else put_all(std::false_type{});
+    return whole;
+  };
+  // the fewest stores of the three
+  gemm_tiles<Tile::template kStores<Type>>(t, a.g, Op{}, start, [] {}, put);
 }
 
 struct JoinArgs {
@@ -578,12 +604,11 @@ struct Shape {
   int32_t dtype;
   bool gq, gi;  // which gradients
   bool pack_q, pack_i;
-  bool big;          // tiles of 256 x 256 for the logits
   int64_t piece;     // rows of a piece, a multiple of 64
   int64_t ld_g;      // items, padded
   int32_t block;     // columns of a block of statistics
   int64_t blocks;
-  sps::TilePlan plan_q, plan_i;  // of the products for the queries and the items
+  sps::TilePlan plan_l, plan_q, plan_i;  // of the logits, and the products for the queries and the items
 };
 
 struct Layout {
@@ -630,8 +655,8 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   const int seg = s.dtype == SPS_F32 ? sps::kSegments : 1;
   const int64_t at_once = s.piece < s.n ? s.piece : s.n;
   const auto steps = [&](int64_t k) { return ceil_div(k * 2, sps::kStep) * seg; };
-  s.big = sps::plan_tiles(at_once, s.m, steps(s.d), 1).big;
-  s.block = s.big ? 128 : 64;
+  s.plan_l = sps::plan_tiles(at_once, s.m, steps(s.d), 1);
+  s.block = s.plan_l.big ? 128 : 64;
   s.blocks = ceil_div(s.m, s.block);
   // the queries' product: few tiles and a long k, split to fill the card
   s.plan_q = sps::plan_tiles(at_once, s.d, steps(s.m), 64);
@@ -719,12 +744,12 @@ void launch_lay(int32_t dtype, const sps::LayArgs &a, hipStream_t s) {
 }
 
 template <class Op, class Code>
-void launch_logits(bool big, sps::LogitArgs a, hipStream_t s) {
-  const int64_t t = big ? 256 : 128;
+void launch_logits(const sps::TilePlan &plan, sps::LogitArgs a, hipStream_t s) {
+  const int64_t t = plan.big ? 256 : 128;
   a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
   a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
-  const dim3 grid((uint32_t)a.g.tiles_c * (uint32_t)a.g.tiles_r);
-  if (big) hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
+  const dim3 grid(plan.grid((int64_t)a.g.tiles_c * a.g.tiles_r));
+  if (plan.big) hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
@@ -734,7 +759,7 @@ void launch_product(sps::TilePlan plan, sps::ProductArgs a, hipStream_t s) {
   a.g.splits = plan.splits;
   a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
   a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
-  const dim3 grid((uint32_t)a.g.tiles_c * (uint32_t)a.g.tiles_r * (uint32_t)a.g.splits);
+  const dim3 grid(plan.grid((int64_t)a.g.tiles_c * a.g.tiles_r * a.g.splits));
   if (plan.big) hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
@@ -859,9 +884,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
     a.blocks = h.blocks;
     a.z_target = reinterpret_cast<float *>(ws + L.z_target);
-    if (wide) launch_logits<sps::OpF32, sps::CodeF32>(h.big, a, s);
-    else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, sps::CodeF16>(h.big, a, s);
-    else launch_logits<sps::OpBf16, sps::CodeBf16>(h.big, a, s);
+    if (wide) launch_logits<sps::OpF32, sps::CodeF32>(h.plan_l, a, s);
+    else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, sps::CodeF16>(h.plan_l, a, s);
+    else launch_logits<sps::OpBf16, sps::CodeBf16>(h.plan_l, a, s);
 
     sps::GradArgs c{};
     c.stats = a.stats;

@@ -14,7 +14,9 @@
 // one row: rows of D are stored, reduced and scaled without a move between
 // lanes. Tiles of both operands go straight from memory to LDS (no registers,
 // no ds_write), two buffers deep: the next step's loads are issued behind the
-// barrier that frees their buffer and have a whole step to arrive.
+// barrier that frees their buffer and have a whole step to arrive. A workgroup
+// goes from tile to tile, and the next one's first two steps are loaded while
+// this one's sums are put away.
 //
 // LDS: a row's 128 bytes in eight 16-byte places, chunk c at place c ^ (row &
 // 7): a direct load fills 64 lanes' places in order, so the permutation is
@@ -139,17 +141,41 @@ __device__ __forceinline__ void put_four(T *out, int64_t col, int64_t cols, cons
   }
 }
 
-// Four values of a type, side by side.
+// Four values in a type's bits, side by side.
 template <typename T>
-struct alignas(4 * sizeof(T)) Quad {
-  T e[4];
+struct QuadOf {
+  typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T))));
 };
 template <typename T>
-__device__ __forceinline__ Quad<T> quad_of(const float v[4]) {
-  return {{from_f32<T>(v[0]), from_f32<T>(v[1]), from_f32<T>(v[2]), from_f32<T>(v[3])}};
+__device__ __forceinline__ typename QuadOf<T>::Bits quad_of(const float v[4]) {
+  struct {
+    T e[4];
+  } q = {{from_f32<T>(v[0]), from_f32<T>(v[1]), from_f32<T>(v[2]), from_f32<T>(v[3])}};
+  return __builtin_bit_cast(typename QuadOf<T>::Bits, q);
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// A tile's rows and columns and its part of the steps.
+struct GemmPlace {
+  int64_t row0, col0;
+  int begin, end;
+  int32_t z;
+};
+template <class Op, int TC, int TR>
+__device__ __forceinline__ GemmPlace gemm_place(const GemmArgs &a, uint32_t id) {
+  GemmPlace g;
+  int tc, tr;
+  const uint32_t tiles = (uint32_t)a.tiles_c * (uint32_t)a.tiles_r;
+  g.z = (int32_t)(id / tiles);
+  tile_of(id % tiles, a.tiles_c, a.tiles_r, &tc, &tr);
+  g.row0 = (int64_t)tr * TR;
+  g.col0 = (int64_t)tc * TC;
+  const int steps = (int)((a.k_bytes + kStep - 1) / kStep) * (Op::kPlanes > 1 ? kSegments : 1);
+  g.begin = (int)((int64_t)steps * g.z / a.splits);
+  g.end = (int)((int64_t)steps * (g.z + 1) / a.splits);
+  return g;
+}
 
 template <class Op, int TC, int TR, int WC, int WR, bool QT = false>
 struct GemmTile {
@@ -157,22 +183,125 @@ struct GemmTile {
   static constexpr int kC = TC, kR = TR;
   static constexpr int kFragC = TC / WC / 16, kFragR = TR / WR / 16;
   static constexpr int kBuf = (TC + TR) * kStep;  // bytes of one step
-  static constexpr int kLds = 2 * kBuf;
+  static constexpr int kWaveLds = 4096;           // a wave's part for what it stores
+  static constexpr int kLds = 2 * kBuf + kWaveLds * WC * WR;
   static constexpr int kRowsLoad = 8 * WC * WR;   // rows that one load of every wave fills
   static constexpr int kLoadsP = TC / kRowsLoad, kLoadsQ = TR / kRowsLoad;
+  static constexpr int kLoads = kLoadsP + kLoadsQ;
   static_assert(TC % kRowsLoad == 0 && TR % kRowsLoad == 0, "whole loads");
   static_assert(kLds <= 160 * 1024, "LDS");
   using Acc = typename Op::Acc;
   using Frag = typename Op::Frag;
 
+  const GemmArgs &a;
+  uint8_t *const lds;
+  int lane;
+  const int wave, wc, wr;
+  const uint32_t ld_p, ld_q, chunk;
+  uint32_t off_p, off_q;
   Acc acc[kFragC][kFragR];
+  GemmPlace at;  // of the sums
+  // of the loads, which are ahead of them
+  uint8_t *base_p, *base_q;
+  int size_p, size_q, begin, end, at_step, seg;
+  int64_t col_q;
+  uint32_t k;
+  bool any;
 
-  // This wave's loads and reads are done, and behind the barrier every wave's.
-  static __device__ __forceinline__ void arrive() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+  // Turned: 1024 bytes are 1024 / (2 TR) rows of k. A transposing read takes 32 bytes of 16 of
+  // them, rows k and k + 8 apart among them: pair p of 16-byte chunks of row k stands at p ^ turn(k),
+  // turn(k) = k % 4 + 4 (k / 8 % 2), so that 8 rows meet every bank once.
+  static constexpr int kPlaces = TR * 2 / 16;
+  static constexpr int kNextQ = QT ? (64 / kPlaces) * WC * WR : kRowsLoad;  // rows between a wave's loads
+  static_assert(!QT || kNextQ % 16 == 0, "one turn(k) for all loads of a lane");
+
+  __device__ __forceinline__ GemmTile(const GemmArgs &args, uint8_t *shared)
+      : a(args), lds(shared), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), wc(wave % WC),
+        wr(wave / WC), ld_p((uint32_t)args.p.ld), ld_q((uint32_t)args.q.ld),
+        // this lane's place in a load: row lane / 8 of the wave's eight, and the chunk that belongs there
+        chunk((uint32_t)(((lane & 7) ^ (lane >> 3)) * 16)) {
+    const uint32_t row = (uint32_t)(wave * 8 + (lane >> 3));
+    off_p = row * ld_p + chunk;
+    const uint32_t k_row = (uint32_t)(wave * (64 / kPlaces) + lane / kPlaces), q = (uint32_t)(lane % kPlaces);
+    const uint32_t turn = (k_row & 3) | (k_row >> 3 & 1) << 2;
+    off_q = QT ? k_row * ld_q + (q ^ (turn << 1)) * 16 : row * ld_q + chunk;
   }
+
+  // What is computed from the lane is computed again in each part of a tile: held over the loop of
+  // tiles, it would not leave registers for the sums.
+  __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(lane)); }
+
+  // ---- loads
+
+  static __device__ __forceinline__ int left(int64_t rows, int64_t first, int64_t ld, int64_t in = 0) {
+    const int64_t b = (rows - first) * ld - in;  // rows past the last read as zeros
+    return (int)(b < (int64_t)kMostBytes ? b : (int64_t)kMostBytes);
+  }
+  __device__ __forceinline__ void place_step(int step) {
+    at_step = step;
+    seg = 0;
+    if constexpr (Op::kPlanes > 1) {
+      const int steps = (int)(((uint32_t)a.k_bytes + kStep - 1) / kStep);
+      seg = step / steps;
+      step -= seg * steps;
+    }
+    k = (uint32_t)step * kStep;
+  }
+  // One step of k into a buffer; past the last one as many loads, of nothing.
+  __device__ __forceinline__ void load(uint8_t *buf) {
+    uint8_t *const b = buf + wave * 1024;
+    const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
+        base_p + (Op::kPlanes > 1 ? seg_p(seg) * a.p.plane : 0), 0, size_p, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+        base_q + (Op::kPlanes > 1 ? seg_q(seg) * a.q.plane : 0) + (QT ? (int64_t)(k / 2) * a.q.ld : 0),
+        0, QT ? left(a.k_rows, (int64_t)(k / 2), a.q.ld, col_q) : size_q, 0x00020000);
+    // past the end of k: an offset past the buffer's, which reads zeros
+    const bool in = any && k + chunk < (uint32_t)a.k_bytes;
+    const uint32_t at_p = in ? off_p + k : 0x80000000u;
+    const uint32_t at_q = (QT ? any : in) ? off_q + (QT ? 0u : k) : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < kLoadsP; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_u8 *)(b + i * kRowsLoad * kStep), 16,
+                                               (int)(at_p + (uint32_t)i * kRowsLoad * ld_p), 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kLoadsQ; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_u8 *)(b + (TC + i * kRowsLoad) * kStep), 16,
+                                               (int)(at_q + (uint32_t)i * kNextQ * ld_q), 0, 0, 0);
+    if (at_step + 1 == end) {
+      place_step(begin);
+    } else {
+      ++at_step;
+      k += kStep;
+      if (Op::kPlanes > 1 && k >= (uint32_t)a.k_bytes) {
+        k = 0;
+        ++seg;
+      }
+    }
+  }
+  // The first two steps of a tile's. Steps are taken from the turn-th on, round: rows whose length
+  // is a large power of two have equal steps in few of L2's channels, and neighbouring tiles would
+  // ask for them at once.
+  __device__ __forceinline__ void prefetch(const GemmPlace &next) {
+    base_p = const_cast<uint8_t *>(a.p.base) + next.col0 * a.p.ld;
+    base_q = const_cast<uint8_t *>(a.q.base) + (QT ? next.row0 * 2 : next.row0 * a.q.ld);
+    size_p = left(a.p.rows, next.col0, a.p.ld);
+    size_q = QT ? 0 : left(a.q.rows, next.row0, a.q.ld);
+    col_q = next.row0 * 2;
+    begin = next.begin;
+    end = next.end;
+    const int many = end - begin;
+    place_step(begin + (int)(((uint32_t)(next.col0 / TC) * 2u) % (uint32_t)many));
+    any = true;
+    load(lds);
+    any = many > 1;
+    load(lds + kBuf);
+    any = true;
+    // nothing that follows goes before these loads: they are counted
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // ---- sums
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -181,16 +310,16 @@ struct GemmTile {
       for (int j = 0; j < kFragR; ++j) acc[i][j] = Acc{};
   }
   // Sums that go on from those in rows of cols values.
-  __device__ __forceinline__ void start(const float *before, int64_t rows, int64_t cols, int64_t row0,
-                                        int64_t col0) {
+  __device__ __forceinline__ void start(const float *before, int64_t rows, int64_t cols) {
+    const bool whole = full();
 #pragma unroll
     for (int j = 0; j < kFragR; ++j) {
-      const int64_t r = row0 + row_of(j);
+      const int64_t r = at.row0 + row_of(j);
 #pragma unroll
       for (int i = 0; i < kFragC; ++i) {
-        const int64_t c = col0 + col_of(i);
+        const int64_t c = at.col0 + col_of(i);
         const float *const x = before + r * cols + c;
-        if (r < rows && c + 4 <= cols) {
+        if (whole) {
           const Four<float> f = *reinterpret_cast<const Four<float> *>(x);
           acc[i][j] = Acc{f.e[0], f.e[1], f.e[2], f.e[3]};
         } else {
@@ -201,278 +330,271 @@ struct GemmTile {
     }
   }
 
-  // Adds the sum over steps [begin, end) for the tile at (row0, col0). The steps are
-  // taken from the turn-th on, round: rows whose length is a large power of two
-  // have equal steps in few of L2's channels, and neighbouring tiles would ask
-  // for them at once.
-  __device__ __forceinline__ void run(const GemmArgs &a, int64_t row0, int64_t col0, int begin,
-                                      int end, uint8_t *lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wc = wave % WC, wr = wave / WC;
-    if (begin >= end) return;
+  // All but the latest N of this wave's memory operations and its reads of LDS are done, and behind
+  // the barrier every wave's.
+  template <int N>
+  static __device__ __forceinline__ void wait() {
+    static_assert(N < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+  }
+  static __device__ __forceinline__ void barrier() {
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
 
-    const uint32_t ld_p = (uint32_t)a.p.ld, ld_q = (uint32_t)a.q.ld;
-    const auto left = [](int64_t rows, int64_t first, int64_t ld, int64_t in = 0) {
-      const int64_t b = (rows - first) * ld - in;  // rows past the last read as zeros
-      return (int)(b < (int64_t)kMostBytes ? b : (int64_t)kMostBytes);
-    };
-    const int size_p = left(a.p.rows, col0, a.p.ld);
-    const int size_q = QT ? 0 : left(a.q.rows, row0, a.q.ld);
-    uint8_t *const base_p = const_cast<uint8_t *>(a.p.base) + col0 * a.p.ld;
-    uint8_t *const base_q = const_cast<uint8_t *>(a.q.base) + (QT ? row0 * 2 : row0 * a.q.ld);
-
-    // this lane's place in a load: row lane / 8 of the wave's eight, and the chunk that belongs there
-    const uint32_t row = (uint32_t)(wave * 8 + (lane >> 3));
-    const uint32_t chunk = (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16);
-    const uint32_t off_p = row * ld_p + chunk;
-    // Turned: 1024 bytes are 1024 / (2 TR) rows of k. A transposing read takes 32 bytes of 16 of
-    // them, rows k and k + 8 apart among them: pair p of 16-byte chunks of row k stands at p ^ turn(k),
-    // turn(k) = k % 4 + 4 (k / 8 % 2), so that 8 rows meet every bank once.
-    constexpr int kPlaces = TR * 2 / 16;
-    const uint32_t k_row = (uint32_t)(wave * (64 / kPlaces) + lane / kPlaces), place_q = (uint32_t)(lane % kPlaces);
-    const uint32_t turn = (k_row & 3) | (k_row >> 3 & 1) << 2;
-    const uint32_t off_q = QT ? k_row * ld_q + (place_q ^ (turn << 1)) * 16 : row * ld_q + chunk;
-    constexpr int kNextQ = QT ? (64 / kPlaces) * WC * WR : kRowsLoad;  // rows between a wave's loads
-    static_assert(!QT || kNextQ % 16 == 0, "one turn(k) for all loads of a lane");
-
-    const uint32_t k_end = (uint32_t)a.k_bytes;  // of one segment
-    const int many = end - begin;
-    int at_step = begin + (int)(((uint32_t)(col0 / TC) * 2u) % (uint32_t)many);
-    int seg = 0;
-    uint32_t k;
-    const auto place = [&](int step) {
-      if constexpr (Op::kPlanes > 1) {
-        const int steps = (int)((k_end + kStep - 1) / kStep);
-        seg = step / steps;
-        k = (uint32_t)(step - seg * steps) * kStep;
-      } else {
-        k = (uint32_t)step * kStep;
-      }
-    };
-    place(at_step);
-    auto load = [&](uint8_t *buf) {
-      uint8_t *const b = buf + wave * 1024;
-      const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
-          base_p + (Op::kPlanes > 1 ? seg_p(seg) * a.p.plane : 0), 0, size_p, 0x00020000);
-      const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
-          base_q + (Op::kPlanes > 1 ? seg_q(seg) * a.q.plane : 0) +
-              (QT ? (int64_t)(k / 2) * a.q.ld : 0),
-          0, QT ? left(a.k_rows, (int64_t)(k / 2), a.q.ld, row0 * 2) : size_q, 0x00020000);
-      // past the end of k: an offset past the buffer's, which reads zeros
-      const bool in = k + chunk < k_end;
-      const uint32_t at_p = in ? off_p + k : 0x80000000u;
-      const uint32_t at_q = QT ? off_q : in ? off_q + k : 0x80000000u;
-#pragma unroll
-      for (int i = 0; i < kLoadsP; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_u8 *)(b + i * kRowsLoad * kStep), 16,
-                                                 (int)(at_p + (uint32_t)i * kRowsLoad * ld_p), 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < kLoadsQ; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_u8 *)(b + (TC + i * kRowsLoad) * kStep), 16,
-                                                 (int)(at_q + (uint32_t)i * kNextQ * ld_q), 0, 0, 0);
-      if (++at_step == end) {
-        at_step = begin;
-        place(begin);
-      } else {
-        k += kStep;
-        if (Op::kPlanes > 1 && k >= k_end) {
-          k = 0;
-          ++seg;
-        }
-      }
-    };
-
+  __device__ __forceinline__ void read_p(const uint8_t *b, bool half, Frag (&p)[kFragC]) const {
     // a fragment: row lane % 16, bytes 16 (lane / 16) of 64; the other 64 bytes are places ^ 4
-    const int at0 = (lane & 15) * kStep + (((lane >> 4) ^ (lane & 7)) * 16), at1 = at0 ^ 64;
-    const int from_p = wc * (kFragC * 16) * kStep, from_q = (TC + wr * (kFragR * 16)) * kStep;
-    // turned: four lanes' 8 bytes are 16 columns of a row of k, 16 lanes' four rows, and a lane
-    // receives a column of them: rows 8 (lane / 16) to + 3 of 32, and the four behind with a second read
-    int turned[kFragR];
+    const int in = (lane & 15) * kStep + (((lane >> 4) ^ (lane & 7)) * 16);
 #pragma unroll
-    for (int j = 0; j < kFragR; ++j) {
+    for (int i = 0; i < kFragC; ++i)
+      p[i] = *reinterpret_cast<const Frag *>(b + (wc * kFragC + i) * 16 * kStep + (half ? in ^ 64 : in));
+  }
+  __device__ __forceinline__ void read_q(const uint8_t *b, bool half, Frag (&q)[kFragR]) const {
+    if constexpr (QT) {
+      // Four lanes' 8 bytes are 16 columns of a row of k, 16 lanes' four rows, and a lane receives a
+      // column of them: rows 8 (lane / 16) to + 3 of 32, and the four behind with a second read. In
+      // assembly, since the compiler makes the builtin wait for every load to LDS on its way, also
+      // those to the other buffer; the block ends with its own wait.
+      static_assert(kFragR == 4, "four fragments a block");
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
       const int four = (lane & 15) >> 2, k_at = (lane >> 4) * 8 + four;
-      turned[j] = TC * kStep + k_at * TR * 2 +
-                  ((wr * kFragR + j) ^ (four | ((lane >> 4) & 1) << 2)) * 32 + (lane & 3) * 8;
+      const int turn = four | ((lane >> 4) & 1) << 2;
+      s16x4 x[8];
+      uint32_t from[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        from[j] = (uint32_t)(uintptr_t)(lds_u8 *)const_cast<uint8_t *>(b) +
+                  (uint32_t)(TC * kStep + k_at * TR * 2 + ((wr * kFragR + j) ^ turn) * 32 + (lane & 3) * 8 +
+                             (half ? 32 * TR * 2 : 0));
+      asm volatile(
+          "ds_read_b64_tr_b16 %0, %8\n\t"
+          "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %2, %9\n\t"
+          "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %4, %10\n\t"
+          "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
+          "ds_read_b64_tr_b16 %6, %11\n\t"
+          "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]),
+            "=&v"(x[6]), "=&v"(x[7])
+          : "v"(from[0]), "v"(from[1]), "v"(from[2]), "v"(from[3]), "n"(4 * TR * 2)
+          : "memory");
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const s16x4 lo = x[2 * j], hi = x[2 * j + 1];
+        const s16x8 both = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        q[j] = __builtin_bit_cast(Frag, both);
+      }
+    } else {
+      const int in = (lane & 15) * kStep + (((lane >> 4) ^ (lane & 7)) * 16);
+#pragma unroll
+      for (int j = 0; j < kFragR; ++j)
+        q[j] = *reinterpret_cast<const Frag *>(b + (TC + (wr * kFragR + j) * 16) * kStep +
+                                               (half ? in ^ 64 : in));
     }
-    auto read_p = [&](const uint8_t *b, bool half, Frag (&p)[kFragC]) {
+  }
+  // Half a step from registers, while the next half is read into others.
+  __device__ __forceinline__ void half_step(Frag (&p)[kFragC], Frag (&q)[kFragR], bool more,
+                                            const uint8_t *b, bool half, Frag (&pn)[kFragC],
+                                            Frag (&qn)[kFragR]) {
+    if (more && !QT) read_q(b, half, qn);
+    if (more) read_p(b, half, pn);
 #pragma unroll
-      for (int i = 0; i < kFragC; ++i)
-        p[i] = *reinterpret_cast<const Frag *>(b + from_p + i * 16 * kStep + (half ? at1 : at0));
-    };
-    auto read_q = [&](const uint8_t *b, bool half, Frag (&q)[kFragR]) {
-      if constexpr (QT) {
-        // In assembly, since the compiler makes the builtin wait for every load to LDS on its way,
-        // also those to the other buffer; the block ends with its own wait.
-        static_assert(kFragR == 4, "four fragments a block");
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        s16x4 x[8];
-        uint32_t at[4];
+    for (int i = 0; i < kFragC; ++i) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          at[j] = (uint32_t)(uintptr_t)(lds_u8 *)const_cast<uint8_t *>(b) + turned[j] +
-                  (half ? 32 * TR * 2 : 0);
-        asm volatile(
-            "ds_read_b64_tr_b16 %0, %8\n\t"
-            "ds_read_b64_tr_b16 %1, %8 offset:%12\n\t"
-            "ds_read_b64_tr_b16 %2, %9\n\t"
-            "ds_read_b64_tr_b16 %3, %9 offset:%12\n\t"
-            "ds_read_b64_tr_b16 %4, %10\n\t"
-            "ds_read_b64_tr_b16 %5, %10 offset:%12\n\t"
-            "ds_read_b64_tr_b16 %6, %11\n\t"
-            "ds_read_b64_tr_b16 %7, %11 offset:%12\n\t"
-            "s_waitcnt lgkmcnt(0)"
-            : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(x[4]), "=&v"(x[5]),
-              "=&v"(x[6]), "=&v"(x[7])
-            : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(4 * TR * 2)
-            : "memory");
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const s16x4 lo = x[2 * j], hi = x[2 * j + 1];
-          const s16x8 both = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          q[j] = __builtin_bit_cast(Frag, both);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kFragR; ++j)
-          q[j] = *reinterpret_cast<const Frag *>(b + from_q + j * 16 * kStep + (half ? at1 : at0));
+      for (int j = 0; j < kFragR; ++j) acc[i][j] = Op::mma(p[i], q[j], acc[i][j]);
+      if (QT && i == kFragC / 2 - 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) read_q(b, half, qn);
+        __builtin_amdgcn_sched_barrier(0);
       }
-    };
-    // Half a step from registers, while the next half is read into others.
-    auto half_step = [&](Frag (&p)[kFragC], Frag (&q)[kFragR], bool more, const uint8_t *b, bool half,
-                         Frag (&pn)[kFragC], Frag (&qn)[kFragR]) {
-      if (more && !QT) read_q(b, half, qn);
-      if (more) read_p(b, half, pn);
+    }
+    if (!QT) {  // matrix instructions between the reads
+      constexpr int kReads = kFragC + kFragR, kEach = kFragC * kFragR / kReads;
 #pragma unroll
-      for (int i = 0; i < kFragC; ++i) {
-#pragma unroll
-        for (int j = 0; j < kFragR; ++j) acc[i][j] = Op::mma(p[i], q[j], acc[i][j]);
-        if (QT && i == kFragC / 2 - 1) {
-          __builtin_amdgcn_sched_barrier(0);
-          if (more) read_q(b, half, qn);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      for (int i = 0; i < kReads; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
-      if (!QT) {  // matrix instructions between the reads
-        constexpr int kReads = kFragC + kFragR, kEach = kFragC * kFragR / kReads;
-#pragma unroll
-        for (int i = 0; i < kReads; ++i) {
-          __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    };
-
-    // Behind the barrier in a step's middle its buffer has been read to the end and is loaded again,
-    // and the next step, which had a whole step's time, is in the other.
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // Adds the sums over the steps of `at`, whose first two are on their way. `counted`: behind
+  // their loads this wave has at least STORES memory operations, which need not be done.
+  template <int STORES>
+  __device__ __forceinline__ void run(bool counted) {
+    const int many = at.end - at.begin;
+    fresh();
+    if (counted) wait<STORES + kLoads>();
+    else wait<0>();
+    barrier();
     Frag p0[kFragC], q0[kFragR], p1[kFragC], q1[kFragR];
-    load(lds);
-    arrive();
-    if (many > 1) load(lds + kBuf);
     read_q(lds, false, q0);
     read_p(lds, false, p0);
     __builtin_amdgcn_sched_barrier(0);
     int here = 0;
     for (int s = 0; s < many; ++s) {
       half_step(p0, q0, true, lds + here, true, p1, q1);
-      arrive();
+      // behind the barrier this step's buffer has been read to the end and is loaded again, and the
+      // next step, which had a whole step's time, is in the other
+      if (counted && s == 0) wait<STORES>();
+      else wait<0>();
+      barrier();
       if (s + 2 < many) load(lds + here);
       __builtin_amdgcn_sched_barrier(0);
       here ^= kBuf;
       half_step(p1, q1, s + 1 < many, lds + here, false, p0, q0);
     }
-    arrive();  // LDS is free for what follows
+    // the buffers are free: their loads have been waited for, and behind the barrier the reads
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    barrier();
   }
 
-  // Rows out of the registers' layout (16 rows of four values a lane) into whole runs: 16 rows at
-  // a time go through this wave's own part of LDS, whose rows are 16 bytes longer than a run, so
-  // that 16 lanes of 16 rows meet every bank once. Stores of 16-byte runs of 16 rows each reach
-  // 3.2 TB/s, runs of 256 bytes and more what a fill does.
-  static constexpr int kWaveLds = kLds / (WC * WR);
+  // ---- what becomes of them
+
+  // Rows out of the registers' layout (16 rows of four values a lane) into whole runs: up to 16
+  // rows at a time go through this wave's own part of LDS, whose 16-byte places are permuted by the
+  // row so that every bank is met equally. Stores of 16-byte runs of 16 rows each reached 3.2 TB/s.
   template <typename T>
   static constexpr int kRun = TC / WC * (int)sizeof(T);
+  template <typename T>
+  static constexpr int kPass = kWaveLds / kRun<T> < 16 ? kWaveLds / kRun<T> : 16;  // rows
+  // Stores of a tile whose rows and columns are all there.
+  template <typename T>
+  static constexpr int kStores = kFragR * 16 * kRun<T> / 1024;
   template <typename T>
   struct __attribute__((packed, aligned(sizeof(T)))) Words {
     uint32_t w[4];
   };
-  __device__ __forceinline__ uint8_t *wave_lds(uint8_t *lds) const {
-    return lds + (threadIdx.x >> 6) * kWaveLds;
-  }
-  // This lane's four values of column group i, as 4 sizeof(T) bytes.
-  template <typename T, typename W>
-  __device__ __forceinline__ void stage(uint8_t *mine, int i, const W &v) const {
-    static_assert(sizeof(W) == 4 * sizeof(T), "four values");
-    static_assert(16 * (kRun<T> + 16) <= kWaveLds, "LDS");
-    const int lane = threadIdx.x & 63;
-    typedef uint32_t Bits __attribute__((ext_vector_type(sizeof(T))));
-    *reinterpret_cast<Bits *>(mine + (lane & 15) * (kRun<T> + 16) +
-                              (i * 16 + (lane >> 4) * 4) * (int)sizeof(T)) = __builtin_bit_cast(Bits, v);
-  }
-  // The staged 16 rows to `out` (row 0 of them, this wave's first column) for `rows` rows and
-  // `cols` columns at the most.
   template <typename T>
-  __device__ __forceinline__ void store(const uint8_t *mine, T *out, int64_t ld, int64_t rows,
+  static __device__ __forceinline__ int place(int row, int byte) {
+    constexpr int kOf = kRun<T> / 16;  // places of a row: 8, 16 or 32
+    static_assert(kOf == 8 || kOf == 16 || kOf == 32, "permutation");
+    const int turn = kOf == 8 ? row >> 1 : kOf == 16 ? row : (row & 7) << 1;
+    return row * kRun<T> + (((byte >> 4) ^ turn) << 4) + (byte & 15);
+  }
+  // What other lanes of the wave wrote to LDS is read behind here: a wave's LDS operations stay in
+  // their order once the compiler leaves them so.
+  static __device__ __forceinline__ void lanes_meet() {
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("" ::: "memory");
+  }
+  // To LDS in assembly: the compiler would make it wait for the loads to LDS that are on their way.
+  static __device__ __forceinline__ void write_lds(const uint8_t *to, u32x2 v) {
+    asm volatile("ds_write_b64 %0, %1" ::"v"((uint32_t)(uintptr_t)(lds_u8 *)const_cast<uint8_t *>(to)), "v"(v)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void write_lds(const uint8_t *to, u32x4 v) {
+    asm volatile("ds_write_b128 %0, %1" ::"v"((uint32_t)(uintptr_t)(lds_u8 *)const_cast<uint8_t *>(to)), "v"(v)
+                 : "memory");
+  }
+  // Rows 16 j to 16 j + 15 of this wave: v[i] are the bits of this lane's four values of column group
+  // i, to `out` (row 0, column 0 of D) of the given rows and columns; FULL: the tile's are all there.
+  template <typename T, bool FULL, typename Bits>
+  __device__ __forceinline__ void store(int j, const Bits (&v)[kFragC], T *out, int64_t ld, int64_t rows,
                                         int64_t cols) const {
+    static_assert(sizeof(Bits) == 4 * sizeof(T), "four values");
     constexpr int kLanes = kRun<T> / 16, kOnce = 64 / kLanes, V = 16 / (int)sizeof(T);
-    const int lane = threadIdx.x & 63;
+    const uint8_t *const mine = lds + 2 * kBuf + wave * kWaveLds;
+    const int64_t r0 = at.row0 + (wr * kFragR + j) * 16, c0 = at.col0 + wc * (kFragC * 16);
     const int in = lane % kLanes;
-    if (lane >= kOnce * kLanes) return;
+    const int64_t c = c0 + in * V;
+    T *const to0 = out + (r0 + lane / kLanes) * ld + c;
 #pragma unroll
-    for (int r = 0; r < (16 + kOnce - 1) / kOnce; ++r) {
-      const int row = r * kOnce + lane / kLanes;
-      if (row >= 16 || row >= rows) continue;
-      const u32x4 w = *reinterpret_cast<const u32x4 *>(mine + row * (kRun<T> + 16) + in * 16);
-      T *const to = out + row * ld + in * V;
-      if ((in + 1) * V <= cols) {
-        *reinterpret_cast<Words<T> *>(to) = {{w[0], w[1], w[2], w[3]}};
-      } else {
+    for (int pass = 0; pass < 16 / kPass<T>; ++pass) {
+      const int row = (lane & 15) - pass * kPass<T>;
+      if (kPass<T> == 16 || (row >= 0 && row < kPass<T>))
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (in * V + e < cols) {
-            const uint32_t u = w[e * (int)sizeof(T) / 4];
-            if constexpr (sizeof(T) == 4) to[e] = __builtin_bit_cast(T, u);
-            else to[e] = __builtin_bit_cast(T, (uint16_t)(u >> (16 * (e & 1))));
-          }
+        for (int i = 0; i < kFragC; ++i)
+          write_lds(mine + place<T>(row, (i * 16 + (lane >> 4) * 4) * (int)sizeof(T)), v[i]);
+      lanes_meet();
+#pragma unroll
+      for (int n = 0; n < kPass<T> / kOnce; ++n) {
+        const int from = n * kOnce + lane / kLanes;
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(mine + place<T>(from, in * 16));
+        T *const to = to0 + (int64_t)(pass * kPass<T> + n * kOnce) * ld;
+        const bool there = r0 + pass * kPass<T> + from < rows;
+        if (FULL || (there && c + V <= cols)) {
+          *reinterpret_cast<Words<T> *>(to) = {{w[0], w[1], w[2], w[3]}};
+        } else if (there) {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (c + e < cols) {
+              const uint32_t u = w[e * (int)sizeof(T) / 4];
+              if constexpr (sizeof(T) == 4) to[e] = __builtin_bit_cast(T, u);
+              else to[e] = __builtin_bit_cast(T, (uint16_t)(u >> (16 * (e & 1))));
+            }
+        }
       }
+      lanes_meet();
     }
   }
-  // First row of row group j and first column of this wave in the tile.
-  __device__ __forceinline__ int rows_at(int j) const {
-    return ((threadIdx.x >> 6) / WC) * (kFragR * 16) + j * 16;
+  __device__ __forceinline__ bool full() const {
+    return at.row0 + TR <= a.q.rows && at.col0 + TC <= a.p.rows;
   }
-  __device__ __forceinline__ int cols_at() const { return ((threadIdx.x >> 6) % WC) * (kFragC * 16); }
+  // Values of this lane's columns, `beyond` past the last.
+  __device__ __forceinline__ void of_columns(const float *x, float beyond, float (&v)[kFragC][4]) const {
+    const int64_t cols = a.p.rows;
+    if (at.col0 + TC <= cols) {
+#pragma unroll
+      for (int i = 0; i < kFragC; ++i) {
+        const Four<float> f = *reinterpret_cast<const Four<float> *>(x + at.col0 + col_of(i));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = f.e[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kFragC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int64_t c = at.col0 + col_of(i) + e;
+          const float f = x[c < cols ? c : cols - 1];
+          v[i][e] = c < cols ? f : beyond;
+        }
+    }
+  }
 
   // Place of acc[i][j][e] in the tile: row_of(j), col_of(i) + e.
   __device__ __forceinline__ int row_of(int j) const {
-    const int wave = threadIdx.x >> 6;
-    return (wave / WC) * (kFragR * 16) + j * 16 + (threadIdx.x & 15);
+    return wr * (kFragR * 16) + j * 16 + (lane & 15);
   }
   __device__ __forceinline__ int col_of(int i) const {
-    const int wave = threadIdx.x >> 6;
-    return (wave % WC) * (kFragC * 16) + i * 16 + ((threadIdx.x & 63) >> 4) * 4;
+    return wc * (kFragC * 16) + i * 16 + (lane >> 4) * 4;
   }
 };
 
-// The tile, its rows and columns and its part of the steps.
-struct GemmPlace {
-  int64_t row0, col0;
-  int begin, end;
-  int32_t z;
-};
-template <class Op, int TC, int TR>
-__device__ __forceinline__ GemmPlace gemm_place(const GemmArgs &a) {
-  GemmPlace g;
-  int tc, tr;
-  const uint32_t tiles = (uint32_t)a.tiles_c * (uint32_t)a.tiles_r;
-  g.z = (int32_t)(blockIdx.x / tiles);
-  tile_of(blockIdx.x % tiles, a.tiles_c, a.tiles_r, &tc, &tr);
-  g.row0 = (int64_t)tr * TR;
-  g.col0 = (int64_t)tc * TC;
-  const int steps = (int)((a.k_bytes + kStep - 1) / kStep) * (Op::kPlanes > 1 ? kSegments : 1);
-  g.begin = (int)((int64_t)steps * g.z / a.splits);
-  g.end = (int)((int64_t)steps * (g.z + 1) / a.splits);
-  return g;
+// A workgroup goes through tiles blockIdx.x, blockIdx.x + gridDim.x, ...: the
+// next one's first steps are loaded while this one's sums are put away.
+//   take(tile) is called before those loads, with the sums: what it loads is
+//   there first; put(tile) after, and says whether the next tile may count
+//   STORES memory operations behind them.
+template <int STORES, class Tile, class Op, class Start, class Take, class Put>
+__device__ __forceinline__ void gemm_tiles(Tile &t, const GemmArgs &a, Op, const Start &start,
+                                           const Take &take, const Put &put) {
+  const uint32_t all = (uint32_t)a.tiles_c * (uint32_t)a.tiles_r * (uint32_t)a.splits;
+  uint32_t id = blockIdx.x;
+  bool counted = false;
+  t.at = gemm_place<Op, Tile::kC, Tile::kR>(a, id);
+  t.prefetch(t.at);
+  for (;;) {
+    start();
+    t.template run<STORES>(counted);
+    t.fresh();
+    take();
+    id += gridDim.x;
+    const bool more = id < all;
+    GemmPlace next{};
+    if (more) {
+      next = gemm_place<Op, Tile::kC, Tile::kR>(a, id);
+      t.prefetch(next);
+    }
+    t.fresh();
+    counted = put();
+    if (!more) break;
+    t.at = next;
+  }
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -482,15 +604,20 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // each its steps and what comes before and after them, and sums of parts
 // written and read. Measured in us: a step of a large tile 1.7, of a small one
 // 1.2 (two at a time); before and after 8 and 6.
+constexpr int kCus = 256;
 struct TilePlan {
   bool big;
   int32_t splits;
+  uint32_t grid(int64_t tiles) const {
+    const int64_t at_once = big ? kCus : 2 * kCus;
+    return (uint32_t)(tiles < at_once ? tiles : at_once);
+  }
 };
 inline TilePlan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int most_splits) {
   TilePlan best{false, 1};
   double least = 1e300;
   for (int big = 0; big < 2; ++big) {
-    const int64_t t = big ? 256 : 128, slots = big ? 256 : 512;
+    const int64_t t = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
     const int64_t tiles = ceil_div(rows, t) * ceil_div(cols, t);
     for (int z = 1; z <= most_splits && (z == 1 || z * 4 <= steps); ++z) {
       const double each = (double)ceil_div(steps, z) * (big ? 1.7 : 1.2) + (big ? 8.0 : 6.0);

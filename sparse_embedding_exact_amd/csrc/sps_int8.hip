@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "sps_gemm.h"
 
 namespace sps {
@@ -158,34 +160,38 @@ template <typename T, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
   using Tile = GemmTile<OpI8, TC, TR, WC, WR>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
-  const GemmPlace at = gemm_place<OpI8, TC, TR>(a.g);
-  Tile t;
-  t.clear();
-  t.run(a.g, at.row0, at.col0, at.begin, at.end, lds);
-  float sp[Tile::kFragC][4];
+  Tile t(a.g, lds);
+  const int64_t rows = a.g.q.rows, cols = a.g.p.rows;
+  float sp[Tile::kFragC][4], sq[Tile::kFragR];
+  const auto take = [&] {
+    t.of_columns(a.scale_p, 0.0f, sp);
 #pragma unroll
-  for (int i = 0; i < Tile::kFragC; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t c = at.col0 + t.col_of(i) + e;
-      sp[i][e] = c < a.g.p.rows ? a.scale_p[c] : 0.0f;
+    for (int j = 0; j < Tile::kFragR; ++j) {
+      const int64_t r = t.at.row0 + t.row_of(j);
+      sq[j] = a.scale_q[r < rows ? r : rows - 1];
     }
-  uint8_t *const mine = t.wave_lds(lds);
+  };
+  const auto put_all = [&](auto whole) {
 #pragma unroll
-  for (int j = 0; j < Tile::kFragR; ++j) {
-    const int64_t r = at.row0 + t.row_of(j);
-    const float sq = r < a.g.q.rows ? a.scale_q[r] : 0.0f;
+    for (int j = 0; j < Tile::kFragR; ++j) {
+      typename QuadOf<T>::Bits w[Tile::kFragC];
 #pragma unroll
-    for (int i = 0; i < Tile::kFragC; ++i) {
-      float v[4];
+      for (int i = 0; i < Tile::kFragC; ++i) {
+        float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)t.acc[i][j][e] * sq * sp[i][e];
-      t.template stage<T>(mine, i, quad_of<T>(v));
+        for (int e = 0; e < 4; ++e) v[e] = (float)t.acc[i][j][e] * sq[j] * sp[i][e];
+        w[i] = quad_of<T>(v);
+      }
+      t.template store<T, whole.value>(j, w, static_cast<T *>(a.out), a.ld, rows, cols);
     }
-    const int64_t r0 = at.row0 + t.rows_at(j), c0 = at.col0 + t.cols_at();
-    t.template store<T>(mine, static_cast<T *>(a.out) + r0 * a.ld + c0, a.ld, a.g.q.rows - r0,
-                        a.g.p.rows - c0);
-  }
+  };
+  const auto put = [&] {
+    const bool whole = t.full();
+    if (whole) put_all(std::true_type{});
+    else put_all(std::false_type{});
+    return whole;
+  };
+  gemm_tiles<Tile::template kStores<T>>(t, a.g, OpI8{}, [&] { t.clear(); }, take, put);
 }
 
 // Few queries (up to 16 NQ): bound by reading the items once. A wave takes 16
@@ -308,11 +314,11 @@ void launch_few(const sps::Int8Args &a, hipStream_t s) {
 }
 
 template <typename T, int TC, int TR, int WC, int WR>
-void launch_tiles(sps::Int8Args &a, hipStream_t s) {
+void launch_tiles(const sps::TilePlan &plan, sps::Int8Args &a, hipStream_t s) {
   a.g.tiles_c = (int32_t)sps::ceil_div(a.g.p.rows, TC);
   a.g.tiles_r = (int32_t)sps::ceil_div(a.g.q.rows, TR);
   const int64_t tiles = (int64_t)a.g.tiles_c * a.g.tiles_r;
-  hipLaunchKernelGGL((sps::int8_scores_kernel<T, TC, TR, WC, WR>), dim3((uint32_t)tiles),
+  hipLaunchKernelGGL((sps::int8_scores_kernel<T, TC, TR, WC, WR>), dim3(plan.grid(tiles)),
                      dim3(64 * WC * WR), 0, s, a);
 }
 
@@ -324,9 +330,10 @@ void launch_scores(sps::Int8Args &a, hipStream_t s) {
   if (n <= 16 && steps * 1024 <= kFewLds) return launch_few<T, 1>(a, s);
   if (n <= 32 && steps * 2048 <= kFewLds) return launch_few<T, 2>(a, s);
   if (n <= 64 && steps * 4096 <= kFewLds) return launch_few<T, 4>(a, s);
-  if (sps::plan_tiles(n, a.g.p.rows, sps::ceil_div(a.g.k_bytes, sps::kStep), 1).big)
-    launch_tiles<T, 256, 256, 2, 4>(a, s);
-  else launch_tiles<T, 128, 128, 2, 2>(a, s);
+  const sps::TilePlan plan =
+      sps::plan_tiles(n, a.g.p.rows, sps::ceil_div(a.g.k_bytes, sps::kStep), 1);
+  if (plan.big) launch_tiles<T, 256, 256, 2, 4>(plan, a, s);
+  else launch_tiles<T, 128, 128, 2, 2>(plan, a, s);
 }
 
 }  // namespace
