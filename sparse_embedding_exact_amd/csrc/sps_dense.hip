@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
         else w[i] = quad_of<float>(p);
       }
       if (a.code)  // rows of codes are padded to a multiple of 64
-        t.template store<Word, whole.value>(j, w, static_cast<Word *>(a.code), a.ld, rows,
+        t.template store<Word, whole.value, true>(j, w, static_cast<Word *>(a.code), a.ld, rows,
                                             (cols + 63) & ~63ll);
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
@@ -504,7 +504,7 @@ __device__ __forceinline__ void product_out(Tile &t, T *out, int64_t ld, float a
       for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : t.acc[i][j][e] * alpha;
       w[i] = quad_of<T>(v);
     }
-    t.template store<T, FULL>(j, w, out, ld, rows, cols);
+    t.template store<T, FULL, false>(j, w, out, ld, rows, cols);
   }
 }
 

@@ -492,7 +492,9 @@ struct GemmTile {
   }
   // Rows 16 j to 16 j + 15 of this wave: v[i] are the bits of this lane's four values of column group
   // i, to `out` (row 0, column 0 of D) of the given rows and columns; FULL: the tile's are all there.
-  template <typename T, bool FULL, typename Bits>
+  // Whole lines that nobody reads soon (STREAM) leave L2 as they come: 4.3 to 5.0 TB/s of float32
+  // scores; lines in parts are better off waiting there for their other parts (3.0 against 2.8).
+  template <typename T, bool FULL, bool STREAM, typename Bits>
   __device__ __forceinline__ void store(int j, const Bits (&v)[kFragC], T *out, int64_t ld, int64_t rows,
                                         int64_t cols) const {
     static_assert(sizeof(Bits) == 4 * sizeof(T), "four values");
@@ -517,7 +519,8 @@ struct GemmTile {
         T *const to = to0 + (int64_t)(pass * kPass<T> + n * kOnce) * ld;
         const bool there = r0 + pass * kPass<T> + from < rows;
         if (FULL || (there && c + V <= cols)) {
-          *reinterpret_cast<Words<T> *>(to) = {{w[0], w[1], w[2], w[3]}};
+          if constexpr (STREAM) __builtin_nontemporal_store(w, reinterpret_cast<u32x4 *>(to));
+          else *reinterpret_cast<Words<T> *>(to) = {{w[0], w[1], w[2], w[3]}};
         } else if (there) {
 #pragma unroll
           for (int e = 0; e < V; ++e)

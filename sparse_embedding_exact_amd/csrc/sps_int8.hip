@@ -156,7 +156,7 @@ struct Int8Args {
 
 // The integers' sums are exact; a score is rounded as an integer above 2^24,
 // by either scale and to its type.
-template <typename T, int TC, int TR, int WC, int WR>
+template <typename T, bool STREAM, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
   using Tile = GemmTile<OpI8, TC, TR, WC, WR>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
         for (int e = 0; e < 4; ++e) v[e] = (float)t.acc[i][j][e] * sq[j] * sp[i][e];
         w[i] = quad_of<T>(v);
       }
-      t.template store<T, whole.value>(j, w, static_cast<T *>(a.out), a.ld, rows, cols);
+      t.template store<T, whole.value, STREAM>(j, w, static_cast<T *>(a.out), a.ld, rows, cols);
     }
   };
   const auto put = [&] {
@@ -318,8 +318,12 @@ void launch_tiles(const sps::TilePlan &plan, sps::Int8Args &a, hipStream_t s) {
   a.g.tiles_c = (int32_t)sps::ceil_div(a.g.p.rows, TC);
   a.g.tiles_r = (int32_t)sps::ceil_div(a.g.q.rows, TR);
   const int64_t tiles = (int64_t)a.g.tiles_c * a.g.tiles_r;
-  hipLaunchKernelGGL((sps::int8_scores_kernel<T, TC, TR, WC, WR>), dim3(plan.grid(tiles)),
-                     dim3(64 * WC * WR), 0, s, a);
+  const dim3 grid(plan.grid(tiles)), block(64 * WC * WR);
+  // rows on whole lines: so is every tile's run of them
+  if (((uint64_t)(uintptr_t)a.out | (uint64_t)a.ld * sizeof(T)) % 128 == 0)
+    hipLaunchKernelGGL((sps::int8_scores_kernel<T, true, TC, TR, WC, WR>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((sps::int8_scores_kernel<T, false, TC, TR, WC, WR>), grid, block, 0, s, a);
 }
 
 constexpr int64_t kFewLds = 64 * 1024;
