@@ -84,11 +84,52 @@ template <typename T>
 struct __attribute__((packed, aligned(sizeof(T)))) Eight {
   T e[8];
 };
+// The power of two that takes the largest weight to [2^14, 2^15).
+struct ScaleArgs {
+  const float *weights;
+  const int32_t *targets;
+  int64_t n, m;
+  float *scale;  // nullable: not wanted
+};
+__device__ __forceinline__ void find_scale(const ScaleArgs &a) {
+  __shared__ float tops[4];
+  float top = 0.0f;
+  for (int64_t r = threadIdx.x; r < a.n; r += 256) {
+    const int32_t t = a.targets[r];
+    const float w = a.weights ? fabsf(a.weights[r]) : 1.0f;
+    if (t >= 0 && t < a.m && w < __builtin_inff()) top = fmaxf(top, w);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < 4; ++i) top = fmaxf(top, tops[i]);
+  int e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) - 127);
+  e = top == 0.0f ? 0 : (e > 100 ? 100 : (e < -100 ? -100 : e));
+  *a.scale = __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+}
+
+// One launch for both sides and the scale: `blocks` of each side, and one.
+struct LayBoth {
+  LayArgs side[2];
+  uint32_t blocks[2];
+  ScaleArgs scale;
+};
 template <typename T>
-__global__ __launch_bounds__(256) void lay_kernel(LayArgs a) {
+__global__ __launch_bounds__(256) void lay_kernel(LayBoth both) {
   constexpr int NP = kPlanes<T>;
   __shared__ __attribute__((aligned(16))) uint16_t tile[NP][64][72];
-  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+  uint32_t id = blockIdx.x;
+  if (id >= both.blocks[0] + both.blocks[1]) {
+    find_scale(both.scale);
+    return;
+  }
+  const bool second = id >= both.blocks[0];
+  if (second) id -= both.blocks[0];
+  const LayArgs a = second ? both.side[1] : both.side[0];
+  const uint32_t across = (uint32_t)((a.cols + 63) / 64);
+  const int64_t r0 = (int64_t)(id / across) * 64, c0 = (int64_t)(id % across) * 64;
   const int in = (threadIdx.x & 7) * 8;
   const T *const x = static_cast<const T *>(a.x);
 #pragma unroll
@@ -182,14 +223,14 @@ struct CodeF32 {
 
 struct LogitArgs {
   GemmArgs g;         // q: the piece's queries, p: items
-  float c;            // log2(e) / tau: everything is in powers of two
+  float c, c_low;     // log2(e) / tau in two parts: everything is in powers of two
   const float *bias;  // nullable
   const int32_t *targets;
   void *code;  // nullable: uint16 (float32: float) [rows][ld]
   int64_t ld;
   float2 *stats;  // [rows][blocks]: of a block of columns (max, sum of 2^(z - max))
   int64_t blocks;
-  float *z_target;
+  float2 *z_target;  // and what its rounding left
 };
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -204,12 +245,19 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   constexpr int FC = Tile::kFragC, FR = Tile::kFragR;
   const int64_t rows = a.g.q.rows, cols = a.g.p.rows;
   const int wave_col = t.wc * (TC / WC);
-  float c;
+  // float32: the factor's second part, so that its rounding does not change the temperature
+  constexpr bool kLow = sizeof(Word) == 4;
+  float c, c_low;
   int32_t target[FR];
+  const auto times = [&](float x, float y) {
+    // (where the sums are logits already, c_low is 0 and they may be -inf)
+    return __builtin_fmaf(x, c, kLow && c_low != 0.0f ? __builtin_fmaf(x, c_low, y) : y);
+  };
   const auto take = [&] {
     // The logits are c times the sums, and where there is a bias or an edge, what is put in their
     // place here.
     c = a.c;
+    c_low = kLow ? a.c_low : 0.0f;
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
       const int64_t r = t.at.row0 + t.row_of(j);
@@ -235,8 +283,9 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int j = 0; j < FR; ++j)  // a column that is struck out has no logit, whatever its item holds
-          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], c, b[i][e]);
+          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : times(t.acc[i][j][e], b[i][e]);
     c = 1.0f;
+    c_low = 0.0f;
   };
   const auto put_all = [&](auto whole) {
     const int64_t block = (t.at.col0 + wave_col) / (TC / WC);
@@ -257,7 +306,10 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
         for (int i = 0; i < FC; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (first == t.col_of(i) + e) a.z_target[r] = t.acc[i][j][e] * c;
+            if (first == t.col_of(i) + e) {
+              const float z = t.acc[i][j][e] * c;
+              a.z_target[r] = {z, fabsf(z) < kInf ? times(t.acc[i][j][e], -z) : 0.0f};
+            }
       }
       const float base = (float)Code::kShift - (top == -kInf ? 0.0f : top);
       float sum = 0.0f;
@@ -267,7 +319,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e], c, base));
+          p[e] = __builtin_amdgcn_exp2f(times(t.acc[i][j][e], base));
           sum += p[e];
         }
         if constexpr (sizeof(Word) == 2) w[i] = {Code::two(p[0], p[1]), Code::two(p[2], p[3])};
@@ -298,7 +350,8 @@ struct GradArgs {
   const float2 *stats;
   int64_t rows, cols;
   int32_t blocks, block;  // their number and columns
-  const float *z_target, *weights;  // weights nullable
+  const float2 *z_target;
+  const float *weights;  // nullable
   const int32_t *targets;
   const float *scale;  // nullable: 1
   float *loss;
@@ -344,7 +397,8 @@ __device__ __forceinline__ bool loss_of(const GradArgs &a, int64_t r, const Runn
     *loss = 0.0;
     return false;
   }
-  *loss = (((double)x.top - (double)a.z_target[r]) + log2(x.sum)) * 0.69314718055994530942;
+  const float2 z = a.z_target[r];
+  *loss = (((double)x.top - (double)z.x) - (double)z.y + log2(x.sum)) * 0.69314718055994530942;
   return true;
 }
 
@@ -393,7 +447,7 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
     a.loss[r] = (float)loss;
     a.factor[r] = factor;
   }
-  const float lse2 = (float)((double)x.top + log2(x.sum)) + (float)Code::kShift;
+  const double lse2 = (double)x.top + log2(x.sum) + (double)Code::kShift;
   const float at_target = takes ? (float)expm1(-loss) * factor : 0.0f;
   const int32_t target = a.targets[r];
 
@@ -402,7 +456,9 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
     uint16_t o[NP][8] = {};
     if (factor != 0.0f) {
       const float f = col < a.cols
-                          ? __builtin_amdgcn_exp2f(stats[col / a.block].x - lse2) * factor : 0.0f;
+                          ? __builtin_amdgcn_exp2f((float)((double)stats[col / a.block].x - lse2)) *
+                                factor
+                          : 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         float p;
@@ -434,27 +490,6 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
   for (int64_t v = threadIdx.x + 256 * kGradAhead; v < vecs; v += 256) put(v, fetch(v));
 }
 
-// The power of two that takes the largest weight to [2^14, 2^15).
-__global__ __launch_bounds__(1024) void ce_scale_kernel(const float *weights, const int32_t *targets,
-                                                        int64_t n, int64_t m, float *scale) {
-  __shared__ float tops[16];
-  float top = 0.0f;
-  for (int64_t r = threadIdx.x; r < n; r += 1024) {
-    const int32_t t = targets[r];
-    const float w = weights ? fabsf(weights[r]) : 1.0f;
-    if (t >= 0 && t < m && w < __builtin_inff()) top = fmaxf(top, w);
-  }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int i = 1; i < 16; ++i) top = fmaxf(top, tops[i]);
-  int e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) - 127);
-  e = top == 0.0f ? 0 : (e > 100 ? 100 : (e < -100 ? -100 : e));
-  *scale = __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
-}
-
 // ---------------------------------------------------------------------------
 // 3. products with the gradient
 
@@ -470,9 +505,9 @@ struct OutMask {
 struct ProductArgs {
   GemmArgs g;
   const float *before;  // nullable: [rows][cols] sums of earlier pieces
-  float *part;          // nullable: sums as they are, split z at z * stride
-  int64_t stride;
-  void *out;  // where part is NULL
+  float *part;          // sums of the tail's parts: part z, from the tail's first row, at z * stride
+  int64_t stride, tail_row;
+  void *out;
   int64_t ld;
   int32_t dtype;
   float alpha;
@@ -516,12 +551,14 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a)
   const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
   using Type = typename Op::Type;  // the rows' own: that of the products
   const auto start = [&] {
-    if (a.before) t.start(a.before, a.g.q.rows, a.g.p.rows);
+    if (a.before && t.at.z < 0) t.start(a.before, a.g.q.rows, a.g.p.rows);
     else t.clear();
   };
   const auto put_all = [&](auto whole) {
     constexpr bool FULL = whole.value;
-    if (a.part) product_out<float, FULL>(t, a.part + t.at.z * a.stride, a.g.p.rows, 1.0f, {});
+    if (t.at.z >= 0)
+      product_out<float, FULL>(t, a.part + t.at.z * a.stride - a.tail_row * a.g.p.rows, a.g.p.rows,
+                               1.0f, {});
     else if (a.dtype == SPS_F32)
       product_out<float, FULL>(t, static_cast<float *>(a.out), a.ld, alpha, a.mask);
     else product_out<Type, FULL>(t, static_cast<Type *>(a.out), a.ld, alpha, a.mask);
@@ -538,7 +575,8 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a)
 
 struct JoinArgs {
   const float *part;
-  int64_t stride, rows, cols;
+  const float *before;  // nullable: [first + rows][cols]
+  int64_t stride, first, rows, cols;
   int32_t splits;
   void *out;
   int64_t ld;
@@ -555,6 +593,10 @@ __global__ __launch_bounds__(256) void ce_join_kernel(JoinArgs a) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / per, c = (i - r * per) * 4;
     float v[4] = {};
+    if (a.before)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < a.cols) v[e] = a.before[(a.first + r) * a.cols + c + e];
     for (int32_t z = 0; z < a.splits; ++z) {
       const float *const p = a.part + z * a.stride + r * a.cols + c;
       if (c + 4 <= a.cols) {
@@ -567,10 +609,10 @@ __global__ __launch_bounds__(256) void ce_join_kernel(JoinArgs a) {
           if (c + e < a.cols) v[e] += p[e];
       }
     }
-    const bool zero = a.mask.out(r);
+    const bool zero = a.mask.out(a.first + r);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : v[e] * alpha;
-    put_typed(a.out, a.dtype, r * a.ld, c, a.cols, v);
+    put_typed(a.out, a.dtype, (a.first + r) * a.ld, c, a.cols, v);
   }
 }
 
@@ -605,11 +647,26 @@ struct Shape {
   bool gq, gi;  // which gradients
   bool pack_q, pack_i;
   int64_t piece;     // rows of a piece, a multiple of 64
+  int64_t at_once;   // of them there are
   int64_t ld_g;      // items, padded
   int32_t block;     // columns of a block of statistics
   int64_t blocks;
   sps::TilePlan plan_l, plan_q, plan_i;  // of the logits, and the products for the queries and the items
 };
+
+int64_t steps_of(const Shape &s, int64_t k) {
+  return ceil_div(k * 2, sps::kStep) * (s.dtype == SPS_F32 ? sps::kSegments : 1);
+}
+constexpr int kMostSplits = 64;
+sps::TilePlan plan_queries(const Shape &s, int64_t rows) {
+  return sps::plan_tiles(rows, s.d, steps_of(s, s.m), kMostSplits);
+}
+sps::TilePlan plan_items(const Shape &s, int64_t rows) {
+  return sps::plan_tiles(s.m, s.d, steps_of(s, rows), kMostSplits);
+}
+int64_t part_values(const sps::TilePlan &p, int64_t rows, int64_t cols) {
+  return p.tail_r ? p.splits * (rows - p.tail_row()) * cols : 0;
+}
 
 struct Layout {
   size_t scale, factor, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, part, sum_i,
@@ -652,15 +709,12 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   if (rows < 256) rows = 256;
   if (rows > kMaxPiece) rows = kMaxPiece;
   s.piece = rows < s.n ? up(ceil_div(s.n, ceil_div(s.n, rows)), 256) : up(s.n, 64);
-  const int seg = s.dtype == SPS_F32 ? sps::kSegments : 1;
-  const int64_t at_once = s.piece < s.n ? s.piece : s.n;
-  const auto steps = [&](int64_t k) { return ceil_div(k * 2, sps::kStep) * seg; };
-  s.plan_l = sps::plan_tiles(at_once, s.m, steps(s.d), 1);
+  s.at_once = s.piece < s.n ? s.piece : s.n;
+  s.plan_l = sps::plan_tiles(s.at_once, s.m, steps_of(s, s.d), 1);
   s.block = s.plan_l.big ? 128 : 64;
   s.blocks = ceil_div(s.m, s.block);
-  // the queries' product: few tiles and a long k, split to fill the card
-  s.plan_q = sps::plan_tiles(at_once, s.d, steps(s.m), 64);
-  s.plan_i = sps::plan_tiles(s.m, s.d, steps(at_once), 1);
+  s.plan_q = plan_queries(s, s.at_once);
+  s.plan_i = plan_items(s, s.at_once);
   return s;
 }
 
@@ -674,7 +728,7 @@ Layout layout_of(const Shape &s) {
   };
   const int p = planes(s);
   L.scale = take(4);
-  L.z_target = take(s.piece * 4);
+  L.z_target = take(s.piece * 8);
   L.stats = take(s.blocks * s.piece * 8);
   if (s.pack_q) L.packed_q = take(s.n * packed_ld(s) * 2 * p);
   if (s.pack_i) L.packed_i = take(s.m * packed_ld(s) * 2 * p);
@@ -684,12 +738,22 @@ Layout layout_of(const Shape &s) {
     L.g = p == 3 ? take(s.piece * s.ld_g * 6) : L.code;
     if (s.gq) {
       L.turned_i = take(s.d * turned_ld(s.m) * 2 * p);
-      if (s.plan_q.splits > 1) L.part = take((int64_t)s.plan_q.splits * s.piece * s.d * 4);
     }
     if (s.gi) {
       L.turned_q = take(s.d * turned_ld(s.n) * 2 * p);
       if (s.piece < s.n) L.sum_i = take(s.m * s.d * 4);
     }
+    // parts of either product, also of a last piece that is shorter
+    int64_t part = 0;
+    const auto count = [&](int64_t rows, const sps::TilePlan &q, const sps::TilePlan &i) {
+      const int64_t pq = s.gq ? part_values(q, rows, s.d) : 0, pi = s.gi ? part_values(i, s.m, s.d) : 0;
+      part = part > pq ? part : pq;
+      part = part > pi ? part : pi;
+    };
+    count(s.at_once, s.plan_q, s.plan_i);
+    if (const int64_t last = s.n % s.piece; last && last != s.at_once)
+      count(last, plan_queries(s, last), plan_items(s, last));
+    L.part = take(part * 4);
   }
   L.total = at;
   return L;
@@ -732,36 +796,49 @@ sps_status check_out(const sps_scores *q, const sps_scores *i, const sps_scores 
   return SPS_OK;
 }
 
-template <typename T>
-void launch_lay_t(const sps::LayArgs &a, hipStream_t s) {
-  const dim3 grid((uint32_t)ceil_div(a.rows, 64), (uint32_t)ceil_div(a.cols, 64));
-  hipLaunchKernelGGL((sps::lay_kernel<T>), grid, dim3(256), 0, s, a);
-}
-void launch_lay(int32_t dtype, const sps::LayArgs &a, hipStream_t s) {
-  if (dtype == SPS_F32) launch_lay_t<float>(a, s);
-  else if (dtype == SPS_F16) launch_lay_t<sps::f16_t>(a, s);
-  else launch_lay_t<sps::bf16_t>(a, s);
+void launch_lay(int32_t dtype, sps::LayBoth *a, hipStream_t s) {
+  for (int i = 0; i < 2; ++i) {
+    const sps::LayArgs &x = a->side[i];
+    a->blocks[i] = x.packed || x.turned ? (uint32_t)(ceil_div(x.rows, 64) * ceil_div(x.cols, 64)) : 0;
+  }
+  const dim3 grid(a->blocks[0] + a->blocks[1] + (a->scale.scale ? 1 : 0)), block(256);
+  if (grid.x == 0) return;
+  if (dtype == SPS_F32) hipLaunchKernelGGL((sps::lay_kernel<float>), grid, block, 0, s, *a);
+  else if (dtype == SPS_F16) hipLaunchKernelGGL((sps::lay_kernel<sps::f16_t>), grid, block, 0, s, *a);
+  else hipLaunchKernelGGL((sps::lay_kernel<sps::bf16_t>), grid, block, 0, s, *a);
 }
 
 template <class Op, class Code>
 void launch_logits(const sps::TilePlan &plan, sps::LogitArgs a, hipStream_t s) {
-  const int64_t t = plan.big ? 256 : 128;
-  a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
-  a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
-  const dim3 grid(plan.grid((int64_t)a.g.tiles_c * a.g.tiles_r));
+  plan.give(&a.g);
+  const dim3 grid(plan.grid());
   if (plan.big) hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
 template <class Op, bool QT>
-void launch_product(sps::TilePlan plan, sps::ProductArgs a, hipStream_t s) {
-  const int64_t t = plan.big ? 256 : 128;
-  a.g.splits = plan.splits;
-  a.g.tiles_c = (int32_t)ceil_div(a.g.p.rows, t);
-  a.g.tiles_r = (int32_t)ceil_div(a.g.q.rows, t);
-  const dim3 grid(plan.grid((int64_t)a.g.tiles_c * a.g.tiles_r * a.g.splits));
+void launch_product_tiles(const sps::TilePlan &plan, const sps::ProductArgs &a, hipStream_t s) {
+  const dim3 grid(plan.grid());
   if (plan.big) hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
   else hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
+}
+
+// The product and, where its tail was split, the sum of the parts.
+template <bool QT>
+void launch_product(int32_t dtype, const sps::TilePlan &plan, sps::ProductArgs a, hipStream_t s) {
+  plan.give(&a.g);
+  a.tail_row = plan.tail_row();
+  const int64_t rows = a.g.q.rows - a.tail_row, cols = a.g.p.rows;
+  a.stride = rows * cols;
+  if (dtype == SPS_F32) launch_product_tiles<sps::OpF32, QT>(plan, a, s);
+  else if (dtype == SPS_F16) launch_product_tiles<sps::OpF16, QT>(plan, a, s);
+  else launch_product_tiles<sps::OpBf16, QT>(plan, a, s);
+  if (plan.tail_r == 0) return;
+  const sps::JoinArgs j{a.part, a.before, a.stride, a.tail_row, rows, cols, plan.splits,
+                        a.out,  a.ld,     a.dtype,  a.alpha,    a.scale, a.mask};
+  int64_t blocks = ceil_div(rows * ceil_div(cols, 4), 256);
+  if (blocks > 4096) blocks = 4096;
+  hipLaunchKernelGGL(sps::ce_join_kernel, dim3((uint32_t)blocks), dim3(256), 0, s, j);
 }
 
 void launch_grad(int32_t dtype, const sps::GradArgs &a, hipStream_t s) {
@@ -836,15 +913,13 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
   const int np = planes(h);
   const bool wide = np == 3, grad = h.gq || h.gi;
   float *const scale = h.dtype == SPS_F16 && grad ? reinterpret_cast<float *>(ws + L.scale) : nullptr;
-  if (scale)
-    hipLaunchKernelGGL(sps::ce_scale_kernel, dim3(1), dim3(1024), 0, s, row_weights, targets, n, m,
-                       scale);
-
   // operands: as they lie, or laid out with 16-byte rows; transposed for the products
-  const auto lay = [&](const sps_scores *x, bool pack, size_t packed, bool turn, size_t turned,
+  sps::LayBoth both{};
+  both.scale = {row_weights, targets, n, m, scale};
+  const auto lay = [&](int side, const sps_scores *x, bool pack, size_t packed, bool turn, size_t turned,
                        sps::RowMask mask) {
     GemmOperand o{static_cast<const uint8_t *>(x->data), x->n_rows, x->ld * 2, 0};
-    sps::LayArgs a{};
+    sps::LayArgs &a = both.side[side];
     a.x = x->data;
     a.ld = x->ld;
     a.rows = x->n_rows;
@@ -861,12 +936,13 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       a.plane_t = a.ld_t * a.cols;
       a.mask = mask;
     }
-    if (pack || turn) launch_lay(h.dtype, a, s);
     return o;
   };
-  const GemmOperand oq = lay(queries, h.pack_q, L.packed_q, h.gi, L.turned_q,
+  const GemmOperand oq = lay(0, queries, h.pack_q, L.packed_q, h.gi, L.turned_q,
                              {targets, row_weights, m, nullptr});
-  const GemmOperand oi = lay(items, h.pack_i, L.packed_i, h.gq, L.turned_i, {nullptr, nullptr, 0, bias});
+  const GemmOperand oi = lay(1, items, h.pack_i, L.packed_i, h.gq, L.turned_i, {nullptr, nullptr, 0, bias});
+
+  launch_lay(h.dtype, &both, s);
 
   const int64_t k_logits = up(d, 8) * 2;
   for (int64_t r0 = 0; r0 < n; r0 += h.piece) {
@@ -876,17 +952,22 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.g.p = oi;
     a.g.k_bytes = k_logits;
     a.g.splits = 1;
-    a.c = (float)(1.44269504088896340736 / (double)temperature);
+    const double c2 = 1.44269504088896340736 / (double)temperature;
+    a.c = (float)c2;
+    a.c_low = (float)(c2 - (double)a.c);
     a.bias = bias;
     a.targets = targets + r0;
     a.code = grad ? ws + L.code : nullptr;
     a.ld = h.ld_g;
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
     a.blocks = h.blocks;
-    a.z_target = reinterpret_cast<float *>(ws + L.z_target);
-    if (wide) launch_logits<sps::OpF32, sps::CodeF32>(h.plan_l, a, s);
-    else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, sps::CodeF16>(h.plan_l, a, s);
-    else launch_logits<sps::OpBf16, sps::CodeBf16>(h.plan_l, a, s);
+    a.z_target = reinterpret_cast<float2 *>(ws + L.z_target);
+    // a last piece that is shorter: the same tiles, whose columns the statistics go by, but fewer
+    sps::TilePlan plan = h.plan_l;
+    plan.main_r = (int32_t)ceil_div(rows, plan.size());
+    if (wide) launch_logits<sps::OpF32, sps::CodeF32>(plan, a, s);
+    else if (h.dtype == SPS_F16) launch_logits<sps::OpF16, sps::CodeF16>(plan, a, s);
+    else launch_logits<sps::OpBf16, sps::CodeBf16>(plan, a, s);
 
     sps::GradArgs c{};
     c.stats = a.stats;
@@ -918,41 +999,34 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       p.g.q = {reinterpret_cast<const uint8_t *>(c.g), rows, h.ld_g * 2, c.plane_g * 2};
       p.g.p = {ws + L.turned_i, d, turned_ld(m) * 2, turned_ld(m) * d * 2};
       p.g.k_bytes = up(m, 64) * 2;
+      p.part = reinterpret_cast<float *>(ws + L.part);
       p.out = static_cast<uint8_t *>(grad_queries) + r0 * ld_queries * sg;
       p.ld = ld_queries;
       p.mask = {c.factor, nullptr};
-      if (h.plan_q.splits > 1) {
-        p.part = reinterpret_cast<float *>(ws + L.part);
-        p.stride = rows * d;
-      }
-      if (wide) launch_product<sps::OpF32, false>(h.plan_q, p, s);
-      else if (h.dtype == SPS_F16) launch_product<sps::OpF16, false>(h.plan_q, p, s);
-      else launch_product<sps::OpBf16, false>(h.plan_q, p, s);
-      if (h.plan_q.splits > 1) {
-        const sps::JoinArgs j{p.part, p.stride, rows, d, h.plan_q.splits, p.out, p.ld, grad_dtype, p.alpha,
-                              scale, p.mask};
-        int64_t blocks = ceil_div(rows * ceil_div(d, 4), 256);
-        if (blocks > 4096) blocks = 4096;
-        hipLaunchKernelGGL(sps::ce_join_kernel, dim3((uint32_t)blocks), dim3(256), 0, s, j);
-      }
+      launch_product<false>(h.dtype, rows == h.at_once ? h.plan_q : plan_queries(h, rows), p, s);
     }
     if (h.gi) {
       const bool last = r0 + rows == n;
-      p.part = nullptr;
       p.g.q = {reinterpret_cast<const uint8_t *>(c.g), m, h.ld_g * 2, c.plane_g * 2};
       p.g.k_rows = rows;
       p.g.p = {ws + L.turned_q + r0 * 2, d, turned_ld(n) * 2, turned_ld(n) * d * 2};
       p.g.k_bytes = up(rows, 8) * 2;
       float *const sum = reinterpret_cast<float *>(ws + L.sum_i);
+      p.part = reinterpret_cast<float *>(ws + L.part);
       p.before = r0 > 0 ? sum : nullptr;
-      p.part = last ? nullptr : sum;
-      p.stride = 0;
-      p.out = grad_items;
-      p.ld = ld_items;
-      p.mask = {nullptr, bias};
-      if (wide) launch_product<sps::OpF32, true>(h.plan_i, p, s);
-      else if (h.dtype == SPS_F16) launch_product<sps::OpF16, true>(h.plan_i, p, s);
-      else launch_product<sps::OpBf16, true>(h.plan_i, p, s);
+      if (last) {
+        p.out = grad_items;
+        p.ld = ld_items;
+        p.mask = {nullptr, bias};
+      } else {  // as they are
+        p.out = sum;
+        p.ld = d;
+        p.dtype = SPS_F32;
+        p.alpha = 1.0f;
+        p.scale = nullptr;
+        p.mask = {};
+      }
+      launch_product<true>(h.dtype, rows == h.at_once ? h.plan_i : plan_items(h, rows), p, s);
     }
   }
   return sps::launch_status(what);

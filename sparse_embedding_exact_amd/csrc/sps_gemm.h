@@ -83,14 +83,14 @@ struct GemmOperand {
 
 // k_bytes of every row take part (a multiple of 16). With planes the six
 // products of planes that reach 2^-24 of a product are summed one after
-// another, as if k were six times as long. splits > 1: workgroup (tile, z)
-// sums the z-th part of the steps.
+// another, as if k were six times as long. The first main_r rows of tiles are
+// summed whole; of the tail_r behind them part z of `splits` takes the z-th
+// part of the steps.
 struct GemmArgs {
   GemmOperand q, p;
   int64_t k_bytes;
   int64_t k_rows;  // of a turned q
-  int32_t splits;
-  int32_t tiles_c, tiles_r;
+  int32_t tiles_c, main_r, tail_r, splits;
 };
 
 constexpr int kStep = 128;                    // bytes of k a step
@@ -156,7 +156,7 @@ __device__ __forceinline__ typename QuadOf<T>::Bits quad_of(const float v[4]) {
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-// A tile's rows and columns and its part of the steps.
+// A tile's rows and columns and its part of the steps (z < 0: all of them).
 struct GemmPlace {
   int64_t row0, col0;
   int begin, end;
@@ -166,14 +166,24 @@ template <class Op, int TC, int TR>
 __device__ __forceinline__ GemmPlace gemm_place(const GemmArgs &a, uint32_t id) {
   GemmPlace g;
   int tc, tr;
-  const uint32_t tiles = (uint32_t)a.tiles_c * (uint32_t)a.tiles_r;
-  g.z = (int32_t)(id / tiles);
-  tile_of(id % tiles, a.tiles_c, a.tiles_r, &tc, &tr);
+  const int steps = (int)((a.k_bytes + kStep - 1) / kStep) * (Op::kPlanes > 1 ? kSegments : 1);
+  const uint32_t main = (uint32_t)a.tiles_c * (uint32_t)a.main_r;
+  if (id < main) {
+    g.z = -1;
+    tile_of(id, a.tiles_c, a.main_r, &tc, &tr);
+    g.begin = 0;
+    g.end = steps;
+  } else {
+    const uint32_t tail = (uint32_t)a.tiles_c * (uint32_t)a.tail_r;
+    id -= main;
+    g.z = (int32_t)(id / tail);
+    tile_of(id % tail, a.tiles_c, a.tail_r, &tc, &tr);
+    tr += a.main_r;
+    g.begin = (int)((int64_t)steps * g.z / a.splits);
+    g.end = (int)((int64_t)steps * (g.z + 1) / a.splits);
+  }
   g.row0 = (int64_t)tr * TR;
   g.col0 = (int64_t)tc * TC;
-  const int steps = (int)((a.k_bytes + kStep - 1) / kStep) * (Op::kPlanes > 1 ? kSegments : 1);
-  g.begin = (int)((int64_t)steps * g.z / a.splits);
-  g.end = (int)((int64_t)steps * (g.z + 1) / a.splits);
   return g;
 }
 
@@ -576,7 +586,7 @@ struct GemmTile {
 template <int STORES, class Tile, class Op, class Start, class Take, class Put>
 __device__ __forceinline__ void gemm_tiles(Tile &t, const GemmArgs &a, Op, const Start &start,
                                            const Take &take, const Put &put) {
-  const uint32_t all = (uint32_t)a.tiles_c * (uint32_t)a.tiles_r * (uint32_t)a.splits;
+  const uint32_t all = (uint32_t)a.tiles_c * ((uint32_t)a.main_r + (uint32_t)a.tail_r * (uint32_t)a.splits);
   uint32_t id = blockIdx.x;
   bool counted = false;
   t.at = gemm_place<Op, Tile::kC, Tile::kR>(a, id);
@@ -602,35 +612,55 @@ __device__ __forceinline__ void gemm_tiles(Tile &t, const GemmArgs &a, Op, const
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles of 256 x 256 (one workgroup a CU) or 128 x 128 (two), and into how
-// many parts k goes, by what each would take on 256 CUs: rounds of workgroups,
-// each its steps and what comes before and after them, and sums of parts
-// written and read. Measured in us: a step of a large tile 1.7, of a small one
-// 1.2 (two at a time); before and after 8 and 6.
+// Tiles of 256 x 256 (one workgroup a CU) or 128 x 128 (two), and how many of
+// their rows are summed whole and the others in how many parts of k, by what
+// each would take on 256 CUs: rounds of workgroups, each its steps and what
+// comes before and after them, and the parts' sums written and read. Measured
+// in us: a step of a large tile 1.7, of a small one 1.2 (two at a time);
+// before and after 8 and 6. Whole rounds come first, so that only what would
+// leave most of the card idle at the end is split.
 constexpr int kCus = 256;
 struct TilePlan {
   bool big;
-  int32_t splits;
-  uint32_t grid(int64_t tiles) const {
+  int32_t tiles_c, main_r, tail_r, splits;
+  int64_t size() const { return big ? 256 : 128; }
+  int64_t tail_row() const { return main_r * size(); }  // the first row of the tail
+  uint32_t grid() const {
+    const int64_t tiles = (int64_t)tiles_c * (main_r + (int64_t)tail_r * splits);
     const int64_t at_once = big ? kCus : 2 * kCus;
     return (uint32_t)(tiles < at_once ? tiles : at_once);
   }
+  void give(GemmArgs *a) const {
+    a->tiles_c = tiles_c;
+    a->main_r = main_r;
+    a->tail_r = tail_r;
+    a->splits = splits;
+  }
 };
 inline TilePlan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int most_splits) {
-  TilePlan best{false, 1};
+  TilePlan best{};
   double least = 1e300;
   for (int big = 0; big < 2; ++big) {
     const int64_t t = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
-    const int64_t tiles = ceil_div(rows, t) * ceil_div(cols, t);
-    for (int z = 1; z <= most_splits && (z == 1 || z * 4 <= steps); ++z) {
-      const double each = (double)ceil_div(steps, z) * (big ? 1.7 : 1.2) + (big ? 8.0 : 6.0);
-      const double join = z > 1 ? 5.0 + (double)z * (double)rows * (double)cols * 8.0 / 4e6 : 0.0;
-      const double us = (double)ceil_div(tiles * z, slots) * each + join;
-      if (us < least) {
-        least = us;
-        best = {big != 0, z};
-      }
-    }
+    const int64_t tr = ceil_div(rows, t), tc = ceil_div(cols, t);
+    const double step = big ? 1.7 : 1.2, around = big ? 8.0 : 6.0;
+    const double whole = (double)steps * step + around;
+    const auto offer = [&](int64_t main_r, int z, double us) {
+      if (us >= least) return;
+      least = us;
+      best = {big != 0, (int32_t)tc, (int32_t)main_r, (int32_t)(tr - main_r), z};
+    };
+    offer(tr, 1, (double)ceil_div(tr * tc, slots) * whole);
+    const int64_t rounds = tr * tc / slots, main_r = rounds * slots / tc;
+    const int64_t tail = (tr - main_r) * tc;
+    if (tail == 0) continue;
+    const double values = (double)(rows - main_r * t) * (double)cols;
+    // 2, 3, 4, 5, 6, 7, 8, 10, 12, ...: an eighth apart at the least
+    for (int z = 2; z <= most_splits && z * 4 <= steps; z += z < 8 ? 1 : z / 8 * 2)
+      offer(main_r, z,
+            (double)rounds * whole +
+                (double)ceil_div(tail * z, slots) * ((double)ceil_div(steps, z) * step + around) + 5.0 +
+                (double)z * values * 8.0 / 4e6);
   }
   return best;
 }

@@ -315,10 +315,8 @@ void launch_few(const sps::Int8Args &a, hipStream_t s) {
 
 template <typename T, int TC, int TR, int WC, int WR>
 void launch_tiles(const sps::TilePlan &plan, sps::Int8Args &a, hipStream_t s) {
-  a.g.tiles_c = (int32_t)sps::ceil_div(a.g.p.rows, TC);
-  a.g.tiles_r = (int32_t)sps::ceil_div(a.g.q.rows, TR);
-  const int64_t tiles = (int64_t)a.g.tiles_c * a.g.tiles_r;
-  const dim3 grid(plan.grid(tiles)), block(64 * WC * WR);
+  plan.give(&a.g);
+  const dim3 grid(plan.grid()), block(64 * WC * WR);
   // rows on whole lines: so is every tile's run of them
   if (((uint64_t)(uintptr_t)a.out | (uint64_t)a.ld * sizeof(T)) % 128 == 0)
     hipLaunchKernelGGL((sps::int8_scores_kernel<T, true, TC, TR, WC, WR>), grid, block, 0, s, a);
@@ -416,7 +414,6 @@ sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *it
   a.g.q = {reinterpret_cast<const uint8_t *>(queries->values), queries->n_rows, queries->ld, 0};
   a.g.p = {reinterpret_cast<const uint8_t *>(items->values), items->n_rows, items->ld, 0};
   a.g.k_bytes = k;
-  a.g.splits = 1;
   a.scale_q = queries->scales;
   a.scale_p = items->scales;
   a.out = out;
