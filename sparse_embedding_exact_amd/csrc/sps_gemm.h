@@ -107,12 +107,11 @@ __device__ __forceinline__ int seg_p(int s) { return (0x010201 >> (4 * (5 - s)))
 // still in that L2.
 constexpr int kXcds = 8;
 constexpr int kGroup = 4;
-__device__ __forceinline__ void tile_of(uint32_t id, int32_t tiles_c, int32_t tiles_r, int *tc,
-                                        int *tr) {
-  const uint32_t all = (uint32_t)tiles_c * (uint32_t)tiles_r;
-  const uint32_t x = id % kXcds, at = id / kXcds;
-  const uint32_t each = all / kXcds, more = all % kXcds;
-  const uint32_t t = x * each + (x < more ? x : more) + at;
+__device__ __forceinline__ uint32_t in_xcd_order(uint32_t id, uint32_t all) {
+  const uint32_t x = id % kXcds, each = all / kXcds, more = all % kXcds;
+  return x * each + (x < more ? x : more) + id / kXcds;
+}
+__device__ __forceinline__ void tile_of(uint32_t t, int32_t tiles_c, int32_t tiles_r, int *tc, int *tr) {
   const uint32_t per = kGroup * (uint32_t)tiles_c;
   const uint32_t g = t / per, in = t % per;
   const uint32_t first = g * kGroup;
@@ -170,12 +169,12 @@ __device__ __forceinline__ GemmPlace gemm_place(const GemmArgs &a, uint32_t id) 
   const uint32_t main = (uint32_t)a.tiles_c * (uint32_t)a.main_r;
   if (id < main) {
     g.z = -1;
-    tile_of(id, a.tiles_c, a.main_r, &tc, &tr);
+    tile_of(in_xcd_order(id, main), a.tiles_c, a.main_r, &tc, &tr);
     g.begin = 0;
     g.end = steps;
   } else {
     const uint32_t tail = (uint32_t)a.tiles_c * (uint32_t)a.tail_r;
-    id -= main;
+    id = in_xcd_order(id - main, tail * (uint32_t)a.splits);
     g.z = (int32_t)(id / tail);
     tile_of(id % tail, a.tiles_c, a.tail_r, &tc, &tr);
     tr += a.main_r;
