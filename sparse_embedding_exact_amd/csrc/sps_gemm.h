@@ -404,28 +404,33 @@ struct GemmTile {
                                                (half ? in ^ 64 : in));
     }
   }
-  // Half a step from registers, while the next half is read into others.
-  __device__ __forceinline__ void half_step(Frag (&p)[kFragC], Frag (&q)[kFragR], bool more,
+  // Half a step from registers, while the next half is read into others and, in a step's second
+  // half, the step after the next is loaded. No branches: past the end nothing is loaded, and what
+  // is read is not used.
+  template <bool LOAD>
+  __device__ __forceinline__ void half_step(Frag (&p)[kFragC], Frag (&q)[kFragR], uint8_t *freed,
                                             const uint8_t *b, bool half, Frag (&pn)[kFragC],
                                             Frag (&qn)[kFragR]) {
-    if (more && !QT) read_q(b, half, qn);
-    if (more) read_p(b, half, pn);
+    if (LOAD) load(freed);
+    if (!QT) read_q(b, half, qn);
+    read_p(b, half, pn);
 #pragma unroll
     for (int i = 0; i < kFragC; ++i) {
 #pragma unroll
       for (int j = 0; j < kFragR; ++j) acc[i][j] = Op::mma(p[i], q[j], acc[i][j]);
       if (QT && i == kFragC / 2 - 1) {
         __builtin_amdgcn_sched_barrier(0);
-        if (more) read_q(b, half, qn);
+        read_q(b, half, qn);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (!QT) {  // matrix instructions between the reads
+    if (!QT) {  // the matrix instructions among the reads and loads
       constexpr int kReads = kFragC + kFragR, kEach = kFragC * kFragR / kReads;
 #pragma unroll
       for (int i = 0; i < kReads; ++i) {
         __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (LOAD && i < kLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -445,19 +450,18 @@ struct GemmTile {
     __builtin_amdgcn_sched_barrier(0);
     int here = 0;
     for (int s = 0; s < many; ++s) {
-      half_step(p0, q0, true, lds + here, true, p1, q1);
+      half_step<false>(p0, q0, nullptr, lds + here, true, p1, q1);
       // behind the barrier this step's buffer has been read to the end and is loaded again, and the
       // next step, which had a whole step's time, is in the other
       if (counted && s == 0) wait<STORES>();
       else wait<0>();
       barrier();
-      if (s + 2 < many) load(lds + here);
-      __builtin_amdgcn_sched_barrier(0);
+      any = s + 2 < many;
+      half_step<true>(p1, q1, lds + here, lds + (here ^ kBuf), false, p0, q0);
       here ^= kBuf;
-      half_step(p1, q1, s + 1 < many, lds + here, false, p0, q0);
     }
-    // the buffers are free: their loads have been waited for, and behind the barrier the reads
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // the buffers are free: their loads are done, and behind the barrier the reads
+    wait<0>();
     barrier();
   }
 
