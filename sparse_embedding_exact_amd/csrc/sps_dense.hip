@@ -340,7 +340,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
     else put_all(std::false_type{});
     return a.code && whole;
   };
-  gemm_tiles<Tile::template kStores<Word>>(t, a.g, Op{}, [&] { t.clear(); }, take, put);
+  gemm_tiles<Tile::template kStores<Word>>(t, a.g, Op{}, blockIdx.x, [&] { t.clear(); }, take, put);
 }
 
 // ---------------------------------------------------------------------------
@@ -544,9 +544,8 @@ __device__ __forceinline__ void product_out(Tile &t, T *out, int64_t ld, float a
 }
 
 template <class Op, bool QT, int TC, int TR, int WC, int WR>
-__global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a) {
+__device__ __forceinline__ void product_tiles(const ProductArgs &a, uint32_t first, uint8_t *lds) {
   using Tile = GemmTile<Op, TC, TR, WC, WR, QT>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile::kLds];
   Tile t(a.g, lds);
   const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
   using Type = typename Op::Type;  // the rows' own: that of the products
@@ -570,7 +569,23 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_product_kernel(ProductArgs a)
     return whole;
   };
   // the fewest stores of the three
-  gemm_tiles<Tile::template kStores<Type>>(t, a.g, Op{}, start, [] {}, put);
+  gemm_tiles<Tile::template kStores<Type>>(t, a.g, Op{}, first, start, [] {}, put);
+}
+
+// Both products in one launch, either without tiles where it is not wanted:
+// the items' tiles go on where the queries' end, so that no part of the card
+// waits for the last of these.
+struct ProductsArgs {
+  ProductArgs queries, items;
+};
+template <class Op, int TC, int TR, int WC, int WR>
+__global__ __launch_bounds__(64 * WC * WR) void ce_products_kernel(ProductsArgs a) {
+  constexpr int kLds = GemmTile<Op, TC, TR, WC, WR, false>::kLds;
+  static_assert((kLds == GemmTile<Op, TC, TR, WC, WR, true>::kLds), "one size");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  product_tiles<Op, false, TC, TR, WC, WR>(a.queries, blockIdx.x, lds);
+  const uint32_t before = gemm_all(a.queries.g) % gridDim.x;
+  product_tiles<Op, true, TC, TR, WC, WR>(a.items, (blockIdx.x + gridDim.x - before) % gridDim.x, lds);
 }
 
 struct JoinArgs {
@@ -585,12 +600,21 @@ struct JoinArgs {
   const float *scale;
   OutMask mask;
 };
+// Of both products: `blocks` workgroups each.
+struct JoinBoth {
+  JoinArgs side[2];
+  uint32_t blocks[2];
+};
 
 // The splits' sums in their order, four values a thread.
-__global__ __launch_bounds__(256) void ce_join_kernel(JoinArgs a) {
+__global__ __launch_bounds__(256) void ce_join_kernel(JoinBoth both) {
+  const bool second = blockIdx.x >= both.blocks[0];
+  const JoinArgs a = second ? both.side[1] : both.side[0];
+  const uint32_t block = second ? blockIdx.x - both.blocks[0] : blockIdx.x;
+  const uint32_t blocks = second ? both.blocks[1] : both.blocks[0];
   const int64_t per = (a.cols + 3) / 4, all = a.rows * per;
   const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < all; i += (int64_t)blocks * 256) {
     const int64_t r = i / per, c = (i - r * per) * 4;
     float v[4] = {};
     if (a.before)
@@ -651,26 +675,40 @@ struct Shape {
   int64_t ld_g;      // items, padded
   int32_t block;     // columns of a block of statistics
   int64_t blocks;
-  sps::TilePlan plan_l, plan_q, plan_i;  // of the logits, and the products for the queries and the items
+  sps::TilePlan plan_l;  // of the logits
 };
 
 int64_t steps_of(const Shape &s, int64_t k) {
   return ceil_div(k * 2, sps::kStep) * (s.dtype == SPS_F32 ? sps::kSegments : 1);
 }
 constexpr int kMostSplits = 64;
-sps::TilePlan plan_queries(const Shape &s, int64_t rows) {
-  return sps::plan_tiles(rows, s.d, steps_of(s, s.m), kMostSplits);
-}
-sps::TilePlan plan_items(const Shape &s, int64_t rows) {
-  return sps::plan_tiles(s.m, s.d, steps_of(s, rows), kMostSplits);
+// The plans of both products, which are one launch: tiles of one size, that
+// of the lesser time together.
+struct PlanBoth {
+  bool big;
+  sps::TilePlan q, i;
+};
+PlanBoth plan_products(const Shape &s, int64_t rows) {
+  PlanBoth best{};
+  double least = 1e300;
+  for (const bool big : {false, true}) {
+    PlanBoth p{big, {}, {}};
+    if (s.gq) p.q = sps::plan_tiles(big, rows, s.d, steps_of(s, s.m), kMostSplits);
+    if (s.gi) p.i = sps::plan_tiles(big, s.m, s.d, steps_of(s, rows), kMostSplits);
+    if (p.q.us + p.i.us < least) {
+      least = p.q.us + p.i.us;
+      best = p;
+    }
+  }
+  return best;
 }
 int64_t part_values(const sps::TilePlan &p, int64_t rows, int64_t cols) {
   return p.tail_r ? p.splits * (rows - p.tail_row()) * cols : 0;
 }
 
 struct Layout {
-  size_t scale, factor, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, part, sum_i,
-      total;
+  size_t scale, factor, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, part_q, part_i,
+      sum_i, total;
 };
 
 int planes(const Shape &s) { return s.dtype == SPS_F32 ? 3 : 1; }
@@ -713,8 +751,6 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   s.plan_l = sps::plan_tiles(s.at_once, s.m, steps_of(s, s.d), 1);
   s.block = s.plan_l.big ? 128 : 64;
   s.blocks = ceil_div(s.m, s.block);
-  s.plan_q = plan_queries(s, s.at_once);
-  s.plan_i = plan_items(s, s.at_once);
   return s;
 }
 
@@ -743,17 +779,18 @@ Layout layout_of(const Shape &s) {
       L.turned_q = take(s.d * turned_ld(s.n) * 2 * p);
       if (s.piece < s.n) L.sum_i = take(s.m * s.d * 4);
     }
-    // parts of either product, also of a last piece that is shorter
-    int64_t part = 0;
-    const auto count = [&](int64_t rows, const sps::TilePlan &q, const sps::TilePlan &i) {
-      const int64_t pq = s.gq ? part_values(q, rows, s.d) : 0, pi = s.gi ? part_values(i, s.m, s.d) : 0;
-      part = part > pq ? part : pq;
-      part = part > pi ? part : pi;
+    // parts of the products, also of a last piece that is shorter
+    int64_t pq = 0, pi = 0;
+    const auto count = [&](int64_t rows) {
+      const PlanBoth p = plan_products(s, rows);
+      const int64_t q = part_values(p.q, rows, s.d), i = part_values(p.i, s.m, s.d);
+      pq = pq > q ? pq : q;
+      pi = pi > i ? pi : i;
     };
-    count(s.at_once, s.plan_q, s.plan_i);
-    if (const int64_t last = s.n % s.piece; last && last != s.at_once)
-      count(last, plan_queries(s, last), plan_items(s, last));
-    L.part = take(part * 4);
+    count(s.at_once);
+    if (s.n % s.piece && s.n > s.piece) count(s.n % s.piece);
+    L.part_q = take(pq * 4);
+    L.part_i = take(pi * 4);
   }
   L.total = at;
   return L;
@@ -816,29 +853,37 @@ void launch_logits(const sps::TilePlan &plan, sps::LogitArgs a, hipStream_t s) {
   else hipLaunchKernelGGL((sps::ce_logits_kernel<Op, Code, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
 }
 
-template <class Op, bool QT>
-void launch_product_tiles(const sps::TilePlan &plan, const sps::ProductArgs &a, hipStream_t s) {
-  const dim3 grid(plan.grid());
-  if (plan.big) hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 256, 256, 2, 4>), grid, dim3(512), 0, s, a);
-  else hipLaunchKernelGGL((sps::ce_product_kernel<Op, QT, 128, 128, 2, 2>), grid, dim3(256), 0, s, a);
+template <class Op>
+void launch_product_tiles(bool big, uint32_t grid, const sps::ProductsArgs &a, hipStream_t s) {
+  if (big) hipLaunchKernelGGL((sps::ce_products_kernel<Op, 256, 256, 2, 4>), dim3(grid), dim3(512), 0, s, a);
+  else hipLaunchKernelGGL((sps::ce_products_kernel<Op, 128, 128, 2, 2>), dim3(grid), dim3(256), 0, s, a);
 }
 
-// The product and, where its tail was split, the sum of the parts.
-template <bool QT>
-void launch_product(int32_t dtype, const sps::TilePlan &plan, sps::ProductArgs a, hipStream_t s) {
-  plan.give(&a.g);
-  a.tail_row = plan.tail_row();
-  const int64_t rows = a.g.q.rows - a.tail_row, cols = a.g.p.rows;
-  a.stride = rows * cols;
-  if (dtype == SPS_F32) launch_product_tiles<sps::OpF32, QT>(plan, a, s);
-  else if (dtype == SPS_F16) launch_product_tiles<sps::OpF16, QT>(plan, a, s);
-  else launch_product_tiles<sps::OpBf16, QT>(plan, a, s);
-  if (plan.tail_r == 0) return;
-  const sps::JoinArgs j{a.part, a.before, a.stride, a.tail_row, rows, cols, plan.splits,
-                        a.out,  a.ld,     a.dtype,  a.alpha,    a.scale, a.mask};
-  int64_t blocks = ceil_div(rows * ceil_div(cols, 4), 256);
-  if (blocks > 4096) blocks = 4096;
-  hipLaunchKernelGGL(sps::ce_join_kernel, dim3((uint32_t)blocks), dim3(256), 0, s, j);
+// The products and, where a tail was split, the sums of its parts.
+void launch_products(int32_t dtype, const PlanBoth &plan, sps::ProductsArgs *a, hipStream_t s) {
+  sps::JoinBoth join{};
+  const sps::TilePlan *const plans[2] = {&plan.q, &plan.i};
+  sps::ProductArgs *const sides[2] = {&a->queries, &a->items};
+  for (int k = 0; k < 2; ++k) {
+    const sps::TilePlan &p = *plans[k];
+    sps::ProductArgs &x = *sides[k];
+    p.give(&x.g);
+    if (p.tail_r == 0) continue;
+    x.tail_row = p.tail_row();
+    const int64_t rows = x.g.q.rows - x.tail_row, cols = x.g.p.rows;
+    x.stride = rows * cols;
+    join.side[k] = {x.part, x.before, x.stride, x.tail_row, rows,    cols,  p.splits,
+                    x.out,  x.ld,     x.dtype,  x.alpha,    x.scale, x.mask};
+    const int64_t blocks = ceil_div(rows * ceil_div(cols, 4), 256);
+    join.blocks[k] = (uint32_t)(blocks < 4096 ? blocks : 4096);
+  }
+  const int64_t all = plan.q.all() + plan.i.all(), at_once = plan.big ? sps::kCus : 2 * sps::kCus;
+  const uint32_t grid = (uint32_t)(all < at_once ? all : at_once);
+  if (dtype == SPS_F32) launch_product_tiles<sps::OpF32>(plan.big, grid, *a, s);
+  else if (dtype == SPS_F16) launch_product_tiles<sps::OpF16>(plan.big, grid, *a, s);
+  else launch_product_tiles<sps::OpBf16>(plan.big, grid, *a, s);
+  if (join.blocks[0] + join.blocks[1])
+    hipLaunchKernelGGL(sps::ce_join_kernel, dim3(join.blocks[0] + join.blocks[1]), dim3(256), 0, s, join);
 }
 
 void launch_grad(int32_t dtype, const sps::GradArgs &a, hipStream_t s) {
@@ -944,6 +989,7 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
 
   launch_lay(h.dtype, &both, s);
 
+  const float alpha = (float)(1.0 / (double)temperature);
   const int64_t k_logits = up(d, 8) * 2;
   for (int64_t r0 = 0; r0 < n; r0 += h.piece) {
     const int64_t rows = n - r0 < h.piece ? n - r0 : h.piece;
@@ -991,43 +1037,44 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     c.factor = reinterpret_cast<float *>(ws + L.factor);
     launch_grad(h.dtype, c, s);
 
-    sps::ProductArgs p{};
-    p.dtype = grad_dtype;
-    p.alpha = (float)(1.0 / (double)temperature);
-    p.scale = scale;
+    sps::ProductsArgs p{};
     if (h.gq) {
-      p.g.q = {reinterpret_cast<const uint8_t *>(c.g), rows, h.ld_g * 2, c.plane_g * 2};
-      p.g.p = {ws + L.turned_i, d, turned_ld(m) * 2, turned_ld(m) * d * 2};
-      p.g.k_bytes = up(m, 64) * 2;
-      p.part = reinterpret_cast<float *>(ws + L.part);
-      p.out = static_cast<uint8_t *>(grad_queries) + r0 * ld_queries * sg;
-      p.ld = ld_queries;
-      p.mask = {c.factor, nullptr};
-      launch_product<false>(h.dtype, rows == h.at_once ? h.plan_q : plan_queries(h, rows), p, s);
+      sps::ProductArgs &x = p.queries;
+      x.g.q = {reinterpret_cast<const uint8_t *>(c.g), rows, h.ld_g * 2, c.plane_g * 2};
+      x.g.p = {ws + L.turned_i, d, turned_ld(m) * 2, turned_ld(m) * d * 2};
+      x.g.k_bytes = up(m, 64) * 2;
+      x.part = reinterpret_cast<float *>(ws + L.part_q);
+      x.out = static_cast<uint8_t *>(grad_queries) + r0 * ld_queries * sg;
+      x.ld = ld_queries;
+      x.dtype = grad_dtype;
+      x.alpha = alpha;
+      x.scale = scale;
+      x.mask = {c.factor, nullptr};
     }
     if (h.gi) {
-      const bool last = r0 + rows == n;
-      p.g.q = {reinterpret_cast<const uint8_t *>(c.g), m, h.ld_g * 2, c.plane_g * 2};
-      p.g.k_rows = rows;
-      p.g.p = {ws + L.turned_q + r0 * 2, d, turned_ld(n) * 2, turned_ld(n) * d * 2};
-      p.g.k_bytes = up(rows, 8) * 2;
+      sps::ProductArgs &x = p.items;
+      x.g.q = {reinterpret_cast<const uint8_t *>(c.g), m, h.ld_g * 2, c.plane_g * 2};
+      x.g.k_rows = rows;
+      x.g.p = {ws + L.turned_q + r0 * 2, d, turned_ld(n) * 2, turned_ld(n) * d * 2};
+      x.g.k_bytes = up(rows, 8) * 2;
       float *const sum = reinterpret_cast<float *>(ws + L.sum_i);
-      p.part = reinterpret_cast<float *>(ws + L.part);
-      p.before = r0 > 0 ? sum : nullptr;
-      if (last) {
-        p.out = grad_items;
-        p.ld = ld_items;
-        p.mask = {nullptr, bias};
+      x.part = reinterpret_cast<float *>(ws + L.part_i);
+      x.before = r0 > 0 ? sum : nullptr;
+      if (r0 + rows == n) {
+        x.out = grad_items;
+        x.ld = ld_items;
+        x.dtype = grad_dtype;
+        x.alpha = alpha;
+        x.scale = scale;
+        x.mask = {nullptr, bias};
       } else {  // as they are
-        p.out = sum;
-        p.ld = d;
-        p.dtype = SPS_F32;
-        p.alpha = 1.0f;
-        p.scale = nullptr;
-        p.mask = {};
+        x.out = sum;
+        x.ld = d;
+        x.dtype = SPS_F32;
+        x.alpha = 1.0f;
       }
-      launch_product<true>(h.dtype, rows == h.at_once ? h.plan_i : plan_items(h, rows), p, s);
     }
+    launch_products(h.dtype, plan_products(h, rows), &p, s);
   }
   return sps::launch_status(what);
 }

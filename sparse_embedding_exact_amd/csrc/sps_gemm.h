@@ -581,16 +581,21 @@ struct GemmTile {
   }
 };
 
-// A workgroup goes through tiles blockIdx.x, blockIdx.x + gridDim.x, ...: the
-// next one's first steps are loaded while this one's sums are put away.
+__device__ __forceinline__ uint32_t gemm_all(const GemmArgs &a) {
+  return (uint32_t)a.tiles_c * ((uint32_t)a.main_r + (uint32_t)a.tail_r * (uint32_t)a.splits);
+}
+
+// A workgroup goes through tiles first, first + gridDim.x, ...: the next one's
+// first steps are loaded while this one's sums are put away.
 //   take(tile) is called before those loads, with the sums: what it loads is
 //   there first; put(tile) after, and says whether the next tile may count
 //   STORES memory operations behind them.
 template <int STORES, class Tile, class Op, class Start, class Take, class Put>
-__device__ __forceinline__ void gemm_tiles(Tile &t, const GemmArgs &a, Op, const Start &start,
-                                           const Take &take, const Put &put) {
-  const uint32_t all = (uint32_t)a.tiles_c * ((uint32_t)a.main_r + (uint32_t)a.tail_r * (uint32_t)a.splits);
-  uint32_t id = blockIdx.x;
+__device__ __forceinline__ void gemm_tiles(Tile &t, const GemmArgs &a, Op, uint32_t first,
+                                           const Start &start, const Take &take, const Put &put) {
+  const uint32_t all = gemm_all(a);
+  uint32_t id = first;
+  if (id >= all) return;
   bool counted = false;
   t.at = gemm_place<Op, Tile::kC, Tile::kR>(a, id);
   t.prefetch(t.at);
@@ -626,13 +631,12 @@ constexpr int kCus = 256;
 struct TilePlan {
   bool big;
   int32_t tiles_c, main_r, tail_r, splits;
+  double us;
   int64_t size() const { return big ? 256 : 128; }
   int64_t tail_row() const { return main_r * size(); }  // the first row of the tail
-  uint32_t grid() const {
-    const int64_t tiles = (int64_t)tiles_c * (main_r + (int64_t)tail_r * splits);
-    const int64_t at_once = big ? kCus : 2 * kCus;
-    return (uint32_t)(tiles < at_once ? tiles : at_once);
-  }
+  int64_t all() const { return (int64_t)tiles_c * (main_r + (int64_t)tail_r * splits); }
+  int64_t at_once() const { return big ? kCus : 2 * kCus; }
+  uint32_t grid() const { return (uint32_t)(all() < at_once() ? all() : at_once()); }
   void give(GemmArgs *a) const {
     a->tiles_c = tiles_c;
     a->main_r = main_r;
@@ -640,32 +644,33 @@ struct TilePlan {
     a->splits = splits;
   }
 };
-inline TilePlan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int most_splits) {
+inline TilePlan plan_tiles(bool big, int64_t rows, int64_t cols, int64_t steps, int most_splits) {
   TilePlan best{};
-  double least = 1e300;
-  for (int big = 0; big < 2; ++big) {
-    const int64_t t = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
-    const int64_t tr = ceil_div(rows, t), tc = ceil_div(cols, t);
-    const double step = big ? 1.7 : 1.2, around = big ? 8.0 : 6.0;
-    const double whole = (double)steps * step + around;
-    const auto offer = [&](int64_t main_r, int z, double us) {
-      if (us >= least) return;
-      least = us;
-      best = {big != 0, (int32_t)tc, (int32_t)main_r, (int32_t)(tr - main_r), z};
-    };
-    offer(tr, 1, (double)ceil_div(tr * tc, slots) * whole);
-    const int64_t rounds = tr * tc / slots, main_r = rounds * slots / tc;
-    const int64_t tail = (tr - main_r) * tc;
-    if (tail == 0) continue;
-    const double values = (double)(rows - main_r * t) * (double)cols;
-    // 2, 3, 4, 5, 6, 7, 8, 10, 12, ...: an eighth apart at the least
-    for (int z = 2; z <= most_splits && z * 4 <= steps; z += z < 8 ? 1 : z / 8 * 2)
-      offer(main_r, z,
-            (double)rounds * whole +
-                (double)ceil_div(tail * z, slots) * ((double)ceil_div(steps, z) * step + around) + 5.0 +
-                (double)z * values * 8.0 / 4e6);
-  }
+  best.us = 1e300;
+  const int64_t t = big ? 256 : 128, slots = big ? kCus : 2 * kCus;
+  const int64_t tr = ceil_div(rows, t), tc = ceil_div(cols, t);
+  const double step = big ? 1.7 : 1.2, around = big ? 8.0 : 6.0;
+  const double whole = (double)steps * step + around;
+  const auto offer = [&](int64_t main_r, int z, double us) {
+    if (us < best.us) best = {big, (int32_t)tc, (int32_t)main_r, (int32_t)(tr - main_r), z, us};
+  };
+  offer(tr, 1, (double)ceil_div(tr * tc, slots) * whole);
+  const int64_t rounds = tr * tc / slots, main_r = rounds * slots / tc;
+  const int64_t tail = (tr - main_r) * tc;
+  if (tail == 0) return best;
+  const double values = (double)(rows - main_r * t) * (double)cols;
+  // 2, 3, 4, 5, 6, 7, 8, 10, 12, ...: an eighth apart at the least
+  for (int z = 2; z <= most_splits && z * 4 <= steps; z += z < 8 ? 1 : z / 8 * 2)
+    offer(main_r, z,
+          (double)rounds * whole +
+              (double)ceil_div(tail * z, slots) * ((double)ceil_div(steps, z) * step + around) + 5.0 +
+              (double)z * values * 8.0 / 4e6);
   return best;
+}
+inline TilePlan plan_tiles(int64_t rows, int64_t cols, int64_t steps, int most_splits) {
+  const TilePlan small = plan_tiles(false, rows, cols, steps, most_splits);
+  const TilePlan large = plan_tiles(true, rows, cols, steps, most_splits);
+  return large.us < small.us ? large : small;
 }
 
 }  // namespace sps

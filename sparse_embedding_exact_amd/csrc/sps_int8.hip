@@ -191,7 +191,7 @@ __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
     else put_all(std::false_type{});
     return whole;
   };
-  gemm_tiles<Tile::template kStores<T>>(t, a.g, OpI8{}, [&] { t.clear(); }, take, put);
+  gemm_tiles<Tile::template kStores<T>>(t, a.g, OpI8{}, blockIdx.x, [&] { t.clear(); }, take, put);
 }
 
 // Few queries (up to 16 NQ): bound by reading the items once. A wave takes 16
