@@ -655,7 +655,8 @@ using sps::set_error;
 
 namespace {
 
-constexpr int64_t kMaxItems = 1ll << 22;  // a tile's rows of G stay below 2^31 bytes
+// 256 rows of G, or of a transposed operand, stay below 2^31 bytes.
+constexpr int64_t kMaxRows = 4000000;
 constexpr int64_t kMaxDim = 1ll << 16;
 // Bytes of a piece's codes and gradients, and of statistics where there are no
 // codes.
@@ -808,12 +809,15 @@ sps_status check_shape(const sps_scores *q, const sps_scores *i, const char *wha
   if (q->n_cols < 1) return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: no dims", what);
   if (q->n_cols > kMaxDim)
     return set_error(SPS_ERR_UNSUPPORTED, "%s: at most %lld dims", what, (long long)kMaxDim);
-  if (i->n_rows > kMaxItems)
-    return set_error(SPS_ERR_UNSUPPORTED, "%s: at most %lld items", what, (long long)kMaxItems);
+  if (q->n_rows > kMaxRows || i->n_rows > kMaxRows)
+    return set_error(SPS_ERR_UNSUPPORTED, "%s: at most %lld queries and items", what,
+                     (long long)kMaxRows);
   const int64_t most = sps::kMostBytes / 256 / 4;  // a tile's rows in 31 bits of bytes
   if (q->ld > most || i->ld > most)
     return set_error(SPS_ERR_OVERFLOW, "%s: ld must be at most %lld", what, (long long)most);
-  return sps::check_grid(ceil_div(q->n_rows, 64) * ceil_div(q->n_cols, 64), 256, what);
+  // the tiles of both sides that are laid out, and one workgroup
+  return sps::check_grid((ceil_div(q->n_rows, 64) + ceil_div(i->n_rows, 64)) * ceil_div(q->n_cols, 64) + 1,
+                         256, what);
 }
 
 sps_status check_out(const sps_scores *q, const sps_scores *i, const sps_scores *of,

@@ -116,7 +116,10 @@ def test_cross_entropy_refusals(lib):
         assert ce(lib, gq=at) == INV and ce(lib, gi=at) == INV
     assert ce(lib, gq=7 * P + 8) == INV  # and in each other
     assert ce(lib, q=view(cols=70000, ld=70000), i=view(cols=70000, ld=70000), gq=None, gi=None) == UNS
-    assert ce(lib, i=view(rows=2**22 + 1), gq=None, gi=None) == UNS
+    assert ce(lib, i=view(rows=4000001), gq=None, gi=None) == UNS
+    assert ce(lib, q=view(rows=4000001), gq=None, gi=None) == UNS
+    assert ce(lib, q=view(rows=4000000, cols=65536, ld=65536), i=view(rows=4000000, cols=65536, ld=65536),
+              gq=None, gi=None) == OVF  # more tiles than a launch has
     assert ce(lib, i=view(ld=2**22), gq=None, gi=None) == OVF
 
 

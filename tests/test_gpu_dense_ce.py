@@ -114,6 +114,65 @@ def test_pieces(env, dtype):
     assert (off <= bar).all()
 
 
+def exact_on_gpu(env, x, w, t, tau, weights, rows=2048):
+    """Losses and gradients in float64, and the bars of both gradients, a batch of rows at a time."""
+    torch = env[0]
+    d = str(x.dtype).split(".")[1]
+    half = do.HALF["bfloat16" if d == "float32" else d] if d != "float32" else 0.0
+    w64 = w.double()
+    wt = w64.t().contiguous()
+    loss, gq, bq = [], [], []
+    gi, bi = torch.zeros_like(w64), torch.zeros_like(w64)
+    for a in range(0, len(x), rows):
+        xb, tb = x[a:a + rows].double(), t[a:a + rows].long()
+        live = tb >= 0
+        z = xb @ wt / tau
+        r = torch.arange(len(xb), device=x.device)
+        lse = z.logsumexp(1)
+        loss.append(torch.where(live, lse - z[r, tb.clamp(min=0)], 0.0))
+        p = torch.exp(z - lse[:, None])
+        # Logits in float32 are off by ez: a sum of dim products by 2 dim u of their magnitudes, the
+        # factor and the maximum by a few u; a p by a factor of 1 + 2 ez and its sums' 200 u, and the
+        # target's 1 - p, which comes from the loss, by as much as the loss, whatever is left of it
+        size = xb.abs() @ wt.abs() / tau
+        ez = ((2 * x.shape[1] + 8) * do.U * size + 4 * do.U * z.abs()).amax(1) + 8 * do.U * z.abs().amax(1)
+        eg = p * (4 * ez[:, None] + 200 * do.U + half * 2.0 ** -3)
+        eg[r[live], tb[live]] = 2 * ez[live] + 160 * do.U
+        p[r[live], tb[live]] -= 1
+        factor = torch.where(live, weights[a:a + rows].double() / tau, 0.0)[:, None]
+        eg = (eg + half * (p.abs() + eg)) * factor
+        p *= factor
+        # float32 sums of the products
+        eg += p.abs() * (2 * max(w64.shape[0], len(x)) * do.U)
+        gq.append(p @ w64)
+        bq.append(eg @ w64.abs())
+        xt = xb.t().contiguous()
+        gi += (xt @ p).t()
+        bi += (xt.abs() @ eg).t()
+    return torch.cat(loss), torch.cat(gq), gi, torch.cat(bq), bi
+
+
+@pytest.mark.parametrize("n,m,d,dtype", [
+    (1024, 70000, 256, "bfloat16"),   # whole rounds of tiles of the items' product, then a split rest
+    (1000, 66000, 264, "float32"),
+    (8200, 66304, 256, "float16"),    # two pieces of rows: sums that go on, whole and split
+    (8200, 70001, 250, "bfloat16"),
+    (130, 300000, 520, "float16"),    # a long k in many parts
+])
+def test_rounds_and_parts(env, n, m, d, dtype):
+    torch, sps, dev = env
+    x, w, t, _, ww = make(env, n, m, d, dtype, 5, masked=False)
+    t[::17] = -1
+    loss, gq, gi, bq, bi = exact_on_gpu(env, x, w, t, 0.5, ww)
+    got = sps.dense_cross_entropy(x, w, t, 0.5, row_weights=ww)
+    assert ((got[0].double() - loss).abs() <= 1e-5 * (1 + loss.abs())).all()
+    for g, want, bar in ((got[1], gq, bq), (got[2], gi, bi)):
+        off = (g.double() - want).abs() - bar - want.abs() * do.HALF[dtype] - do.STEP[dtype]
+        if dtype == "float16":  # G's step below 2^-14 of the largest weight's range
+            off -= 2.0 ** -38 * 64
+        assert (off <= 0).all(), (float(off.max()), int((off > 0).sum()))
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_choices(env, dtype):
     """Losses alone, one side's gradient, float32 gradients: the same numbers."""
