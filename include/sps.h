@@ -658,13 +658,15 @@ sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *it
  * bias is a constant (masks, sampling corrections) and gets no gradient.
  * Otherwise NaN and infinities of a row that takes part make its own loss and
  * gradient NaN, and those of the other side's rows that it reaches.
- * Products of 16-bit rows are exact and summed in float32, float32 rows are
- * multiplied to 2^-24 of each product; statistics of the softmax are float32
+ * Products of 16-bit rows are exact and summed in float32; float32 rows are
+ * multiplied with 22 bits of each value (fewer below 2^-18 of the largest of
+ * its row, for the gradients of the whole matrix: an absolute 2^-40 of that);
+ * statistics of the softmax are float32
  * within a block of columns and float64 beyond; G is rounded to the rows' type
- * (float32: kept to 24 bits) before its two products, whose float32 sums are
- * rounded once to grad_dtype. fp16: G is scaled by a power of two so that the
- * largest weight uses the type's range; weights more than about 2^24 below it
- * lose precision. Bitwise reproducible. */
+ * (float32: to 22 bits) before its two products, whose float32 sums are
+ * rounded once to grad_dtype. fp16 and float32: G is scaled by a power of two
+ * so that the largest weight uses fp16's range; gradients of weights more than
+ * about 2^24 below it lose precision. Bitwise reproducible. */
 
 /* Bytes of the workspace of sps_dense_ce for these rows (their addresses and
  * ld matter, nothing is read), with either gradient or both. Pure host. It

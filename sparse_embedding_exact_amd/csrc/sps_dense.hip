@@ -16,8 +16,11 @@
 // target is 1 - p from the loss, never p - 1 of a rounded p.
 // fp16: G is held 2^k times as large, 2^k the power of two that takes the
 // largest weight to [2^14, 2^15), so that p down to 2^-29 keeps all its bits.
-// float32: operands and G stand as three bf16 planes, their values' 24 bits;
-// six products of planes leave out what is below 2^-24 of a product.
+// float32: operands and G stand in two planes of fp16, scaled by powers of two
+// (each row for the logits, the matrix for the products with G, whose sums go
+// over rows), so that a value keeps 22 bits down to 2^-18 of the largest and
+// an absolute 2^-40 of it below; three products of planes leave out what is
+// below 2^-22 of a product.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -30,26 +33,32 @@ namespace sps {
 // ---------------------------------------------------------------------------
 // operands
 
-// 16-bit planes of a value: itself, or a float32 as hi + mid + low in bf16.
+// 16-bit planes of a value: itself, or a float32 as lead + rest in fp16.
 template <typename T>
 constexpr int kPlanes = 1;
 template <>
-constexpr int kPlanes<float> = 3;
+constexpr int kPlanes<float> = 2;
 
 __device__ __forceinline__ void split(f16_t x, uint16_t o[1]) { o[0] = x.u; }
 __device__ __forceinline__ void split(bf16_t x, uint16_t o[1]) { o[0] = x.u; }
-// Nearest bf16 of what is left each time: the last one is exact. Infinities and
-// NaN, and what rounds to infinity, stand in the leading plane.
-__device__ __forceinline__ void split(float x, uint16_t o[3]) {
-  const bf16_t hi = from_f32<bf16_t>(x);
-  const float h = to_f32(hi);
-  const bool fine = fabsf(h) < __builtin_inff();
-  const float r = fine ? x - h : 0.0f;
-  const bf16_t mid = from_f32<bf16_t>(r);
-  o[0] = hi.u;
-  o[1] = mid.u;
-  o[2] = from_f32<bf16_t>(r - to_f32(mid)).u;
+// Infinities and NaN stand in the leading plane.
+__device__ __forceinline__ void split(float x, uint16_t o[2]) {
+  const f16_t lead = from_f32<f16_t>(x);
+  const float h = to_f32(lead);
+  o[0] = lead.u;
+  o[1] = from_f32<f16_t>(fabsf(h) < __builtin_inff() ? x - h : 0.0f).u;
 }
+// The power of two that takes a largest magnitude to [2^14, 2^15) (1 for 0).
+__device__ __forceinline__ float scale_for(float top) {
+  int e = 14 - ((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127);
+  e = top == 0.0f ? 0 : (e > 100 ? 100 : (e < -120 ? -120 : e));
+  return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+}
+// fp16 x power of two: the type does not change
+template <typename T>
+__device__ __forceinline__ T scaled(T x, float) { return x; }
+template <>
+__device__ __forceinline__ float scaled(float x, float s) { return x * s; }
 
 // Rows that take no part are zeros in the transposed copy, so that what they
 // hold (padding, NaN) meets the gradient's zeros as zero: rows of queries
@@ -76,7 +85,61 @@ struct LayArgs {
   uint16_t *turned;  // nullable: [cols][ld_t], zeros from rows on
   int64_t ld_t, plane_t;
   RowMask mask;
+  // float32: the scales, of every row in the packed planes and of all rows that take part in the
+  // turned ones (kMaxBlocks partial maxima)
+  float *row_scale;
+  float *tops;
 };
+constexpr int kMaxBlocks = 256;
+
+// float32: scales of rows and partial maxima, a wave a row; bound by memory.
+// What is not finite has no part in a scale.
+struct MaxBoth {
+  LayArgs side[2];
+};
+constexpr int kMaxWaves = 16, kMaxRowsOnce = 4;
+__global__ __launch_bounds__(64 * kMaxWaves) void ce_max_kernel(MaxBoth both) {
+  const LayArgs a = blockIdx.x >= kMaxBlocks ? both.side[1] : both.side[0];
+  const int block = blockIdx.x % kMaxBlocks, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float tops[kMaxWaves];
+  const float *const x = static_cast<const float *>(a.x);
+  float most = 0.0f;
+  // a few rows at a time, so that their loads are on their way together
+  for (int64_t r0 = ((int64_t)block * kMaxWaves + wave) * kMaxRowsOnce; r0 < a.rows;
+       r0 += kMaxBlocks * kMaxWaves * kMaxRowsOnce) {
+    float top[kMaxRowsOnce] = {};
+    for (int64_t c = lane; c < a.cols; c += 64)
+#pragma unroll
+      for (int i = 0; i < kMaxRowsOnce; ++i) {
+        const int64_t r = r0 + i < a.rows ? r0 + i : r0;
+        const float f = fabsf(x[r * a.ld + c]);
+        if (f < __builtin_inff()) top[i] = fmaxf(top[i], f);
+      }
+#pragma unroll
+    for (int i = 0; i < kMaxRowsOnce; ++i) {
+#pragma unroll
+      for (int o = 32; o > 0; o >>= 1) top[i] = fmaxf(top[i], __shfl_xor(top[i], o, 64));
+      if (r0 + i >= a.rows) continue;
+      if (lane == 0) a.row_scale[r0 + i] = scale_for(top[i]);
+      if (!a.mask.out(r0 + i)) most = fmaxf(most, top[i]);
+    }
+  }
+  if (lane == 0) tops[wave] = most;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < kMaxWaves; ++i) most = fmaxf(most, tops[i]);
+  a.tops[block] = most;
+}
+// The scale of a turned matrix; every thread of 256 calls it.
+__device__ __forceinline__ float turned_scale(const float *parts) {
+  __shared__ float tops[4];
+  float top = parts[threadIdx.x];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  return scale_for(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
+}
 
 // Tiles of 64 x 64 through LDS, 8 values a thread and step both ways; bound by
 // memory. Planes in elements.
@@ -103,11 +166,7 @@ __device__ __forceinline__ void find_scale(const ScaleArgs &a) {
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
   if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
   __syncthreads();
-  if (threadIdx.x != 0) return;
-  for (int i = 1; i < 4; ++i) top = fmaxf(top, tops[i]);
-  int e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) - 127);
-  e = top == 0.0f ? 0 : (e > 100 ? 100 : (e < -100 ? -100 : e));
-  *a.scale = __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+  if (threadIdx.x == 0) *a.scale = scale_for(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])));
 }
 
 // One launch for both sides and the scale: `blocks` of each side, and one.
@@ -128,6 +187,9 @@ __global__ __launch_bounds__(256) void lay_kernel(LayBoth both) {
   const bool second = id >= both.blocks[0];
   if (second) id -= both.blocks[0];
   const LayArgs a = second ? both.side[1] : both.side[0];
+  float whole = 1.0f;
+  if constexpr (NP > 1)
+    if (a.turned) whole = turned_scale(a.tops);
   const uint32_t across = (uint32_t)((a.cols + 63) / 64);
   const int64_t r0 = (int64_t)(id / across) * 64, c0 = (int64_t)(id % across) * 64;
   const int in = (threadIdx.x & 7) * 8;
@@ -136,34 +198,38 @@ __global__ __launch_bounds__(256) void lay_kernel(LayBoth both) {
   for (int h = 0; h < 2; ++h) {
     const int i = (threadIdx.x >> 3) + 32 * h;
     const int64_t r = r0 + i, c = c0 + in;
-    uint16_t v[NP][8] = {};
+    Eight<T> t{};
     bool out = true;
     if (r < a.rows) {
-      Eight<T> t{};
       if (c + 8 <= a.cols) t = *reinterpret_cast<const Eight<T> *>(x + r * a.ld + c);
       else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (c + e < a.cols) t.e[e] = x[r * a.ld + c + e];
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint16_t w[NP];
-        split(t.e[e], w);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) v[p][e] = w[p];
-      }
       out = a.turned && a.mask.out(r);
     }
+    const auto planes = [&](float scale, u32x4 (&w)[NP]) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      u32x4 w;
+      for (int e = 0; e < 8; e += 2) {
+        uint16_t lo[NP], hi[NP];
+        split(scaled(t.e[e], scale), lo);
+        split(scaled(t.e[e + 1], scale), hi);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = (uint32_t)v[p][2 * e] | (uint32_t)v[p][2 * e + 1] << 16;
-      if (a.packed && r < a.rows && c < a.ld_p)
-        *reinterpret_cast<u32x4 *>(a.packed + p * a.plane_p + r * a.ld_p + c) = w;
-      *reinterpret_cast<u32x4 *>(&tile[p][i][in]) = out ? u32x4{} : w;
+        for (int p = 0; p < NP; ++p) w[p][e / 2] = (uint32_t)lo[p] | (uint32_t)hi[p] << 16;
+      }
+    };
+    u32x4 w[NP];
+    if (a.packed && r < a.rows && c < a.ld_p) {
+      planes(NP > 1 ? a.row_scale[r] : 1.0f, w);
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        *reinterpret_cast<u32x4 *>(a.packed + p * a.plane_p + r * a.ld_p + c) = w[p];
     }
+    if (!a.turned) continue;
+    planes(whole, w);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(&tile[p][i][in]) = out ? u32x4{} : w[p];
   }
   if (!a.turned) return;
   __syncthreads();
@@ -225,6 +291,7 @@ struct LogitArgs {
   GemmArgs g;         // q: the piece's queries, p: items
   float c, c_low;     // log2(e) / tau in two parts: everything is in powers of two
   const float *bias;  // nullable
+  const float *scale_q, *scale_p;  // float32: those of the packed rows
   const int32_t *targets;
   void *code;  // nullable: uint16 (float32: float) [rows][ld]
   int64_t ld;
@@ -249,6 +316,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   constexpr bool kLow = sizeof(Word) == 4;
   float c, c_low;
   int32_t target[FR];
+  float unscale[FR];  // float32: of the rows
   const auto times = [&](float x, float y) {
     // (where the sums are logits already, c_low is 0 and they may be -inf)
     return __builtin_fmaf(x, c, kLow && c_low != 0.0f ? __builtin_fmaf(x, c_low, y) : y);
@@ -262,6 +330,19 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
     for (int j = 0; j < FR; ++j) {
       const int64_t r = t.at.row0 + t.row_of(j);
       target[j] = a.targets[r < rows ? r : rows - 1];
+      if (kLow) unscale[j] = 1.0f / a.scale_q[r < rows ? r : rows - 1];
+    }
+    if constexpr (kLow) {  // powers of two: exact
+      float s[FC][4];
+      t.of_columns(a.scale_p, 1.0f, s);
+#pragma unroll
+      for (int i = 0; i < FC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float unscale_c = 1.0f / s[i][e];
+#pragma unroll
+          for (int j = 0; j < FR; ++j) t.acc[i][j][e] = t.acc[i][j][e] * unscale_c * unscale[j];
+        }
     }
     if (!a.bias && t.at.col0 + TC <= cols) return;
     float b[FC][4];
@@ -512,8 +593,20 @@ struct ProductArgs {
   int32_t dtype;
   float alpha;
   const float *scale;  // nullable: divides alpha
+  const float *tops;   // float32: the maxima behind the turned operand's scale, which divides it too
   OutMask mask;
 };
+__device__ __forceinline__ float alpha_of(float alpha, const float *scale, const float *tops) {
+  if (scale) alpha /= *scale;
+  if (tops) {
+    float top = 0.0f;
+    for (int i = threadIdx.x & 63; i < kMaxBlocks; i += 64) top = fmaxf(top, tops[i]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    alpha /= scale_for(top);
+  }
+  return alpha;
+}
 
 __device__ __forceinline__ void put_typed(void *out, int32_t dtype, int64_t at, int64_t col,
                                           int64_t cols, const float v[4]) {
@@ -547,7 +640,7 @@ template <class Op, bool QT, int TC, int TR, int WC, int WR>
 __device__ __forceinline__ void product_tiles(const ProductArgs &a, uint32_t first, uint8_t *lds) {
   using Tile = GemmTile<Op, TC, TR, WC, WR, QT>;
   Tile t(a.g, lds);
-  const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
+  const float alpha = alpha_of(a.alpha, a.scale, a.tops);
   using Type = typename Op::Type;  // the rows' own: that of the products
   const auto start = [&] {
     if (a.before && t.at.z < 0) t.start(a.before, a.g.q.rows, a.g.p.rows);
@@ -597,7 +690,7 @@ struct JoinArgs {
   int64_t ld;
   int32_t dtype;
   float alpha;
-  const float *scale;
+  const float *scale, *tops;
   OutMask mask;
 };
 // Of both products: `blocks` workgroups each.
@@ -613,7 +706,7 @@ __global__ __launch_bounds__(256) void ce_join_kernel(JoinBoth both) {
   const uint32_t block = second ? blockIdx.x - both.blocks[0] : blockIdx.x;
   const uint32_t blocks = second ? both.blocks[1] : both.blocks[0];
   const int64_t per = (a.cols + 3) / 4, all = a.rows * per;
-  const float alpha = a.scale ? a.alpha / *a.scale : a.alpha;
+  const float alpha = alpha_of(a.alpha, a.scale, a.tops);
   for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < all; i += (int64_t)blocks * 256) {
     const int64_t r = i / per, c = (i - r * per) * 4;
     float v[4] = {};
@@ -708,11 +801,11 @@ int64_t part_values(const sps::TilePlan &p, int64_t rows, int64_t cols) {
 }
 
 struct Layout {
-  size_t scale, factor, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, part_q, part_i,
+  size_t scale, tops_q, tops_i, rows_q, rows_i, factor, z_target, stats, packed_q, packed_i, turned_q, turned_i, code, g, part_q, part_i,
       sum_i, total;
 };
 
-int planes(const Shape &s) { return s.dtype == SPS_F32 ? 3 : 1; }
+int planes(const Shape &s) { return s.dtype == SPS_F32 ? 2 : 1; }
 
 // Rows of 16-bit values that hold `k`, an odd number of 128 bytes: equal places
 // of neighbouring rows fall into different channels of L2.
@@ -741,7 +834,7 @@ Shape shape_of(const sps_scores *q, const sps_scores *i, bool gq, bool gi) {
   s.pack_i = must_pack(i);
   s.ld_g = odd_ld(s.m);
   const bool grad = gq || gi;
-  const int64_t each = s.dtype == SPS_F32 ? 10 : 2;
+  const int64_t each = s.dtype == SPS_F32 ? 8 : 2;
   s.block = 64;
   int64_t rows = grad ? kPieceBytes / (s.ld_g * each) : kStatBytes / (8 * ceil_div(s.m, 64));
   rows = rows / 256 * 256;
@@ -765,14 +858,20 @@ Layout layout_of(const Shape &s) {
   };
   const int p = planes(s);
   L.scale = take(4);
+  if (p > 1) {
+    L.tops_q = take(sps::kMaxBlocks * 4);
+    L.tops_i = take(sps::kMaxBlocks * 4);
+    L.rows_q = take(s.n * 4);
+    L.rows_i = take(s.m * 4);
+  }
   L.z_target = take(s.piece * 8);
   L.stats = take(s.blocks * s.piece * 8);
   if (s.pack_q) L.packed_q = take(s.n * packed_ld(s) * 2 * p);
   if (s.pack_i) L.packed_i = take(s.m * packed_ld(s) * 2 * p);
   if (s.gq || s.gi) {
     L.factor = take(s.piece * 4);
-    L.code = take(s.piece * s.ld_g * (p == 3 ? 4 : 2));
-    L.g = p == 3 ? take(s.piece * s.ld_g * 6) : L.code;
+    L.code = take(s.piece * s.ld_g * (p > 1 ? 4 : 2));
+    L.g = p > 1 ? take(s.piece * s.ld_g * 2 * p) : L.code;
     if (s.gq) {
       L.turned_i = take(s.d * turned_ld(s.m) * 2 * p);
     }
@@ -877,7 +976,7 @@ void launch_products(int32_t dtype, const PlanBoth &plan, sps::ProductsArgs *a, 
     const int64_t rows = x.g.q.rows - x.tail_row, cols = x.g.p.rows;
     x.stride = rows * cols;
     join.side[k] = {x.part, x.before, x.stride, x.tail_row, rows,    cols,  p.splits,
-                    x.out,  x.ld,     x.dtype,  x.alpha,    x.scale, x.mask};
+                    x.out,  x.ld,     x.dtype,  x.alpha,    x.scale, x.tops, x.mask};
     const int64_t blocks = ceil_div(rows * ceil_div(cols, 4), 256);
     join.blocks[k] = (uint32_t)(blocks < 4096 ? blocks : 4096);
   }
@@ -960,8 +1059,8 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", what);
   uint8_t *const ws = static_cast<uint8_t *>(workspace);
   const int np = planes(h);
-  const bool wide = np == 3, grad = h.gq || h.gi;
-  float *const scale = h.dtype == SPS_F16 && grad ? reinterpret_cast<float *>(ws + L.scale) : nullptr;
+  const bool wide = np > 1, grad = h.gq || h.gi;
+  float *const scale = h.dtype != SPS_BF16 && grad ? reinterpret_cast<float *>(ws + L.scale) : nullptr;
   // operands: as they lie, or laid out with 16-byte rows; transposed for the products
   sps::LayBoth both{};
   both.scale = {row_weights, targets, n, m, scale};
@@ -983,7 +1082,11 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       a.turned = reinterpret_cast<uint16_t *>(ws + turned);
       a.ld_t = turned_ld(a.rows);
       a.plane_t = a.ld_t * a.cols;
-      a.mask = mask;
+    }
+    a.mask = mask;
+    if (wide) {
+      a.row_scale = reinterpret_cast<float *>(ws + (side ? L.rows_i : L.rows_q));
+      a.tops = reinterpret_cast<float *>(ws + (side ? L.tops_i : L.tops_q));
     }
     return o;
   };
@@ -991,6 +1094,11 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
                              {targets, row_weights, m, nullptr});
   const GemmOperand oi = lay(1, items, h.pack_i, L.packed_i, h.gq, L.turned_i, {nullptr, nullptr, 0, bias});
 
+  if (wide) {
+    const sps::MaxBoth max{{both.side[0], both.side[1]}};
+    hipLaunchKernelGGL(sps::ce_max_kernel, dim3(2 * sps::kMaxBlocks),
+                       dim3(64 * sps::kMaxWaves), 0, s, max);
+  }
   launch_lay(h.dtype, &both, s);
 
   const float alpha = (float)(1.0 / (double)temperature);
@@ -1006,6 +1114,10 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.c = (float)c2;
     a.c_low = (float)(c2 - (double)a.c);
     a.bias = bias;
+    if (wide) {
+      a.scale_q = both.side[0].row_scale + r0;
+      a.scale_p = both.side[1].row_scale;
+    }
     a.targets = targets + r0;
     a.code = grad ? ws + L.code : nullptr;
     a.ld = h.ld_g;
@@ -1053,6 +1165,7 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
       x.dtype = grad_dtype;
       x.alpha = alpha;
       x.scale = scale;
+      x.tops = wide ? both.side[1].tops : nullptr;
       x.mask = {c.factor, nullptr};
     }
     if (h.gi) {
@@ -1070,6 +1183,7 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
         x.dtype = grad_dtype;
         x.alpha = alpha;
         x.scale = scale;
+        x.tops = wide ? both.side[0].tops : nullptr;
         x.mask = {nullptr, bias};
       } else {  // as they are
         x.out = sum;

@@ -65,15 +65,15 @@ struct OpI8 {
   }
 };
 
-// float32 as three planes of bf16
-struct OpF32 : OpBf16 {
+// float32 as two planes of fp16
+struct OpF32 : OpF16 {
   using Type = float;
-  static constexpr int kPlanes = 3;
+  static constexpr int kPlanes = 2;
 };
 
 // Rows of an operand: `rows` rows, ld bytes apart, base and ld on 16-byte
-// boundaries. A float32 matrix stands in three planes of bf16 (a value's
-// leading, middle and last 8 bits), `plane` bytes apart.
+// boundaries. A float32 matrix stands, scaled, in two planes of fp16 (a value's
+// leading 11 bits, and 11 of what is left), `plane` bytes apart.
 struct GemmOperand {
   const uint8_t *base;
   int64_t rows;
@@ -81,9 +81,9 @@ struct GemmOperand {
   int64_t plane;
 };
 
-// k_bytes of every row take part (a multiple of 16). With planes the six
-// products of planes that reach 2^-24 of a product are summed one after
-// another, as if k were six times as long. The first main_r rows of tiles are
+// k_bytes of every row take part (a multiple of 16). With planes their three
+// products but that of both rests (2^-22 of a product) are summed one after
+// another, as if k were three times as long. The first main_r rows of tiles are
 // summed whole; of the tail_r behind them part z of `splits` takes the z-th
 // part of the steps.
 struct GemmArgs {
@@ -95,11 +95,11 @@ struct GemmArgs {
 
 constexpr int kStep = 128;                    // bytes of k a step
 constexpr uint32_t kMostBytes = 0x7fffffffu;  // of a tile's rows: offsets are 32 bits
-constexpr int kSegments = 6;
+constexpr int kSegments = 3;
 
-// planes of a float32 product's six parts: hi hi, hi mid, mid hi, hi low, low hi, mid mid
-__device__ __forceinline__ int seg_q(int s) { return (0x001021 >> (4 * (5 - s))) & 15; }
-__device__ __forceinline__ int seg_p(int s) { return (0x010201 >> (4 * (5 - s))) & 15; }
+// planes of a float32 product's parts: lead lead, lead rest, rest lead
+__device__ __forceinline__ int seg_q(int s) { return s == 2; }
+__device__ __forceinline__ int seg_p(int s) { return s == 1; }
 
 // Workgroups go to the 8 XCDs in turn; each XCD has an L2 of its own. A run of
 // neighbouring tiles goes to one XCD, and within it kGroup rows of tiles are

@@ -39,7 +39,14 @@ def rounding(v, dtype):
     return np.abs(v) * HALF[dtype] + STEP[dtype] / 2
 
 
-def cross_entropy(x, w, t, tau, bias=None, weights=None):
+# float32 rows are multiplied as lead + rest in fp16: a value is off by half a step of the rest,
+# 2^-11 2^-11 of it, in both factors, and the product of both rests, as much again, is left out
+PLANES = 3 * 2.0 ** -22
+# and below 2^-14 2^-15 of the largest by an absolute half of fp16's least step, 2^-25 of 2^15
+FLOOR = 2.0 ** -40
+
+
+def cross_entropy(x, w, t, tau, bias=None, weights=None, dtype="float32"):
     """loss, grad of x, grad of w in float64 and the bars of each for rows of `dtype` (given as
     float64 values): a function of the type, since only then is G rounded."""
     n, m = len(x), len(w)
@@ -72,14 +79,20 @@ def cross_entropy(x, w, t, tau, bias=None, weights=None):
     G = g * (ww / tau)[:, None]
     # logits: products, the factor of base two, the bias; in units of z
     a = np.abs(x) @ np.abs(wl).T / tau
+    wide = dtype == "float32"
     with np.errstate(invalid="ignore"):
-        ez = (2 * d + 8) * U * a + 4 * U * np.where(struck, 0.0, np.abs(b)) + 4 * U * np.abs(
+        if wide:  # both rows' values have that floor
+            top = np.abs(x).max(1, initial=0)[:, None], np.abs(wl).max(1, initial=0)[None, :]
+            floor = FLOOR / tau * (top[0] * np.abs(wl).sum(1)[None, :] + top[1] * np.abs(x).sum(1)[:, None])
+        else:
+            floor = 0.0
+        ez = ((2 * d + 8) * U + PLANES * wide) * a + floor + 4 * U * np.where(struck, 0.0, np.abs(b)) + 4 * U * np.abs(
             np.where(np.isfinite(z), z, 0.0))
     big = (ez.max(1) if m else np.zeros(n)) + 8 * U * np.abs(base)
     # sums of a block in float32 (128 columns), exponentials, logarithm
     e_loss = 2 * big + 160 * U + 4 * U * np.abs(np.where(np.isfinite(loss), loss, 0.0))
 
-    def bars(dtype, out):
+    def bars(out):
         fine = np.where(live, big, 0.0)
         rel = 4 * fine + 200 * U + (0.0 if dtype == "float32" else 2.0 ** -13)
         pm = np.where(live[:, None], p, 0.0)
@@ -88,20 +101,23 @@ def cross_entropy(x, w, t, tau, bias=None, weights=None):
         r = np.arange(n)
         eg[r, at] = np.where(live, (1 - pm[r, at]) * 4 * U + np.where(np.isfinite(e_loss), e_loss, 0.0),
                              0.0)
-        eg = eg + HALF[dtype] * (np.abs(g) + eg)
+        eg = eg + (2.0 ** -22 if wide else HALF[dtype]) * (np.abs(g) + eg)
         ww_abs = np.abs(ww)[:, None]
         if dtype != "float32":  # codes below 2^-14 of their block's maximum
             eg = eg + 2.0 ** -27 * live[:, None]
         eG = eg * ww_abs / tau
-        if dtype == "float16":  # G stands 2^14 to 2^15 over the largest weight
+        if dtype != "bfloat16":  # G stands 2^14 to 2^15 over the largest weight
             eG = eG + 2.0 ** -25 * 2.0 ** -14 * ww_abs.max(initial=0) / tau
         else:
             eG = eG + STEP["bfloat16"] / tau
-        sums = 4 * U + 2.0 ** -22 * (dtype == "float32")
+        sums = 4 * U + PLANES * wide
         xa, wa = np.abs(xl), np.abs(wl)
         Ga = np.abs(G)
         bq = eG @ wa + (Ga @ wa) * (2 * (m + 8) * U + sums)
         bi = eG.T @ xa + (Ga.T @ xa) * (2 * (n + 8) * U + sums)
+        if wide:
+            bq += FLOOR * wa.max(initial=0) * Ga.sum(1)[:, None]
+            bi += FLOOR * xa.max(initial=0) * Ga.sum(0)[:, None]
         gq, gi = G @ wl, G.T @ xl
         return bq + rounding(np.abs(gq) + bq, out), bi + rounding(np.abs(gi) + bi, out)
 

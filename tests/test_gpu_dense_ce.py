@@ -46,8 +46,8 @@ def check(env, got, x, w, t, tau, bias, weights, out=None):
     n64 = lambda a: None if a is None else a.double().cpu().numpy()  # noqa: E731
     dtype = str(x.dtype).split(".")[1]
     loss, e_loss, gq, gi, bars = do.cross_entropy(n64(x), n64(w), t.cpu().numpy().astype(np.int64),
-                                                  tau, n64(bias), n64(weights))
-    bq, bi = bars(dtype, dtype if out is None else out)
+                                                  tau, n64(bias), n64(weights), dtype)
+    bq, bi = bars(dtype if out is None else out)
     worst = []
     for name, g, want, bar in (("loss", got[0], loss, e_loss), ("queries", got[1], gq, bq),
                                ("items", got[2], gi, bi)):
@@ -118,7 +118,8 @@ def exact_on_gpu(env, x, w, t, tau, weights, rows=2048):
     """Losses and gradients in float64, and the bars of both gradients, a batch of rows at a time."""
     torch = env[0]
     d = str(x.dtype).split(".")[1]
-    half = do.HALF["bfloat16" if d == "float32" else d] if d != "float32" else 0.0
+    half = 2.0 ** -22 if d == "float32" else do.HALF[d]
+    planes = do.PLANES * (d == "float32")
     w64 = w.double()
     wt = w64.t().contiguous()
     loss, gq, bq = [], [], []
@@ -135,7 +136,7 @@ def exact_on_gpu(env, x, w, t, tau, weights, rows=2048):
         # factor and the maximum by a few u; a p by a factor of 1 + 2 ez and its sums' 200 u, and the
         # target's 1 - p, which comes from the loss, by as much as the loss, whatever is left of it
         size = xb.abs() @ wt.abs() / tau
-        ez = ((2 * x.shape[1] + 8) * do.U * size + 4 * do.U * z.abs()).amax(1) + 8 * do.U * z.abs().amax(1)
+        ez = (((2 * x.shape[1] + 8) * do.U + planes) * size + 4 * do.U * z.abs()).amax(1) + 8 * do.U * z.abs().amax(1)
         eg = p * (4 * ez[:, None] + 200 * do.U + half * 2.0 ** -3)
         eg[r[live], tb[live]] = 2 * ez[live] + 160 * do.U
         p[r[live], tb[live]] -= 1
@@ -143,7 +144,7 @@ def exact_on_gpu(env, x, w, t, tau, weights, rows=2048):
         eg = (eg + half * (p.abs() + eg)) * factor
         p *= factor
         # float32 sums of the products
-        eg += p.abs() * (2 * max(w64.shape[0], len(x)) * do.U)
+        eg += p.abs() * (2 * max(w64.shape[0], len(x)) * do.U + planes)
         gq.append(p @ w64)
         bq.append(eg @ w64.abs())
         xt = xb.t().contiguous()
@@ -168,7 +169,7 @@ def test_rounds_and_parts(env, n, m, d, dtype):
     assert ((got[0].double() - loss).abs() <= 1e-5 * (1 + loss.abs())).all()
     for g, want, bar in ((got[1], gq, bq), (got[2], gi, bi)):
         off = (g.double() - want).abs() - bar - want.abs() * do.HALF[dtype] - do.STEP[dtype]
-        if dtype == "float16":  # G's step below 2^-14 of the largest weight's range
+        if dtype != "bfloat16":  # G's step below 2^-14 of the largest weight's range
             off -= 2.0 ** -38 * 64
         assert (off <= 0).all(), (float(off.max()), int((off > 0).sum()))
 
@@ -232,6 +233,11 @@ def test_rows_without_part_hold_anything(env):
                 assert torch.equal(g, e)
         assert (want[0][pad] == 0).all() and (want[1][pad] == 0).all()
         assert (want[1][ww == 0] == 0).all() and (want[2][torch.isneginf(b)] == 0).all()
+        big = torch.finfo(torch.float16 if dtype == "float16" else torch.float32).max
+        for x3, w3 in ((x2.clone(), w2.clone()),):  # and neither does what is large there
+            x3[pad], w3[torch.isneginf(b)] = big, -big
+            for g, e in zip(sps.dense_cross_entropy(x3, w3, t, 0.5, b, ww), want):
+                assert torch.equal(g, e)
         x2[ww == 0] = float("nan")  # its loss is its own affair
         got = sps.dense_cross_entropy(x2, w2, t, 0.5, b, ww)
         assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
@@ -276,6 +282,17 @@ def test_large_logits(env, dtype):
     got = sps.dense_cross_entropy(x, w, t, 0.05, b, ww)
     check(env, got, x, w, t, 0.05, b, ww)
     assert got[0].max() > 100
+
+
+def test_float32_scales(env):
+    """Rows of very different lengths, and matrices of very large and very small values."""
+    torch, sps, dev = env
+    for sx, sw in ((1.0, 1.0), (1e15, 1e-15), (1e-20, 1e20), (1e-30, 1e30)):
+        x, w, t, b, ww = make(env, 70, 300, 40, "float32", 8)
+        x *= torch.logspace(-3, 0, 70, device=dev)[:, None] * sx
+        w *= torch.logspace(0, -3, 300, device=dev)[:, None] * sw
+        got = sps.dense_cross_entropy(x, w, t, 0.1, b, ww)
+        check(env, got, x, w, t, 0.1, b, ww)
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
