@@ -632,10 +632,10 @@ sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype,
  * queries[q][d] * items[i][d]) * scale_q * scale_i, n_query x n_item, of type
  * dtype: rows of scores as sps_cosine_chunk's (cosines, where the rows that
  * were put into 8 bits have norm 1). A chunk of the items is a part of their
- * rows. The sum is exact; its float32, the two products with the scales and
- * the type are rounded. Bitwise reproducible, whatever the number of queries.
- * Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH, SPS_ERR_OVERFLOW,
- * SPS_ERR_UNSUPPORTED. */
+ * rows. The sum is exact; its float32, the two products with the scales (the
+ * smaller one first) and the type are rounded. Bitwise reproducible, whatever
+ * the number of queries. Errors: SPS_ERR_INVALID_ARGUMENT,
+ * SPS_ERR_DIM_MISMATCH, SPS_ERR_OVERFLOW, SPS_ERR_UNSUPPORTED. */
 sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *items, void *out,
                            int32_t dtype, int64_t ld_out, void *stream);
 

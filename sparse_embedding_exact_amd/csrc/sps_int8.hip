@@ -155,7 +155,13 @@ struct Int8Args {
 };
 
 // The integers' sums are exact; a score is rounded as an integer above 2^24,
-// by either scale and to its type.
+// by either scale and to its type. The smaller scale first: a sum times it
+// overflows only where the score does.
+__device__ __forceinline__ float score_of(int32_t sum, float sq, float sp) {
+  const bool less = sq < sp;
+  return (float)sum * (less ? sq : sp) * (less ? sp : sq);  // either scale's NaN stays
+}
+
 template <typename T, bool STREAM, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
   using Tile = GemmTile<OpI8, TC, TR, WC, WR>;
@@ -179,7 +185,7 @@ __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
       for (int i = 0; i < Tile::kFragC; ++i) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = (float)t.acc[i][j][e] * sq[j] * sp[i][e];
+        for (int e = 0; e < 4; ++e) v[e] = score_of(t.acc[i][j][e], sq[j], sp[i][e]);
         w[i] = quad_of<T>(v);
       }
       t.template store<T, whole.value, STREAM>(j, w, static_cast<T *>(a.out), a.ld, rows, cols);
@@ -244,7 +250,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
       const float sq = a.scale_q[r];
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (float)acc[f][e] * sq * sp[e];
+      for (int e = 0; e < 4; ++e) v[e] = score_of(acc[f][e], sq, sp[e]);
       put_four<T>(static_cast<T *>(a.out) + r * a.ld, c0, a.g.p.rows, v);
     }
   }

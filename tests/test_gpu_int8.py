@@ -182,6 +182,20 @@ def test_rows_that_hold_nan(env):
         assert bad[3].all() and bad[:, 8].all() and int(bad.sum()) == 90 + n - 1
 
 
+def test_scores_of_scales_far_apart(env):
+    """Scales of either side near the ends of float32's range: the scores are inside it."""
+    torch, sps, dev = env
+    for sq, si in ((2.0 ** 110, 2.0 ** -115), (2.0 ** -115, 2.0 ** 110)):
+        for n in (5, 70):
+            q = sps.quantize_rows(rows_of(env, n, 200, "float32", 3))
+            i = sps.quantize_rows(rows_of(env, 90, 200, "float32", 4))
+            q.scales *= sq
+            i.scales *= si
+            got = sps.int8_scores(q, i)
+            assert got.isfinite().all()
+            check_scores(env, q, i, got)
+
+
 def test_empty(env):
     torch, sps, dev = env
     none = sps.quantize_rows(torch.empty(0, 24, device=dev))
