@@ -48,11 +48,16 @@ __device__ __forceinline__ void split(float x, uint16_t o[2]) {
   o[0] = lead.u;
   o[1] = from_f32<f16_t>(fabsf(h) < __builtin_inff() ? x - h : 0.0f).u;
 }
-// The power of two that takes a largest magnitude to [2^14, 2^15) (1 for 0).
+// The power of two that takes a largest magnitude to [2^14, 2^15) (1 for 0; at most 2^127).
 __device__ __forceinline__ float scale_for(float top) {
   int e = 14 - ((int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127);
-  e = top == 0.0f ? 0 : (e > 100 ? 100 : (e < -120 ? -120 : e));
+  e = top == 0.0f ? 0 : (e > 127 ? 127 : e);
   return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+}
+// And back: scales are divided out by their exponents together, since one of two may leave the
+// range where both do not.
+__device__ __forceinline__ int exponent_of(float scale) {
+  return (int)(__builtin_bit_cast(uint32_t, scale) >> 23) - 127;
 }
 // fp16 x power of two: the type does not change
 template <typename T>
@@ -316,7 +321,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   constexpr bool kLow = sizeof(Word) == 4;
   float c, c_low;
   int32_t target[FR];
-  float unscale[FR];  // float32: of the rows
+  int up[FR];  // float32: exponents of the rows' scales
   const auto times = [&](float x, float y) {
     // (where the sums are logits already, c_low is 0 and they may be -inf)
     return __builtin_fmaf(x, c, kLow && c_low != 0.0f ? __builtin_fmaf(x, c_low, y) : y);
@@ -330,18 +335,19 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
     for (int j = 0; j < FR; ++j) {
       const int64_t r = t.at.row0 + t.row_of(j);
       target[j] = a.targets[r < rows ? r : rows - 1];
-      if (kLow) unscale[j] = 1.0f / a.scale_q[r < rows ? r : rows - 1];
+      if (kLow) up[j] = exponent_of(a.scale_q[r < rows ? r : rows - 1]);
     }
-    if constexpr (kLow) {  // powers of two: exact
+    if constexpr (kLow) {
       float s[FC][4];
       t.of_columns(a.scale_p, 1.0f, s);
 #pragma unroll
       for (int i = 0; i < FC; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float unscale_c = 1.0f / s[i][e];
+          const int up_c = exponent_of(s[i][e]);
 #pragma unroll
-          for (int j = 0; j < FR; ++j) t.acc[i][j][e] = t.acc[i][j][e] * unscale_c * unscale[j];
+          for (int j = 0; j < FR; ++j)
+            t.acc[i][j][e] = __builtin_amdgcn_ldexpf(t.acc[i][j][e], -(up_c + up[j]));
         }
     }
     if (!a.bias && t.at.col0 + TC <= cols) return;
@@ -592,20 +598,21 @@ struct ProductArgs {
   int64_t ld;
   int32_t dtype;
   float alpha;
-  const float *scale;  // nullable: divides alpha
-  const float *tops;   // float32: the maxima behind the turned operand's scale, which divides it too
+  const float *scale;  // nullable: G's, which is divided out
+  const float *tops;   // float32: the maxima behind the turned operand's scale, likewise
   OutMask mask;
 };
-__device__ __forceinline__ float alpha_of(float alpha, const float *scale, const float *tops) {
-  if (scale) alpha /= *scale;
+// The exponent of both scales.
+__device__ __forceinline__ int ups_of(const float *scale, const float *tops) {
+  int up = scale ? exponent_of(*scale) : 0;
   if (tops) {
     float top = 0.0f;
     for (int i = threadIdx.x & 63; i < kMaxBlocks; i += 64) top = fmaxf(top, tops[i]);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-    alpha /= scale_for(top);
+    up += exponent_of(scale_for(top));
   }
-  return alpha;
+  return up;
 }
 
 __device__ __forceinline__ void put_typed(void *out, int32_t dtype, int64_t at, int64_t col,
@@ -615,9 +622,9 @@ __device__ __forceinline__ void put_typed(void *out, int32_t dtype, int64_t at, 
   else put_four<bf16_t>(static_cast<bf16_t *>(out) + at, col, cols, v);
 }
 
-// The tile's sums times alpha, to rows of T.
+// The tile's sums times alpha 2^-up, to rows of T.
 template <typename T, bool FULL, class Tile>
-__device__ __forceinline__ void product_out(Tile &t, T *out, int64_t ld, float alpha,
+__device__ __forceinline__ void product_out(Tile &t, T *out, int64_t ld, float alpha, int up,
                                             const OutMask &mask) {
   const int64_t rows = t.a.q.rows, cols = t.a.p.rows;
 #pragma unroll
@@ -629,7 +636,7 @@ __device__ __forceinline__ void product_out(Tile &t, T *out, int64_t ld, float a
     for (int i = 0; i < Tile::kFragC; ++i) {
       float v[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : t.acc[i][j][e] * alpha;
+      for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : __builtin_amdgcn_ldexpf(t.acc[i][j][e] * alpha, -up);
       w[i] = quad_of<T>(v);
     }
     t.template store<T, FULL, false>(j, w, out, ld, rows, cols);
@@ -640,7 +647,7 @@ template <class Op, bool QT, int TC, int TR, int WC, int WR>
 __device__ __forceinline__ void product_tiles(const ProductArgs &a, uint32_t first, uint8_t *lds) {
   using Tile = GemmTile<Op, TC, TR, WC, WR, QT>;
   Tile t(a.g, lds);
-  const float alpha = alpha_of(a.alpha, a.scale, a.tops);
+  const int up = ups_of(a.scale, a.tops);
   using Type = typename Op::Type;  // the rows' own: that of the products
   const auto start = [&] {
     if (a.before && t.at.z < 0) t.start(a.before, a.g.q.rows, a.g.p.rows);
@@ -650,10 +657,10 @@ __device__ __forceinline__ void product_tiles(const ProductArgs &a, uint32_t fir
     constexpr bool FULL = whole.value;
     if (t.at.z >= 0)
       product_out<float, FULL>(t, a.part + t.at.z * a.stride - a.tail_row * a.g.p.rows, a.g.p.rows,
-                               1.0f, {});
+                               1.0f, 0, {});
     else if (a.dtype == SPS_F32)
-      product_out<float, FULL>(t, static_cast<float *>(a.out), a.ld, alpha, a.mask);
-    else product_out<Type, FULL>(t, static_cast<Type *>(a.out), a.ld, alpha, a.mask);
+      product_out<float, FULL>(t, static_cast<float *>(a.out), a.ld, a.alpha, up, a.mask);
+    else product_out<Type, FULL>(t, static_cast<Type *>(a.out), a.ld, a.alpha, up, a.mask);
   };
   const auto put = [&] {
     const bool whole = t.full();
@@ -706,7 +713,7 @@ __global__ __launch_bounds__(256) void ce_join_kernel(JoinBoth both) {
   const uint32_t block = second ? blockIdx.x - both.blocks[0] : blockIdx.x;
   const uint32_t blocks = second ? both.blocks[1] : both.blocks[0];
   const int64_t per = (a.cols + 3) / 4, all = a.rows * per;
-  const float alpha = alpha_of(a.alpha, a.scale, a.tops);
+  const int up = ups_of(a.scale, a.tops);
   for (int64_t i = (int64_t)block * 256 + threadIdx.x; i < all; i += (int64_t)blocks * 256) {
     const int64_t r = i / per, c = (i - r * per) * 4;
     float v[4] = {};
@@ -728,7 +735,7 @@ __global__ __launch_bounds__(256) void ce_join_kernel(JoinBoth both) {
     }
     const bool zero = a.mask.out(a.first + r);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : v[e] * alpha;
+    for (int e = 0; e < 4; ++e) v[e] = zero ? 0.0f : __builtin_amdgcn_ldexpf(v[e] * a.alpha, -up);
     put_typed(a.out, a.dtype, (a.first + r) * a.ld, c, a.cols, v);
   }
 }

@@ -295,6 +295,17 @@ def test_float32_scales(env):
         check(env, got, x, w, t, 0.1, b, ww)
 
 
+@pytest.mark.parametrize("ex,ew", [(-112, 114), (114, -112), (-60, 60), (100, -100)])
+def test_float32_rows_near_the_range_s_ends(env, ex, ew):
+    """Sums that leave the range when one side's scale is taken out, logits that do not."""
+    torch, sps, dev = env
+    x, w, t, b, ww = make(env, 70, 300, 40, "float32", 9)
+    x, w = x * 2.0 ** ex, w * 2.0 ** ew
+    got = sps.dense_cross_entropy(x, w, t, 0.3, b, ww)
+    assert got[0].isfinite().all() and got[1].isfinite().all() and got[2].isfinite().all()
+    check(env, got, x, w, t, 0.3, b, ww)
+
+
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("scale", [1e-6, 65536.0])
 def test_scaled_losses(env, dtype, scale):
