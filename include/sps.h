@@ -624,7 +624,8 @@ sps_status sps_quantize_rows(const sps_scores *x, int8_t *values, int64_t ld, fl
 
 /* The values that 8-bit rows stand for (asynchronous): out[r * ld_out + d] =
  * values[r][d] * scales[r], to half a step of dtype (16-bit types: and half a
- * step of float32, which the product may be rounded to before). */
+ * step of float32, which the product may be rounded to before). out shares no
+ * byte with the 8-bit rows (SPS_ERR_INVALID_ARGUMENT). */
 sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype, int64_t ld_out,
                                void *stream);
 
@@ -656,8 +657,8 @@ sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *it
  * whatever its row holds; a row whose target is struck out has loss +inf and
  * G[r] without the target's term; a row without any item left has loss 0 and gradient 0.
  * bias is a constant (masks, sampling corrections) and gets no gradient.
- * Otherwise NaN and infinities of a row that takes part make its own loss and
- * gradient NaN, and those of the other side's rows that it reaches.
+ * Otherwise NaN and infinities of a row that takes part may make NaN of its own
+ * loss and gradient, and of all that its products enter.
  * Products of 16-bit rows are exact and summed in float32; float32 rows are
  * multiplied with 22 bits of each value (fewer below 2^-18 of the largest of
  * its row, for the gradients of the whole matrix: an absolute 2^-40 of that);
@@ -682,9 +683,9 @@ sps_status sps_dense_ce_workspace_size(const sps_scores *queries, const sps_scor
  * values). targets: DEVICE int32[n_query]. bias (nullable): DEVICE
  * float[n_item]. temperature: 1e-6 to 1e6. row_weights (nullable: 1): DEVICE
  * float[n_query], the gradient of what is minimised about each loss. loss:
- * DEVICE float[n_query]. grad_queries, grad_items (each nullable: not
- * computed): of the rows' type or SPS_F32, sharing no byte with the rows or
- * each other. workspace: DEVICE, 256-byte aligned, free again once the stream
+ * DEVICE float[n_query], sharing no byte with any other argument.
+ * grad_queries, grad_items (each nullable: not computed): of the rows' type or
+ * SPS_F32, sharing no byte with the rows or each other. workspace: DEVICE, 256-byte aligned, free again once the stream
  * work has completed. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,
  * SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW, SPS_ERR_UNSUPPORTED. */
 sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, const int32_t *targets,

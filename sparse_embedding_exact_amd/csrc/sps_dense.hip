@@ -1045,6 +1045,16 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
   if (grad_queries && grad_items &&
       sps::rows_overlap({grad_queries, n, d * sg, ld_queries * sg}, {grad_items, m, d * sg, ld_items * sg}))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the gradients overlap", what);
+  const int64_t sx = sps::dtype_size(queries->dtype);
+  const sps::RowBytes losses{loss, 1, n * 4, n * 4};
+  if (loss && (sps::rows_overlap(losses, {queries->data, n, d * sx, queries->ld * sx}) ||
+               sps::rows_overlap(losses, {items->data, m, d * sx, items->ld * sx}) ||
+               sps::rows_overlap(losses, {targets, 1, n * 4, n * 4}) ||
+               (bias && sps::rows_overlap(losses, {bias, 1, m * 4, m * 4})) ||
+               (row_weights && sps::rows_overlap(losses, {row_weights, 1, n * 4, n * 4})) ||
+               (grad_queries && sps::rows_overlap(losses, {grad_queries, n, d * sg, ld_queries * sg})) ||
+               (grad_items && sps::rows_overlap(losses, {grad_items, m, d * sg, ld_items * sg}))))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the losses overlap other arguments", what);
   if (!(temperature >= 1e-6f && temperature <= 1e6f))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: temperature must be in [1e-6, 1e6]", what);
   if (n > 0 && (!targets || !loss))

@@ -359,9 +359,12 @@ sps_status sps_quantize_rows(const sps_scores *x, int8_t *values, int64_t ld, fl
   if (st != SPS_OK) return st;
   if (x->n_rows == 0) return SPS_OK;
   const int64_t size = sps::dtype_size(x->dtype);
-  if (sps::rows_overlap({x->data, x->n_rows, x->n_cols * size, x->ld * size},
-                        {values, x->n_rows, (x->n_cols + 15) & ~15ll, ld}))
-    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the integers overlap the rows", what);
+  const sps::RowBytes rows{x->data, x->n_rows, x->n_cols * size, x->ld * size};
+  const sps::RowBytes integers{values, x->n_rows, (x->n_cols + 15) & ~15ll, ld};
+  const sps::RowBytes of_scales{scales, 1, x->n_rows * 4, x->n_rows * 4};
+  if (sps::rows_overlap(rows, integers) || sps::rows_overlap(rows, of_scales) ||
+      sps::rows_overlap(integers, of_scales))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: rows, integers and scales overlap", what);
   sps::QuantArgs a{x->data, x->ld, x->n_rows, x->n_cols, values, ld, scales};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (x->dtype == SPS_F32) launch_lanes<float, Quantize>(a, s);
@@ -381,9 +384,10 @@ sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype,
   if (st != SPS_OK) return st;
   if (x->n_rows == 0) return SPS_OK;
   const int64_t size = sps::dtype_size(dtype);
-  if (sps::rows_overlap({out, x->n_rows, x->dim * size, ld_out * size},
-                        {x->values, x->n_rows, (x->dim + 15) & ~15ll, x->ld}))
-    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the output overlaps the integers", what);
+  const sps::RowBytes o{out, x->n_rows, x->dim * size, ld_out * size};
+  if (sps::rows_overlap(o, {x->values, x->n_rows, (x->dim + 15) & ~15ll, x->ld}) ||
+      sps::rows_overlap(o, {x->scales, 1, x->n_rows * 4, x->n_rows * 4}))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the output overlaps the 8-bit rows", what);
   sps::DequantArgs a{x->values, x->ld, x->scales, x->n_rows, x->dim, out, ld_out};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SPS_F32) launch_lanes<float, Dequantize>(a, s);

@@ -67,12 +67,17 @@ def test_int8_refusals(lib):
     # integers in the rows themselves
     assert lib.sps_quantize_rows(view(), P + 16, 112, 3 * P, None) == INV
     assert b"overlap" in lib.sps_last_error_message()
+    # scales in the rows, or in the integers
+    assert lib.sps_quantize_rows(view(), 2 * P, 112, P + 16, None) == INV
+    assert lib.sps_quantize_rows(view(), 2 * P, 112, 2 * P + 16, None) == INV
+    assert b"overlap" in lib.sps_last_error_message()
     assert lib.sps_quantize_rows(view(rows=2**30, ld=100), 2**50, 112, 3 * P, None) == OVF
     assert lib.sps_dequantize_rows(None, P, 0, 100, None) == INV
     assert lib.sps_dequantize_rows(rows8(), P, 3, 100, None) == INV
     assert lib.sps_dequantize_rows(rows8(), P, 0, 99, None) == INV
     assert lib.sps_dequantize_rows(rows8(), None, 0, 100, None) == INV
     assert lib.sps_dequantize_rows(rows8(), 2 * P + 16, 0, 100, None) == INV
+    assert lib.sps_dequantize_rows(rows8(), 3 * P, 0, 100, None) == INV
     assert lib.sps_int8_scores(None, rows8(), P, 0, 8, None) == INV
     assert lib.sps_int8_scores(rows8(), None, P, 0, 8, None) == INV
     assert lib.sps_int8_scores(rows8(), rows8(dim=99), P, 0, 8, None) == DIM
@@ -115,6 +120,9 @@ def test_cross_entropy_refusals(lib):
     for at in (P, P + 8 * 400 - 4, 2 * P + 4):  # gradients in the rows
         assert ce(lib, gq=at) == INV and ce(lib, gi=at) == INV
     assert ce(lib, gq=7 * P + 8) == INV  # and in each other
+    for at in (P + 4, 2 * P + 4, 4 * P, 6 * P + 8, 7 * P + 8, 9 * P + 28, 10 * P):  # losses in anything
+        assert ce(lib, loss=at, bias=9 * P, weights=10 * P) == INV
+        assert b"losses" in lib.sps_last_error_message()
     assert ce(lib, q=view(cols=70000, ld=70000), i=view(cols=70000, ld=70000), gq=None, gi=None) == UNS
     assert ce(lib, i=view(rows=4000001), gq=None, gi=None) == UNS
     assert ce(lib, q=view(rows=4000001), gq=None, gi=None) == UNS
