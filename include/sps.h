@@ -671,7 +671,7 @@ sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *it
 
 /* Bytes of the workspace of sps_dense_ce for these rows (their addresses and
  * ld matter, nothing is read), with either gradient or both. Pure host. It
- * grows with the rows and with a piece of the logits of at most about 1 GiB
+ * grows with the rows and with a piece of the logits of at most about 2 GiB
  * (or 256 queries). At most 4,000,000 queries and as many items, and 65536
  * dims (SPS_ERR_UNSUPPORTED). */
 sps_status sps_dense_ce_workspace_size(const sps_scores *queries, const sps_scores *items,

@@ -212,7 +212,7 @@ struct GemmTile {
   GemmPlace at;  // of the sums
   // of the loads, which are ahead of them
   uint8_t *base_p, *base_q;
-  int size_p, size_q, begin, end, at_step, seg;
+  int size_p, size_q, seg;
   int64_t col_q;
   uint32_t k;
   bool any;
@@ -247,7 +247,6 @@ struct GemmTile {
     return (int)(b < (int64_t)kMostBytes ? b : (int64_t)kMostBytes);
   }
   __device__ __forceinline__ void place_step(int step) {
-    at_step = step;
     seg = 0;
     if constexpr (Op::kPlanes > 1) {
       const int steps = (int)(((uint32_t)a.k_bytes + kStep - 1) / kStep);
@@ -263,7 +262,7 @@ struct GemmTile {
         base_p + (Op::kPlanes > 1 ? seg_p(seg) * a.p.plane : 0), 0, size_p, 0x00020000);
     const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
         base_q + (Op::kPlanes > 1 ? seg_q(seg) * a.q.plane : 0) + (QT ? (int64_t)(k / 2) * a.q.ld : 0),
-        0, QT ? left(a.k_rows, (int64_t)(k / 2), a.q.ld, col_q) : size_q, 0x00020000);
+        0, QT ? any ? left(a.k_rows, (int64_t)(k / 2), a.q.ld, col_q) : 0 : size_q, 0x00020000);
     // past the end of k: an offset past the buffer's, which reads zeros
     const bool in = any && k + chunk < (uint32_t)a.k_bytes;
     const uint32_t at_p = in ? off_p + k : 0x80000000u;
@@ -276,30 +275,21 @@ struct GemmTile {
     for (int i = 0; i < kLoadsQ; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_u8 *)(b + (TC + i * kRowsLoad) * kStep), 16,
                                                (int)(at_q + (uint32_t)i * kNextQ * ld_q), 0, 0, 0);
-    if (at_step + 1 == end) {
-      place_step(begin);
-    } else {
-      ++at_step;
-      k += kStep;
-      if (Op::kPlanes > 1 && k >= (uint32_t)a.k_bytes) {
-        k = 0;
-        ++seg;
-      }
+    k += kStep;
+    if (Op::kPlanes > 1 && k >= (uint32_t)a.k_bytes) {
+      k = 0;
+      ++seg;
     }
   }
-  // The first two steps of a tile's. Steps are taken from the turn-th on, round: rows whose length
-  // is a large power of two have equal steps in few of L2's channels, and neighbouring tiles would
-  // ask for them at once.
+  // The first two steps of a tile's.
   __device__ __forceinline__ void prefetch(const GemmPlace &next) {
     base_p = const_cast<uint8_t *>(a.p.base) + next.col0 * a.p.ld;
     base_q = const_cast<uint8_t *>(a.q.base) + (QT ? next.row0 * 2 : next.row0 * a.q.ld);
     size_p = left(a.p.rows, next.col0, a.p.ld);
     size_q = QT ? 0 : left(a.q.rows, next.row0, a.q.ld);
     col_q = next.row0 * 2;
-    begin = next.begin;
-    end = next.end;
-    const int many = end - begin;
-    place_step(begin + (int)(((uint32_t)(next.col0 / TC) * 2u) % (uint32_t)many));
+    const int many = next.end - next.begin;
+    place_step(next.begin);
     any = true;
     load(lds);
     any = many > 1;

@@ -95,7 +95,7 @@ def test_large_dims(env):
 def test_pieces(env, dtype):
     """More rows than a piece of the logits holds: the items' gradient is a sum over pieces."""
     torch, sps, dev = env
-    n, m, d = 600, 700001, 8
+    n, m, d = 600, 1700001, 8
     x, w, t, b, ww = make(env, n, m, d, dtype, 3)
     got = sps.dense_cross_entropy(x, w, t, 0.5, b, ww)
     # by parts of the rows that are a piece each: equal losses and rows, and sums that add up
