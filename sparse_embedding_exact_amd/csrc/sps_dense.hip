@@ -20,7 +20,11 @@
 // (each row for the logits, the matrix for the products with G, whose sums go
 // over rows), so that a value keeps 22 bits down to 2^-18 of the largest and
 // an absolute 2^-40 of it below; three products of planes leave out what is
-// below 2^-22 of a product.
+// below 2^-22 of a product. (Three planes of bf16 and six products of them:
+// 1000 x 30,522 x 384 605 us instead of 389.)
+// Bound by the three products: 8192 x 100,000 x 1024 bf16 takes 5.08 ms, of which
+// the logits 1.64 (1.02 PFLOP/s with codes stored), both other products 2.63
+// (1.28), codes to G 0.69, rows laid out 0.12.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -97,7 +101,8 @@ struct LayArgs {
 };
 constexpr int kMaxBlocks = 256;
 
-// float32: scales of rows and partial maxima, a wave a row; bound by memory.
+// float32: scales of rows and partial maxima, a wave for kMaxRowsOnce rows; bound
+// by memory: 31,522 rows of 384 in 14 us, 3.5 TB/s (a row at a time: 64).
 // What is not finite has no part in a scale.
 struct MaxBoth {
   LayArgs side[2];
@@ -147,7 +152,8 @@ __device__ __forceinline__ float turned_scale(const float *parts) {
 }
 
 // Tiles of 64 x 64 through LDS, 8 values a thread and step both ways; bound by
-// memory. Planes in elements.
+// memory (30,522 + 4095 rows of 768 in 16 bits turned: 28 us, 3.8 TB/s). Planes
+// in elements.
 template <typename T>
 struct __attribute__((packed, aligned(sizeof(T)))) Eight {
   T e[8];

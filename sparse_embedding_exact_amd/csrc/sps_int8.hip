@@ -208,7 +208,10 @@ __global__ __launch_bounds__(64 * WC * WR) void int8_scores_kernel(Int8Args a) {
 // Few queries (up to 16 NQ): bound by reading the items once. A wave takes 16
 // items at a time straight from memory into a matrix instruction's operand,
 // the queries lie in LDS in the order the instructions read them. 1 x 2M of 384
-// dims: 182 us, 4.3 TB/s.
+// dims: 152 us, 5.0 TB/s (the next items' loads behind the last products of
+// these: 183), 2 or 8 loads ahead 150 or 158, of 768 dims 283 or 276 instead of
+// 279, 1 x 500,000 of 200 dims 24 or 20 instead of 19.
+constexpr int kFewAhead = 4;
 template <typename T, int NQ>
 __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t few_lds[];
@@ -224,41 +227,57 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
   }
   __syncthreads();
   const int64_t groups = (a.g.p.rows + 15) / 16, stride = (int64_t)gridDim.x * 4;
-  for (int64_t g = (int64_t)blockIdx.x * 4 + wave; g < groups; g += stride) {
-    const int64_t item = g * 16 + (lane & 15);
-    const bool there = item < a.g.p.rows;
-    const uint8_t *const row = a.g.p.base + (there ? item : a.g.p.rows - 1) * a.g.p.ld;
-    const int64_t c0 = g * 16 + (lane >> 4) * 4;
-    i32x4 acc[NQ] = {};
-    constexpr int U = 4;  // loads of items in flight
-    for (int s = 0; s < steps; s += U) {
-      i32x4 p[U];
+  // kFewAhead loads of items at a time, and as many of what comes next, be it the next items', on
+  // their way while these are multiplied
+  i32x4 p[kFewAhead], next[kFewAhead];
+  const auto fetch = [&](int64_t g, int s, i32x4 (&to)[kFewAhead]) {
+    const int64_t item = g * 16 + (lane & 15), last = a.g.p.rows - 1;
+    const uint8_t *const row = a.g.p.base + (item < last ? item : last) * a.g.p.ld;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t k = (int64_t)(s + u) * 64 + (lane >> 4) * 16;
-        // past the row's end the queries are zeros: any finite bytes do
-        p[u] = *reinterpret_cast<const i32x4 *>(row + (k < a.g.k_bytes ? k : 0));
+    for (int u = 0; u < kFewAhead; ++u) {
+      const int64_t k = (int64_t)(s + u) * 64 + (lane >> 4) * 16;
+      // past the row's end the queries are zeros: any finite bytes do
+      if (s + u < steps) to[u] = *reinterpret_cast<const i32x4 *>(row + (k < a.g.k_bytes ? k : 0));
+    }
+  };
+  int64_t g = (int64_t)blockIdx.x * 4 + wave;
+  if (g >= groups) return;
+  i32x4 acc[NQ] = {};
+  int s = 0;
+  fetch(g, 0, p);
+  for (;;) {
+    const bool ends = s + kFewAhead >= steps;
+    const int64_t g_next = ends ? g + stride : g;
+    const int s_next = ends ? 0 : s + kFewAhead;
+    if (g_next < groups) fetch(g_next, s_next, next);
+#pragma unroll
+    for (int u = 0; u < kFewAhead; ++u)
+      if (s + u < steps)
+#pragma unroll
+        for (int f = 0; f < NQ; ++f) acc[f] = OpI8::mma(p[u], qs[((s + u) * NQ + f) * 64 + lane], acc[f]);
+    if (ends) {
+      const int64_t c0 = g * 16 + (lane >> 4) * 4;
+      float sp[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sp[e] = c0 + e < a.g.p.rows ? a.scale_p[c0 + e] : 0.0f;
+#pragma unroll
+      for (int f = 0; f < NQ; ++f) {
+        const int64_t r = f * 16 + (lane & 15);
+        if (r < a.g.q.rows) {
+          const float sq = a.scale_q[r];
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = score_of(acc[f][e], sq, sp[e]);
+          put_four<T>(static_cast<T *>(a.out) + r * a.ld, c0, a.g.p.rows, v);
+        }
+        acc[f] = i32x4{};
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u < steps)
-#pragma unroll
-          for (int f = 0; f < NQ; ++f)
-            acc[f] = OpI8::mma(p[u], qs[((s + u) * NQ + f) * 64 + lane], acc[f]);
+      if (g_next >= groups) break;
     }
-    float sp[4];
+    g = g_next;
+    s = s_next;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sp[e] = c0 + e < a.g.p.rows ? a.scale_p[c0 + e] : 0.0f;
-#pragma unroll
-    for (int f = 0; f < NQ; ++f) {
-      const int64_t r = f * 16 + (lane & 15);
-      if (r >= a.g.q.rows) continue;
-      const float sq = a.scale_q[r];
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = score_of(acc[f][e], sq, sp[e]);
-      put_four<T>(static_cast<T *>(a.out) + r * a.ld, c0, a.g.p.rows, v);
-    }
+    for (int u = 0; u < kFewAhead; ++u) p[u] = next[u];
   }
 }
 
@@ -338,7 +357,7 @@ void launch_tiles(const sps::TilePlan &plan, sps::Int8Args &a, hipStream_t s) {
 
 // Queries in LDS. Few queries read the items once, in the order they lie in; more have the tiles,
 // whose rows of scores are put together before they are stored. 384 dims, few against tiles: 1 x 2M
-// 182 against 240 us, 16 x 2M 214 against 241, 32 x 500,000 47 against 58, 64 x 500,000 89 against 64.
+// 152 against 240 us, 16 x 2M 196 against 241, 32 x 500,000 45 against 58, 64 x 500,000 89 against 63.
 constexpr int64_t kFewLds = 64 * 1024;
 
 template <typename T>

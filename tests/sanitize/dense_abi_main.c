@@ -57,9 +57,9 @@ static void sizing(void) {
           if (s == SPS_OK) CHECK(one <= both);
           /* no workspace: refused, or nothing to do (no rows: not called here) */
           if (s == SPS_OK && kSizes[i] > 0 && kSizes[j] > 0) {
-            CHECK(sps_dense_ce(&q, &m, at(0x1000), NULL, 1.0f, NULL, at(0x1000), NULL, 0, NULL, 0, t,
+            CHECK(sps_dense_ce(&q, &m, at(0x1000), NULL, 1.0f, NULL, at(1ull << 60), NULL, 0, NULL, 0, t,
                                NULL, 0, NULL) == SPS_ERR_INVALID_ARGUMENT);
-            CHECK(sps_dense_ce(&q, &m, at(0x1000), NULL, 1.0f, NULL, at(0x1000), NULL, 0, NULL, 0, t,
+            CHECK(sps_dense_ce(&q, &m, at(0x1000), NULL, 1.0f, NULL, at(1ull << 60), NULL, 0, NULL, 0, t,
                                at(0x100000), 255, NULL) == SPS_ERR_WORKSPACE_TOO_SMALL);
           }
         }
