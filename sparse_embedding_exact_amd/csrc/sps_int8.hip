@@ -229,7 +229,7 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
   const int64_t groups = (a.g.p.rows + 15) / 16, stride = (int64_t)gridDim.x * 4;
   // kFewAhead loads of items at a time, and as many of what comes next, be it the next items', on
   // their way while these are multiplied
-  i32x4 p[kFewAhead], next[kFewAhead];
+  i32x4 p[kFewAhead] = {}, next[kFewAhead] = {};
   const auto fetch = [&](int64_t g, int s, i32x4 (&to)[kFewAhead]) {
     const int64_t item = g * 16 + (lane & 15), last = a.g.p.rows - 1;
     const uint8_t *const row = a.g.p.base + (item < last ? item : last) * a.g.p.ld;
@@ -276,7 +276,6 @@ __global__ __launch_bounds__(256) void int8_few_kernel(Int8Args a) {
     }
     g = g_next;
     s = s_next;
-#pragma unroll
     for (int u = 0; u < kFewAhead; ++u) p[u] = next[u];
   }
 }
