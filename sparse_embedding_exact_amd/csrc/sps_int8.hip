@@ -12,6 +12,28 @@ namespace sps {
 // ---------------------------------------------------------------------------
 // rows to 8 bits
 
+// 16 bytes of values on any boundary of T, one load or store: as an array of
+// values (Vec) the compiler takes it in parts (500,000 x 200 bf16 97 us to 8
+// bits instead of 70, 100,000 x 1024 float32 133 us back instead of 96).
+typedef uint32_t u32x4_at2 __attribute__((ext_vector_type(4), aligned(2), may_alias));
+typedef uint32_t u32x4_at4 __attribute__((ext_vector_type(4), aligned(4), may_alias));
+template <typename T>
+using Sixteen = std::conditional_t<sizeof(T) == 4, u32x4_at4, u32x4_at2>;
+template <typename T>
+__device__ __forceinline__ u32x4 load16(const T *x) {
+  return *reinterpret_cast<const Sixteen<T> *>(x);
+}
+template <typename T>
+__device__ __forceinline__ void store16(T *x, u32x4 v) {
+  *reinterpret_cast<Sixteen<T> *>(x) = v;
+}
+template <typename T>
+__device__ __forceinline__ float value16(u32x4 v, int e) {
+  const uint32_t w = v[e * (int)sizeof(T) / 4];
+  if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w);
+  else return to_f32(__builtin_bit_cast(T, (uint16_t)(w >> (16 * (e & 1)))));
+}
+
 struct QuantArgs {
   const void *x;
   int64_t ld;  // elements
@@ -37,9 +59,10 @@ __device__ __forceinline__ int32_t nearest_int8(float x, float y, float amax) {
 
 // L lanes a row, so that most rows fit the four vectors that a lane keeps in
 // registers between the maximum and the integers and few lanes are left over;
-// what does not fit is read again (from the caches). Bound by memory: 500,000 x
-// 333 float32 in 173 us, 4.8 TB/s (64 lanes for every row: 224), 100,000 x 96
-// fp16 in 10.4 (34.9).
+// what does not fit is read again (from the caches). 500,000 x 333 float32 in 166
+// us, 5.0 TB/s, bound by memory; bf16 in 139, 3.6 TB/s, by its instructions, a
+// wave's 4 cycles each (two vectors a lane: 182, eight spill: 275; 64 lanes for
+// every row, before: 230 instead of 144).
 constexpr int kQuantKeep = 4;
 template <typename T, int L>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
@@ -51,21 +74,24 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   const int dim = (int)a.dim, whole = dim / V;  // whole vectors; the rest of the row is one short one
   const int tail = dim - whole * V, vecs = whole + (tail > 0);
   const auto fetch = [&](int v) {
-    Vec<T> t{};
-    if (v < whole) t = *reinterpret_cast<const Vec<T> *>(x + v * V);
+    u32x4 t{};
+    if (v < whole) t = load16(x + v * V);
     else if (v == whole) {
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        if (e < tail) t.e[e] = x[v * V + e];
+        if (e < tail) {
+          if constexpr (sizeof(T) == 4) t[e] = __builtin_bit_cast(uint32_t, x[v * V + e]);
+          else t[e / 2] |= (uint32_t)x[v * V + e].u << (16 * (e & 1));
+        }
     }
     return t;
   };
-  Vec<T> keep[kQuantKeep] = {};
+  u32x4 keep[kQuantKeep] = {};
   uint32_t top = 0;  // bits of magnitudes: their order, NaN above infinity
-  const auto see = [&](const Vec<T> &t) {
+  const auto see = [&](u32x4 t) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const uint32_t b = __builtin_bit_cast(uint32_t, to_f32(t.e[e])) & 0x7fffffffu;
+      const uint32_t b = __builtin_bit_cast(uint32_t, value16<T>(t, e)) & 0x7fffffffu;
       top = b > top ? b : top;
     }
   };
@@ -89,7 +115,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   const float inv = finite && top ? 127.0f / (amax * up) : 0.0f;
   int8_t *const q = a.q + r * a.ld_q;
   const int room = (dim + 15) & ~15;  // up to there the row is filled with zeros
-  const auto put = [&](int v, const Vec<T> &t) {
+  const auto put = [&](int v, u32x4 t) {
     if (v * V >= room) return;
     uint32_t w[V / 4];
 #pragma unroll
@@ -97,7 +123,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
       w[j] = 0;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float f = to_f32(t.e[4 * j + e]);
+        const float f = value16<T>(t, 4 * j + e);
         const int32_t k = inv > 0.0f ? nearest_int8(f, f * up * inv, amax) : 0;
         w[j] |= (uint32_t)(k & 255) << (8 * e);
       }
@@ -120,10 +146,12 @@ struct DequantArgs {
   int64_t ld;  // elements
 };
 
-// L lanes a row, 16 bytes of values a lane and step: nothing is kept, so a row
-// has as many lanes as vectors, up to 64. Bound by memory: 500,000 x 333 float32
-// in 218 us, 3.8 TB/s (rows off their 16-byte boundaries; a lane for four
-// vectors: 256, rows as one run of vectors: 258), 100,000 x 1024 in 132, 3.9 TB/s.
+// L lanes a row, 16 bytes of values a lane and step, kDequantAhead steps' bytes
+// loaded together. Bound by memory: 100,000 x 1024 float32 in 88 us, 5.8 TB/s,
+// 500,000 x 333 in 217, 3.8 TB/s (rows off their 16-byte boundaries; with lanes
+// that start on them 250), bf16 in 108, 4.6 TB/s. One step at a time: 96, 227 and
+// 135 us, four: 86, 216 and 109, a lane a vector: 88, 217 and 138.
+constexpr int kDequantAhead = 2;
 template <typename T, int L>
 __global__ __launch_bounds__(256) void dequantize_rows_kernel(DequantArgs a) {
   constexpr int V = kVec<T>;
@@ -133,19 +161,33 @@ __global__ __launch_bounds__(256) void dequantize_rows_kernel(DequantArgs a) {
   const int8_t *const q = a.q + r * a.ld_q;
   const float s = a.scales[r];
   T *const out = static_cast<T *>(a.out) + r * a.ld;
-#pragma unroll 4
-  for (int c = (int)(threadIdx.x % L) * V; c < dim; c += L * V) {
-    int8_t w[V];  // the row's bytes reach to the next multiple of 16
-    __builtin_memcpy(w, __builtin_assume_aligned(q + c, V), V);
-    Vec<T> t;
+  typedef int8_t Bytes __attribute__((ext_vector_type(V)));
+  const auto put = [&](int c, Bytes w) {
+    T t[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) t.e[e] = from_f32<T>((float)w[e] * s);
-    if (c + V <= dim) *reinterpret_cast<Vec<T> *>(out + c) = t;
-    else {
+    for (int e = 0; e < V; ++e) t[e] = from_f32<T>((float)w[e] * s);
+    if (c + V <= dim) {
+      u32x4 v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) v[j] = __builtin_bit_cast(uint32_t, t[j]);
+        else v[j] = (uint32_t)t[2 * j].u | (uint32_t)t[2 * j + 1].u << 16;
+      }
+      store16(out + c, v);
+    } else {
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        if (c + e < dim) out[c + e] = t.e[e];
+        if (c + e < dim) out[c + e] = t[e];
     }
+  };
+  for (int c = (int)(threadIdx.x % L) * V; c < dim; c += kDequantAhead * L * V) {
+    Bytes w[kDequantAhead];  // the row's bytes reach to the next multiple of 16
+#pragma unroll
+    for (int i = 0; i < kDequantAhead; ++i)
+      if (c + i * L * V < dim) w[i] = *reinterpret_cast<const Bytes *>(q + c + i * L * V);
+#pragma unroll
+    for (int i = 0; i < kDequantAhead; ++i)
+      if (c + i * L * V < dim) put(c + i * L * V, w[i]);
   }
 }
 
@@ -416,9 +458,9 @@ sps_status sps_dequantize_rows(const sps_int8_rows *x, void *out, int32_t dtype,
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the output overlaps the 8-bit rows", what);
   sps::DequantArgs a{x->values, x->ld, x->scales, x->n_rows, x->dim, out, ld_out};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == SPS_F32) launch_lanes<float, Dequantize>(a, 1, s);
-  else if (dtype == SPS_F16) launch_lanes<sps::f16_t, Dequantize>(a, 1, s);
-  else launch_lanes<sps::bf16_t, Dequantize>(a, 1, s);
+  if (dtype == SPS_F32) launch_lanes<float, Dequantize>(a, sps::kDequantAhead, s);
+  else if (dtype == SPS_F16) launch_lanes<sps::f16_t, Dequantize>(a, sps::kDequantAhead, s);
+  else launch_lanes<sps::bf16_t, Dequantize>(a, sps::kDequantAhead, s);
   return sps::launch_status(what);
 }
 
