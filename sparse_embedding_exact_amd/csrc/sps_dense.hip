@@ -300,15 +300,17 @@ struct CodeF32 {
 
 struct LogitArgs {
   GemmArgs g;         // q: the piece's queries, p: items
-  float c, c_low;     // log2(e) / tau in two parts: everything is in powers of two
+  // Logits stand as the sums themselves, or with a bias as powers of two: c (log2(e) / tau in two
+  // parts) takes the sums, or their differences, to powers of two.
+  float c, c_low;
   const float *bias;  // nullable
   const float *scale_q, *scale_p;  // float32: those of the packed rows
   const int32_t *targets;
   void *code;  // nullable: uint16 (float32: float) [rows][ld]
   int64_t ld;
-  float2 *stats;  // [rows][blocks]: of a block of columns (max, sum of 2^(z - max))
+  float2 *stats;  // [rows][blocks]: of a block of columns (max of z, sum of 2^(c (z - max)))
   int64_t blocks;
-  float2 *z_target;  // and what its rounding left
+  float *z_target;
 };
 
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -325,18 +327,11 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   const int wave_col = t.wc * (TC / WC);
   // float32: the factor's second part, so that its rounding does not change the temperature
   constexpr bool kLow = sizeof(Word) == 4;
-  float c, c_low;
   int32_t target[FR];
   int up[FR];  // float32: exponents of the rows' scales
-  const auto times = [&](float x, float y) {
-    // (where the sums are logits already, c_low is 0 and they may be -inf)
-    return __builtin_fmaf(x, c, kLow && c_low != 0.0f ? __builtin_fmaf(x, c_low, y) : y);
-  };
+  // With a bias the logits are powers of two already.
+  const float c = a.bias ? 1.0f : a.c;
   const auto take = [&] {
-    // The logits are c times the sums, and where there is a bias or an edge, what is put in their
-    // place here.
-    c = a.c;
-    c_low = kLow ? a.c_low : 0.0f;
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
       const int64_t r = t.at.row0 + t.row_of(j);
@@ -370,15 +365,16 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) b[i][e] = t.at.col0 + t.col_of(i) + e < cols ? 0.0f : -kInf;
     }
+    const float f = a.bias ? a.c : 1.0f, f_low = kLow && a.bias ? a.c_low : 0.0f;
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int j = 0; j < FR; ++j)  // a column that is struck out has no logit, whatever its item holds
-          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : times(t.acc[i][j][e], b[i][e]);
-    c = 1.0f;
-    c_low = 0.0f;
+        for (int j = 0; j < FR; ++j) {  // a column that is struck out has no logit, whatever its item holds
+          const float y = kLow && f_low != 0.0f ? __builtin_fmaf(t.acc[i][j][e], f_low, b[i][e]) : b[i][e];
+          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], f, y);
+        }
   };
   const auto put_all = [&](auto whole) {
     const int64_t block = (t.at.col0 + wave_col) / (TC / WC);
@@ -391,7 +387,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = fmaxf(top, t.acc[i][j][e]);
       top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64)) * c;
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
       // the target's logit, where it is one of this wave's columns
       const int first = (int)(target[j] - t.at.col0);
       if (r < rows && (uint32_t)(first - wave_col) < (uint32_t)(TC / WC)) {
@@ -399,12 +395,9 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
         for (int i = 0; i < FC; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (first == t.col_of(i) + e) {
-              const float z = t.acc[i][j][e] * c;
-              a.z_target[r] = {z, fabsf(z) < kInf ? times(t.acc[i][j][e], -z) : 0.0f};
-            }
+            if (first == t.col_of(i) + e) a.z_target[r] = t.acc[i][j][e];
       }
-      const float base = (float)Code::kShift - (top == -kInf ? 0.0f : top);
+      const float base = top == -kInf ? 0.0f : top;
       float sum = 0.0f;
       typename QuadOf<Word>::Bits w[FC];
 #pragma unroll
@@ -412,7 +405,9 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(times(t.acc[i][j][e], base));
+          // The difference to the largest first, 0 there and exact near by however large both are; then
+          // the shift. (c's second part would be a part of this rounding.)
+          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e] - base, c, (float)Code::kShift));
           sum += p[e];
         }
         if constexpr (sizeof(Word) == 2) w[i] = {Code::two(p[0], p[1]), Code::two(p[2], p[3])};
@@ -443,7 +438,8 @@ struct GradArgs {
   const float2 *stats;
   int64_t rows, cols;
   int32_t blocks, block;  // their number and columns
-  const float2 *z_target;
+  const float *z_target;
+  double unit;  // a difference of logits times unit is one of powers of two
   const float *weights;  // nullable
   const int32_t *targets;
   const float *scale;  // nullable: 1
@@ -455,43 +451,44 @@ struct GradArgs {
   float *factor;  // [rows]: 0 where a row has no gradient
 };
 
-// Sums beyond a block in float64.
+// Sums beyond a block in float64, as are differences of maxima, whose size does not matter so.
 struct Running {
   float top;
   double sum;
-  __device__ __forceinline__ void join(float t, double s) {
+  __device__ __forceinline__ void join(float t, double s, double unit) {
     const float m = fmaxf(top, t);
     if (m == -__builtin_inff()) sum += s;  // 0, or NaN
     else
-      sum = sum * (double)__builtin_amdgcn_exp2f(top - m) + s * (double)__builtin_amdgcn_exp2f(t - m);
+      sum = sum * (double)__builtin_amdgcn_exp2f((float)(((double)top - (double)m) * unit)) +
+            s * (double)__builtin_amdgcn_exp2f((float)(((double)t - (double)m) * unit));
     top = m;
   }
 };
 template <int LANES>
-__device__ __forceinline__ Running run_row(const float2 *stats, int32_t blocks, int lane, int step) {
+__device__ __forceinline__ Running run_row(const float2 *stats, int32_t blocks, int lane, int step,
+                                           double unit) {
   Running x{-__builtin_inff(), 0.0};
   for (int32_t b = lane; b < blocks; b += step) {
     const float2 s = stats[b];
-    x.join(s.x, (double)s.y);
+    x.join(s.x, (double)s.y, unit);
   }
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) {
     const float t = __shfl_xor(x.top, o, 64);
     const double s = __shfl_xor(x.sum, o, 64);
-    x.join(t, s);
+    x.join(t, s, unit);
   }
   return x;
 }
 // The loss of a row, and whether it has one: its target is a column and some
-// column is left.
+// column is left (its largest logit adds 1 to the sum, or NaN).
 __device__ __forceinline__ bool loss_of(const GradArgs &a, int64_t r, const Running &x, double *loss) {
   const int32_t t = a.targets[r];
   if (t < 0 || t >= a.cols || x.sum == 0.0) {
     *loss = 0.0;
     return false;
   }
-  const float2 z = a.z_target[r];
-  *loss = (((double)x.top - (double)z.x) - (double)z.y + log2(x.sum)) * 0.69314718055994530942;
+  *loss = (((double)x.top - (double)a.z_target[r]) * a.unit + log2(x.sum)) * 0.69314718055994530942;
   return true;
 }
 
@@ -499,7 +496,7 @@ __device__ __forceinline__ bool loss_of(const GradArgs &a, int64_t r, const Runn
 __global__ __launch_bounds__(256) void ce_loss_kernel(GradArgs a) {
   const int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   const int lane = threadIdx.x & 15;
-  const Running x = run_row<16>(a.stats + (r < a.rows ? r : 0) * a.blocks, a.blocks, lane, 16);
+  const Running x = run_row<16>(a.stats + (r < a.rows ? r : 0) * a.blocks, a.blocks, lane, 16, a.unit);
   if (r >= a.rows || lane != 0) return;
   double loss;
   loss_of(a, r, x, &loss);
@@ -526,11 +523,11 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
   if (threadIdx.x < vecs) ahead = fetch(threadIdx.x);
 
   const float2 *const stats = a.stats + r * a.blocks;
-  const Running mine = run_row<64>(stats, a.blocks, threadIdx.x, 256);
+  const Running mine = run_row<64>(stats, a.blocks, threadIdx.x, 256, a.unit);
   if ((threadIdx.x & 63) == 0) parts[threadIdx.x >> 6] = mine;
   __syncthreads();
   Running x = parts[0];
-  for (int i = 1; i < 4; ++i) x.join(parts[i].top, parts[i].sum);
+  for (int i = 1; i < 4; ++i) x.join(parts[i].top, parts[i].sum, a.unit);
   double loss;
   const bool takes = loss_of(a, r, x, &loss);
   const float factor =
@@ -539,7 +536,7 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
     a.loss[r] = (float)loss;
     a.factor[r] = factor;
   }
-  const double lse2 = (double)x.top + log2(x.sum) + (double)Code::kShift;
+  const double top = (double)x.top, rest = log2(x.sum) + (double)Code::kShift;
   const float at_target = takes ? (float)expm1(-loss) * factor : 0.0f;
   const int32_t target = a.targets[r];
 
@@ -548,7 +545,8 @@ __global__ __launch_bounds__(256) void ce_grad_kernel(GradArgs a) {
     uint16_t o[NP][8] = {};
     if (factor != 0.0f) {
       const float f = col < a.cols
-                          ? __builtin_amdgcn_exp2f((float)((double)stats[col / a.block].x - lse2)) *
+                          ? __builtin_amdgcn_exp2f(
+                                (float)(((double)stats[col / a.block].x - top) * a.unit - rest)) *
                                 factor
                           : 0.0f;
 #pragma unroll
@@ -873,7 +871,7 @@ Layout layout_of(const Shape &s) {
     L.rows_q = take(s.n * 4);
     L.rows_i = take(s.m * 4);
   }
-  L.z_target = take(s.piece * 8);
+  L.z_target = take(s.piece * 4);
   L.stats = take(s.blocks * s.piece * 8);
   if (s.pack_q) L.packed_q = take(s.n * packed_ld(s) * 2 * p);
   if (s.pack_i) L.packed_i = take(s.m * packed_ld(s) * 2 * p);
@@ -1142,7 +1140,7 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.ld = h.ld_g;
     a.stats = reinterpret_cast<float2 *>(ws + L.stats);
     a.blocks = h.blocks;
-    a.z_target = reinterpret_cast<float2 *>(ws + L.z_target);
+    a.z_target = reinterpret_cast<float *>(ws + L.z_target);
     // a last piece that is shorter: the same tiles, whose columns the statistics go by, but fewer
     sps::TilePlan plan = h.plan_l;
     plan.main_r = (int32_t)ceil_div(rows, plan.size());
@@ -1157,6 +1155,7 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     c.blocks = (int32_t)h.blocks;
     c.block = h.block;
     c.z_target = a.z_target;
+    c.unit = bias ? 1.0 : c2;
     c.weights = row_weights ? row_weights + r0 : nullptr;
     c.targets = a.targets;
     c.scale = scale;
