@@ -300,9 +300,10 @@ struct CodeF32 {
 
 struct LogitArgs {
   GemmArgs g;         // q: the piece's queries, p: items
-  // Logits stand as the sums themselves, or with a bias as powers of two: c (log2(e) / tau in two
-  // parts) takes the sums, or their differences, to powers of two.
-  float c, c_low;
+  // Logits stand as the sums themselves, or with a bias as f (1 / tau in two parts; else 1) times the
+  // sums and the bias as it is: scaled, one of the type's lowest value would be -inf. c (log2(e) / tau,
+  // or with a bias log2(e)) takes their differences to powers of two.
+  float c, f, f_low;
   const float *bias;  // nullable
   const float *scale_q, *scale_p;  // float32: those of the packed rows
   const int32_t *targets;
@@ -313,7 +314,7 @@ struct LogitArgs {
   float *z_target;
 };
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLog2e = 1.44269504088896340736;
 
 template <class Op, class Code, int TC, int TR, int WC, int WR>
 __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
@@ -329,8 +330,6 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
   constexpr bool kLow = sizeof(Word) == 4;
   int32_t target[FR];
   int up[FR];  // float32: exponents of the rows' scales
-  // With a bias the logits are powers of two already.
-  const float c = a.bias ? 1.0f : a.c;
   const auto take = [&] {
 #pragma unroll
     for (int j = 0; j < FR; ++j) {
@@ -355,25 +354,20 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
     float b[FC][4];
     if (a.bias) {
       t.of_columns(a.bias, -kInf, b);
-#pragma unroll
-      for (int i = 0; i < FC; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[i][e] *= kLog2e;
     } else {
 #pragma unroll
       for (int i = 0; i < FC; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) b[i][e] = t.at.col0 + t.col_of(i) + e < cols ? 0.0f : -kInf;
     }
-    const float f = a.bias ? a.c : 1.0f, f_low = kLow && a.bias ? a.c_low : 0.0f;
 #pragma unroll
     for (int i = 0; i < FC; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int j = 0; j < FR; ++j) {  // a column that is struck out has no logit, whatever its item holds
-          const float y = kLow && f_low != 0.0f ? __builtin_fmaf(t.acc[i][j][e], f_low, b[i][e]) : b[i][e];
-          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], f, y);
+          const float y = kLow && a.f_low != 0.0f ? __builtin_fmaf(t.acc[i][j][e], a.f_low, b[i][e]) : b[i][e];
+          t.acc[i][j][e] = b[i][e] == -kInf ? -kInf : __builtin_fmaf(t.acc[i][j][e], a.f, y);
         }
   };
   const auto put_all = [&](auto whole) {
@@ -406,8 +400,8 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // The difference to the largest first, 0 there and exact near by however large both are; then
-          // the shift. (c's second part would be a part of this rounding.)
-          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e] - base, c, (float)Code::kShift));
+          // the shift. (A second part of c would be a part of this rounding.)
+          p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e] - base, a.c, (float)Code::kShift));
           sum += p[e];
         }
         if constexpr (sizeof(Word) == 2) w[i] = {Code::two(p[0], p[1]), Code::two(p[2], p[3])};
@@ -1127,9 +1121,11 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     a.g.p = oi;
     a.g.k_bytes = k_logits;
     a.g.splits = 1;
-    const double c2 = 1.44269504088896340736 / (double)temperature;
-    a.c = (float)c2;
-    a.c_low = (float)(c2 - (double)a.c);
+    const double f = bias ? 1.0 / (double)temperature : 1.0;
+    const double unit = bias ? sps::kLog2e : sps::kLog2e / (double)temperature;
+    a.c = (float)unit;
+    a.f = (float)f;
+    a.f_low = (float)(f - (double)a.f);
     a.bias = bias;
     if (wide) {
       a.scale_q = both.side[0].row_scale + r0;
@@ -1155,7 +1151,7 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
     c.blocks = (int32_t)h.blocks;
     c.block = h.block;
     c.z_target = a.z_target;
-    c.unit = bias ? 1.0 : c2;
+    c.unit = unit;
     c.weights = row_weights ? row_weights + r0 : nullptr;
     c.targets = a.targets;
     c.scale = scale;

@@ -122,3 +122,59 @@ def test_logits_that_differ_by_little(env, dtype, m):  # noqa: F811
     got = sps.dense_cross_entropy(x, w, t, tau)
     assert 1 < got[0].median() < 30
     check_exact(env, got, x, w, t, tau)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("low", [-1.5e38, -3e38, float(np.finfo(np.float32).min)])
+def test_the_lowest_finite_masks(env, dtype, low):  # noqa: F811
+    """A finite bias strikes nothing out: some items, all of them, and targets that have it."""
+    torch, sps, dev = env
+    x, w, t, b, ww = make(env, 150, 700, 72, dtype, 4, masked=False)
+    some = torch.zeros(700, device=dev)
+    some[64:256] = low
+    some[3] = low
+    none = torch.where(some < 0, -float("inf"), some)
+    free = torch.where(some[t.long()] < 0, 5, t)
+    want = sps.dense_cross_entropy(x, w, free, 0.5, none, ww)
+    for g, v in zip(sps.dense_cross_entropy(x, w, free, 0.5, some, ww), want):
+        assert g.isfinite().all() and torch.equal(g, v)
+    # a target under the mask: the loss is its bias, the gradient that of a row that is all wrong
+    t[:] = 100
+    got = sps.dense_cross_entropy(x, w, t, 0.5, some, ww, grad_dtype=torch.float32)
+    assert torch.allclose(got[0], torch.full_like(got[0], -low), rtol=2.0 ** -22)
+    live = sps.dense_cross_entropy(x, w, t * 0 - 1, 0.5, some, ww, grad_dtype=torch.float32)
+    assert (live[2] == 0).all()
+    item = got[2][100].double()
+    exact = -(ww.double()[:, None] * x.double()).sum(0) / 0.5
+    size = (ww.double()[:, None] * x.double().abs()).sum(0) / 0.5
+    half = 2.0 ** -22 if dtype == "float32" else do.HALF[dtype]
+    assert ((item - exact).abs() <= size * (half + do.PLANES + 320 * do.U) + 2.0 ** -30).all()
+    # on every item (the products vanish beside it)
+    x = torch.zeros_like(x)
+    every = torch.full((700,), low, device=dev)
+    check_exact(env, sps.dense_cross_entropy(x, w, t, 1.0, every, ww), x, w, t, 1.0, ww)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_mask_and_products(env, dtype):  # noqa: F811
+    """-1e9 on every item and products of whole 64, which float32 holds beside it: the mask is taken
+    as it is, not rounded with a factor of the logarithm."""
+    torch, sps, dev = env
+    x, w = whole(env, (150, 16), 1, dtype, 1) * 16, whole(env, (300, 16), 1, dtype, 2) * 8
+    t = torch.arange(150, device=dev, dtype=torch.int32) * 2
+    for tau in (1.0, 2.0):
+        bias = torch.full((300,), -1e9, device=dev)
+        got = sps.dense_cross_entropy(x, w, t, tau, bias)
+        check_exact(env, got, x, w, t, tau)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_large_bias(env, dtype):  # noqa: F811
+    """The largest value on some items: they share the softmax."""
+    torch, sps, dev = env
+    w = whole(env, (300, 16), 2, dtype, 1)
+    x = torch.zeros(40, 16, device=dev, dtype=w.dtype)
+    bias = torch.zeros(300, device=dev)
+    bias[[7, 8, 290]] = torch.finfo(torch.float32).max
+    t = torch.full((40,), 8, device=dev, dtype=torch.int32)
+    check_exact(env, sps.dense_cross_entropy(x, w, t, 1.0, bias), x, w, t, 1.0, bias=bias)
