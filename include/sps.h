@@ -663,8 +663,11 @@ sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *it
  * multiplied with 22 bits of each value (fewer below 2^-18 of the largest of
  * its row, for the gradients of the whole matrix: an absolute 2^-40 of that);
  * statistics of the softmax are float32
- * within a block of columns and float64 beyond; G is rounded to the rows' type
- * (float32: to 22 bits) before its two products, whose float32 sums are
+ * within a block of columns and float64 beyond; exponentials of 16-bit rows are
+ * kept with 11 bits of mantissa (bf16: 10), down to 2^-30 (2^-29) of the largest
+ * of their block of 64 or 128 columns and to an absolute 2^-42 (2^-40) of it
+ * below; G is rounded to the rows' type (float32: to 22 bits) before its two
+ * products, also where grad_dtype is SPS_F32, and their float32 sums are
  * rounded once to grad_dtype. fp16 and float32: G is scaled by a power of two
  * so that the largest weight uses fp16's range; gradients of weights more than
  * about 2^24 below it lose precision. Bitwise reproducible. */

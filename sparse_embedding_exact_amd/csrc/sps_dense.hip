@@ -10,12 +10,13 @@
 //      G in place;
 //   3. two products with G: for the queries its k (items) lies in one run, for
 //      the items it is read turned.
-// Code: a 16-bit float below the block's maximum, with 3 or 2 bits more than
-// G keeps when it is rounded to enter the matrix instructions, so z is not
-// computed twice. G's own column at the
-// target is 1 - p from the loss, never p - 1 of a rounded p.
+// Code: a 16-bit float below the block's maximum, so that z is not computed
+// twice. It has a bit more than fp16's G and three more than bf16's, down to
+// 2^-30 (bf16: 2^-29) of the block's maximum, and runs out gradually below. G's
+// own column at the target is 1 - p from the loss, never p - 1 of a rounded p.
 // fp16: G is held 2^k times as large, 2^k the power of two that takes the
-// largest weight to [2^14, 2^15), so that p down to 2^-29 keeps all its bits.
+// largest weight to [2^14, 2^15), so that where p times its row's weight is down
+// to 2^-28 of that weight G keeps all its bits.
 // float32: operands and G stand in two planes of fp16, scaled by powers of two
 // (each row for the logits, the matrix for the products with G, whose sums go
 // over rows), so that a value keeps 22 bits down to 2^-18 of the largest and
@@ -267,7 +268,7 @@ __global__ __launch_bounds__(256) void lay_kernel(LayBoth both) {
 
 // How e^(z - max) is kept, in units of 2^-kShift, so that small ones stay
 // normal numbers.
-// bf16: as fp16 (an error of 2^-12 where G is rounded by 2^-9).
+// bf16: as fp16 (an error of 2^-11 where G is rounded by 2^-8).
 struct CodeBf16 {
   using Word = uint16_t;
   static constexpr int kShift = 15;
@@ -279,18 +280,20 @@ struct CodeBf16 {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
   }
 };
-// fp16: float32's own bits of p 2^-112 but the last 11: 4 bits of exponent, 12
-// of mantissa (an error of 2^-13 where G is rounded by 2^-12), running out
-// gradually below 2^-14.
+// fp16: as fp16 whose sign's bit is one more of mantissa, which is float32's own
+// bits of p 2^-96 but the last 12: 5 bits of exponent, 11 of mantissa (an error
+// of 2^-12 where G is rounded by 2^-11), running out gradually below 2^-30. (4
+// bits of exponent and 12 of mantissa ran out below 2^-14, so that items beside
+// one that is nearly certain lost their gradients.)
 struct CodeF16 {
   using Word = uint16_t;
   static constexpr int kShift = 0;
   static __device__ __forceinline__ uint32_t one(float p) {
-    return (__builtin_bit_cast(uint32_t, p * 0x1p-112f) + 0x400u) >> 11;
+    return (__builtin_bit_cast(uint32_t, p * 0x1p-96f) + 0x800u) >> 12;
   }
   static __device__ __forceinline__ uint32_t two(float a, float b) { return one(a) | one(b) << 16; }
   static __device__ __forceinline__ float value(uint32_t w) {
-    return __builtin_bit_cast(float, w << 11) * 0x1p112f;
+    return __builtin_bit_cast(float, w << 12) * 0x1p96f;
   }
 };
 struct CodeF32 {
