@@ -688,8 +688,9 @@ sps_status sps_dense_ce_workspace_size(const sps_scores *queries, const sps_scor
  * float[n_query], the gradient of what is minimised about each loss. loss:
  * DEVICE float[n_query], sharing no byte with any other argument.
  * grad_queries, grad_items (each nullable: not computed): of the rows' type or
- * SPS_F32, sharing no byte with the rows or each other. workspace: DEVICE, 256-byte aligned, free again once the stream
- * work has completed. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,
+ * SPS_F32, sharing no byte with any other argument. workspace: DEVICE, 256-byte
+ * aligned, sharing none of the bytes asked for with any other argument, free
+ * again once the stream work has completed. Errors: SPS_ERR_INVALID_ARGUMENT, SPS_ERR_DIM_MISMATCH,
  * SPS_ERR_WORKSPACE_TOO_SMALL, SPS_ERR_OVERFLOW, SPS_ERR_UNSUPPORTED. */
 sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, const int32_t *targets,
                         const float *bias, float temperature, const float *row_weights, float *loss,

@@ -1042,16 +1042,27 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
   if (grad_queries && grad_items &&
       sps::rows_overlap({grad_queries, n, d * sg, ld_queries * sg}, {grad_items, m, d * sg, ld_items * sg}))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the gradients overlap", what);
+  // what is written is so while the rest is still read, by a later piece of the rows at the latest
   const int64_t sx = sps::dtype_size(queries->dtype);
-  const sps::RowBytes losses{loss, 1, n * 4, n * 4};
-  if (loss && (sps::rows_overlap(losses, {queries->data, n, d * sx, queries->ld * sx}) ||
-               sps::rows_overlap(losses, {items->data, m, d * sx, items->ld * sx}) ||
-               sps::rows_overlap(losses, {targets, 1, n * 4, n * 4}) ||
-               (bias && sps::rows_overlap(losses, {bias, 1, m * 4, m * 4})) ||
-               (row_weights && sps::rows_overlap(losses, {row_weights, 1, n * 4, n * 4})) ||
-               (grad_queries && sps::rows_overlap(losses, {grad_queries, n, d * sg, ld_queries * sg})) ||
-               (grad_items && sps::rows_overlap(losses, {grad_items, m, d * sg, ld_items * sg}))))
+  const auto some = [](const void *at, sps::RowBytes b) { return at ? b : sps::RowBytes{}; };
+  const sps::RowBytes losses = some(loss, {loss, 1, n * 4, n * 4});
+  const sps::RowBytes grads[2] = {some(grad_queries, {grad_queries, n, d * sg, ld_queries * sg}),
+                                  some(grad_items, {grad_items, m, d * sg, ld_items * sg})};
+  const sps::RowBytes rows[2] = {{queries->data, n, d * sx, queries->ld * sx},
+                                 {items->data, m, d * sx, items->ld * sx}};
+  const sps::RowBytes lists[3] = {some(targets, {targets, 1, n * 4, n * 4}),
+                                  some(bias, {bias, 1, m * 4, m * 4}),
+                                  some(row_weights, {row_weights, 1, n * 4, n * 4})};
+  const auto in_any = [](const sps::RowBytes &x, const sps::RowBytes *of, int many) {
+    for (int k = 0; k < many; ++k)
+      if (sps::rows_overlap(x, of[k])) return true;
+    return false;
+  };
+  if (in_any(losses, rows, 2) || in_any(losses, lists, 3) || in_any(losses, grads, 2))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the losses overlap other arguments", what);
+  if (in_any(grads[0], lists, 3) || in_any(grads[1], lists, 3))
+    return set_error(SPS_ERR_INVALID_ARGUMENT,
+                     "%s: a gradient overlaps the targets, the bias or the weights", what);
   if (!(temperature >= 1e-6f && temperature <= 1e6f))
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: temperature must be in [1e-6, 1e6]", what);
   if (n > 0 && (!targets || !loss))
@@ -1071,6 +1082,9 @@ sps_status sps_dense_ce(const sps_scores *queries, const sps_scores *items, cons
                      workspace_bytes);
   if (reinterpret_cast<uintptr_t>(workspace) & 255)
     return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: workspace must be 256-byte aligned", what);
+  const sps::RowBytes used{workspace, 1, (int64_t)L.total, (int64_t)L.total};
+  if (in_any(used, rows, 2) || in_any(used, lists, 3) || in_any(used, grads, 2) || in_any(used, &losses, 1))
+    return set_error(SPS_ERR_INVALID_ARGUMENT, "%s: the workspace overlaps other arguments", what);
   uint8_t *const ws = static_cast<uint8_t *>(workspace);
   const int np = planes(h);
   const bool wide = np > 1, grad = h.gq || h.gi;
