@@ -659,18 +659,23 @@ sps_status sps_int8_scores(const sps_int8_rows *queries, const sps_int8_rows *it
  * bias is a constant (masks, sampling corrections) and gets no gradient.
  * Otherwise NaN and infinities of a row that takes part may make NaN of its own
  * loss and gradient, and of all that its products enter.
- * Products of 16-bit rows are exact and summed in float32; float32 rows are
- * multiplied with 22 bits of each value (fewer below 2^-18 of the largest of
- * its row, for the gradients of the whole matrix: an absolute 2^-40 of that);
- * statistics of the softmax are float32
- * within a block of columns and float64 beyond; exponentials of 16-bit rows are
- * kept with 11 bits of mantissa (bf16: 10), down to 2^-30 (2^-29) of the largest
- * of their block of 64 or 128 columns and to an absolute 2^-42 (2^-40) of it
- * below; G is rounded to the rows' type (float32: to 22 bits) before its two
- * products, also where grad_dtype is SPS_F32, and their float32 sums are
- * rounded once to grad_dtype. fp16 and float32: G is scaled by a power of two
- * so that the largest weight uses fp16's range; gradients of weights more than
- * about 2^24 below it lose precision. Bitwise reproducible. */
+ * Roundings. Products of 16-bit rows are exact and summed in float32; float32
+ * rows are multiplied with 22 bits of each value (fewer below 2^-17 of the
+ * largest of its row, for the gradients of the whole matrix: an absolute 2^-39
+ * of that). Without a bias a softmax goes by differences of these sums, exact
+ * near the largest; with one, z is rounded to float32 first. Statistics of the
+ * softmax are float32 within a block of 64 or 128 columns and float64 beyond.
+ * Exponentials of 16-bit rows are kept with 11 bits of mantissa (bf16: 10), down
+ * to 2^-30 (2^-29) of the largest of their block and to an absolute 2^-42
+ * (2^-40) of it below. G is rounded to the rows' type (float32: to 22 bits)
+ * before its two products, also where grad_dtype is SPS_F32; their float32 sums
+ * are rounded once to grad_dtype. fp16 and float32: G is scaled by a power of
+ * two so that the largest weight uses fp16's range. What counts is a row's
+ * weight times a probability: from 2^-28 (float32: 2^-17) of the largest weight
+ * on it keeps all its bits, and below it is off by up to an absolute 2^-39 of
+ * the largest weight, whatever its row's own. (At 2^-24 of the largest weight a
+ * row's gradient over many items is little more than its target's term.)
+ * Bitwise reproducible. */
 
 /* Bytes of the workspace of sps_dense_ce for these rows (their addresses and
  * ld matter, nothing is read), with either gradient or both. Pure host. It

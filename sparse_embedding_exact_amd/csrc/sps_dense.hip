@@ -19,8 +19,8 @@
 // to 2^-28 of that weight G keeps all its bits.
 // float32: operands and G stand in two planes of fp16, scaled by powers of two
 // (each row for the logits, the matrix for the products with G, whose sums go
-// over rows), so that a value keeps 22 bits down to 2^-18 of the largest and
-// an absolute 2^-40 of it below; three products of planes leave out what is
+// over rows), so that a value keeps 22 bits down to 2^-17 of the largest and
+// an absolute 2^-39 of it below; three products of planes leave out what is
 // below 2^-22 of a product. (Three planes of bf16 and six products of them:
 // 1000 x 30,522 x 384 605 us instead of 389.)
 // Bound by the three products: 8192 x 100,000 x 1024 bf16 takes 5.08 ms, of which

@@ -1,9 +1,9 @@
 """Small parts of the cross entropy's gradient: items of little probability beside one that is
-nearly certain."""
+nearly certain, rows of little weight."""
 import pytest
 
 import dense_oracle as do
-from test_gpu_dense_ce import env  # noqa: F401
+from test_gpu_dense_ce import TYPES, check, env, make  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +28,16 @@ def test_little_probability_beside_a_certain_item(env, dtype, m):  # noqa: F811
     off = ((gi[:, 0].double() - p).abs() / p)[1:]
     code = 2.0 ** -12 if dtype == "float16" else 2.0 ** -11
     assert (off <= do.HALF[dtype] + code + 2.0 ** -15).all(), float(off.max())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m", [300, 20000])
+def test_weights_far_apart(env, dtype, m):  # noqa: F811
+    """Weights from 1 down to 2^-20 over a softmax without favourites: every row within the bound
+    that goes by the weight times the probability."""
+    torch, sps, dev = env
+    x, w, t, _, _ = make(env, 63, m, 40, dtype, 8, masked=False, weighted=False)
+    ww = torch.exp2(-torch.arange(63, device=dev) / 3.0).float()
+    x = x * 0.05
+    got = sps.dense_cross_entropy(x, w, t, 1.0, None, ww, grad_dtype=torch.float32)
+    check(env, got, x, w, t, 1.0, None, ww, out="float32")
