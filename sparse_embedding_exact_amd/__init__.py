@@ -1119,7 +1119,9 @@ def int8_scores(queries: Int8Rows, items: Int8Rows, out: torch.Tensor | None = N
 def int8_select(queries: Int8Rows, items: Int8Rows, k: int, chunk_size: int = 65536) -> TopRows:
     """The best k items of every query by their 8-bit rows' scores, exact, ties to the lower
     item: every chunk scored and joined to the running lists (bulk_select's loop). Queries go
-    in batches, so that a chunk's scores stay within 2 GiB."""
+    in batches, so that a chunk's scores stay within 2 GiB. A chunk is two calls: for few
+    queries a chunk_size of all the items is the fastest (one query, 2M items of 768 dims: 744
+    us in chunks of 65,536, 334 in one)."""
     _here(queries.values, queries.scales, items.values, items.scales)
     n, m = queries.n_rows, items.n_rows
     dev = queries.values.device

@@ -23,9 +23,10 @@
 // an absolute 2^-39 of it below; three products of planes leave out what is
 // below 2^-22 of a product. (Three planes of bf16 and six products of them:
 // 1000 x 30,522 x 384 605 us instead of 389.)
-// Bound by the three products: 8192 x 100,000 x 1024 bf16 takes 5.08 ms, of which
-// the logits 1.64 (1.02 PFLOP/s with codes stored), both other products 2.63
-// (1.28), codes to G 0.69, rows laid out 0.12.
+// Bound by the three products: 8192 x 100,000 x 1024 bf16 takes 5.03 ms, of which
+// the logits 1.62 to 1.68 (1.03 to 1.0 PFLOP/s; a library's product of that shape
+// 1.34 ms, without exponentials, sums and codes), both other products 2.59 to
+// 2.74 (1.29 to 1.22), codes to G 0.70, rows laid out 0.12.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -402,7 +403,7 @@ __global__ __launch_bounds__(64 * WC * WR) void ce_logits_kernel(LogitArgs a) {
         float p[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // The difference to the largest first, 0 there and exact near by however large both are; then
+          // The difference to the largest first: 0 there, and exact near by, however large both are. Then
           // the shift. (A second part of c would be a part of this rounding.)
           p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(t.acc[i][j][e] - base, a.c, (float)Code::kShift));
           sum += p[e];

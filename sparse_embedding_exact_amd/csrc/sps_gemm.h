@@ -632,7 +632,9 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // and without parts (us): 256 x 256 x 128 float32 43.5, 44.0, 66.7, 44.9;
 // 400 x 5000 x 512 bf16 50, 50, 68, 83; 2000 x 8192 x 768 138, 143, 158, 155;
 // 1000 x 30,522 x 384 float32 390, 402, 391, 1253; 4095 x 30,522 x 768 701, 776,
-// 692, 896; 8192 x 100,000 x 1024 5206, 6612, 5147, 6666.
+// 692, 896; 8192 x 100,000 x 1024 5206, 6612, 5147, 6666. Over 24 other sizes (64 to
+// 8192 queries, 600 to 130,000 items, 76 to 1012 dims, every type) at most 5 % above
+// the better of small and large tiles, the losses alone at most 6 %.
 constexpr int kCus = 256;
 struct TilePlan {
   bool big;

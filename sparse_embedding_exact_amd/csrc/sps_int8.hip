@@ -59,9 +59,9 @@ __device__ __forceinline__ int32_t nearest_int8(float x, float y, float amax) {
 
 // L lanes a row, so that most rows fit the four vectors that a lane keeps in
 // registers between the maximum and the integers and few lanes are left over;
-// what does not fit is read again (from the caches). 500,000 x 333 float32 in 166
-// us, 5.0 TB/s, bound by memory; bf16 in 139, 3.6 TB/s, by its instructions, a
-// wave's 4 cycles each (two vectors a lane: 182, eight spill: 275; 64 lanes for
+// what does not fit is read again (from the caches). 500,000 x 333 float32 in 151
+// to 173 us, 5.5 to 4.8 TB/s, bound by memory; bf16 in 132 to 158 and fp16 in 134
+// to 144, 3.8 to 3.2 TB/s, by their instructions, a wave's 4 cycles each (two vectors a lane: 182, eight spill: 275; 64 lanes for
 // every row, before: 230 instead of 144).
 constexpr int kQuantKeep = 4;
 template <typename T, int L>
